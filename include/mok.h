@@ -264,6 +264,20 @@ mok_status mok_forward(mok_workspace* ws, mok_mode mode, const void* schedule, s
                        void* out, void* context, size_t context_bytes, void* stream);
 
 /*
+ * The MXFP8 forward of mok_forward for tokens that are already in MXFP8
+ * (codes from mok_rms_norm or mok_mxfp8_quantize): x_codes E4M3 [T, H] and
+ * x_scale E8M0 [T, H/32], both dense, 16- and 4-byte aligned
+ * (MOK_ERR_UNSUPPORTED otherwise). The launch that quantizes x is left out;
+ * everything else, arguments and results, is as in mok_forward with
+ * MOK_MODE_MXFP8, and with the codes that mok_mxfp8_quantize(axis = 1) gives
+ * for a bf16 x the output bits are those of mok_forward on that x. A
+ * backward on the context still takes x in bf16.
+ */
+mok_status mok_forward_mxfp8(mok_workspace* ws, const void* schedule, size_t schedule_bytes, const uint8_t* x_codes,
+                             const uint8_t* x_scale, const float* router_weights, const mok_weights* weights,
+                             void* out, void* context, size_t context_bytes, void* stream);
+
+/*
  * Backward ([A] _MoKRuntime.backward): gradients of sum(grad_out * out) for
  * every float input, reusing the forward's schedule and context. grad_out,
  * x bf16 [T, H]; router_weights fp32 [T, k]. In BF16 mode `weights` are the
@@ -352,6 +366,159 @@ mok_status mok_mxfp8_quantize(const void* src, int src_is_fp32, int64_t rows, in
  */
 mok_status mok_mxfp8_quantize_transposed(const void* src, int64_t batches, int64_t rows, int64_t cols, uint8_t* dst,
                                          uint8_t* dst_scale, void* stream);
+
+/* ---- the operators around the layer ----------------------------------
+ *
+ * What the block that holds the layer needs next to it: the norm in front,
+ * the router, and the optimizer's step. They need no workspace and keep
+ * nothing between calls; they run on the current device, to which `stream`
+ * and every pointer must belong. As everywhere, they only enqueue work, and
+ * are deterministic: the same inputs give the same bits. Row strides (ld_*)
+ * are in elements and at least the row's length; outputs are dense. */
+
+/*
+ * RMS norm with the residual's addition. Per row of `cols` elements:
+ *   s = x + residual (s = x without one)
+ *   rstd = (mean(s^2) + eps)^-1/2,   y = s * rstd * weight
+ * in fp32, each output rounded once: y comes from the fp32 sum, not from its
+ * rounding. x is bf16 or fp32; residual (nullable) has x's type or, for bf16
+ * x, may be fp32 (fp32 x with a bf16 residual: MOK_ERR_UNSUPPORTED); weight
+ * [cols] bf16 or fp32. Outputs:
+ *   sum    [rows, cols] in the residual's type; non-NULL iff residual is. It
+ *          may be the residual's own buffer (dense), or x's if of its type.
+ *   y      bf16 [rows, cols], nullable.
+ *   codes, scale   y in MXFP8 along a row (both or neither): E4M3 [rows,
+ *          cols] and E8M0 [rows, cols/32] by the rule of mok_mxfp8_quantize,
+ *          taken from the fp32 y (not from its bf16 rounding), the form that
+ *          mok_forward_mxfp8 reads. A block that holds an infinity or a NaN
+ *          gets the NaN scale 0xFF. Needs cols % 32 == 0, cols <= 16384, row
+ *          strides % 8 == 0, 16-byte aligned tensors and 8-byte aligned
+ *          codes (MOK_ERR_UNSUPPORTED otherwise).
+ *   rstd   fp32 [rows], nullable: what the backward needs besides s.
+ * At least one output must be asked for. Without codes every width, stride
+ * and alignment is accepted; cols % 8 == 0, cols <= 16384, strides % 8 == 0
+ * and 16-byte alignment run the fast kernel. The sum of squares is an fp32
+ * sum: rows with |s| above about 1e18 overflow it (rstd 0).
+ */
+mok_status mok_rms_norm(const void* x, int x_is_fp32, int64_t ld_x, const void* residual, int residual_is_fp32,
+                        int64_t ld_residual, const void* weight, int weight_is_fp32, int64_t rows, int64_t cols,
+                        float eps, void* sum, void* y, uint8_t* codes, uint8_t* scale, float* rstd, void* stream);
+
+/* Bytes of mok_rms_norm_backward's scratch; 0 if the sizes are invalid. */
+size_t mok_rms_norm_scratch_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Backward of mok_rms_norm from the saved s (the forward's sum, or its x
+ * without a residual; bf16 or fp32) and rstd. dy bf16. With xh = s * rstd
+ * and g = dy * weight:
+ *   ds = rstd * (g - xh * mean(g * xh)) + d_sum,   d_weight = sum over rows of dy * xh
+ * ds [rows, cols] in s's type is the gradient of both x and the residual;
+ * dx (nullable) receives it in bf16 as well, for a bf16 x with an fp32
+ * residual. d_sum (nullable, s's type) is the gradient that arrives through
+ * the sum; ds may be its buffer (dense). d_weight [cols] in weight's type is
+ * written in full, zeros for rows = 0. scratch: 16-byte aligned device
+ * memory of at least mok_rms_norm_scratch_bytes(rows, cols), the call's own
+ * until its work has run.
+ */
+mok_status mok_rms_norm_backward(const void* dy, int64_t ld_dy, const void* s, int s_is_fp32, int64_t ld_s,
+                                 const float* rstd, const void* weight, int weight_is_fp32, const void* d_sum,
+                                 int64_t ld_d_sum, int64_t rows, int64_t cols, void* ds, void* dx, void* d_weight,
+                                 void* scratch, size_t scratch_bytes, void* stream);
+
+/* Scores of the router. */
+typedef enum mok_router_scoring {
+  MOK_ROUTER_SOFTMAX = 0, /* softmax over the experts */
+  MOK_ROUTER_SIGMOID = 1  /* sigmoid of each logit */
+} mok_router_scoring;
+
+/* Bytes of mok_router_topk's scratch (needed only with counts); 0 if the
+ * sizes are invalid. */
+size_t mok_router_scratch_bytes(int64_t T, int32_t experts);
+
+/*
+ * Top-k routing of T tokens from logits [T, experts] (bf16 or fp32): the
+ * router_weights and top_experts that the layer takes.
+ *   key   = logit + bias, one fp32 addition (bias fp32 [experts], nullable:
+ *           it selects only, the weights do not see it)
+ *   ids   int64 [T, k]: the k largest keys in descending order, ties to the
+ *         lowest expert id. A key of -inf is never chosen: where fewer than
+ *         k are left, id -1 and weight 0 (mok_build_schedule does not
+ *         dispatch such an assignment).
+ *   weights fp32 [T, k]: the scores of the chosen, divided by their sum if
+ *         `renormalize`, times `scale`.
+ * token_mask (nullable, one byte per token): tokens with a 0 get ids -1 and
+ * weights 0, whatever their logits hold. A row with a NaN key or a +inf
+ * logit has no order: ids -1 and weights NaN.
+ * Statistics (counts and losses, both or neither; then scratch is needed):
+ *   counts int32 [experts + 1]: choices of each expert, then the number n of
+ *         live tokens: kept by the mask, with a key above -inf (or no order)
+ *   losses fp32 [2], with p = the scores divided by their sum over the
+ *         experts and N = max(n, 1): the load-balance loss experts / (k N^2)
+ *         * sum_e counts_e * (sum of p_e over live tokens), and the z loss,
+ *         the mean over live tokens of logsumexp(logits)^2 (0 for sigmoid).
+ * 1 <= k <= min(experts, 64), experts <= 1024.
+ */
+mok_status mok_router_topk(const void* logits, int logits_is_fp32, int64_t T, int64_t ld, int32_t experts, int32_t k,
+                           const float* bias, const uint8_t* token_mask, int32_t scoring, int renormalize, float scale,
+                           float* weights, int64_t* ids, int32_t* counts, float* losses, void* scratch,
+                           size_t scratch_bytes, void* stream);
+
+/*
+ * Gradient to the logits: d_logits [T, experts] (dense, the logits' type),
+ * every element written, from d_weights fp32 [T, k], the forward's ids and,
+ * if the losses have a gradient, d_losses fp32 [2] with the forward's counts
+ * (both or neither). The choice itself and counts are constants. Choices
+ * with an id outside [0, experts) get no gradient; tokens that are masked
+ * out or have no key above -inf get zeros, a row without an order NaN.
+ */
+mok_status mok_router_topk_backward(const float* d_weights, const void* logits, int logits_is_fp32, int64_t T,
+                                    int64_t ld, int32_t experts, int32_t k, const float* bias,
+                                    const uint8_t* token_mask, int32_t scoring, int renormalize, float scale,
+                                    const int64_t* ids, const int32_t* counts, const float* d_losses, void* d_logits,
+                                    void* stream);
+
+/*
+ * One AdamW step of `count` dense tensors. The arrays are host arrays of
+ * `count` device pointers, read before the call returns. Set struct_size =
+ * sizeof(mok_adamw). Per element, in fp32:
+ *   g = grad * grad_scale,  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+ *   p = p (1 - lr wd) - lr / (1 - b1^step) * m / (sqrt(v / (1 - b2^step)) + eps)
+ * params bf16 or fp32; with masters (bf16 params only) p is the fp32 master
+ * and the param receives its rounding. exp_avgs hold m, exp_avg_sqs v, in
+ * fp32 (state_bits 32), or (state_bits 8) as E4M3 codes [numel] of m and of
+ * sqrt(v), with one E8M0 scale byte per 32 consecutive elements (the last
+ * block may be shorter), [ceil(numel/32)]; all-zero bytes are zero moments.
+ * A block's scale is the smallest power of two that keeps its largest
+ * magnitude within 448 of it (0xFF, NaN, if that is not finite). m is
+ * rounded to the nearest code; sqrt(v) to one of the two codes around it,
+ * chosen at random so that the mean of its square is v, from `seed` and the
+ * element's number in the call (tensors are numbered one after the other,
+ * each from a multiple of 32, modulo 2^32): the same seed gives the same
+ * bits, and each step should have its own.
+ * Tensors of the call must not overlap. grad_scale (nullable): a device
+ * fp32, read when the kernel runs. lr, step and seed are values of the call:
+ * a captured graph repeats them.
+ */
+typedef struct mok_adamw {
+  uint32_t struct_size;
+  int32_t count;
+  void* const* params;
+  const void* const* grads;
+  void* const* masters;           /* NULL: none */
+  void* const* exp_avgs;
+  void* const* exp_avg_sqs;
+  void* const* exp_avg_scales;    /* NULL iff state_bits is 32 */
+  void* const* exp_avg_sq_scales;
+  const int64_t* numels;
+  const float* grad_scale;        /* device; NULL: 1 */
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;                   /* from 1 */
+  int32_t param_fp32, grad_fp32;  /* 0: bf16 */
+  int32_t state_bits;             /* 32 or 8 */
+  uint32_t seed;
+} mok_adamw;
+
+mok_status mok_adamw_step(const mok_adamw* step, void* stream);
 
 /* ---- diagnostics (these synchronise; never on the hot path) ---------- */
 

@@ -22,11 +22,14 @@ import torch
 
 from . import _lib
 from ._lib import (MOK_MODE_BF16, MOK_MODE_MXFP8, HDR_FIELDS, TILE_BMS, MokError)
+from .ops import adamw_step, rms_norm, rms_norm_backward, rms_norm_mxfp8, router_topk, router_topk_backward
 
 __all__ = ["MoKConfig", "Workspace", "create_workspace", "get_workspace", "clear_workspace_cache",
            "build_schedule", "forward", "forward_static", "backward", "mxfp8_quantize",
            "mxfp8_quantize_transposed", "mxfp8_backward_weights", "schedule_fields",
-           "schedule_bytes", "context_bytes", "workspace_bytes", "MokError", "MOK_MODE_BF16", "MOK_MODE_MXFP8", "lib"]
+           "schedule_bytes", "context_bytes", "workspace_bytes", "MokError", "MOK_MODE_BF16", "MOK_MODE_MXFP8", "lib",
+           "forward_mxfp8", "rms_norm", "rms_norm_mxfp8", "rms_norm_backward", "router_topk", "router_topk_backward",
+           "adamw_step"]
 
 
 def lib():
@@ -249,6 +252,26 @@ def forward(ws: Workspace, schedule: torch.Tensor, x: torch.Tensor, router_weigh
     _lib.check("mok_forward", lib().mok_forward(
         ws.handle, mode, _ptr(schedule), schedule.numel(), _ptr(x), _ptr(router_weights), C.byref(ws_w),
         _ptr(out), _ptr(context), 0 if context is None else context.numel(), _stream()))
+    return out
+
+
+def forward_mxfp8(ws: Workspace, schedule: torch.Tensor, x_codes: torch.Tensor, x_scale: torch.Tensor,
+                  router_weights: torch.Tensor, weights: dict, out: torch.Tensor | None = None,
+                  context: torch.Tensor | None = None) -> torch.Tensor:
+    """The MXFP8 ``forward`` for tokens already in MXFP8: codes uint8 [T, H]
+    and scales uint8 [T, H/32], as ``rms_norm_mxfp8`` or ``mxfp8_quantize``
+    give them. Skips the launch that quantizes x."""
+    H = ws.cfg.hidden
+    if x_codes.dtype != torch.uint8 or x_scale.dtype != torch.uint8 or router_weights.dtype != torch.float32:
+        raise ValueError("x_codes and x_scale must be uint8 and router_weights fp32")
+    if x_codes.dim() != 2 or x_codes.shape[1] != H or x_scale.shape != (x_codes.shape[0], H // 32):
+        raise ValueError("x_codes must be [T, hidden] and x_scale [T, hidden/32]")
+    if out is None:
+        out = torch.empty(x_codes.shape, dtype=torch.bfloat16, device=x_codes.device)
+    ws_w = _weights(weights)
+    _lib.check("mok_forward_mxfp8", lib().mok_forward_mxfp8(
+        ws.handle, _ptr(schedule), schedule.numel(), _ptr(x_codes), _ptr(x_scale), _ptr(router_weights),
+        C.byref(ws_w), _ptr(out), _ptr(context), 0 if context is None else context.numel(), _stream()))
     return out
 
 

@@ -19,13 +19,18 @@ MOK_ERR_HIP = 5
 MOK_MODE_BF16 = 0
 MOK_MODE_MXFP8 = 1
 
+MOK_ROUTER_SOFTMAX = 0
+MOK_ROUTER_SIGMOID = 1
+
 # Every symbol include/mok.h declares (checked by the CPU tests).
 EXPORTS = (
     "mok_status_string", "mok_validate_config", "mok_schedule_bytes", "mok_schedule_layout_query",
     "mok_context_bytes", "mok_workspace_bytes", "mok_workspace_create", "mok_workspace_destroy",
     "mok_build_schedule", "mok_forward", "mok_forward_static", "mok_backward", "mok_mxfp8_quantize", "mok_mxfp8_quantize_transposed", "mok_kernel_name",
     "mok_workspace_set_timing", "mok_workspace_set_timing_mask", "mok_workspace_read_timing",
-    "mok_workspace_read_status",
+    "mok_workspace_read_status", "mok_forward_mxfp8", "mok_rms_norm", "mok_rms_norm_scratch_bytes",
+    "mok_rms_norm_backward", "mok_router_scratch_bytes", "mok_router_topk", "mok_router_topk_backward",
+    "mok_adamw_step",
 )
 
 HDR_FIELDS = ("T", "k", "E", "C", "P", "rows_cap", "n_mb", "minibatch", "dropped", "invalid",
@@ -72,6 +77,14 @@ class MokScheduleLayout(C.Structure):
         ("rows_cap_max", C.c_int64), ("n_mb_max", C.c_int64)]
 
 
+class MokAdamW(C.Structure):
+    _fields_ = [("struct_size", C.c_uint32), ("count", C.c_int32)] + [(n, C.c_void_p) for n in (
+        "params", "grads", "masters", "exp_avgs", "exp_avg_sqs", "exp_avg_scales", "exp_avg_sq_scales", "numels",
+        "grad_scale")] + [(n, C.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", C.c_int64), ("param_fp32", C.c_int32), ("grad_fp32", C.c_int32), ("state_bits", C.c_int32),
+        ("seed", C.c_uint32)]
+
+
 _lib = None
 
 
@@ -108,6 +121,20 @@ def load() -> C.CDLL:
         "mok_workspace_read_timing": (i32, [vp, C.POINTER(C.c_float), C.POINTER(i64), i32]),
         "mok_workspace_read_status": (i32, [vp, C.POINTER(C.c_int32), C.POINTER(C.c_int32)]),
     }
+    f32 = C.c_float
+    sig.update({
+        "mok_forward_mxfp8": (i32, [vp, vp, sz, vp, vp, vp, C.POINTER(MokWeights), vp, vp, sz, vp]),
+        "mok_rms_norm": (i32, [vp, i32, i64, vp, i32, i64, vp, i32, i64, i64, f32, vp, vp, vp, vp, vp, vp]),
+        "mok_rms_norm_scratch_bytes": (sz, [i64, i64]),
+        "mok_rms_norm_backward": (i32, [vp, i64, vp, i32, i64, vp, vp, i32, vp, i64, i64, i64, vp, vp, vp, vp, sz,
+                                        vp]),
+        "mok_router_scratch_bytes": (sz, [i64, C.c_int32]),
+        "mok_router_topk": (i32, [vp, i32, i64, i64, C.c_int32, C.c_int32, vp, vp, C.c_int32, i32, f32, vp, vp, vp,
+                                  vp, vp, sz, vp]),
+        "mok_router_topk_backward": (i32, [vp, vp, i32, i64, i64, C.c_int32, C.c_int32, vp, vp, C.c_int32, i32, f32,
+                                           vp, vp, vp, vp, vp]),
+        "mok_adamw_step": (i32, [C.POINTER(MokAdamW), vp]),
+    })
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
         f.restype = res

@@ -26,6 +26,11 @@ read for one GPU:
   in-place version counter moves (an optimizer step, a ``copy_``), so a
   step never runs on stale codes.
 
+Around the layer: ``rms_norm`` and ``MoKRMSNorm`` (the norm in front of it,
+with the residual's addition) and ``router_topk`` and ``MoKRouter`` (the
+top-k router, with its load statistics and losses), differentiable in every
+float input; the schedule takes their expert ids as they are.
+
 Every step of the layer runs in the library's HIP kernels; tensors on the
 CPU are rejected.
 """
@@ -37,9 +42,10 @@ import weakref
 import torch
 
 from . import (MOK_MODE_BF16, MOK_MODE_MXFP8, MoKConfig, backward, build_schedule, context_bytes, forward,
-               get_workspace, mxfp8_quantize, mxfp8_quantize_transposed)
+               get_workspace, mxfp8_quantize, mxfp8_quantize_transposed, ops)
 
-__all__ = ["MoKRuntime", "MoKAutogradFunction", "MoKExperts", "moe_layer"]
+__all__ = ["MoKRuntime", "MoKAutogradFunction", "MoKExperts", "moe_layer", "rms_norm", "MoKRMSNorm", "router_topk",
+           "MoKRouter"]
 
 _WEIGHT_NAMES = ("shared_gate", "shared_up", "shared_down", "routed_gate", "routed_up", "routed_down")
 
@@ -244,3 +250,123 @@ class MoKExperts(torch.nn.Module):
         return (f"hidden={c.hidden}, intermediate={c.intermediate}, experts={c.num_experts}, topk={c.topk}, "
                 f"shared_intermediate={c.shared_intermediate}, max_tokens={c.max_tokens}, mode={mode}")
 
+
+
+class RMSNormFunction(torch.autograd.Function):
+    """(y, sum) of the RMS norm with the residual's addition; sum is None
+    without a residual. Keeps the sum (or x) and one fp32 per row."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        y, total, rstd = ops.rms_norm(x, weight, residual, eps)
+        ctx.save_for_backward(x if total is None else total, rstd, weight)
+        ctx.x_dtype = x.dtype
+        ctx.set_materialize_grads(False)
+        return y, total
+
+    @staticmethod
+    def backward(ctx, dy, d_sum):
+        s, rstd, weight = ctx.saved_tensors
+        need_x, need_w, need_r = ctx.needs_input_grad[:3]
+        if d_sum is not None:
+            d_sum = d_sum.contiguous()
+        if dy is None:  # only the sum was used
+            dw = torch.zeros_like(weight) if need_w else None
+            dx = d_sum.to(ctx.x_dtype) if need_x and d_sum is not None else None
+            return dx, dw, d_sum if need_r else None, None
+        narrow = torch.empty(s.shape, dtype=ctx.x_dtype, device=s.device) if ctx.x_dtype != s.dtype else None
+        ds, dw = ops.rms_norm_backward(dy.contiguous(), s, rstd, weight, d_sum, dx=narrow)
+        dx = ds if narrow is None else narrow
+        return dx if need_x else None, dw if need_w else None, ds if need_r else None, None
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6):
+    """Differentiable ``ops.rms_norm``: (y, sum) with y bf16 and sum = x +
+    residual in the residual's type (None without a residual)."""
+    return RMSNormFunction.apply(x, weight, residual, eps)
+
+
+class MoKRMSNorm(torch.nn.Module):
+    """The norm in front of the layer: forward(x, residual) -> (y, sum)."""
+
+    def __init__(self, hidden: int, eps: float = 1e-6, dtype: torch.dtype = torch.bfloat16, device=None):
+        super().__init__()
+        self.eps = eps
+        self.weight = torch.nn.Parameter(torch.ones(hidden, dtype=dtype, device=device))
+
+    def forward(self, x, residual=None):
+        return rms_norm(x, self.weight, residual, self.eps)
+
+    def extra_repr(self) -> str:
+        return f"hidden={self.weight.shape[0]}, eps={self.eps}"
+
+
+class RouterFunction(torch.autograd.Function):
+    """(weights, ids, counts, losses) of the top-k router, differentiable in
+    the logits through weights and losses (counts and losses None unless
+    asked for)."""
+
+    @staticmethod
+    def forward(ctx, logits, k, how, want_losses):
+        out = ops.router_topk(logits, k, losses=want_losses, **how)
+        weights, ids = out[:2]
+        counts, losses = out[2:] if want_losses else (None, None)
+        ctx.how = {n: v for n, v in how.items() if not isinstance(v, torch.Tensor)}
+        ctx.tensors = [n for n, v in how.items() if isinstance(v, torch.Tensor)]
+        ctx.save_for_backward(logits, ids, counts, *[how[n] for n in ctx.tensors])
+        ctx.mark_non_differentiable(*[t for t in (ids, counts) if t is not None])
+        ctx.set_materialize_grads(False)
+        return weights, ids, counts, losses
+
+    @staticmethod
+    def backward(ctx, d_weights, _ids, _counts, d_losses):
+        logits, ids, counts, *rest = ctx.saved_tensors
+        if d_weights is None and d_losses is None:
+            return None, None, None, None
+        if d_weights is None:
+            d_weights = torch.zeros(ids.shape, dtype=torch.float32, device=ids.device)
+        dl = ops.router_topk_backward(d_weights.contiguous(), logits, ids, **ctx.how, **dict(zip(ctx.tensors, rest)),
+                                      counts=counts if d_losses is not None else None,
+                                      d_losses=None if d_losses is None else d_losses.contiguous())
+        return dl, None, None, None
+
+
+def router_topk(logits: torch.Tensor, k: int, *, scoring: str = "softmax", renormalize: bool = True,
+                scale: float = 1.0, bias: torch.Tensor | None = None, token_mask: torch.Tensor | None = None,
+                losses: bool = False):
+    """Differentiable ``ops.router_topk``: (weights, ids), and with
+    ``losses`` also (counts, losses). ``bias`` only selects: it gets no
+    gradient."""
+    how = dict(scoring=scoring, renormalize=renormalize, scale=scale,
+               bias=None if bias is None else bias.detach(), token_mask=token_mask)
+    out = RouterFunction.apply(logits, k, how, losses)
+    return out if losses else out[:2]
+
+
+class MoKRouter(torch.nn.Module):
+    """Router of the layer: logits = x W^T in fp32 (a library product), then
+    ``router_topk``. forward(x [T, H], token_mask) -> (weights fp32 [T, k],
+    ids int64 [T, k]), and with ``losses`` also (counts, losses). With
+    ``selection_bias`` the module keeps an fp32 buffer that shifts the choice
+    alone, for balancing without a loss: move it by the counts."""
+
+    def __init__(self, hidden: int, num_experts: int, topk: int, scoring: str = "softmax", renormalize: bool = True,
+                 scale: float = 1.0, selection_bias: bool = False, losses: bool = False, device=None):
+        super().__init__()
+        self.topk, self.scoring, self.renormalize, self.scale, self.losses = topk, scoring, renormalize, scale, losses
+        self.weight = torch.nn.Parameter(torch.zeros(num_experts, hidden, dtype=torch.float32, device=device))
+        bias = torch.zeros(num_experts, dtype=torch.float32, device=device) if selection_bias else None
+        self.register_buffer("bias", bias)
+
+    @torch.no_grad()
+    def init_weights(self, init_std: float = 0.02, generator: torch.Generator | None = None) -> None:
+        self.weight.copy_(torch.randn(self.weight.shape, generator=generator, dtype=torch.float32).mul_(init_std))
+
+    def forward(self, x, token_mask=None):
+        logits = torch.nn.functional.linear(x.float(), self.weight)
+        return router_topk(logits, self.topk, scoring=self.scoring, renormalize=self.renormalize, scale=self.scale,
+                           bias=self.bias, token_mask=token_mask, losses=self.losses)
+
+    def extra_repr(self) -> str:
+        return (f"hidden={self.weight.shape[1]}, experts={self.weight.shape[0]}, topk={self.topk}, "
+                f"scoring={self.scoring}, renormalize={self.renormalize}, scale={self.scale}")

@@ -525,10 +525,13 @@ mok_status check_weights(const mok_config& c, mok_mode mode, const mok_weights* 
 }
 }  // namespace mok
 
-extern "C" mok_status mok_forward(mok_workspace* ws, mok_mode mode, const void* schedule, size_t schedule_bytes,
-                                  const void* x, const float* router_weights, const mok_weights* weights, void* out,
-                                  void* context, size_t context_bytes, void* stream) {
-  if (!ws || !schedule || !x || !router_weights || !out) return MOK_ERR_INVALID_ARGUMENT;
+// The forward of x in bf16, or (xq non-null, MXFP8 only) of x already in
+// codes and scales.
+static mok_status forward_entry(mok_workspace* ws, mok_mode mode, const void* schedule, size_t schedule_bytes,
+                                const void* x, const uint8_t* xq, const uint8_t* xq_scale,
+                                const float* router_weights, const mok_weights* weights, void* out, void* context,
+                                size_t context_bytes, void* stream) {
+  if (!ws || !schedule || !router_weights || !out) return MOK_ERR_INVALID_ARGUMENT;
   if (mode != MOK_MODE_BF16 && mode != MOK_MODE_MXFP8) return MOK_ERR_INVALID_ARGUMENT;
   if (schedule_bytes < ws->layout.total) return MOK_ERR_BUFFER_TOO_SMALL;
   mok_status st = check_weights(ws->cfg, mode, weights, true);
@@ -541,6 +544,8 @@ extern "C" mok_status mok_forward(mok_workspace* ws, mok_mode mode, const void* 
   FwdArgs a{};
   a.w = weights;
   a.x = x;
+  a.xq = xq;
+  a.xq_scale = xq_scale;
   a.router_w = router_weights;
   a.out = out;
   a.mxfp8 = mode == MOK_MODE_MXFP8;
@@ -572,13 +577,36 @@ extern "C" mok_status mok_forward(mok_workspace* ws, mok_mode mode, const void* 
     hipError_t e = launch_sched_slice(ws, schedule, (int)pass, ws->pass_sched, s);
     if (e != hipSuccess) return to_status(e);
     FwdArgs b = a;
-    b.x = (const uint16_t*)x + pass * M * H;
+    if (xq) {
+      b.xq = xq + pass * M * H;
+      b.xq_scale = xq_scale + pass * M * (H / 32);
+    } else {
+      b.x = (const uint16_t*)x + pass * M * H;
+    }
     b.router_w = router_weights + pass * M * k;
     b.out = (uint16_t*)out + pass * M * H;
     e = launch_forward(ws, qc, QL, ws->pass_sched, b, s);
     if (e != hipSuccess) return to_status(e);
   }
   return MOK_OK;
+}
+
+extern "C" mok_status mok_forward(mok_workspace* ws, mok_mode mode, const void* schedule, size_t schedule_bytes,
+                                  const void* x, const float* router_weights, const mok_weights* weights, void* out,
+                                  void* context, size_t context_bytes, void* stream) {
+  if (!x) return MOK_ERR_INVALID_ARGUMENT;
+  return forward_entry(ws, mode, schedule, schedule_bytes, x, nullptr, nullptr, router_weights, weights, out, context,
+                       context_bytes, stream);
+}
+
+extern "C" mok_status mok_forward_mxfp8(mok_workspace* ws, const void* schedule, size_t schedule_bytes,
+                                        const uint8_t* x_codes, const uint8_t* x_scale, const float* router_weights,
+                                        const mok_weights* weights, void* out, void* context, size_t context_bytes,
+                                        void* stream) {
+  if (!x_codes || !x_scale) return MOK_ERR_INVALID_ARGUMENT;
+  if ((((uintptr_t)x_codes) & 15) || (((uintptr_t)x_scale) & 3)) return MOK_ERR_UNSUPPORTED;
+  return forward_entry(ws, MOK_MODE_MXFP8, schedule, schedule_bytes, nullptr, x_codes, x_scale, router_weights,
+                       weights, out, context, context_bytes, stream);
 }
 
 extern "C" mok_status mok_backward(mok_workspace* ws, mok_mode mode, const void* schedule, size_t schedule_bytes,
@@ -660,6 +688,191 @@ extern "C" mok_status mok_mxfp8_quantize_transposed(const void* src, int64_t bat
                  hipSuccess
              ? MOK_OK
              : MOK_ERR_HIP;
+}
+
+// ------------------------------------------------------------------------
+// The operators around the layer
+// ------------------------------------------------------------------------
+namespace {
+// Compute units of the current device (0 = no device).
+int current_cus() {
+  int dev = -1, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+    return 0;
+  return cus;
+}
+bool flag(int f) { return f == 0 || f == 1; }
+// p (bf16 or fp32) sits at a multiple of its element size
+bool element_aligned(const void* p, int fp32) { return (((uintptr_t)p) & (fp32 ? 3 : 1)) == 0; }
+constexpr int64_t kMaxNormRows = (int64_t)1 << 40, kMaxNormCols = (int64_t)1 << 24;
+}  // namespace
+
+extern "C" mok_status mok_rms_norm(const void* x, int x_is_fp32, int64_t ld_x, const void* residual,
+                                   int residual_is_fp32, int64_t ld_residual, const void* weight, int weight_is_fp32,
+                                   int64_t rows, int64_t cols, float eps, void* sum, void* y, uint8_t* codes,
+                                   uint8_t* scale, float* rstd, void* stream) {
+  if (rows < 0 || cols < 1 || !flag(x_is_fp32) || !flag(residual_is_fp32) || !flag(weight_is_fp32))
+    return MOK_ERR_INVALID_ARGUMENT;
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return MOK_ERR_INVALID_ARGUMENT;
+  if ((codes != nullptr) != (scale != nullptr) || (residual != nullptr) != (sum != nullptr))
+    return MOK_ERR_INVALID_ARGUMENT;
+  if (rows > kMaxNormRows || cols > kMaxNormCols) return MOK_ERR_UNSUPPORTED;
+  if (residual && x_is_fp32 && !residual_is_fp32) return MOK_ERR_UNSUPPORTED;
+  if (rows == 0) return MOK_OK;
+  if (!x || !weight || (!y && !codes && !sum && !rstd)) return MOK_ERR_INVALID_ARGUMENT;
+  if (ld_x < cols || (residual && ld_residual < cols)) return MOK_ERR_INVALID_ARGUMENT;
+  if (!element_aligned(x, x_is_fp32) || !element_aligned(residual, residual_is_fp32) ||
+      !element_aligned(weight, weight_is_fp32) || !element_aligned(sum, residual_is_fp32) || !element_aligned(y, 0) ||
+      !element_aligned(rstd, 1))
+    return MOK_ERR_INVALID_ARGUMENT;
+  if (codes) {
+    if (cols % 32 != 0 || cols > kNormMaxVecCols || ld_x % 8 != 0 || (residual && ld_residual % 8 != 0))
+      return MOK_ERR_UNSUPPORTED;
+    if ((((uintptr_t)x | (uintptr_t)residual | (uintptr_t)weight | (uintptr_t)sum | (uintptr_t)y) & 15) ||
+        (((uintptr_t)codes) & 7))
+      return MOK_ERR_UNSUPPORTED;
+  }
+  const int cus = current_cus();
+  if (cus <= 0) return MOK_ERR_HIP;
+  NormArgs n{};
+  n.x = x, n.residual = residual, n.w = weight;
+  n.x_fp32 = x_is_fp32, n.res_fp32 = residual_is_fp32, n.w_fp32 = weight_is_fp32;
+  n.rows = rows, n.cols = cols, n.ld_x = ld_x, n.ld_res = residual ? ld_residual : 0;
+  n.eps = eps;
+  n.sum = sum, n.y = y, n.codes = codes, n.scale = scale, n.rstd = rstd;
+  return to_status(launch_rms_norm(n, cus, (hipStream_t)stream));
+}
+
+extern "C" size_t mok_rms_norm_scratch_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 1 || rows > kMaxNormRows || cols > kMaxNormCols) return 0;
+  return sizeof(float) * (size_t)std::max<int64_t>(norm_bwd_parts(rows), 1) * (size_t)cols;
+}
+
+extern "C" mok_status mok_rms_norm_backward(const void* dy, int64_t ld_dy, const void* s, int s_is_fp32, int64_t ld_s,
+                                            const float* rstd, const void* weight, int weight_is_fp32,
+                                            const void* d_sum, int64_t ld_d_sum, int64_t rows, int64_t cols, void* ds,
+                                            void* dx, void* d_weight, void* scratch, size_t scratch_bytes,
+                                            void* stream) {
+  if (rows < 0 || cols < 1 || !flag(s_is_fp32) || !flag(weight_is_fp32)) return MOK_ERR_INVALID_ARGUMENT;
+  if (rows > kMaxNormRows || cols > kMaxNormCols) return MOK_ERR_UNSUPPORTED;
+  if (!d_weight || !element_aligned(d_weight, weight_is_fp32)) return MOK_ERR_INVALID_ARGUMENT;
+  if (rows > 0) {
+    if (!dy || !s || !rstd || !weight || !ds || !scratch) return MOK_ERR_INVALID_ARGUMENT;
+    if (ld_dy < cols || ld_s < cols || (d_sum && ld_d_sum < cols)) return MOK_ERR_INVALID_ARGUMENT;
+    if (!element_aligned(dy, 0) || !element_aligned(s, s_is_fp32) || !element_aligned(rstd, 1) ||
+        !element_aligned(weight, weight_is_fp32) || !element_aligned(d_sum, s_is_fp32) ||
+        !element_aligned(ds, s_is_fp32) || !element_aligned(dx, 0) || (((uintptr_t)scratch) & 15))
+      return MOK_ERR_INVALID_ARGUMENT;
+    if (scratch_bytes < mok_rms_norm_scratch_bytes(rows, cols)) return MOK_ERR_BUFFER_TOO_SMALL;
+  }
+  NormBwdArgs n{};
+  n.dy = dy, n.s = s, n.dsum = d_sum, n.w = weight, n.rstd = rstd;
+  n.s_fp32 = s_is_fp32, n.w_fp32 = weight_is_fp32;
+  n.rows = rows, n.cols = cols, n.ld_dy = ld_dy, n.ld_s = ld_s, n.ld_dsum = d_sum ? ld_d_sum : 0;
+  n.ds = ds, n.dx = dx, n.dw = d_weight, n.dw_part = (float*)scratch;
+  return to_status(launch_rms_norm_bwd(n, (hipStream_t)stream));
+}
+
+// What both directions of the router ask of their arguments.
+static mok_status check_router(const void* logits, int logits_is_fp32, int64_t T, int64_t ld, int32_t experts,
+                               int32_t k, const float* bias, int32_t scoring, int renormalize, float scale) {
+  if (T < 0 || experts < 1 || k < 1 || !flag(logits_is_fp32) || !flag(renormalize) || !std::isfinite(scale))
+    return MOK_ERR_INVALID_ARGUMENT;
+  if (scoring != MOK_ROUTER_SOFTMAX && scoring != MOK_ROUTER_SIGMOID) return MOK_ERR_INVALID_ARGUMENT;
+  if (k > experts) return MOK_ERR_INVALID_ARGUMENT;
+  if (experts > 1024 || k > 64 || T > ((int64_t)1 << 40)) return MOK_ERR_UNSUPPORTED;
+  if (T > 0 && (!logits || ld < experts)) return MOK_ERR_INVALID_ARGUMENT;
+  if (!element_aligned(logits, logits_is_fp32) || !element_aligned(bias, 1)) return MOK_ERR_INVALID_ARGUMENT;
+  return MOK_OK;
+}
+
+extern "C" size_t mok_router_scratch_bytes(int64_t T, int32_t experts) {
+  if (T < 0 || experts < 1 || experts > 1024) return 0;
+  return sizeof(float) * (size_t)router_parts(T, experts) * 2 * (size_t)(experts + 1);
+}
+
+extern "C" mok_status mok_router_topk(const void* logits, int logits_is_fp32, int64_t T, int64_t ld, int32_t experts,
+                                      int32_t k, const float* bias, const uint8_t* token_mask, int32_t scoring,
+                                      int renormalize, float scale, float* weights, int64_t* ids, int32_t* counts,
+                                      float* losses, void* scratch, size_t scratch_bytes, void* stream) {
+  const mok_status st = check_router(logits, logits_is_fp32, T, ld, experts, k, bias, scoring, renormalize, scale);
+  if (st != MOK_OK) return st;
+  if ((counts != nullptr) != (losses != nullptr)) return MOK_ERR_INVALID_ARGUMENT;
+  if (T > 0 && (!weights || !ids)) return MOK_ERR_INVALID_ARGUMENT;
+  if (!element_aligned(weights, 1) || (((uintptr_t)ids) & 7) || !element_aligned(counts, 1) ||
+      !element_aligned(losses, 1) || !element_aligned(scratch, 1))
+    return MOK_ERR_INVALID_ARGUMENT;
+  if (counts) {
+    if (!scratch) return MOK_ERR_INVALID_ARGUMENT;
+    if (scratch_bytes < mok_router_scratch_bytes(T, experts)) return MOK_ERR_BUFFER_TOO_SMALL;
+  } else if (T == 0) {
+    return MOK_OK;
+  }
+  const int cus = current_cus();
+  if (cus <= 0) return MOK_ERR_HIP;
+  RouterArgs r{};
+  r.logits = logits, r.logits_fp32 = logits_is_fp32, r.T = T, r.ld = ld, r.E = experts, r.k = k;
+  r.bias = bias, r.mask = token_mask, r.sigmoid = scoring == MOK_ROUTER_SIGMOID, r.renorm = renormalize;
+  r.scale = scale, r.weights = weights, r.ids = ids, r.counts = counts, r.losses = losses, r.part = (float*)scratch;
+  return to_status(launch_router(r, cus, (hipStream_t)stream));
+}
+
+extern "C" mok_status mok_router_topk_backward(const float* d_weights, const void* logits, int logits_is_fp32,
+                                               int64_t T, int64_t ld, int32_t experts, int32_t k, const float* bias,
+                                               const uint8_t* token_mask, int32_t scoring, int renormalize,
+                                               float scale, const int64_t* ids, const int32_t* counts,
+                                               const float* d_losses, void* d_logits, void* stream) {
+  const mok_status st = check_router(logits, logits_is_fp32, T, ld, experts, k, bias, scoring, renormalize, scale);
+  if (st != MOK_OK) return st;
+  if ((counts != nullptr) != (d_losses != nullptr)) return MOK_ERR_INVALID_ARGUMENT;
+  if (T == 0) return MOK_OK;
+  if (!d_weights || !ids || !d_logits) return MOK_ERR_INVALID_ARGUMENT;
+  if (!element_aligned(d_weights, 1) || (((uintptr_t)ids) & 7) || !element_aligned(counts, 1) ||
+      !element_aligned(d_losses, 1) || !element_aligned(d_logits, logits_is_fp32))
+    return MOK_ERR_INVALID_ARGUMENT;
+  const int cus = current_cus();
+  if (cus <= 0) return MOK_ERR_HIP;
+  RouterBwdArgs r{};
+  r.logits = logits, r.logits_fp32 = logits_is_fp32, r.T = T, r.ld = ld, r.E = experts, r.k = k;
+  r.bias = bias, r.mask = token_mask, r.sigmoid = scoring == MOK_ROUTER_SIGMOID, r.renorm = renormalize;
+  r.scale = scale, r.d_weights = d_weights, r.ids = ids, r.counts = counts, r.d_losses = d_losses;
+  r.d_logits = d_logits;
+  return to_status(launch_router_bwd(r, cus, (hipStream_t)stream));
+}
+
+extern "C" mok_status mok_adamw_step(const mok_adamw* u, void* stream) {
+  if (!u || u->struct_size != sizeof(mok_adamw) || u->count < 0) return MOK_ERR_INVALID_ARGUMENT;
+  if (!flag(u->param_fp32) || !flag(u->grad_fp32)) return MOK_ERR_INVALID_ARGUMENT;
+  if (u->state_bits != 8 && u->state_bits != 32) return MOK_ERR_UNSUPPORTED;
+  const double h[5] = {u->lr, u->beta1, u->beta2, u->eps, u->weight_decay};
+  for (double v : h)
+    if (!std::isfinite(v)) return MOK_ERR_INVALID_ARGUMENT;
+  if (u->lr < 0 || u->beta1 < 0 || u->beta1 >= 1 || u->beta2 < 0 || u->beta2 >= 1 || u->eps < 0 ||
+      u->weight_decay < 0 || u->step < 1)
+    return MOK_ERR_INVALID_ARGUMENT;
+  if (!element_aligned(u->grad_scale, 1)) return MOK_ERR_INVALID_ARGUMENT;
+  if (u->param_fp32 && u->masters) return MOK_ERR_INVALID_ARGUMENT;
+  if (u->count == 0) return MOK_OK;
+  const bool s8 = u->state_bits == 8;
+  if (!u->params || !u->grads || !u->exp_avgs || !u->exp_avg_sqs || !u->numels) return MOK_ERR_INVALID_ARGUMENT;
+  if (s8 != (u->exp_avg_scales != nullptr) || s8 != (u->exp_avg_sq_scales != nullptr)) return MOK_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < u->count; ++i) {
+    const int64_t n = u->numels[i];
+    if (n < 0) return MOK_ERR_INVALID_ARGUMENT;
+    if (n == 0) continue;
+    if (n > ((int64_t)1 << 40)) return MOK_ERR_UNSUPPORTED;
+    if (!u->params[i] || !u->grads[i] || !u->exp_avgs[i] || !u->exp_avg_sqs[i] || (u->masters && !u->masters[i]) ||
+        (s8 && (!u->exp_avg_scales[i] || !u->exp_avg_sq_scales[i])))
+      return MOK_ERR_INVALID_ARGUMENT;
+    if (!element_aligned(u->params[i], u->param_fp32) || !element_aligned(u->grads[i], u->grad_fp32) ||
+        (u->masters && !element_aligned(u->masters[i], 1)) ||
+        (!s8 && (!element_aligned(u->exp_avgs[i], 1) || !element_aligned(u->exp_avg_sqs[i], 1))))
+      return MOK_ERR_INVALID_ARGUMENT;
+  }
+  const int cus = current_cus();
+  if (cus <= 0) return MOK_ERR_HIP;
+  return to_status(launch_adamw(*u, cus, (hipStream_t)stream));
 }
 
 // ------------------------------------------------------------------------

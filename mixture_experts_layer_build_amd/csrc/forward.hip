@@ -74,13 +74,15 @@ hipError_t launch_forward(mok_workspace* ws, const mok_config& c, const Layout& 
   if (a.mxfp8) {
     hq = a.ctx_g ? (uint8_t*)a.h : ws->hq;
     hq_scale = a.ctx_g ? (uint8_t*)a.h + ce : ws->hq_scale;
-    LaunchTimer tm(ws, MOK_K_QUANT_X, s);
-    MOK_HIP_TRY(launch_quantize_rows_dev(a.x, v, c.max_tokens, c.hidden, ws->xq, ws->xq_scale, s));
+    if (!a.xq) {
+      LaunchTimer tm(ws, MOK_K_QUANT_X, s);
+      MOK_HIP_TRY(launch_quantize_rows_dev(a.x, v, c.max_tokens, c.hidden, ws->xq, ws->xq_scale, s));
+    }
   }
   // gate/up
   if (a.mxfp8) {
-    p.a_tok = ws->xq;
-    p.a_tok_scale = ws->xq_scale;
+    p.a_tok = a.xq ? a.xq : ws->xq;
+    p.a_tok_scale = a.xq ? a.xq_scale : ws->xq_scale;
     p.out = hq;
     p.out_scale = hq_scale;
     p.b0s = a.w->routed_gate_scale;

@@ -191,6 +191,8 @@ struct FwdArgs {
   void* h;                    // h (routed rows then shared rows): bf16, or MXFP8 codes + scales
   void* y;                    // bf16 [(rows_cap_max + T_max), H]
   int mxfp8;
+  const uint8_t* xq = nullptr;        // MXFP8: x already quantized (codes, scales); null = quantize x here
+  const uint8_t* xq_scale = nullptr;
 };
 // One forward over the schedule `sched` (layout L) of configuration c: the
 // workspace's own, or one pass of its token ring.
@@ -228,6 +230,70 @@ struct BwdArgs {
   int weights_t;  // MXFP8: `w` holds the weights transposed and quantized (mok_mxfp8_quantize_transposed)
 };
 hipError_t launch_backward(mok_workspace* ws, const void* sched, const BwdArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// The operators around the layer: norm, router, optimizer step
+// ---------------------------------------------------------------------------
+constexpr int64_t kNormMaxVecCols = 16384;  // widest row that is held in registers
+
+struct NormArgs {
+  const void *x, *residual, *w;
+  int x_fp32, res_fp32, w_fp32;
+  int64_t rows, cols, ld_x, ld_res;
+  float eps;
+  void *sum, *y;
+  uint8_t *codes, *scale;
+  float* rstd;
+};
+hipError_t launch_rms_norm(const NormArgs& n, int cus, hipStream_t s);
+
+struct NormBwdArgs {
+  const void *dy, *s, *dsum, *w;
+  const float* rstd;
+  int s_fp32, w_fp32;
+  int64_t rows, cols, ld_dy, ld_s, ld_dsum;
+  void *ds, *dx, *dw;
+  float* dw_part;  // [norm_bwd_parts(rows), cols]
+};
+int64_t norm_bwd_parts(int64_t rows);
+hipError_t launch_rms_norm_bwd(const NormBwdArgs& n, hipStream_t s);
+
+struct RouterArgs {
+  const void* logits;
+  int logits_fp32;
+  int64_t T, ld;
+  int E, k;
+  const float* bias;
+  const uint8_t* mask;
+  int sigmoid, renorm;
+  float scale;
+  float* weights;
+  int64_t* ids;
+  int32_t* counts;  // null: no statistics
+  float* losses;
+  float* part;      // [router_parts(T, E), 2 (E + 1)]
+};
+int64_t router_parts(int64_t T, int64_t E);
+hipError_t launch_router(const RouterArgs& r, int cus, hipStream_t s);
+
+struct RouterBwdArgs {
+  const void* logits;
+  int logits_fp32;
+  int64_t T, ld;
+  int E, k;
+  const float* bias;
+  const uint8_t* mask;
+  int sigmoid, renorm;
+  float scale;
+  const float* d_weights;
+  const int64_t* ids;
+  const int32_t* counts;
+  const float* d_losses;
+  void* d_logits;
+};
+hipError_t launch_router_bwd(const RouterBwdArgs& r, int cus, hipStream_t s);
+
+hipError_t launch_adamw(const mok_adamw& u, int cus, hipStream_t s);
 
 // The SwiGLU input limit the kernels apply: +inf (no clamp) unless the
 // configuration sets a positive finite limit.

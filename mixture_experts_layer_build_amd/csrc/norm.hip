@@ -1,0 +1,444 @@
+// RMS norm with the residual's addition, forward and backward.
+//
+//   forward   s = x + residual;  rstd = (mean(s^2) + eps)^-1/2;  y = s * rstd * w
+//   backward  xh = s * rstd, g = dy * w:  ds = rstd * (g - xh * mean(g * xh)) + dsum,
+//             dw = sum over rows of dy * xh
+//
+// Everything between a load and a store is fp32. The sum is stored in the
+// residual's type, and y is computed from the fp32 sum before that rounding,
+// so each output is rounded once. The backward starts from the stored sum.
+//
+// Both directions are bound by HBM: an element costs a few flops and 4 to 14
+// bytes. A row is held in registers between its statistics and its output,
+// so each byte is moved once. 8 elements (16 bytes of bf16) per lane and
+// load, lanes on consecutive chunks; a row belongs to one wave up to 2048
+// columns, whose reduction needs no barrier, and to 256 or 512 threads
+// above (a wave would need more registers than keep enough loads in
+// flight). The grid is persistent: the weights stay in registers from row
+// to row, and the backward adds dw up in registers over a workgroup's rows,
+// writes one partial row per workgroup, and a second launch adds the
+// partials in a fixed order (no atomics: the same bits on every run).
+#include <algorithm>
+#include <type_traits>
+
+#include "mok_internal.h"
+#include "wave_ops.h"
+
+namespace mok {
+namespace {
+
+// E4M3 codes and E8M0 scale of a lane's 8 elements of a 32-element block
+// (4 consecutive lanes), by the block rule of the quantizer (X = clamp(floor(
+// log2 amax) - 8, -127, 127)). A block that holds an infinity or a NaN gets
+// the NaN scale 0xFF, so its consumers see it.
+__device__ __forceinline__ void store_mxfp8(const float (&y)[8], uint8_t* codes, uint8_t* scale, bool first) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = max(amax, f2u(y[i]) & 0x7FFFFFFFu);
+  amax = quad_max(amax);
+  const int X = mx_block_exponent(amax);
+  *reinterpret_cast<uint2*>(codes) =
+      make_uint2(e4m3x4_encode_scaled(y[0], y[1], y[2], y[3], X), e4m3x4_encode_scaled(y[4], y[5], y[6], y[7], X));
+  if (first) *scale = amax >= 0x7F800000u ? 0xFFu : (uint8_t)(X + 127);
+}
+
+// Sum over the TPR threads of a row. Waves join through LDS, in two sets of
+// slots used in turn, so that one barrier per row is enough: a set is
+// written again only after the barrier that follows its last read.
+template <int TPR>
+__device__ __forceinline__ float row_threads_sum(float x, float* slots, int group, int parity) {
+  x = wave_sum(x);
+  if constexpr (TPR == 64) return x;
+  constexpr int W = TPR / 64;
+  float* mine = slots + (parity * (int)(blockDim.x / TPR) + group) * W;
+  const int wave = (int)(threadIdx.x % TPR) / 64;
+  if (lane_id() == 0) mine[wave] = x;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) s += mine[i];
+  return s;
+}
+
+struct NormFwd {
+  const void *x, *residual, *w;
+  int w_fp32;
+  int64_t rows, ld_x, ld_res;
+  int cols;
+  float eps;
+  void* sum;        // residual's type; null without a residual
+  uint16_t* y;      // null: not written
+  uint8_t* codes;   // null: not written
+  uint8_t* scale;
+  float* rstd;      // null: not written
+};
+
+// RT: the residual's type, void for none.
+template <typename XT, typename RT, int BLOCK, int TPR, int NV>
+__global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
+  constexpr bool kRes = !std::is_void<RT>::value;
+  using R = typename std::conditional<kRes, RT, float>::type;
+  constexpr int RPB = BLOCK / TPR;
+  __shared__ float slots[2 * RPB * (TPR / 64)];
+  const int t = (int)threadIdx.x % TPR, group = (int)threadIdx.x / TPR;
+  const int nchunk = a.cols >> 3;
+  float w[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = t + i * TPR;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w[i][q] = 0.f;
+    if (c < nchunk) {
+      if (a.w_fp32)
+        load8((const float*)a.w + c * 8, w[i]);
+      else
+        load8((const uint16_t*)a.w + c * 8, w[i]);
+    }
+  }
+  const float inv_cols = 1.0f / (float)a.cols;
+  int parity = 0;
+  // every thread of the workgroup makes the same number of turns (barrier inside)
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB, parity ^= 1) {
+    const int64_t row = r0 + group;
+    const bool live = row < a.rows;
+    float v[NV][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = t + i * TPR;
+      if (live && c < nchunk) {
+        load8((const XT*)a.x + row * a.ld_x + c * 8, v[i]);
+        if constexpr (kRes) {
+          float r[8];
+          load8((const R*)a.residual + row * a.ld_res + c * 8, r);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) v[i][q] += r[q];
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[i][q] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) ss = __builtin_fmaf(v[i][q], v[i][q], ss);
+    ss = row_threads_sum<TPR>(ss, slots, group, parity);
+    const float rstd = 1.0f / __builtin_sqrtf(ss * inv_cols + a.eps);
+    if (!live) continue;
+    if (a.rstd && t == 0) a.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = t + i * TPR;
+      if (c >= nchunk) continue;
+      const int64_t at = row * a.cols + c * 8;
+      if constexpr (kRes) store8((R*)a.sum + at, v[i]);
+      float y[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) y[q] = v[i][q] * rstd * w[i][q];
+      if (a.y) store8(a.y + at, y);
+      if (a.codes) store_mxfp8(y, a.codes + at, a.scale + (at >> 5), (t & 3) == 0);
+    }
+  }
+}
+
+// Any width, stride and alignment: one workgroup per row, one element per
+// lane and load, the row read twice (the second time from cache).
+template <typename XT, typename RT>
+__global__ void __launch_bounds__(256) rms_norm_any(NormFwd a) {
+  constexpr bool kRes = !std::is_void<RT>::value;
+  using R = typename std::conditional<kRes, RT, float>::type;
+  __shared__ float slots[2 * 4];
+  const float inv_cols = 1.0f / (float)a.cols;
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
+    const XT* x = (const XT*)a.x + row * a.ld_x;
+    const R* res = (const R*)a.residual + row * a.ld_res;
+    float ss = 0.f;
+    for (int c = threadIdx.x; c < a.cols; c += 256) {
+      float v = load1(x + c);
+      if constexpr (kRes) v += load1(res + c);
+      ss = __builtin_fmaf(v, v, ss);
+    }
+    ss = row_threads_sum<256>(ss, slots, 0, parity);
+    const float rstd = 1.0f / __builtin_sqrtf(ss * inv_cols + a.eps);
+    if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
+    for (int c = threadIdx.x; c < a.cols; c += 256) {
+      float v = load1(x + c);
+      if constexpr (kRes) {
+        v += load1(res + c);
+        store1((R*)a.sum + row * a.cols + c, v);
+      }
+      const float w = a.w_fp32 ? ((const float*)a.w)[c] : load1((const uint16_t*)a.w + c);
+      if (a.y) store1(a.y + row * a.cols + c, v * rstd * w);
+    }
+  }
+}
+
+struct NormBwd {
+  const uint16_t* dy;
+  const void *s, *dsum, *w;
+  const float* rstd;
+  int w_fp32;
+  int64_t rows, ld_dy, ld_s, ld_dsum;
+  int cols;
+  void* ds;         // s's type
+  uint16_t* dx;     // bf16 copy of ds; null: not written
+  float* dw_part;   // [workgroups, cols]
+};
+
+template <typename ST, int BLOCK, int TPR, int NV>
+__global__ void __launch_bounds__(BLOCK) rms_norm_bwd_rows(NormBwd a) {
+  constexpr int RPB = BLOCK / TPR;
+  __shared__ float slots[2 * RPB * (TPR / 64)];
+  __shared__ float dw_lds[RPB > 1 ? TPR * NV * 8 : 1];
+  const int t = (int)threadIdx.x % TPR, group = (int)threadIdx.x / TPR;
+  const int nchunk = a.cols >> 3;
+  float w[NV][8], dw[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = t + i * TPR;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w[i][q] = dw[i][q] = 0.f;
+    if (c < nchunk) {
+      if (a.w_fp32)
+        load8((const float*)a.w + c * 8, w[i]);
+      else
+        load8((const uint16_t*)a.w + c * 8, w[i]);
+    }
+  }
+  const float inv_cols = 1.0f / (float)a.cols;
+  int parity = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB, parity ^= 1) {
+    const int64_t row = r0 + group;
+    const bool live = row < a.rows;
+    const float rstd = live ? a.rstd[row] : 0.f;
+    float dy[NV][8], xh[NV][8];
+    float along = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = t + i * TPR;
+      if (live && c < nchunk) {
+        load8(a.dy + row * a.ld_dy + c * 8, dy[i]);
+        load8((const ST*)a.s + row * a.ld_s + c * 8, xh[i]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) dy[i][q] = xh[i][q] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        xh[i][q] *= rstd;
+        dw[i][q] = __builtin_fmaf(dy[i][q], xh[i][q], dw[i][q]);
+        dy[i][q] *= w[i][q];
+        along = __builtin_fmaf(dy[i][q], xh[i][q], along);
+      }
+    along = row_threads_sum<TPR>(along, slots, group, parity) * inv_cols;
+    if (!live) continue;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = t + i * TPR;
+      if (c >= nchunk) continue;
+      const int64_t at = row * a.cols + c * 8;
+      float ds[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) ds[q] = rstd * (dy[i][q] - xh[i][q] * along);
+      if (a.dsum) {
+        float d[8];
+        load8((const ST*)a.dsum + row * a.ld_dsum + c * 8, d);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) ds[q] += d[q];
+      }
+      store8((ST*)a.ds + at, ds);
+      if (a.dx) store8(a.dx + at, ds);
+    }
+  }
+  // the workgroup's partial row: its row groups one after the other
+  for (int g = 0; g < RPB; ++g) {
+    if (RPB > 1) __syncthreads();
+    if (group != g) continue;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = t + i * TPR;
+      if (c >= nchunk) continue;
+      if constexpr (RPB > 1) {
+        if (g > 0) {
+          float have[8];
+          load8(dw_lds + c * 8, have);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) dw[i][q] += have[q];
+        }
+        if (g < RPB - 1) store8(dw_lds + c * 8, dw[i]);
+      }
+      if (g == RPB - 1) store8(a.dw_part + (int64_t)blockIdx.x * a.cols + c * 8, dw[i]);
+    }
+  }
+}
+
+// dw_part is added to by the thread that owns a column of the workgroup
+// (global memory, one workgroup's own row).
+template <typename ST>
+__global__ void __launch_bounds__(256) rms_norm_bwd_any(NormBwd a) {
+  __shared__ float slots[2 * 4];
+  const float inv_cols = 1.0f / (float)a.cols;
+  float* part = a.dw_part + (int64_t)blockIdx.x * a.cols;
+  for (int c = threadIdx.x; c < a.cols; c += 256) part[c] = 0.f;
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
+    const uint16_t* dy = a.dy + row * a.ld_dy;
+    const ST* s = (const ST*)a.s + row * a.ld_s;
+    const ST* dsum = (const ST*)a.dsum + row * a.ld_dsum;
+    const float rstd = a.rstd[row];
+    float along = 0.f;
+    for (int c = threadIdx.x; c < a.cols; c += 256) {
+      const float w = a.w_fp32 ? ((const float*)a.w)[c] : load1((const uint16_t*)a.w + c);
+      const float d = load1(dy + c), xh = load1(s + c) * rstd;
+      part[c] += d * xh;
+      along = __builtin_fmaf(d * w, xh, along);
+    }
+    along = row_threads_sum<256>(along, slots, 0, parity) * inv_cols;
+    for (int c = threadIdx.x; c < a.cols; c += 256) {
+      const float w = a.w_fp32 ? ((const float*)a.w)[c] : load1((const uint16_t*)a.w + c);
+      float ds = rstd * (load1(dy + c) * w - load1(s + c) * rstd * along);
+      if (a.dsum) ds += load1(dsum + c);
+      store1((ST*)a.ds + row * a.cols + c, ds);
+      if (a.dx) store1(a.dx + row * a.cols + c, ds);
+    }
+  }
+}
+
+// dw[c] = sum over the partial rows, in a fixed order: 16 threads per column
+// take every 16th row, then their sums are added in order.
+__global__ void __launch_bounds__(1024) reduce_dw_part(const float* __restrict__ part, int nparts, int cols,
+                                                       void* dw, int w_fp32) {
+  __shared__ float acc[16][64];
+  const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
+  const int c = (int)blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (c < cols)
+#pragma unroll 4
+    for (int r = g; r < nparts; r += 16) s += part[(int64_t)r * cols + c];
+  acc[g][lane] = s;
+  __syncthreads();
+  if (g != 0 || c >= cols) return;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) s += acc[i][lane];
+  if (w_fp32)
+    ((float*)dw)[c] = s;
+  else
+    ((uint16_t*)dw)[c] = f32_to_bf16(s);
+}
+
+__global__ void zero_dw(void* dw, int cols, int w_fp32) {
+  const int c = (int)(blockIdx.x * blockDim.x + threadIdx.x);
+  if (c >= cols) return;
+  if (w_fp32)
+    ((float*)dw)[c] = 0.f;
+  else
+    ((uint16_t*)dw)[c] = 0;
+}
+
+bool aligned16(const void* p) { return (((uintptr_t)p) & 15) == 0; }
+
+template <typename XT, typename RT, int BLOCK, int TPR, int NV>
+void run_fwd(const NormFwd& a, int cus, hipStream_t s) {
+  const int64_t need = (a.rows + BLOCK / TPR - 1) / (BLOCK / TPR);
+  const int grid = (int)std::min<int64_t>(need, (int64_t)cus * (2048 / BLOCK));
+  rms_norm_rows<XT, RT, BLOCK, TPR, NV><<<grid, BLOCK, 0, s>>>(a);
+}
+
+template <typename XT, typename RT>
+void pick_fwd(const NormFwd& a, bool vec, int cus, hipStream_t s) {
+  if (!vec) {
+    rms_norm_any<XT, RT><<<(int)std::min<int64_t>(a.rows, (int64_t)cus * 8), 256, 0, s>>>(a);
+    return;
+  }
+  const int c = a.cols;
+  if (c <= 512)
+    run_fwd<XT, RT, 256, 64, 1>(a, cus, s);
+  else if (c <= 1024)
+    run_fwd<XT, RT, 256, 64, 2>(a, cus, s);
+  else if (c <= 2048)
+    run_fwd<XT, RT, 256, 64, 4>(a, cus, s);
+  else if (c <= 4096)
+    run_fwd<XT, RT, 256, 256, 2>(a, cus, s);
+  else if (c <= 8192)
+    run_fwd<XT, RT, 256, 256, 4>(a, cus, s);
+  else
+    run_fwd<XT, RT, 512, 512, 4>(a, cus, s);
+}
+
+template <typename ST, int BLOCK, int TPR, int NV>
+void run_bwd(const NormBwd& a, int grid, hipStream_t s) {
+  rms_norm_bwd_rows<ST, BLOCK, TPR, NV><<<grid, BLOCK, 0, s>>>(a);
+}
+
+// Workgroups of the backward, at most: enough to fill the chip, few enough
+// that the partial rows of dw stay a small share of the traffic. A constant,
+// so the order of dw's sums does not depend on the device.
+constexpr int kNormBwdParts = 1024;
+
+int bwd_rows_per_block(int64_t cols, bool vec) {
+  if (!vec) return 1;
+  return cols <= 2048 ? 4 : 1;
+}
+
+}  // namespace
+
+int64_t norm_bwd_parts(int64_t rows) { return std::min<int64_t>(rows, kNormBwdParts); }
+
+hipError_t launch_rms_norm(const NormArgs& n, int cus, hipStream_t s) {
+  if (n.rows == 0) return hipSuccess;
+  NormFwd a{n.x, n.residual, n.w, n.w_fp32, n.rows, n.ld_x, n.ld_res, (int)n.cols, n.eps, n.sum, (uint16_t*)n.y,
+            n.codes, n.scale, n.rstd};
+  const bool vec = n.cols % 8 == 0 && n.cols <= kNormMaxVecCols && n.ld_x % 8 == 0 && n.ld_res % 8 == 0 &&
+                   aligned16(n.x) && aligned16(n.residual) && aligned16(n.w) && aligned16(n.sum) && aligned16(n.y);
+  if (!vec && n.codes) return hipErrorInvalidValue;  // refused by the caller's checks
+  if (!n.residual)
+    n.x_fp32 ? pick_fwd<float, void>(a, vec, cus, s) : pick_fwd<uint16_t, void>(a, vec, cus, s);
+  else if (n.x_fp32)
+    pick_fwd<float, float>(a, vec, cus, s);
+  else
+    n.res_fp32 ? pick_fwd<uint16_t, float>(a, vec, cus, s) : pick_fwd<uint16_t, uint16_t>(a, vec, cus, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_rms_norm_bwd(const NormBwdArgs& n, hipStream_t s) {
+  const int cols = (int)n.cols;
+  if (n.rows == 0) {
+    zero_dw<<<(cols + 255) / 256, 256, 0, s>>>(n.dw, cols, n.w_fp32);
+    return hipGetLastError();
+  }
+  NormBwd a{(const uint16_t*)n.dy, n.s, n.dsum, n.w, n.rstd, n.w_fp32, n.rows, n.ld_dy, n.ld_s, n.ld_dsum, cols,
+            n.ds, (uint16_t*)n.dx, n.dw_part};
+  const bool vec = n.cols % 8 == 0 && n.cols <= kNormMaxVecCols && n.ld_dy % 8 == 0 && n.ld_s % 8 == 0 &&
+                   n.ld_dsum % 8 == 0 && aligned16(n.dy) && aligned16(n.s) && aligned16(n.dsum) && aligned16(n.w) &&
+                   aligned16(n.ds) && aligned16(n.dx);
+  const int rpb = bwd_rows_per_block(cols, vec);
+  const int grid = (int)std::min<int64_t>((n.rows + rpb - 1) / rpb, norm_bwd_parts(n.rows));
+  auto go = [&](auto tag) {
+    using ST = decltype(tag);
+    if (!vec)
+      rms_norm_bwd_any<ST><<<grid, 256, 0, s>>>(a);
+    else if (cols <= 512)
+      run_bwd<ST, 256, 64, 1>(a, grid, s);
+    else if (cols <= 1024)
+      run_bwd<ST, 256, 64, 2>(a, grid, s);
+    else if (cols <= 2048)
+      run_bwd<ST, 256, 64, 4>(a, grid, s);
+    else if (cols <= 4096)
+      run_bwd<ST, 256, 256, 2>(a, grid, s);
+    else if (cols <= 8192)
+      run_bwd<ST, 256, 256, 4>(a, grid, s);
+    else
+      run_bwd<ST, 512, 512, 4>(a, grid, s);
+  };
+  n.s_fp32 ? go(float{}) : go(uint16_t{});
+  MOK_HIP_TRY(hipGetLastError());
+  reduce_dw_part<<<(cols + 63) / 64, 1024, 0, s>>>(n.dw_part, grid, cols, n.dw, n.w_fp32);
+  return hipGetLastError();
+}
+
+}  // namespace mok

@@ -1,0 +1,116 @@
+// Cross-lane reductions on DPP (data-parallel primitives): the operand of a
+// VALU instruction comes from another lane of the same row of 16, so a step
+// costs one instruction and no LDS round trip. Rotating a row by 8, 4, 2 and
+// 1 lanes leaves the row's result in every lane; the four rows of a wave64
+// are then joined through scalar registers. Every order is fixed, so a sum
+// has the same bits on every run.
+//
+// All 64 lanes of the wave must be active.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "device_common.h"
+
+namespace mok {
+
+#if defined(__HIP_DEVICE_COMPILE__)
+template <int CTRL>
+__device__ __forceinline__ int dpp_mov(int x) {
+  return __builtin_amdgcn_update_dpp(x, x, CTRL, 0xF, 0xF, true);
+}
+#else
+template <int CTRL>
+__device__ int dpp_mov(int x);  // device only
+#endif
+template <int CTRL>
+__device__ __forceinline__ float dpp_movf(float x) {
+  return u2f((uint32_t)dpp_mov<CTRL>((int)f2u(x)));
+}
+
+constexpr int kRor1 = 0x121, kRor2 = 0x122, kRor4 = 0x124, kRor8 = 0x128;  // row_ror:n
+constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;                          // quad_perm:[1,0,3,2], [2,3,0,1]
+
+// Over the 16 lanes of a row.
+__device__ __forceinline__ float row_sum(float x) {
+  x += dpp_movf<kRor8>(x);
+  x += dpp_movf<kRor4>(x);
+  x += dpp_movf<kRor2>(x);
+  x += dpp_movf<kRor1>(x);
+  return x;
+}
+__device__ __forceinline__ float row_max(float x) {
+  x = __builtin_fmaxf(x, dpp_movf<kRor8>(x));
+  x = __builtin_fmaxf(x, dpp_movf<kRor4>(x));
+  x = __builtin_fmaxf(x, dpp_movf<kRor2>(x));
+  x = __builtin_fmaxf(x, dpp_movf<kRor1>(x));
+  return x;
+}
+__device__ __forceinline__ int row_min(int x) {
+  x = min(x, dpp_mov<kRor8>(x));
+  x = min(x, dpp_mov<kRor4>(x));
+  x = min(x, dpp_mov<kRor2>(x));
+  x = min(x, dpp_mov<kRor1>(x));
+  return x;
+}
+
+// Lane l's value in every lane (a scalar register).
+__device__ __forceinline__ int lane_value(int x, int l) { return __builtin_amdgcn_readlane(x, l); }
+__device__ __forceinline__ float lane_valuef(float x, int l) {
+  return u2f((uint32_t)__builtin_amdgcn_readlane((int)f2u(x), l));
+}
+
+// Over the 64 lanes of the wave.
+__device__ __forceinline__ float wave_sum(float x) {
+  x = row_sum(x);
+  return (lane_valuef(x, 0) + lane_valuef(x, 16)) + (lane_valuef(x, 32) + lane_valuef(x, 48));
+}
+__device__ __forceinline__ float wave_max(float x) {
+  x = row_max(x);
+  return __builtin_fmaxf(__builtin_fmaxf(lane_valuef(x, 0), lane_valuef(x, 16)),
+                         __builtin_fmaxf(lane_valuef(x, 32), lane_valuef(x, 48)));
+}
+__device__ __forceinline__ int wave_min(int x) {
+  x = row_min(x);
+  return min(min(lane_value(x, 0), lane_value(x, 16)), min(lane_value(x, 32), lane_value(x, 48)));
+}
+
+// Largest value of 4 consecutive lanes (a 32-element block at 8 per lane).
+__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
+  x = max(x, (uint32_t)dpp_mov<kQuadXor1>((int)x));
+  return max(x, (uint32_t)dpp_mov<kQuadXor2>((int)x));
+}
+
+// 8 consecutive elements as fp32, from 16-byte aligned bf16 or fp32.
+__device__ __forceinline__ void unpack8(const uint4& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = u2f(w[i] << 16);
+    v[2 * i + 1] = u2f(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+  unpack8(*reinterpret_cast<const uint4*>(p), v);
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = f32_to_bf16(v); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+
+}  // namespace mok

@@ -25,6 +25,8 @@ Modules:
   mxfp8     -- OCP E4M3 codec, E8M0 block scale, quantize / dequantize along
                a chosen axis in 32-element blocks ([R] §"Tuning the five
                hyperparameters before production", MXFP8 workflow).
+  ops       -- the operators around the layer: RMS norm, top-k router, AdamW
+               step, with their gradients.
   moe       -- forward (routed SwiGLU experts + shared expert + router-weighted
                combine) and backward, in float64; MXFP8-emulated variants.
 

@@ -1,0 +1,167 @@
+"""The operators together, as a block runs them: norm -> router -> experts ->
+residual, forward and backward against the float64 oracle, then an optimizer
+step; and the MXFP8 serving path, where the norm's codes go straight into the
+layer."""
+import numpy as np
+import pytest
+
+from mokutil import TOL_BF16, TOL_MXFP8, assert_close_inf
+from oracle import moe as omoe
+from oracle import mxfp8 as omx
+from oracle import ops as oops
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import mixture_experts_layer_build_amd as mok  # noqa: E402
+from mixture_experts_layer_build_amd.autograd import MoKExperts, MoKRMSNorm, MoKRouter  # noqa: E402
+from mixture_experts_layer_build_amd.optim import MoKAdamW  # noqa: E402
+
+BF = torch.bfloat16
+T, H, I, E, K, IS = 200, 256, 128, 8, 2, 64
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def bf(shape, std=1.0):
+    return (torch.randn(shape) * std).to(BF).cuda()
+
+
+class Block(torch.nn.Module):
+    def __init__(self):
+        super().__init__()
+        self.norm = MoKRMSNorm(H, device="cuda")
+        self.router = MoKRouter(H, E, K, losses=True, device="cuda")
+        self.experts = MoKExperts(H, I, E, K, max_tokens=T, shared_intermediate=IS, device="cuda")
+        self.shared = torch.nn.ParameterList([torch.nn.Parameter(bf(s, 0.05)) for s in ((IS, H), (IS, H), (H, IS))])
+        self.experts.init_weights(0.05)
+        self.router.init_weights(0.1)
+
+    def forward(self, x, residual):
+        y, s = self.norm(x, residual)
+        w, ids, counts, losses = self.router(y)
+        return self.experts(y, w, ids, *self.shared), s, w, ids, counts, losses
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_training_step(bits):
+    torch.manual_seed(1)
+    block = Block()
+    x, r = bf((T, H)).requires_grad_(), bf((T, H)).requires_grad_()
+    out, s, w, ids, counts, losses = block(x, r)
+    gout, gs, gl = bf((T, H), 0.1), bf((T, H), 0.1), torch.tensor([0.01, 0.001], device="cuda")
+    ((out.float() * gout.float()).sum() + (s.float() * gs.float()).sum() + (losses * gl).sum()).backward()
+    # the oracle, through the stored y (bf16), as the layer sees it
+    nw, wr = f64(block.norm.weight), f64(block.router.weight)
+    _, rs, rstd = oops.rms_norm(f64(x), nw, f64(r))
+    y = f64(mok.rms_norm(x.detach(), block.norm.weight.detach(), r.detach())[0])
+    sb = f64(s)
+    ew = [f64(p) for p in (block.experts.routed_gate_weights, block.experts.routed_up_weights,
+                           block.experts.routed_down_weights)]
+    sw = [f64(p) for p in block.shared]
+    args = (y, ids.cpu().numpy(), f64(w), *ew, *sw)
+    assert_close_inf(f64(out), omoe.forward(*args), TOL_BF16, "out")
+    g = omoe.backward(f64(gout), *args)
+    logits = (torch.nn.functional.linear(torch.from_numpy(y).float().cuda(), block.router.weight)).detach().cpu().numpy()
+    dl = oops.router_backward(g["d_router_weights"], logits, ids.cpu().numpy(), counts=counts.cpu().numpy(),
+                              d_losses=f64(gl))
+    assert_close_inf(f64(block.router.weight.grad), dl.T @ y, TOL_BF16, "router weight")
+    dy = g["dx"] + dl @ wr
+    ds, dnw = oops.rms_norm_backward(dy, sb, rstd, nw, f64(gs))
+    assert_close_inf(f64(x.grad), ds, TOL_BF16, "x")
+    assert_close_inf(f64(r.grad), ds, TOL_BF16, "residual")
+    assert_close_inf(f64(block.norm.weight.grad), dnw, TOL_BF16, "norm weight")
+    assert_close_inf(f64(block.experts.routed_down_weights.grad), g["d_w_down"], TOL_BF16, "routed down")
+    # the step: every parameter moves by what the oracle says of its gradient
+    opt = MoKAdamW(block.parameters(), lr=1e-2, betas=(0.9, 0.95), weight_decay=0.1, state_bits=bits)
+    want = {n: oops.adamw(f64(p), f64(p.grad), 0.0, 0.0, 1, 1e-2, 0.9, 0.95, 1e-8, 0.1)[0]
+            for n, p in block.named_parameters()}
+    opt.step()
+    for n, p in block.named_parameters():
+        got = f64(opt.state[p].get("master", p))
+        # |p| 2^-22 and 2^-20 of an update of at most lr
+        assert (np.abs(got - want[n]) <= 2.0 ** -22 * np.abs(want[n]) + 2.0 ** -20 * 1.1e-2 + 1e-9).all(), n
+    out2 = block(x.detach(), r.detach())[0]  # the layer reads the new weights
+    assert torch.isfinite(out2.float()).all() and not torch.equal(out2, out)
+
+
+def mx_weights(w):
+    q = {}
+    for n, t in w.items():
+        c, sc = mok.mxfp8_quantize(t.reshape(-1, t.shape[-1]), axis=1)
+        q[n], q[n + "_scale"] = c.view(t.shape), sc
+    return q
+
+
+@pytest.mark.parametrize("macro", [0, 64])
+def test_forward_mxfp8_has_the_bits_of_the_forward(macro):
+    torch.manual_seed(2)
+    cfg = mok.MoKConfig(hidden=H, intermediate=I, num_experts=E, topk=K, max_tokens=T, shared_intermediate=128,
+                        macrobatch_size=macro, forward_only=1 if macro else 0)
+    ws = mok.Workspace(cfg)
+    w = mx_weights(dict(routed_gate=bf((E, I, H), 0.05), routed_up=bf((E, I, H), 0.05), routed_down=bf((E, H, I), 0.05),
+                        shared_gate=bf((128, H), 0.05), shared_up=bf((128, H), 0.05), shared_down=bf((H, 128), 0.05)))
+    for tokens in (T, 1, 77, 0):
+        x = bf((tokens, H))
+        rw, ids = mok.router_topk(torch.randn(tokens, E, device="cuda"), K)
+        sched = mok.build_schedule(ws, ids)
+        want = mok.forward(ws, sched, x, rw, w, mode=mok.MOK_MODE_MXFP8)
+        codes, sc = mok.mxfp8_quantize(x, axis=1) if tokens else \
+            (torch.empty(0, H, dtype=torch.uint8, device="cuda"), torch.empty(0, H // 32, dtype=torch.uint8, device="cuda"))
+        print(f"forward_mxfp8 {tokens} tokens, macrobatch {macro}", flush=True)
+        got = mok.forward_mxfp8(ws, sched, codes, sc, rw, w)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), tokens
+    if not macro:  # a context of it serves the backward as the other forward's does
+        x = bf((T, H))
+        rw, ids = mok.router_topk(torch.randn(T, E, device="cuda"), K)
+        sched = mok.build_schedule(ws, ids)
+        n = mok.context_bytes(cfg, mok.MOK_MODE_MXFP8)
+        ctx = [torch.zeros(n, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        mok.forward(ws, sched, x, rw, w, mode=mok.MOK_MODE_MXFP8, context=ctx[0])
+        mok.forward_mxfp8(ws, sched, *mok.mxfp8_quantize(x, axis=1), rw, w, context=ctx[1])
+        assert torch.equal(*ctx)
+        with pytest.raises(ValueError):
+            mok.forward_mxfp8(ws, sched, x.view(torch.uint8), x.view(torch.uint8), rw, w)
+
+
+def test_serving_step_in_mxfp8():
+    """norm (MXFP8) -> router on the bf16 y -> layer on the codes, with some
+    tokens masked out, against the oracle's MXFP8 forward of the same codes."""
+    torch.manual_seed(3)
+    cfg = mok.MoKConfig(hidden=H, intermediate=I, num_experts=E, topk=K, max_tokens=T, forward_only=1)
+    ws = mok.Workspace(cfg)
+    w16 = dict(routed_gate=bf((E, I, H), 0.05), routed_up=bf((E, I, H), 0.05), routed_down=bf((E, H, I), 0.05))
+    w = mx_weights(w16)
+    x, r, nw, wr = bf((T, H)), bf((T, H)), bf(H), torch.randn(E, H, device="cuda") * 0.1
+    mask = torch.rand(T, device="cuda") < 0.8
+
+    def step():
+        y = torch.empty_like(x)
+        codes, scale, s = mok.rms_norm_mxfp8(x, nw, r, y=y)
+        rw, ids = mok.router_topk(y.float() @ wr.t(), K, token_mask=mask)
+        return mok.forward_mxfp8(ws, mok.build_schedule(ws, ids), codes, scale, rw, w), codes, scale, rw, ids
+
+    out, codes, scale, rw, ids = step()
+    assert not out[~mask].any()
+    xq = oops.decode8(codes.cpu().numpy(), scale.cpu().numpy()).reshape(T, H)
+    q = omoe.quantize_weights_mxfp8(*[f64(w16[n]) for n in ("routed_gate", "routed_up", "routed_down")], None, None, None)
+    want = np.zeros((T, H))
+    gate, up, down = q["Wg_f"], q["Wu_f"], q["Wd_f"]
+    for t in range(T):
+        for j in range(K):
+            e = int(ids[t, j])
+            if e < 0:
+                continue
+            a, b = gate[e] @ xq[t], up[e] @ xq[t]
+            h = omx.qdq((a / (1 + np.exp(-a)) * b)[None], 1)[0]
+            want[t] += float(rw[t, j]) * (down[e] @ h)
+    assert_close_inf(f64(out), want, TOL_MXFP8, "out")
+    for _ in range(2):  # one token, as a decoding loop calls it
+        x1, r1, m1 = x[:1], r[:1], mask[:1].fill_(True)
+        codes, scale, s = mok.rms_norm_mxfp8(x1, nw, r1)
+        rw, ids = mok.router_topk(torch.randn(1, E, device="cuda"), K, token_mask=m1)
+        o = mok.forward_mxfp8(ws, mok.build_schedule(ws, ids), codes, scale, rw, w)
+        assert o.shape == (1, H) and torch.isfinite(o.float()).all()

@@ -1,0 +1,255 @@
+"""Top-k router on the GPU against the float64 oracle: expert counts of each
+layout and between them, every k, ties, masks, rows that are empty or have no
+order, both scores, losses, gradients.
+
+Tolerances. Ids and counts are equal. A score is exp of a rounded difference
+d of two logits: off by |d| 2^-24 of its value, plus 2 ulp of the exponential,
+a sum whose longest chain is 16 + 6 terms, a division: (|d| + 32) 2^-24. Logits
+here span less than 32, so 2^-18 covers it. A gradient's element is a sum of
+products of such scores with terms no larger than M (the row's largest |dw|
+times scale, plus the losses' terms), each off by 2^-18 of M at most, and at
+most 4 of them: 2^-16 M. A stored bf16 adds 2^-8 of its value."""
+import numpy as np
+import pytest
+
+from mokutil import ROOT  # noqa: F401
+from oracle import ops as oops
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import mixture_experts_layer_build_amd as mok  # noqa: E402
+from mixture_experts_layer_build_amd.autograd import MoKRouter, router_topk  # noqa: E402
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def dev(a, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def near(got, ref, rel, absolute, what):
+    got = f64(got)
+    assert got.shape == ref.shape
+    assert np.array_equal(np.isnan(got), np.isnan(ref)), what
+    ok = np.isnan(ref) | (np.abs(got - ref) <= rel * np.abs(ref) + absolute + 1e-37)
+    assert ok.all(), f"{what}: {(~ok).sum()} of {ok.size}, worst {np.nanmax(np.where(ok, 0, np.abs(got - ref))):.3g}"
+
+
+def check(l, k, scoring="softmax", renorm=True, scale=1.0, bias=None, mask=None, losses=True, dtype=F32, seed=0):
+    """Forward and backward of logits l (float32 values of `dtype`)."""
+    T, E = l.shape
+    lt = dev(l, dtype)
+    l = lt.float().cpu().numpy()
+    bt, mt = None if bias is None else dev(bias), None if mask is None else dev(mask)
+    how = dict(scoring=scoring, renormalize=renorm, scale=scale, bias=bt, token_mask=mt)
+    print(f"router T={T} E={E} k={k} {scoring} renorm={renorm} {dtype}", flush=True)
+    out = mok.router_topk(lt, k, losses=losses, **how)
+    rw, rids, rcounts, rlosses = oops.router(l, k, scoring, renorm, scale, bias, mask)
+    np.testing.assert_array_equal(out[1].cpu().numpy(), rids)
+    near(out[0], rw, 2.0 ** -18, 0, "weights")
+    if losses:
+        np.testing.assert_array_equal(out[2].cpu().numpy(), rcounts)
+        near(out[3], rlosses, 2.0 ** -16, 0, "losses")
+        plain = mok.router_topk(lt, k, **how)
+        assert torch.equal(plain[1], out[1])
+        np.testing.assert_array_equal(plain[0].cpu().numpy(), out[0].cpu().numpy())
+    rng = np.random.default_rng(seed)
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    dl = np.array([0.7, 0.01], np.float32)
+    more = dict(counts=out[2], d_losses=dev(dl)) if losses else {}
+    got = mok.router_topk_backward(dev(dw), lt, out[1], **how, **more)
+    assert got.dtype == dtype
+    ref = oops.router_backward(dw.astype(np.float64), l, rids, scoring, renorm, scale, bias, mask,
+                               rcounts if losses else None, dl)
+    M = np.abs(dw).max(1, initial=0, keepdims=True) * abs(scale)
+    if losses:
+        n = max(int(rcounts[E]), 1)
+        M = M + 0.7 * E / k / n / n * rcounts[:E].max() + 0.02 / n * (np.where(np.isfinite(l), np.abs(l), 0).max(1, keepdims=True) + 7)
+    near(got, ref, 2.0 ** -8 if dtype == BF else 0, 2.0 ** -16 * M, "d_logits")
+    return out
+
+
+@pytest.mark.parametrize("E", [1, 2, 7, 16, 17, 32, 50, 64, 100, 128, 129, 256, 257, 500, 512, 600, 1024])
+@pytest.mark.parametrize("scoring,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+def test_expert_counts(E, scoring, renorm):
+    rng = np.random.default_rng(E)
+    l = (rng.standard_normal((23, E)) * 2).astype(np.float32)
+    check(l, min(E, 8), scoring, renorm, scale=1.5)
+
+
+@pytest.mark.parametrize("E,k", [(128, 1), (128, 16), (128, 17), (128, 33), (128, 64), (40, 40), (300, 64), (64, 64)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_every_k(E, k, renorm):
+    rng = np.random.default_rng([E, k])
+    check((rng.standard_normal((9, E)) * 2).astype(np.float32), k, renorm=renorm)
+
+
+@pytest.mark.parametrize("T", [0, 1, 3, 16, 17, 1025, 9001])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_token_counts(T, dtype):
+    rng = np.random.default_rng(T)
+    l = (rng.standard_normal((T, 24)) * 2).astype(np.float32)
+    mask = (rng.random(T) < 0.8).astype(np.uint8)
+    check(l, 4, mask=mask, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("E", [48, 320])
+def test_selection_bias_and_ties(E, dtype):
+    rng = np.random.default_rng(E)
+    # logits on a coarse grid: many equal keys, signed zeros among them
+    l = (np.round(rng.standard_normal((40, E)) * 2) / 2).astype(np.float32)
+    l[l == 0] = rng.choice([0.0, -0.0], (l == 0).sum())
+    check(l, 8, dtype=dtype)
+    bias = (np.round(rng.standard_normal(E) * 4) / 4).astype(np.float32)
+    bias[3] = -np.inf  # an expert that is shut off
+    for scoring in ("softmax", "sigmoid"):
+        out = check(l, 8, scoring, True, bias=bias, dtype=dtype)
+        assert not (out[1] == 3).any()
+    check(l, 8, "softmax", False, bias=bias, dtype=dtype)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [20, 400])
+def test_masked_experts_empty_rows_and_garbage_behind_the_mask(scoring, E):
+    rng = np.random.default_rng(E)
+    l = rng.standard_normal((12, E)).astype(np.float32)
+    l[1, 3:] = -np.inf        # fewer experts than k
+    l[2] = -np.inf            # none
+    l[3] = -1000.0            # all equal: ties
+    l[4, :5] = np.finfo(np.float32).min
+    mask = np.ones(12, np.uint8)
+    mask[5:8] = 0
+    l[5] = np.nan
+    l[6] = np.inf
+    l[7] = -np.inf
+    for renorm in (True, False):
+        out = check(l, 6, scoring, renorm, mask=mask)
+        assert torch.isfinite(out[3]).all()
+    assert int(out[2][E]) == 8
+    l[3] = np.finfo(np.float32).min  # all at the type's lowest value (the z loss would overflow)
+    check(l, 6, scoring, True, mask=mask, losses=False)
+
+
+def test_all_tokens_masked():
+    l = np.random.default_rng(0).standard_normal((33, 16)).astype(np.float32)
+    out = check(l, 2, mask=np.zeros(33, np.uint8))
+    assert not out[2].any() and not out[3].any()
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_rows_without_an_order(scoring):
+    rng = np.random.default_rng(2)
+    l = rng.standard_normal((6, 40)).astype(np.float32)
+    l[1, 30] = np.nan
+    l[4, 2] = np.inf
+    out = check(l, 4, scoring, losses=False)
+    assert (out[1][1] == -1).all() and torch.isnan(out[0][4]).all()
+    assert torch.isnan(mok.router_topk(dev(l), 4, scoring=scoring, losses=True)[3][0])
+
+
+def test_large_logits_and_scores_that_underflow():
+    rng = np.random.default_rng(3)
+    l = (rng.standard_normal((8, 32)) * 3).astype(np.float32)
+    # differences stay below 32, so the tolerance holds; each row shifted as a whole
+    check(l + np.float32(200.0), 4)
+    check(l - np.float32(200.0), 4)
+    check(l - np.float32(200.0), 4, "sigmoid", True, losses=False)
+
+
+def test_strided_logits_and_repeated_or_foreign_ids():
+    rng = np.random.default_rng(4)
+    wide = dev(rng.standard_normal((21, 60)).astype(np.float32))
+    l = wide[:, 5:45]
+    w, ids = mok.router_topk(l, 3)
+    w2, ids2 = mok.router_topk(l.contiguous(), 3)
+    assert torch.equal(w, w2) and torch.equal(ids, ids2)
+    dw = dev(rng.standard_normal((21, 3)).astype(np.float32))
+    assert torch.equal(mok.router_topk_backward(dw, l, ids), mok.router_topk_backward(dw, l.contiguous(), ids))
+    # sigmoid without renormalisation: every choice's gradient stands alone, so a repeated id adds up
+    ids[:, 1] = ids[:, 0]
+    ids[0, 2], ids[1, 2], ids[2, 2] = 40, -7, 1 << 40
+    got = f64(mok.router_topk_backward(dw, l, ids, scoring="sigmoid", renormalize=False))
+    want = np.zeros((21, 40))
+    for t in range(21):
+        for j in range(3):
+            e = int(ids[t, j])
+            if 0 <= e < 40:
+                s = 1 / (1 + np.exp(-float(l[t, e])))
+                want[t, e] += float(dw[t, j]) * s * (1 - s)
+    assert np.abs(got - want).max() <= 2.0 ** -18 * np.abs(dw.cpu().numpy()).max() * 2
+
+
+def test_rows_behind_the_last_token_stay():
+    l = torch.randn(20, 16, device="cuda")
+    w, ids = torch.full((20, 2), 7.0, device="cuda"), torch.full((20, 2), 9, dtype=torch.int64, device="cuda")
+    st = mok.lib().mok_router_topk(l.data_ptr(), 1, 13, 16, 16, 2, None, None, 0, 1, 1.0, w.data_ptr(), ids.data_ptr(),
+                                   None, None, None, 0, torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and (w[13:] == 7).all() and (ids[13:] == 9).all() and (ids[:13] < 9 + 7).all()
+
+
+@pytest.mark.parametrize("scoring,renorm", [("softmax", True), ("sigmoid", False)])
+def test_autograd_and_module(scoring, renorm):
+    rng = np.random.default_rng(5)
+    l = rng.standard_normal((30, 24)).astype(np.float32)
+    lt = dev(l).requires_grad_()
+    w, ids, counts, losses = router_topk(lt, 3, scoring=scoring, renormalize=renorm, losses=True)
+    dw = rng.standard_normal((30, 3)).astype(np.float32)
+    ((w * dev(dw)).sum() + (losses * dev(np.array([0.7, 0.01], np.float32))).sum()).backward()
+    ref = oops.router_backward(dw.astype(np.float64), l, ids.cpu().numpy(), scoring, renorm, counts=counts.cpu().numpy(),
+                               d_losses=np.array([0.7, 0.01]))
+    near(lt.grad, ref, 0, 2.0 ** -16 * 8, "d_logits")
+    assert not ids.requires_grad and not counts.requires_grad
+    lt.grad = None
+    router_topk(lt, 3, losses=True)[3].sum().backward()  # only the losses
+    assert torch.isfinite(lt.grad).all() and lt.grad.any()
+    r = MoKRouter(64, 24, 3, selection_bias=True, losses=True, device="cuda")
+    r.init_weights(0.5, generator=torch.Generator().manual_seed(0))
+    x = torch.randn(30, 64, device="cuda").bfloat16().requires_grad_()
+    w, ids, counts, losses = r(x)
+    (w[:, 0].sum() + losses[0]).backward()
+    assert x.grad is not None and r.weight.grad.any() and "experts=24" in repr(r)
+
+
+def test_python_refusals():
+    l = torch.zeros(4, 8, device="cuda")
+    for bad in (dict(scoring="tanh"), dict(bias=torch.zeros(7, device="cuda")), dict(bias=torch.zeros(8)),
+                dict(token_mask=torch.zeros(3, dtype=torch.bool, device="cuda")),
+                dict(token_mask=torch.zeros(4, device="cuda"))):
+        with pytest.raises(ValueError):
+            mok.router_topk(l, 2, **bad)
+    with pytest.raises(ValueError):
+        mok.router_topk(l.half(), 2)
+    with pytest.raises(ValueError):
+        mok.router_topk(l[0], 2)
+    with pytest.raises(mok.MokError):
+        mok.router_topk(l, 9)
+    with pytest.raises(ValueError, match="together"):
+        mok.router_topk_backward(torch.zeros(4, 2, device="cuda"), l, torch.zeros(4, 2, dtype=torch.int64, device="cuda"),
+                                 d_losses=torch.zeros(2, device="cuda"))
+
+
+def test_replayed_graph():
+    l = torch.randn(3000, 128, device="cuda")
+    dw = torch.randn(3000, 8, device="cuda")
+    dl = torch.tensor([0.1, 0.2], device="cuda")
+
+    def step():
+        w, ids, counts, losses = mok.router_topk(l, 8, losses=True)
+        return w, ids, counts, losses, mok.router_topk_backward(dw, l, ids, counts=counts, d_losses=dl)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(3):
+        l.copy_(torch.randn(3000, 128, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, step())), i
