@@ -86,6 +86,12 @@ __device__ __forceinline__ int state_exponent(uint32_t amax) {
   return (amax >= 0x00800000u && (amax & 0x7FFFFFu) > 0x600000u) ? min(x + 1, 127) : x;
 }
 
+// The products and sums below are rounded one by one, as they are written
+// (no fused multiply-add), and the root of an 8-bit state correctly: codes
+// of 4 significant bits and bf16 gradients make exact ties common, and which
+// way they go should not depend on the compiler's contraction.
+#pragma clang fp contract(off)
+
 // One of the two E4M3 values around r >= 0 (r <= 448), r^2 = sq: up where
 // u * (hi^2 - lo^2) < sq - lo^2.
 __device__ __forceinline__ float round_root(float r, float sq, float u) {
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
       g[q] *= gs;
       m[q] = a.b1 * m[q] + a.c1 * g[q];
       v[q] = a.b2 * v[q] + a.c2 * (g[q] * g[q]);
-      r[q] = __builtin_amdgcn_sqrtf(v[q]);
+      r[q] = S8 ? __builtin_sqrtf(v[q]) : __builtin_amdgcn_sqrtf(v[q]);
       p[q] = p[q] * a.keep - a.rate * m[q] * __builtin_amdgcn_rcpf(r[q] * a.rbc2 + a.eps);
     }
     if (in) {

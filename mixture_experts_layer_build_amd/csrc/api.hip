@@ -789,7 +789,7 @@ static mok_status check_router(const void* logits, int logits_is_fp32, int64_t T
 
 extern "C" size_t mok_router_scratch_bytes(int64_t T, int32_t experts) {
   if (T < 0 || experts < 1 || experts > 1024) return 0;
-  return sizeof(float) * (size_t)router_parts(T, experts) * 2 * (size_t)(experts + 1);
+  return sizeof(float) * (size_t)router_scratch_words(T, experts);
 }
 
 extern "C" mok_status mok_router_topk(const void* logits, int logits_is_fp32, int64_t T, int64_t ld, int32_t experts,

@@ -271,9 +271,9 @@ struct RouterArgs {
   int64_t* ids;
   int32_t* counts;  // null: no statistics
   float* losses;
-  float* part;      // [router_parts(T, E), 2 (E + 1)]
+  float* part;      // [router_scratch_words(T, E)]
 };
-int64_t router_parts(int64_t T, int64_t E);
+int64_t router_scratch_words(int64_t T, int64_t E);
 hipError_t launch_router(const RouterArgs& r, int cus, hipStream_t s);
 
 struct RouterBwdArgs {

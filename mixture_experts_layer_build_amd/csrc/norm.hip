@@ -80,12 +80,14 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
   using R = typename std::conditional<kRes, RT, float>::type;
   constexpr int RPB = BLOCK / TPR;
   __shared__ float slots[2 * RPB * (TPR / 64)];
-  const int t = (int)threadIdx.x % TPR, group = (int)threadIdx.x / TPR;
-  const int nchunk = a.cols >> 3;
+  // (a row's waves are whole waves, so its number and addresses are scalars)
+  const uint32_t t = threadIdx.x % TPR;
+  const int group = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
+  const uint32_t nchunk = (uint32_t)a.cols >> 3;
   float w[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = t + i * TPR;
+    const uint32_t c = t + i * TPR;
 #pragma unroll
     for (int q = 0; q < 8; ++q) w[i][q] = 0.f;
     if (c < nchunk) {
@@ -101,16 +103,18 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB, parity ^= 1) {
     const int64_t row = r0 + group;
     const bool live = row < a.rows;
+    const XT* x = (const XT*)a.x + row * a.ld_x;
+    const R* res = (const R*)a.residual + row * a.ld_res;
     float v[NV][8];
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t + i * TPR;
+      const uint32_t c = t + i * TPR;
       if (live && c < nchunk) {
-        load8((const XT*)a.x + row * a.ld_x + c * 8, v[i]);
+        load8(x + c * 8, v[i]);
         if constexpr (kRes) {
           float r[8];
-          load8((const R*)a.residual + row * a.ld_res + c * 8, r);
+          load8(res + c * 8, r);
 #pragma unroll
           for (int q = 0; q < 8; ++q) v[i][q] += r[q];
         }
@@ -127,17 +131,17 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
     const float rstd = 1.0f / __builtin_sqrtf(ss * inv_cols + a.eps);
     if (!live) continue;
     if (a.rstd && t == 0) a.rstd[row] = rstd;
+    const int64_t out = row * a.cols;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t + i * TPR;
+      const uint32_t c = t + i * TPR;
       if (c >= nchunk) continue;
-      const int64_t at = row * a.cols + c * 8;
-      if constexpr (kRes) store8((R*)a.sum + at, v[i]);
+      if constexpr (kRes) store8((R*)a.sum + out + c * 8, v[i]);
       float y[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) y[q] = v[i][q] * rstd * w[i][q];
-      if (a.y) store8(a.y + at, y);
-      if (a.codes) store_mxfp8(y, a.codes + at, a.scale + (at >> 5), (t & 3) == 0);
+      if (a.y) store8(a.y + out + c * 8, y);
+      if (a.codes) store_mxfp8(y, a.codes + out + c * 8, a.scale + (out >> 5) + (c >> 2), (t & 3) == 0);
     }
   }
 }
@@ -187,25 +191,28 @@ struct NormBwd {
   float* dw_part;   // [workgroups, cols]
 };
 
-template <typename ST, int BLOCK, int TPR, int NV>
-__global__ void __launch_bounds__(BLOCK) rms_norm_bwd_rows(NormBwd a) {
+// A row's dy, s and d_sum stay as they were loaded and are converted twice,
+// in the pass before the row's sum and in the one behind it: in fp32 they
+// would take twice the registers, and half the waves would hide the loads.
+template <typename ST, typename WT, bool DSUM, int BLOCK, int TPR, int NV>
+__global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(4)))
+rms_norm_bwd_rows(NormBwd a) {
   constexpr int RPB = BLOCK / TPR;
+  static_assert(BLOCK % TPR == 0, "whole rows");
   __shared__ float slots[2 * RPB * (TPR / 64)];
   __shared__ float dw_lds[RPB > 1 ? TPR * NV * 8 : 1];
-  const int t = (int)threadIdx.x % TPR, group = (int)threadIdx.x / TPR;
-  const int nchunk = a.cols >> 3;
-  float w[NV][8], dw[NV][8];
+  // (a row's waves are whole waves, so its number and addresses are scalars)
+  const uint32_t t = threadIdx.x % TPR;
+  const int group = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
+  const uint32_t nchunk = (uint32_t)a.cols >> 3;
+  Raw8<WT> w[NV];
+  float dw[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = t + i * TPR;
+    const uint32_t c = t + i * TPR;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) w[i][q] = dw[i][q] = 0.f;
-    if (c < nchunk) {
-      if (a.w_fp32)
-        load8((const float*)a.w + c * 8, w[i]);
-      else
-        load8((const uint16_t*)a.w + c * 8, w[i]);
-    }
+    for (int q = 0; q < 8; ++q) dw[i][q] = 0.f;
+    if (c < nchunk) w[i].load((const WT*)a.w + c * 8);
   }
   const float inv_cols = 1.0f / (float)a.cols;
   int parity = 0;
@@ -213,46 +220,65 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_bwd_rows(NormBwd a) {
     const int64_t row = r0 + group;
     const bool live = row < a.rows;
     const float rstd = live ? a.rstd[row] : 0.f;
-    float dy[NV][8], xh[NV][8];
+    const uint16_t* pdy = a.dy + row * a.ld_dy;
+    const ST* ps = (const ST*)a.s + row * a.ld_s;
+    const ST* pd = (const ST*)a.dsum + row * a.ld_dsum;
+    ST* pds = (ST*)a.ds + row * a.cols;
+    uint16_t* pdx = a.dx + row * a.cols;
+    Raw8<uint16_t> dy[NV];
+    Raw8<ST> s[NV], dsum[DSUM ? NV : 1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t c = t + i * TPR;
+      if (live && c < nchunk) {
+        dy[i].load(pdy + c * 8);
+        s[i].load(ps + c * 8);
+        if constexpr (DSUM) dsum[i].load(pd + c * 8);
+      }
+    }
     float along = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t + i * TPR;
-      if (live && c < nchunk) {
-        load8(a.dy + row * a.ld_dy + c * 8, dy[i]);
-        load8((const ST*)a.s + row * a.ld_s + c * 8, xh[i]);
-      } else {
+      w[i].fresh();
 #pragma unroll
-        for (int q = 0; q < 8; ++q) dy[i][q] = xh[i][q] = 0.f;
+      for (int j = 0; j < 4; ++j) {
+        float d[2], x[2], wv[2];
+        dy[i].pair(j, d[0], d[1]);
+        s[i].pair(j, x[0], x[1]);
+        w[i].pair(j, wv[0], wv[1]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float xh = x[q] * rstd;
+          dw[i][2 * j + q] = __builtin_fmaf(d[q], xh, dw[i][2 * j + q]);
+          along = __builtin_fmaf(d[q] * wv[q], xh, along);
+        }
       }
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        xh[i][q] *= rstd;
-        dw[i][q] = __builtin_fmaf(dy[i][q], xh[i][q], dw[i][q]);
-        dy[i][q] *= w[i][q];
-        along = __builtin_fmaf(dy[i][q], xh[i][q], along);
-      }
     along = row_threads_sum<TPR>(along, slots, group, parity) * inv_cols;
     if (!live) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t + i * TPR;
+      const uint32_t c = t + i * TPR;
       if (c >= nchunk) continue;
-      const int64_t at = row * a.cols + c * 8;
-      float ds[8];
+      w[i].fresh();
+      dy[i].fresh();
+      s[i].fresh();
+      Raw8<ST> ds;
+      Raw8<uint16_t> narrow;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) ds[q] = rstd * (dy[i][q] - xh[i][q] * along);
-      if (a.dsum) {
-        float d[8];
-        load8((const ST*)a.dsum + row * a.ld_dsum + c * 8, d);
+      for (int j = 0; j < 4; ++j) {
+        float d[2], x[2], wv[2], more[2] = {0.f, 0.f};
+        dy[i].pair(j, d[0], d[1]);
+        s[i].pair(j, x[0], x[1]);
+        w[i].pair(j, wv[0], wv[1]);
+        if constexpr (DSUM) dsum[i].pair(j, more[0], more[1]);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) ds[q] += d[q];
+        for (int q = 0; q < 2; ++q) d[q] = rstd * (d[q] * wv[q] - x[q] * rstd * along) + more[q];
+        ds.set(j, d[0], d[1]);
+        narrow.set(j, d[0], d[1]);
       }
-      store8((ST*)a.ds + at, ds);
-      if (a.dx) store8(a.dx + at, ds);
+      ds.store(pds + c * 8);
+      if (a.dx) narrow.store(pdx + c * 8);
     }
   }
   // the workgroup's partial row: its row groups one after the other
@@ -261,7 +287,7 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_bwd_rows(NormBwd a) {
     if (group != g) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = t + i * TPR;
+      const uint32_t c = t + i * TPR;
       if (c >= nchunk) continue;
       if constexpr (RPB > 1) {
         if (g > 0) {
@@ -370,19 +396,35 @@ void pick_fwd(const NormFwd& a, bool vec, int cus, hipStream_t s) {
     run_fwd<XT, RT, 512, 512, 4>(a, cus, s);
 }
 
-template <typename ST, int BLOCK, int TPR, int NV>
-void run_bwd(const NormBwd& a, int grid, hipStream_t s) {
-  rms_norm_bwd_rows<ST, BLOCK, TPR, NV><<<grid, BLOCK, 0, s>>>(a);
-}
+// Workgroups of the backward, at most: two per compute unit, enough to fill
+// the chip, few enough that the partial rows of dw stay a small share of the
+// traffic. A constant, so the order of dw's sums does not depend on the
+// device.
+constexpr int kNormBwdParts = 512;
 
-// Workgroups of the backward, at most: enough to fill the chip, few enough
-// that the partial rows of dw stay a small share of the traffic. A constant,
-// so the order of dw's sums does not depend on the device.
-constexpr int kNormBwdParts = 1024;
-
-int bwd_rows_per_block(int64_t cols, bool vec) {
-  if (!vec) return 1;
-  return cols <= 2048 ? 4 : 1;
+template <typename ST, typename WT, bool DSUM>
+int run_bwd(const NormBwd& a, bool vec, hipStream_t s) {
+  const int c = a.cols;
+  auto grid = [&](int rows_per_block) {
+    return (int)std::min<int64_t>((a.rows + rows_per_block - 1) / rows_per_block, kNormBwdParts);
+  };
+  auto go = [&](auto block, auto tpr, auto nv) {
+    constexpr int BLOCK = decltype(block)::value, TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+    const int g = grid(BLOCK / TPR);
+    rms_norm_bwd_rows<ST, WT, DSUM, BLOCK, TPR, NV><<<g, BLOCK, 0, s>>>(a);
+    return g;
+  };
+  using std::integral_constant;
+  if (!vec) {
+    rms_norm_bwd_any<ST><<<grid(1), 256, 0, s>>>(a);
+    return grid(1);
+  }
+  if (c <= 512) return go(integral_constant<int, 512>{}, integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  if (c <= 1024) return go(integral_constant<int, 512>{}, integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  if (c <= 2048) return go(integral_constant<int, 512>{}, integral_constant<int, 256>{}, integral_constant<int, 1>{});
+  if (c <= 4096) return go(integral_constant<int, 512>{}, integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  if (c <= 8192) return go(integral_constant<int, 512>{}, integral_constant<int, 512>{}, integral_constant<int, 2>{});
+  return go(integral_constant<int, 1024>{}, integral_constant<int, 1024>{}, integral_constant<int, 2>{});
 }
 
 }  // namespace
@@ -416,26 +458,13 @@ hipError_t launch_rms_norm_bwd(const NormBwdArgs& n, hipStream_t s) {
   const bool vec = n.cols % 8 == 0 && n.cols <= kNormMaxVecCols && n.ld_dy % 8 == 0 && n.ld_s % 8 == 0 &&
                    n.ld_dsum % 8 == 0 && aligned16(n.dy) && aligned16(n.s) && aligned16(n.dsum) && aligned16(n.w) &&
                    aligned16(n.ds) && aligned16(n.dx);
-  const int rpb = bwd_rows_per_block(cols, vec);
-  const int grid = (int)std::min<int64_t>((n.rows + rpb - 1) / rpb, norm_bwd_parts(n.rows));
-  auto go = [&](auto tag) {
-    using ST = decltype(tag);
-    if (!vec)
-      rms_norm_bwd_any<ST><<<grid, 256, 0, s>>>(a);
-    else if (cols <= 512)
-      run_bwd<ST, 256, 64, 1>(a, grid, s);
-    else if (cols <= 1024)
-      run_bwd<ST, 256, 64, 2>(a, grid, s);
-    else if (cols <= 2048)
-      run_bwd<ST, 256, 64, 4>(a, grid, s);
-    else if (cols <= 4096)
-      run_bwd<ST, 256, 256, 2>(a, grid, s);
-    else if (cols <= 8192)
-      run_bwd<ST, 256, 256, 4>(a, grid, s);
-    else
-      run_bwd<ST, 512, 512, 4>(a, grid, s);
+  auto with_dsum = [&](auto st, auto wt) {
+    using ST = decltype(st);
+    using WT = decltype(wt);
+    return n.dsum ? run_bwd<ST, WT, true>(a, vec, s) : run_bwd<ST, WT, false>(a, vec, s);
   };
-  n.s_fp32 ? go(float{}) : go(uint16_t{});
+  auto with_weight = [&](auto st) { return n.w_fp32 ? with_dsum(st, float{}) : with_dsum(st, uint16_t{}); };
+  const int grid = n.s_fp32 ? with_weight(float{}) : with_weight(uint16_t{});
   MOK_HIP_TRY(hipGetLastError());
   reduce_dw_part<<<(cols + 63) / 64, 1024, 0, s>>>(n.dw_part, grid, cols, n.dw, n.w_fp32);
   return hipGetLastError();

@@ -77,6 +77,28 @@ __device__ __forceinline__ int wave_min(int x) {
   return min(min(lane_value(x, 0), lane_value(x, 16)), min(lane_value(x, 32), lane_value(x, 48)));
 }
 
+// Lane j's value (j a constant after unrolling) in every lane of each row of 16.
+__device__ __forceinline__ int row_lane_of(int x, int j) {
+  switch (j) {
+    case 0: return dpp_mov<0x150>(x);
+    case 1: return dpp_mov<0x151>(x);
+    case 2: return dpp_mov<0x152>(x);
+    case 3: return dpp_mov<0x153>(x);
+    case 4: return dpp_mov<0x154>(x);
+    case 5: return dpp_mov<0x155>(x);
+    case 6: return dpp_mov<0x156>(x);
+    case 7: return dpp_mov<0x157>(x);
+    case 8: return dpp_mov<0x158>(x);
+    case 9: return dpp_mov<0x159>(x);
+    case 10: return dpp_mov<0x15A>(x);
+    case 11: return dpp_mov<0x15B>(x);
+    case 12: return dpp_mov<0x15C>(x);
+    case 13: return dpp_mov<0x15D>(x);
+    case 14: return dpp_mov<0x15E>(x);
+    default: return dpp_mov<0x15F>(x);
+  }
+}
+
 // Largest value of 4 consecutive lanes (a 32-element block at 8 per lane).
 __device__ __forceinline__ uint32_t quad_max(uint32_t x) {
   x = max(x, (uint32_t)dpp_mov<kQuadXor1>((int)x));
@@ -108,6 +130,39 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
+// 8 elements as they lie in memory: 4 registers of bf16, 8 of fp32. fresh()
+// makes the compiler forget what the registers were converted to, so that a
+// later pair() converts again instead of keeping the fp32 values alive.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  uint4 r = make_uint4(0, 0, 0, 0);
+  __device__ __forceinline__ void load(const uint16_t* p) { r = *reinterpret_cast<const uint4*>(p); }
+  // elements 2j and 2j + 1
+  __device__ __forceinline__ void pair(int j, float& a, float& b) const {
+    const uint32_t x = j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w;
+    a = u2f(x << 16), b = u2f(x & 0xFFFF0000u);
+  }
+  __device__ __forceinline__ void set(int j, float a, float b) {
+    (j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w) = pack_bf16x2(a, b);
+  }
+  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = r; }
+  __device__ __forceinline__ void fresh() {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+v"(r.x), "+v"(r.y), "+v"(r.z), "+v"(r.w));
+#endif
+  }
+};
+template <>
+struct Raw8<float> {
+  float v_[8] = {};
+  __device__ __forceinline__ void load(const float* p) { load8(p, v_); }
+  __device__ __forceinline__ void pair(int j, float& a, float& b) const { a = v_[2 * j], b = v_[2 * j + 1]; }
+  __device__ __forceinline__ void set(int j, float a, float b) { v_[2 * j] = a, v_[2 * j + 1] = b; }
+  __device__ __forceinline__ void store(float* p) const { store8(p, v_); }
+  __device__ __forceinline__ void fresh() {}
+};
 __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = f32_to_bf16(v); }

@@ -8,6 +8,7 @@ workspace. Tensors on the CPU are rejected: there is no fallback.
 from __future__ import annotations
 
 import ctypes as C
+import operator
 
 import torch
 
@@ -16,33 +17,33 @@ from . import _lib
 __all__ = ["rms_norm", "rms_norm_mxfp8", "rms_norm_backward", "router_topk", "router_topk_backward", "adamw_step"]
 
 _BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
-_FLOATS = (_BF16, _F32)
-_CODES = (_U8, torch.float8_e4m3fn)
-_SCALES = (_U8, torch.float8_e8m0fnu)
+_FLOATS = {_BF16, _F32}
+_CODES = {_U8, torch.float8_e4m3fn}
+_SCALES = {_U8, torch.float8_e8m0fnu}
 _SCORING = {"softmax": _lib.MOK_ROUTER_SOFTMAX, "sigmoid": _lib.MOK_ROUTER_SIGMOID}
 
 
-def _call(name: str, device: torch.device, *args) -> None:
-    """Runs one library call on `device` and its current stream."""
-    index = device.index
-    if index is None or index == torch.cuda.current_device():
-        st = getattr(_lib.load(), name)(*args, torch.cuda.current_stream().cuda_stream)
+def _call(name: str, index: int, *args) -> None:
+    """Runs one library call on device `index` and its current stream."""
+    if index == torch._C._cuda_getDevice():
+        st = getattr(_lib.load(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            st = getattr(_lib.load(), name)(*args, torch.cuda.current_stream().cuda_stream)
+            st = getattr(_lib.load(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != _lib.MOK_OK:
         raise _lib.MokError(name, st)
 
 
-def _gpu(name: str, t: torch.Tensor) -> torch.device:
+def _gpu(name: str, t: torch.Tensor) -> int:
+    """Index of the tensor's GPU."""
     if not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU (a CUDA tensor)")
-    return t.device
+    return t.get_device()
 
 
-def _check(name: str, t, device: torch.device, dtypes, shape=None) -> None:
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _check(name: str, t, dev: int, dtypes, shape=None) -> None:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if shape is not None and t.shape != shape:
@@ -65,26 +66,25 @@ def _rows(name: str, t: torch.Tensor) -> tuple[int, int]:
     return t.data_ptr(), t.stride(0)
 
 
-def _row_count(t: torch.Tensor) -> int:
-    return t.numel() // t.shape[-1] if t.shape[-1] else 0
-
-
 def _norm(x, weight, residual, eps, y, codes, scale, rstd):
     dev = _gpu("x", x)
-    if x.dim() < 1 or x.shape[-1] < 1:
+    shape = x.shape
+    cols = shape[-1] if shape else 0
+    if cols < 1:
         raise ValueError("x must have a last dimension of at least 1")
-    _check("x", x, dev, _FLOATS)
-    _check("weight", weight, dev, _FLOATS, x.shape[-1:])
+    if x.dtype not in _FLOATS:
+        raise ValueError(f"x must be bfloat16 or float32, got {x.dtype}")
+    _check("weight", weight, dev, _FLOATS, (cols,))
     px, ldx = _rows("x", x)
     total, pr, ldr, res32, ps = None, None, 0, 0, None
     if residual is not None:
-        _check("residual", residual, dev, _FLOATS, x.shape)
+        _check("residual", residual, dev, _FLOATS, shape)
         pr, ldr = _rows("residual", residual)
-        res32 = int(residual.dtype == _F32)
-        total = torch.empty(x.shape, dtype=residual.dtype, device=dev)
+        res32 = residual.dtype == _F32
+        total = torch.empty_like(residual, memory_format=torch.contiguous_format)
         ps = total.data_ptr()
-    _call("mok_rms_norm", dev, px, int(x.dtype == _F32), ldx, pr, res32, ldr, _dense("weight", weight),
-          int(weight.dtype == _F32), _row_count(x), x.shape[-1], eps, ps, y, codes, scale, rstd)
+    _call("mok_rms_norm", dev, px, x.dtype == _F32, ldx, pr, res32, ldr, _dense("weight", weight),
+          weight.dtype == _F32, x.numel() // cols, cols, eps, ps, y, codes, scale, rstd)
     return total
 
 
@@ -92,9 +92,8 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | Non
     """y = rms_norm(x + residual) * weight in bf16. Returns (y, sum, rstd):
     sum = x + residual in the residual's type (None without a residual), rstd
     fp32 with one value per row. x bf16 or fp32 [..., cols]."""
-    _gpu("x", x)
-    y = torch.empty(x.shape, dtype=_BF16, device=x.device)
-    rstd = torch.empty(x.shape[:-1], dtype=_F32, device=x.device)
+    y = torch.empty_like(x, dtype=_BF16, memory_format=torch.contiguous_format)
+    rstd = x.new_empty(x.shape[:-1], dtype=_F32)
     total = _norm(x, weight, residual, eps, y.data_ptr(), None, None, rstd.data_ptr())
     return y, total, rstd
 
@@ -112,8 +111,8 @@ def rms_norm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor
         _check("y", y, dev, (_BF16,), x.shape)
     if rstd is not None:
         _check("rstd", rstd, dev, (_F32,), x.shape[:-1])
-    codes = torch.empty(x.shape, dtype=_U8, device=dev)
-    scale = torch.empty(x.shape[:-1] + (x.shape[-1] // 32,), dtype=_U8, device=dev)
+    codes = torch.empty_like(x, dtype=_U8, memory_format=torch.contiguous_format)
+    scale = x.new_empty(x.shape[:-1] + (x.shape[-1] // 32,), dtype=_U8)
     total = _norm(x, weight, residual, eps, None if y is None else _dense("y", y), codes.data_ptr(),
                   scale.data_ptr(), None if rstd is None else _dense("rstd", rstd))
     return codes, scale, total
@@ -132,7 +131,7 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, rstd: torch.Tensor, wei
     _check("s", s, dev, _FLOATS, dy.shape)
     _check("rstd", rstd, dev, (_F32,), dy.shape[:-1])
     _check("weight", weight, dev, _FLOATS, dy.shape[-1:])
-    rows, cols = _row_count(dy), dy.shape[-1]
+    rows, cols = dy.numel() // dy.shape[-1], dy.shape[-1]
     pdy, lddy = _rows("dy", dy)
     ps, lds = _rows("s", s)
     pd, ldd = None, 0
@@ -141,10 +140,10 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, rstd: torch.Tensor, wei
         pd, ldd = _rows("d_sum", d_sum)
     if dx is not None:
         _check("dx", dx, dev, (_BF16,), dy.shape)
-    ds = torch.empty(s.shape, dtype=s.dtype, device=dev)
-    d_weight = torch.empty(weight.shape, dtype=weight.dtype, device=dev)
+    ds = torch.empty_like(s, memory_format=torch.contiguous_format)
+    d_weight = torch.empty_like(weight)
     nbytes = _lib.load().mok_rms_norm_scratch_bytes(rows, cols)
-    scratch = torch.empty(nbytes, dtype=_U8, device=dev)
+    scratch = dy.new_empty(nbytes, dtype=_U8)
     _call("mok_rms_norm_backward", dev, pdy, lddy, ps, int(s.dtype == _F32), lds, _dense("rstd", rstd),
           _dense("weight", weight), int(weight.dtype == _F32), pd, ldd, rows, cols, ds.data_ptr(),
           None if dx is None else _dense("dx", dx), d_weight.data_ptr(), scratch.data_ptr(), nbytes)
@@ -178,15 +177,15 @@ def router_topk(logits: torch.Tensor, k: int, *, scoring: str = "softmax", renor
     ``losses`` also (counts int32 [E + 1], losses fp32 [2]): choices per
     expert and the number of live tokens; the load-balance and the z loss."""
     dev, T, E, pl, ld, pb, pm = _router_args(logits, bias, token_mask, scoring)
-    weights = torch.empty((T, k), dtype=_F32, device=dev)
-    ids = torch.empty((T, k), dtype=torch.int64, device=dev)
+    weights = logits.new_empty((T, k), dtype=_F32)
+    ids = logits.new_empty((T, k), dtype=torch.int64)
     counts = loss = scratch = None
     nbytes = 0
     if losses:
-        counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        loss = torch.empty(2, dtype=_F32, device=dev)
+        counts = logits.new_empty(E + 1, dtype=torch.int32)
+        loss = logits.new_empty(2, dtype=_F32)
         nbytes = _lib.load().mok_router_scratch_bytes(T, E)
-        scratch = torch.empty(nbytes, dtype=_U8, device=dev)
+        scratch = logits.new_empty(nbytes, dtype=_U8)
     _call("mok_router_topk", dev, pl, int(logits.dtype == _F32), T, ld, E, k, pb, pm, _SCORING[scoring],
           int(renormalize), scale, weights.data_ptr(), ids.data_ptr(), counts.data_ptr() if losses else None,
           loss.data_ptr() if losses else None, scratch.data_ptr() if losses else None, nbytes)
@@ -211,7 +210,7 @@ def router_topk_backward(d_weights: torch.Tensor, logits: torch.Tensor, ids: tor
     if counts is not None:
         _check("counts", counts, dev, (torch.int32,), (E + 1,))
         _check("d_losses", d_losses, dev, (_F32,), (2,))
-    d_logits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    d_logits = torch.empty_like(logits, memory_format=torch.contiguous_format)
     _call("mok_router_topk_backward", dev, _dense("d_weights", d_weights), pl, int(logits.dtype == _F32), T, ld, E, k,
           pb, pm, _SCORING[scoring], int(renormalize), scale, _dense("ids", ids),
           None if counts is None else _dense("counts", counts),
@@ -219,24 +218,33 @@ def router_topk_backward(d_weights: torch.Tensor, logits: torch.Tensor, ids: tor
     return d_logits
 
 
-def _one_of(name: str, tensors, dtypes) -> torch.dtype:
-    """The one dtype of a list of dense tensors."""
-    found = {t.dtype for t in tensors}
-    if len(found) != 1 or not found <= set(dtypes):
-        raise ValueError(f"{name} must all be {' or all '.join(str(d) for d in dtypes)}, got {found}")
-    for t in tensors:
-        if not t.is_contiguous():
+_dtype = operator.attrgetter("dtype")
+_size, _address, _device = torch.Tensor.numel, torch.Tensor.data_ptr, torch.Tensor.get_device
+
+
+class _Lists:
+    """The tensors of one multi-tensor call: checks a list at a time (the
+    host's share of a step is these checks, so they run in map) and gathers
+    the address arrays."""
+
+    def __init__(self, numels, dev: int):
+        self.numels, self.dev, self.arrays, self.written = numels, dev, {}, []
+
+    def add(self, name: str, tensors, dtypes, numels, written: bool = True) -> torch.dtype:
+        if list(map(_size, tensors)) != numels:
+            raise ValueError(f"the tensors of {name} must have the sizes of the params")
+        found = set(map(_dtype, tensors))
+        if len(found) != 1 or not found <= dtypes:
+            raise ValueError(f"{name} must all be {' or all '.join(map(str, dtypes))}, got {found}")
+        if set(map(_device, tensors)) != {self.dev}:
+            raise ValueError(f"every tensor must be on cuda:{self.dev}: {name}")
+        if not all(map(torch.Tensor.is_contiguous, tensors)):
             raise ValueError(f"every tensor of {name} must be contiguous")
-    return found.pop()
-
-
-def _sizes(name: str, tensors, numels) -> None:
-    if [t.numel() for t in tensors] != numels:
-        raise ValueError(f"the tensors of {name} must have the sizes of the params")
-
-
-def _pointers(tensors):
-    return (C.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
+        addresses = list(map(_address, tensors))
+        self.arrays[name] = (C.c_void_p * len(addresses))(*addresses)
+        if written:
+            self.written += addresses
+        return found.pop()
 
 
 def adamw_step(params, grads, exp_avgs, exp_avg_sqs, masters=None, *, step: int, lr: float,
@@ -251,61 +259,49 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, masters=None, *, step: int,
     (default: the step) chooses the 8-bit states' roundings. No two tensors
     may overlap."""
     n = len(params)
-    lists = dict(grads=grads, exp_avgs=exp_avgs, exp_avg_sqs=exp_avg_sqs)
+    given = [("grads", grads), ("exp_avgs", exp_avgs), ("exp_avg_sqs", exp_avg_sqs)]
     if masters is not None:
-        lists["masters"] = masters
-    for name, ts in lists.items():
+        given.append(("masters", masters))
+    for name, ts in given:
         if len(ts) != n:
             raise ValueError(f"{name} has {len(ts)} tensors, params {n}")
     if n == 0:
         return
     dev = _gpu("params", params[0])
-    numels = [t.numel() for t in params]
-    pdt = _one_of("params", params, _FLOATS)
-    gdt = _one_of("grads", grads, _FLOATS)
-    _sizes("grads", grads, numels)
-    small = isinstance(exp_avgs[0], (tuple, list))
-    written, arrays = list(params), {}
-    arrays["params"], arrays["grads"] = _pointers(params), _pointers(grads)
+    numels = list(map(_size, params))
+    lists = _Lists(numels, dev)
+    pdt = lists.add("params", params, _FLOATS, numels)
+    gdt = lists.add("grads", grads, _FLOATS, numels, written=False)
     if masters is not None:
         if pdt != _BF16:
             raise ValueError("masters go with bf16 params")
-        _one_of("masters", masters, (_F32,))
-        _sizes("masters", masters, numels)
-        arrays["masters"] = _pointers(masters)
-        written += masters
+        lists.add("masters", masters, {_F32}, numels)
+    small = isinstance(exp_avgs[0], (tuple, list))
+    blocks = [(m + 31) // 32 for m in numels] if small else None
     for name, ts in (("exp_avg", exp_avgs), ("exp_avg_sq", exp_avg_sqs)):
         if small:
             try:
                 codes, scales = zip(*ts)
             except (TypeError, ValueError):
                 raise ValueError(f"{name}s must be pairs (codes, scale)") from None
-            _one_of(name + "s", codes, _CODES)
-            _one_of(name + " scales", scales, _SCALES)
-            _sizes(name + "s", codes, numels)
-            _sizes(name + " scales", scales, [(m + 31) // 32 for m in numels])
-            arrays[name + "s"], arrays[name + "_scales"] = _pointers(codes), _pointers(scales)
-            written += codes
-            written += scales
+            lists.add(name + "s", codes, _CODES, numels)
+            lists.add(name + "_scales", scales, _SCALES, blocks)
         else:
-            _one_of(name + "s", ts, (_F32,))
-            _sizes(name + "s", ts, numels)
-            arrays[name + "s"] = _pointers(ts)
-            written += ts
-    if {t.device for t in written} | {t.device for t in grads} != {dev}:
-        raise ValueError(f"every tensor must be on {dev}")
-    where = [t.data_ptr() for t in written if t.numel()]
-    if len(set(where)) != len(where):
-        raise ValueError("a tensor that the step writes is given twice")
+            lists.add(name + "s", ts, {_F32}, numels)
+    if len(set(lists.written)) != len(lists.written):  # (empty tensors have no address: all 0)
+        where = [a for a in lists.written if a]
+        if len(set(where)) != len(where):
+            raise ValueError("a tensor that the step writes is given twice")
     if grad_scale is not None:
         _check("grad_scale", grad_scale, dev, (_F32,))
         if grad_scale.numel() != 1:
             raise ValueError("grad_scale must have one element")
-    a = _lib.MokAdamW(struct_size=C.sizeof(_lib.MokAdamW), count=n, lr=lr, beta1=betas[0], beta2=betas[1], eps=eps,
-                      weight_decay=weight_decay, step=step, param_fp32=int(pdt == _F32), grad_fp32=int(gdt == _F32),
-                      state_bits=8 if small else 32, seed=(step if seed is None else seed) & 0xFFFFFFFF,
-                      grad_scale=None if grad_scale is None else grad_scale.data_ptr())
-    arrays["numels"] = (C.c_int64 * n)(*numels)
-    for name, array in arrays.items():
+    a = _lib.MokAdamW(C.sizeof(_lib.MokAdamW), n)
+    a.lr, (a.beta1, a.beta2), a.eps, a.weight_decay, a.step = lr, betas, eps, weight_decay, step
+    a.param_fp32, a.grad_fp32, a.state_bits = pdt == _F32, gdt == _F32, 8 if small else 32
+    a.seed = (step if seed is None else seed) & 0xFFFFFFFF
+    a.grad_scale = None if grad_scale is None else grad_scale.data_ptr()
+    lists.arrays["numels"] = (C.c_int64 * n)(*numels)
+    for name, array in lists.arrays.items():
         setattr(a, name, C.addressof(array))
     _call("mok_adamw_step", dev, C.byref(a))
