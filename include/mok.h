@@ -447,8 +447,8 @@ size_t mok_router_scratch_bytes(int64_t T, int32_t experts);
  *   weights fp32 [T, k]: the scores of the chosen, divided by their sum if
  *         `renormalize`, times `scale`.
  * token_mask (nullable, one byte per token): tokens with a 0 get ids -1 and
- * weights 0, whatever their logits hold. A row with a NaN key or a +inf
- * logit has no order: ids -1 and weights NaN.
+ * weights 0, whatever their logits hold. A row with a key that is NaN or
+ * +inf has no order: ids -1 and weights NaN.
  * Statistics (counts and losses, both or neither; then scratch is needed):
  *   counts int32 [experts + 1]: choices of each expert, then the number n of
  *         live tokens: kept by the mask, with a key above -inf (or no order)
@@ -456,7 +456,7 @@ size_t mok_router_scratch_bytes(int64_t T, int32_t experts);
  *         experts and N = max(n, 1): the load-balance loss experts / (k N^2)
  *         * sum_e counts_e * (sum of p_e over live tokens), and the z loss,
  *         the mean over live tokens of logsumexp(logits)^2 (0 for sigmoid).
- * 1 <= k <= min(experts, 64), experts <= 1024.
+ * 1 <= k <= min(experts, 64), experts <= 1024, ld <= 2^22 for T > 1.
  */
 mok_status mok_router_topk(const void* logits, int logits_is_fp32, int64_t T, int64_t ld, int32_t experts, int32_t k,
                            const float* bias, const uint8_t* token_mask, int32_t scoring, int renormalize, float scale,

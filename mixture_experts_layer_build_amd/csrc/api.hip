@@ -782,6 +782,7 @@ static mok_status check_router(const void* logits, int logits_is_fp32, int64_t T
   if (scoring != MOK_ROUTER_SOFTMAX && scoring != MOK_ROUTER_SIGMOID) return MOK_ERR_INVALID_ARGUMENT;
   if (k > experts) return MOK_ERR_INVALID_ARGUMENT;
   if (experts > 1024 || k > 64 || T > ((int64_t)1 << 40)) return MOK_ERR_UNSUPPORTED;
+  if (T > 1 && ld > ((int64_t)1 << 22)) return MOK_ERR_UNSUPPORTED;  // a workgroup's rows: 32-bit offsets
   if (T > 0 && (!logits || ld < experts)) return MOK_ERR_INVALID_ARGUMENT;
   if (!element_aligned(logits, logits_is_fp32) || !element_aligned(bias, 1)) return MOK_ERR_INVALID_ARGUMENT;
   return MOK_OK;
@@ -812,7 +813,7 @@ extern "C" mok_status mok_router_topk(const void* logits, int logits_is_fp32, in
   const int cus = current_cus();
   if (cus <= 0) return MOK_ERR_HIP;
   RouterArgs r{};
-  r.logits = logits, r.logits_fp32 = logits_is_fp32, r.T = T, r.ld = ld, r.E = experts, r.k = k;
+  r.logits = logits, r.logits_fp32 = logits_is_fp32, r.T = T, r.ld = T > 1 ? ld : experts, r.E = experts, r.k = k;
   r.bias = bias, r.mask = token_mask, r.sigmoid = scoring == MOK_ROUTER_SIGMOID, r.renorm = renormalize;
   r.scale = scale, r.weights = weights, r.ids = ids, r.counts = counts, r.losses = losses, r.part = (float*)scratch;
   return to_status(launch_router(r, cus, (hipStream_t)stream));
@@ -834,7 +835,7 @@ extern "C" mok_status mok_router_topk_backward(const float* d_weights, const voi
   const int cus = current_cus();
   if (cus <= 0) return MOK_ERR_HIP;
   RouterBwdArgs r{};
-  r.logits = logits, r.logits_fp32 = logits_is_fp32, r.T = T, r.ld = ld, r.E = experts, r.k = k;
+  r.logits = logits, r.logits_fp32 = logits_is_fp32, r.T = T, r.ld = T > 1 ? ld : experts, r.E = experts, r.k = k;
   r.bias = bias, r.mask = token_mask, r.sigmoid = scoring == MOK_ROUTER_SIGMOID, r.renorm = renormalize;
   r.scale = scale, r.d_weights = d_weights, r.ids = ids, r.counts = counts, r.d_losses = d_losses;
   r.d_logits = d_logits;

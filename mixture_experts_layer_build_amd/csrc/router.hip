@@ -10,17 +10,17 @@
 //   balance  = E / (k T^2) * sum_e count_e * sum_t p_te,   z = sum_t lse_t^2 / T
 //
 // T counts the live tokens: those the mask keeps that have a key above -inf.
-// A row with a NaN key or a +inf logit has no order: its ids are -1 and its
+// A row with a key that is NaN or +inf has no order: its ids are -1 and its
 // weights NaN.
 //
-// Layout: a token belongs to 16 lanes (E <= 256) or to a whole wave, lane l
+// Layout: a token belongs to 16 lanes (E <= 512) or to a whole wave, lane l
 // holding experts l, l + 16, ... in registers, so a wave runs four tokens at
 // once and every reduction over a token is four DPP instructions.
 //
 // The choice. Per token it costs instructions, not bytes, so it decides the
 // kernel's time beyond about 64 experts. Up to k = 16 it is a sorting
 // network on 32-bit words, the key's order-preserving bits with the lowest 8
-// (10 with a wave per token) replaced by the complement of the expert id: a
+// (9 and 10 above 256 and 512 experts) replaced by the complement of the expert id: a
 // comparator is one max and one min, a lane sorts its experts' words to the
 // 8 or 16 largest, and four merges with the lists of other lanes (max with a
 // DPP operand, then a half-cleaner) leave the token's list in every lane.
@@ -54,13 +54,19 @@ __device__ __forceinline__ float grp_max(float x) {
   return wave_max(x);
 }
 template <int G>
+__device__ __forceinline__ uint32_t grp_umax(uint32_t x) {
+  if constexpr (G == 16) return row_umax(x);
+  return wave_umax(x);
+}
+template <int G>
 __device__ __forceinline__ int grp_min(int x) {
   if constexpr (G == 16) return row_min(x);
   return wave_min(x);
 }
 
 constexpr float kInf = __builtin_inff();
-constexpr int kStatsHead = 64;  // words of the statistics' scratch before the partial rows
+// words of the statistics' scratch before the partial rows (router_stats)
+constexpr int kStatsHead = 128, kStatsZ = 96;
 
 struct RouterFwd {
   const void* logits;
@@ -76,60 +82,81 @@ struct RouterFwd {
   float* part;            // statistics (router_stats)
 };
 
-// Bits of a key in its order (larger key, larger word; both zeros alike).
+// Bits of a key in its order (larger key, larger word); the key is the sum of
+// a logit and a bias or zero, so never -0. -inf is kNone, words of numbers lie
+// above it, +inf and NaN outside [kNone, kBroken).
+constexpr uint32_t kNone = 0x007FFFFFu, kBroken = 0xFF800000u;
 __device__ __forceinline__ uint32_t ordered(float key) {
-  const uint32_t u = f2u(key + 0.0f);
+  const uint32_t u = f2u(key);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
-// The bits of a word that hold the complement of the expert id.
-constexpr uint32_t word_ids(int G) { return G == 16 ? 255u : 1023u; }
+// The bits of a word that hold the complement of the expert id, with G lanes
+// of V experts each.
+constexpr uint32_t word_ids(int G, int V) { return G * V <= 256 ? 255u : G * V - 1u; }
+// The key that a word without lost bits came from (bf16 keys).
+__device__ __forceinline__ float key_of(uint32_t word, uint32_t ids) {
+  return u2f(word & 0x80000000u ? (word ^ 0x80000000u) & ~ids : ~(word | ids));
+}
 
-// A token's logits and whether it is live or without an order.
+// A token's logits, lane gl of its group holding experts gl, gl + G, ... (-inf
+// past E), and what they say of the token.
 template <typename LT, int G, int VPL, bool WORDS>
 struct Row {
-  static constexpr uint32_t kIds = word_ids(G);
   float l[VPL];
-  uint32_t word[VPL];  // the keys' words for the network, 0 for -inf
-  float top;   // largest logit
-  bool live;   // kept by the mask, and some key above -inf or no order
-  bool broken; // NaN key or +inf logit
+  uint32_t word[VPL];  // WORDS: the keys' words for the network
+  float top;           // largest logit
+  bool live;           // kept by the mask, and some key above -inf or no order
+  bool broken;         // a key that is NaN or +inf
 
-  __device__ __forceinline__ void load(const LT* p, const float* bias, int E, int gl, bool keep) {
-    float mk = -kInf;
-    int bad = 0;
+  // `p`: the workgroup's first token of this turn, `off` this token's offset
+  // from it, `last` the last one that may be read.
+  __device__ __forceinline__ void load(const LT* p, uint32_t off, uint32_t last, const float* bias, int E, int gl,
+                                       bool keep) {
+    constexpr uint32_t kIds = word_ids(G, VPL);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      // (bytes in 32 bits: a scalar base and one register of offset)
+      const uint32_t o = min(off + (uint32_t)(i * G + gl), last) * (uint32_t)sizeof(LT);
+      l[i] = load1((const LT*)((const char*)p + o));
+    }
     top = -kInf;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-      const int e = i * G + gl;
-      l[i] = (keep && e < E) ? load1(p + e) : -kInf;
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      const int e = i * G + gl;
-      const float key = (bias && e < E) ? l[i] + bias[e] : l[i];
-      bad |= !(key == key) | (l[i] == kInf);
-      mk = __builtin_fmaxf(mk, key);
-      if constexpr (WORDS) word[i] = key > -kInf ? (ordered(key) & ~kIds) | (kIds - (uint32_t)e) : 0u;
+      l[i] = i * G + gl < E ? l[i] : -kInf;
       top = __builtin_fmaxf(top, l[i]);
     }
     top = grp_max<G>(top);
-    mk = grp_max<G>(mk);
-    broken = grp_min<G>(-bad) < 0;
-    live = broken || mk > -kInf;
+    uint32_t most = 0;
+    auto see = [&](int i, float key) {
+      const uint32_t w = ordered(key);
+      most = max(most, w - kNone);
+      if constexpr (WORDS) word[i] = (w & ~kIds) | (kIds - (uint32_t)(i * G + gl));
+    };
+    if (bias) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) see(i, l[i] + bias[min(i * G + gl, E - 1)]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) see(i, l[i] + 0.0f);
+    }
+    most = grp_umax<G>(most);
+    broken = keep && most >= kBroken - kNone;
+    live = keep && most > 0;
   }
 };
 
 // Score of a logit up to a factor common to its token, from the token's
 // largest logit `top` (for sigmoid at most 0): e^(l - top), or sigmoid(l) /
 // e^top = e^(min(l, 0) - top) / (1 + e^-|l|), which is not 0 / 0 where every
-// logit is far below 0. l = -inf gives 0.
-__device__ __forceinline__ float score_of(float l, float top, int sigmoid) {
-  if (!sigmoid) return exp_neg(l - top);
-  return exp_neg(__builtin_fminf(l, 0.f) - top) / (1.f + exp_neg(-__builtin_fabsf(l)));
+// logit is far below 0. l = -inf gives 0 (in a token that has a number).
+template <bool SIGMOID>
+__device__ __forceinline__ float score_of(float l, float top) {
+  if constexpr (!SIGMOID) return exp_neg(l - top);
+  return exp_neg(__builtin_fminf(l, 0.f) - top) * __builtin_amdgcn_rcpf(1.f + exp_neg(-__builtin_fabsf(l)));
 }
 // 1 - sigmoid(l)
 __device__ __forceinline__ float one_minus(float l) {
-  return exp_neg(__builtin_fminf(-l, 0.f)) / (1.f + exp_neg(-__builtin_fabsf(l)));
+  return exp_neg(__builtin_fminf(-l, 0.f)) * __builtin_amdgcn_rcpf(1.f + exp_neg(-__builtin_fabsf(l)));
 }
 
 // ---- the sorting network --------------------------------------------
@@ -183,12 +210,13 @@ __device__ __forceinline__ void merge_xor(uint32_t (&w)[N], int d) {
   for (int i = 0; i < N; ++i) w[i] = m[i];
 }
 
-// Choice gl of the token (-1: none) in lane gl of the group, for k <= N <=
-// 16. False (for the whole wave) if some token's order hangs on key bits
-// that the words do not keep.
+// The word of choice gl of the token (kNone or less: none) in lane gl of the
+// group, for k <= N <= 16. False (for the whole wave) if some token's order
+// hangs on key bits that the words do not keep.
 template <int N, int G, int VPL>
-__device__ __forceinline__ bool choose_network(const uint32_t (&word)[VPL], int gl, int k, bool exact, int& pick) {
-  constexpr uint32_t kIds = word_ids(G);
+__device__ __forceinline__ bool choose_network(const uint32_t (&word)[VPL], int gl, int k, bool exact, bool keep,
+                                               uint32_t& mine) {
+  constexpr uint32_t kIds = word_ids(G, VPL);
   uint32_t top[N];
 #pragma unroll
   for (int c = 0; c < VPL; c += N) {
@@ -218,32 +246,35 @@ __device__ __forceinline__ bool choose_network(const uint32_t (&word)[VPL], int 
     merge_xor<N>(top, 16);
     merge_xor<N>(top, 32);
   }
-  uint32_t mine = 0;
+  mine = 0;
 #pragma unroll
   for (int j = 0; j < N; ++j) mine = gl == j && j < k ? top[j] : mine;
-  pick = mine ? (int)(kIds - (mine & kIds)) : -1;
   if (exact) return true;
-  // the first word behind the k chosen
+  // neighbours in the list, and the first word behind the k chosen
+  auto close = [](uint32_t a, uint32_t b) { return b > kNone && ((a ^ b) & ~kIds) == 0; };
   uint32_t last = 0, behind = 0;
+  bool any = false;
 #pragma unroll
-  for (int j = 0; j < N; ++j) last = j == k - 1 ? top[j] : last;
+  for (int j = 0; j < N; ++j) {
+    last = j == k - 1 ? top[j] : last;
+    if (j + 1 < N) any |= j + 1 < k && close(top[j], top[j + 1 < N ? j + 1 : j]);
+  }
 #pragma unroll
   for (int i = 0; i < VPL; ++i) behind = max(behind, word[i] < last ? word[i] : 0u);
-  bool close = behind != 0 && ((behind ^ last) & ~kIds) == 0;
-#pragma unroll
-  for (int j = 0; j + 1 < N; ++j) close |= j + 1 < k && top[j + 1] != 0 && ((top[j] ^ top[j + 1]) & ~kIds) == 0;
-  return __ballot(close) == 0;
+  any |= close(last, behind);
+  return __ballot(keep && any) == 0;
 }
 
+// NET: width of the sorting network, 8 for k <= 8, else 16.
 // STATS: the sums behind the losses and counts. A workgroup then keeps them
 // in registers and LDS over its tokens and writes one partial row.
-template <typename LT, int G, int VPL, int BLOCK, bool STATS>
+template <typename LT, int G, int VPL, int BLOCK, bool STATS, bool SIGMOID, int NET>
 __global__ void __launch_bounds__(BLOCK) router_rows(RouterFwd a) {
   constexpr int GPB = BLOCK / G;
   constexpr int KQ = 64 / G;  // choices a lane may hold (k <= 64)
   extern __shared__ float lds[];  // STATS: int cnt[E + 1], then float sums[waves][E + 1]
   const int E = a.E, k = a.k;
-  const int gl = (int)threadIdx.x % G, group = (int)threadIdx.x / G;
+  const int lane = (int)threadIdx.x % G, group = (int)threadIdx.x / G;
   int* cnt = (int*)lds;
   float psum[VPL];
   float zsum = 0.f;
@@ -257,24 +288,29 @@ __global__ void __launch_bounds__(BLOCK) router_rows(RouterFwd a) {
   for (int64_t t0 = (int64_t)blockIdx.x * GPB; t0 < a.T; t0 += (int64_t)gridDim.x * GPB) {
     const int64_t t = t0 + group;
     const bool in = t < a.T;
+    // (a new value to the compiler in each turn: what follows from it for each
+    // of the lane's experts would otherwise be computed before the loop and
+    // held, in more registers than there are)
+    const int gl = opaque(lane);
     const bool keep = in && (!a.mask || a.mask[t]);
-    const LT* row = (const LT*)a.logits + (in ? t : 0) * a.ld;
+    // (a workgroup's tokens lie within 2^31 elements: the host checks ld)
+    const LT* rows = (const LT*)a.logits + t0 * a.ld;
+    const uint32_t ld = (uint32_t)a.ld, ngrp = (uint32_t)min<int64_t>(GPB, a.T - t0);
+    const uint32_t off = min((uint32_t)group, ngrp - 1) * ld, last = (ngrp - 1) * ld + (uint32_t)E - 1;
+    const LT* row = rows + off;
     Row<LT, G, VPL, true> r;
-    r.load(row, a.bias, E, gl, keep);
+    r.load(rows, off, last, a.bias, E, gl, keep);
     int pick[KQ];
 #pragma unroll
     for (int q = 0; q < KQ; ++q) pick[q] = -1;
-    bool done = false;
-    if (k <= 8)
-      done = choose_network<8, G, VPL>(r.word, gl, k, a.exact_words, pick[0]);
-    else if (k <= 16)
-      done = choose_network<16, G, VPL>(r.word, gl, k, a.exact_words, pick[0]);
+    uint32_t mine = 0;
+    const bool done = k <= NET && choose_network<NET, G, VPL>(r.word, gl, k, a.exact_words, keep, mine);
+    if (done) pick[0] = mine > kNone ? (int)(word_ids(G, VPL) - (mine & word_ids(G, VPL))) : -1;
     if (!done) {
       float key[VPL];
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        const int e = i * G + gl;
-        key[i] = (a.bias && e < E) ? r.l[i] + a.bias[e] : r.l[i];
+        key[i] = a.bias ? r.l[i] + a.bias[min(i * G + gl, E - 1)] : r.l[i];
       }
 #pragma unroll
       for (int q = 0; q < KQ; ++q) {
@@ -296,36 +332,36 @@ __global__ void __launch_bounds__(BLOCK) router_rows(RouterFwd a) {
       }
     }
 #pragma unroll
-    for (int q = 0; q < KQ; ++q) pick[q] = r.broken ? -1 : pick[q];
+    for (int q = 0; q < KQ; ++q) pick[q] = keep && !r.broken ? pick[q] : -1;
     // weights of the choices: lane j of the group holds choice j, j + G, ...
     const float nan = r.broken ? __builtin_nanf("") : 0.f;
     float w[KQ], ltop = -kInf;
 #pragma unroll
     for (int q = 0; q < KQ; ++q) {
       if (q * G >= k) break;
-      w[q] = pick[q] >= 0 ? load1(row + pick[q]) : -kInf;
+      w[q] = pick[q] < 0 ? -kInf : done && a.exact_words ? key_of(mine, word_ids(G, VPL)) : load1(row + pick[q]);
       ltop = __builtin_fmaxf(ltop, w[q]);
     }
     // the scores over all experts, where anything needs them
     float den = 0.f, score[VPL];
-    const float ptop = a.sigmoid ? __builtin_fminf(r.top, 0.f) : r.top;
-    if (STATS || (!a.sigmoid && !a.renorm)) {
+    const float ptop = SIGMOID ? __builtin_fminf(r.top, 0.f) : r.top;
+    if (STATS || (!SIGMOID && !a.renorm)) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        score[i] = score_of(r.l[i], ptop, a.sigmoid);
+        score[i] = score_of<SIGMOID>(r.l[i], ptop);
         den += score[i];
       }
       den = grp_sum<G>(den);
     }
-    const float wtop = a.renorm ? grp_max<G>(ltop) : a.sigmoid ? 0.f : ptop;
+    const float wtop = a.renorm ? grp_max<G>(ltop) : SIGMOID ? 0.f : ptop;
     float sum = 0.f;
 #pragma unroll
     for (int q = 0; q < KQ; ++q) {
       if (q * G >= k) break;
-      w[q] = pick[q] < 0 ? 0.f : score_of(w[q], a.sigmoid ? __builtin_fminf(wtop, 0.f) : wtop, a.sigmoid);
+      w[q] = pick[q] < 0 ? 0.f : score_of<SIGMOID>(w[q], SIGMOID ? __builtin_fminf(wtop, 0.f) : wtop);
       sum += w[q];
     }
-    const float total = a.renorm ? grp_sum<G>(sum) : a.sigmoid ? 1.f : den;
+    const float total = a.scale * __builtin_amdgcn_rcpf(a.renorm ? grp_sum<G>(sum) : SIGMOID ? 1.f : den);
 #pragma unroll
     for (int q = 0; q < KQ; ++q) {
       if (q * G >= k) break;
@@ -333,13 +369,13 @@ __global__ void __launch_bounds__(BLOCK) router_rows(RouterFwd a) {
       if (in && j < k) {
         const int64_t o = t * k + j;
         a.ids[o] = pick[q];
-        a.weights[o] = (pick[q] >= 0 ? w[q] / total * a.scale : 0.f) + nan;
+        a.weights[o] = (pick[q] >= 0 ? w[q] * total : 0.f) + nan;
       }
       if (STATS && pick[q] >= 0) atomicAdd(cnt + pick[q], 1);  // integers: any order gives the same count
     }
     if constexpr (STATS) {
       if (r.live) {
-        const float inv = 1.f / den + nan;
+        const float inv = __builtin_amdgcn_rcpf(den) + nan;
 #pragma unroll
         for (int i = 0; i < VPL; ++i) psum[i] = __builtin_fmaf(score[i], inv, psum[i]);
         if (gl == 0) {
@@ -354,7 +390,7 @@ __global__ void __launch_bounds__(BLOCK) router_rows(RouterFwd a) {
     // a wave's four tokens (or one), then the waves in order
     constexpr int WAVES = BLOCK / 64;
     float* sums = lds + (E + 1);
-    const int wave = threadIdx.x >> 6, lane = lane_id();
+    const int wave = threadIdx.x >> 6, wl = lane_id();
     if constexpr (G == 16) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
@@ -364,10 +400,10 @@ __global__ void __launch_bounds__(BLOCK) router_rows(RouterFwd a) {
     }
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (lane < G && i * G + gl < E) sums[wave * (E + 1) + i * G + gl] = psum[i];
+      if (wl < G && i * G + wl < E) sums[wave * (E + 1) + i * G + wl] = psum[i];
     zsum = wave_sum(zsum);
-    if (lane == 0) sums[wave * (E + 1) + E] = zsum;
-    if (gl == 0 && nlive) atomicAdd(cnt + E, nlive);
+    if (wl == 0) sums[wave * (E + 1) + E] = zsum;
+    if (lane == 0 && nlive) atomicAdd(cnt + E, nlive);
     __syncthreads();
     float* part = a.part + kStatsHead + (int64_t)blockIdx.x * 2 * (E + 1);
     for (int i = threadIdx.x; i <= E; i += BLOCK) {
@@ -382,52 +418,59 @@ __global__ void __launch_bounds__(BLOCK) router_rows(RouterFwd a) {
 }
 
 // Adds the workgroups' partial rows in a fixed order and forms the losses.
-// A workgroup takes 64 columns, 16 adders each; the one that finishes last
-// (a counter that the launch before cleared) adds the columns' products in
-// order, so one launch does both.
+// A workgroup takes 16 columns, 64 adders each, so that every load of a
+// thread is in flight at once; the workgroup that finishes last (a counter
+// that the launch before cleared) adds the columns' products in order, so
+// one launch does both.
 //
 // The scratch: kStatsHead words, [0] the counter, [1 + b] workgroup b's sum
-// of count_e * (sum of p_e), [32] the sum of lse^2, [33] the live tokens;
-// then per workgroup of the forward 2 (E + 1) words, the sums of p and of
-// lse^2 and the counts and live tokens.
+// of count_e * (sum of p_e), [kStatsZ] the sum of lse^2, [kStatsZ + 1] the
+// live tokens; then per workgroup of the forward 2 (E + 1) words, the sums of
+// p and of lse^2 and the counts and live tokens.
 __global__ void __launch_bounds__(1024) router_stats(float* part, int nparts, int E, int k, int sigmoid,
                                                      int32_t* counts, float* losses) {
-  __shared__ float fs[16][64];
-  __shared__ int is[16][64];
-  const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
+  __shared__ float fs[16][16];
+  __shared__ int is[16][16];
+  const int wl = lane_id(), wave = threadIdx.x >> 6;
+  const int c = (int)blockIdx.x * 16 + (wl & 15);
+  const int g = wave * 4 + (wl >> 4);
   const int W = 2 * (E + 1);
-  const int c = (int)blockIdx.x * 64 + lane;
   const float* rows = part + kStatsHead;
   float f = 0.f;
   int n = 0;
   if (c <= E)
-#pragma unroll 8
-    for (int r = g; r < nparts; r += 16) {
+#pragma unroll 4
+    for (int r = g; r < nparts; r += 64) {
       f += rows[(int64_t)r * W + c];
       n += ((const int*)rows)[(int64_t)r * W + E + 1 + c];
     }
-  fs[g][lane] = f;
-  is[g][lane] = n;
+  f += __shfl_xor(f, 16), n += __shfl_xor(n, 16);
+  f += __shfl_xor(f, 32), n += __shfl_xor(n, 32);
+  if (wl < 16) fs[wave][wl] = f, is[wave][wl] = n;
   __syncthreads();
-  if (g != 0) return;
+  if (wave != 0) return;
+  f = 0.f, n = 0;
 #pragma unroll
-  for (int i = 1; i < 16; ++i) f += fs[i][lane], n += is[i][lane];
-  if (c <= E) counts[c] = n;
-  const float dot = wave_sum(c < E ? (float)n * f : 0.f);
-  if (c == E) {
-    __hip_atomic_store(part + 32, f, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store((int*)part + 33, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  for (int i = 0; i < 16; ++i) f += fs[i][wl & 15], n += is[i][wl & 15];
+  if (wl < 16 && c <= E) counts[c] = n;
+  const float dot = row_sum(c < E ? (float)n * f : 0.f);
+  if (wl < 16 && c == E) {
+    __hip_atomic_store(part + kStatsZ, f, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store((int*)part + kStatsZ + 1, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  if (lane == 0) __hip_atomic_store(part + 1 + blockIdx.x, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  uint32_t done = 0;
+  if (wl == 0) __hip_atomic_store(part + 1 + blockIdx.x, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __threadfence();  // every lane's stores, before the count
-  if (lane == 0) done = __hip_atomic_fetch_add((uint32_t*)part, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1;
-  if (lane != 0 || done != gridDim.x) return;
+  uint32_t done = 0;
+  if (wl == 0) done = __hip_atomic_fetch_add((uint32_t*)part, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) + 1;
+  done = (uint32_t)lane_value((int)done, 0);
+  if (done != gridDim.x) return;
   float s = 0.f;
-  for (uint32_t b = 0; b < gridDim.x; ++b)
+  for (uint32_t b = wl; b < gridDim.x; b += 64)
     s += __hip_atomic_load(part + 1 + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const float z = __hip_atomic_load(part + 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  const float live = (float)max(__hip_atomic_load((int*)part + 33, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), 1);
+  s = wave_sum(s);
+  if (wl != 0) return;
+  const float z = __hip_atomic_load(part + kStatsZ, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const float live = (float)max(__hip_atomic_load((int*)part + kStatsZ + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT), 1);
   losses[0] = s / live / live * ((float)E / (float)k);
   losses[1] = sigmoid ? 0.f : z / live;
 }
@@ -453,26 +496,34 @@ struct RouterBwd {
 //   sigmoid:        s (1 - s) dw;  renormalised: (1 - s_c) q_c (dw_c - sum q dw), q = s / sum of the chosen s
 //   losses:         a_e = d_balance * E / (k T^2) * count_e:  p_e (a_e - sum p a), for sigmoid times (1 - s_e);
 //                   softmax: + d_z * 2 lse / T * p_e
-template <typename LT, int G, int VPL, int BLOCK>
+template <typename LT, int G, int VPL, int BLOCK, bool SIGMOID>
 __global__ void __launch_bounds__(BLOCK) router_bwd_rows(RouterBwd a) {
   constexpr int GPB = BLOCK / G;
   constexpr int KQ = 64 / G;
   const int E = a.E, k = a.k;
-  const int gl = (int)threadIdx.x % G, group = (int)threadIdx.x / G;
+  const int lane = (int)threadIdx.x % G, group = (int)threadIdx.x / G;
   const bool losses = a.counts != nullptr;
   float ga = 0.f, gz = 0.f;
   if (losses) {
     const float n = (float)max(a.counts[E], 1);
     ga = a.d_losses[0] * ((float)E / (float)k) / n / n;
-    gz = a.sigmoid ? 0.f : a.d_losses[1] * 2.f / n;
+    gz = SIGMOID ? 0.f : a.d_losses[1] * 2.f / n;
   }
   for (int64_t t0 = (int64_t)blockIdx.x * GPB; t0 < a.T; t0 += (int64_t)gridDim.x * GPB) {
     const int64_t t = t0 + group;
     const bool in = t < a.T;
+    // (a new value to the compiler in each turn: what follows from it for each
+    // of the lane's experts would otherwise be computed before the loop and
+    // held, in more registers than there are)
+    const int gl = opaque(lane);
     const bool keep = in && (!a.mask || a.mask[t]);
-    const LT* row = (const LT*)a.logits + (in ? t : 0) * a.ld;
+    // (a workgroup's tokens lie within 2^31 elements: the host checks ld)
+    const LT* rows = (const LT*)a.logits + t0 * a.ld;
+    const uint32_t ld = (uint32_t)a.ld, ngrp = (uint32_t)min<int64_t>(GPB, a.T - t0);
+    const uint32_t off = min((uint32_t)group, ngrp - 1) * ld, last = (ngrp - 1) * ld + (uint32_t)E - 1;
+    const LT* row = rows + off;
     Row<LT, G, VPL, false> r;
-    r.load(row, a.bias, E, gl, keep);
+    r.load(rows, off, last, a.bias, E, gl, keep);
     // the choices, one or more per lane; an id outside [0, E) has no gradient
     int id[KQ];
     float c[KQ], lc[KQ], ltop = -kInf;
@@ -493,45 +544,45 @@ __global__ void __launch_bounds__(BLOCK) router_bwd_rows(RouterBwd a) {
       }
       ltop = __builtin_fmaxf(ltop, lc[q]);
     }
-    const float ptop = a.sigmoid ? __builtin_fminf(r.top, 0.f) : r.top;
+    const float ptop = SIGMOID ? __builtin_fminf(r.top, 0.f) : r.top;
     const float nan = r.broken ? __builtin_nanf("") : 0.f;
     float p[VPL], den = 0.f;
-    const bool full = losses || (!a.sigmoid && !a.renorm);
+    const bool full = losses || (!SIGMOID && !a.renorm);
     if (full) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        p[i] = score_of(r.l[i], ptop, a.sigmoid);
+        p[i] = score_of<SIGMOID>(r.l[i], ptop);
         den += p[i];
       }
       den = grp_sum<G>(den);
-      const float inv = 1.f / den;
+      const float inv = __builtin_amdgcn_rcpf(den);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) p[i] *= inv;
     }
     // c becomes the gradient to the chosen logits
     float along = 0.f;  // softmax without renormalisation: sum_j p_cj dw_j
     {
-      const float wtop = a.renorm ? grp_max<G>(ltop) : a.sigmoid ? 0.f : ptop;
+      const float wtop = a.renorm ? grp_max<G>(ltop) : SIGMOID ? 0.f : ptop;
       float sc[KQ], sum = 0.f, dot = 0.f;
 #pragma unroll
       for (int q = 0; q < KQ; ++q) {
         if (q * G >= k) break;
-        sc[q] = id[q] < 0 ? 0.f : score_of(lc[q], a.sigmoid ? __builtin_fminf(wtop, 0.f) : wtop, a.sigmoid);
+        sc[q] = id[q] < 0 ? 0.f : score_of<SIGMOID>(lc[q], SIGMOID ? __builtin_fminf(wtop, 0.f) : wtop);
         sum += sc[q];
         dot = __builtin_fmaf(sc[q], c[q], dot);
       }
       if (a.renorm) {
         sum = grp_sum<G>(sum);
         dot = sum > 0.f ? grp_sum<G>(dot) / sum : 0.f;
-      } else if (!a.sigmoid) {
+      } else if (!SIGMOID) {
         along = grp_sum<G>(dot) / den;
       }
 #pragma unroll
       for (int q = 0; q < KQ; ++q) {
         if (q * G >= k) break;
         if (id[q] < 0) continue;
-        c[q] = a.renorm ? sc[q] / sum * (c[q] - dot) : a.sigmoid ? sc[q] * c[q] : sc[q] / den * c[q];
-        if (a.sigmoid) c[q] *= one_minus(lc[q]);
+        c[q] = a.renorm ? sc[q] / sum * (c[q] - dot) : SIGMOID ? sc[q] * c[q] : sc[q] / den * c[q];
+        if (SIGMOID) c[q] *= one_minus(lc[q]);
       }
     }
     float dl[VPL];
@@ -544,11 +595,11 @@ __global__ void __launch_bounds__(BLOCK) router_bwd_rows(RouterBwd a) {
         pa = __builtin_fmaf(p[i], dl[i], pa);
       }
       pa = grp_sum<G>(pa);
-      const float more = (a.sigmoid ? 0.f : gz * (r.top + __logf(den)) - along) - pa;
+      const float more = (SIGMOID ? 0.f : gz * (r.top + __logf(den)) - along) - pa;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         dl[i] = p[i] * (dl[i] + more);
-        if (a.sigmoid && r.l[i] > -kInf) dl[i] *= one_minus(r.l[i]);
+        if (SIGMOID && r.l[i] > -kInf) dl[i] *= one_minus(r.l[i]);
       }
     } else {
 #pragma unroll
@@ -588,18 +639,25 @@ template <typename F>
 void with_layout(int E, F&& f) {
   using std::integral_constant;
   auto go = [&](auto g, auto v) { f(g, v); };
-  if (E <= 16) go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-  else if (E <= 32) go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  else if (E <= 64) go(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  if (E <= 64) go(integral_constant<int, 16>{}, integral_constant<int, 4>{});
   else if (E <= 128) go(integral_constant<int, 16>{}, integral_constant<int, 8>{});
   else if (E <= 256) go(integral_constant<int, 16>{}, integral_constant<int, 16>{});
-  else if (E <= 512) go(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+  else if (E <= 512) go(integral_constant<int, 16>{}, integral_constant<int, 32>{});
   else go(integral_constant<int, 64>{}, integral_constant<int, 16>{});
 }
 
-// Workgroup of the forward with statistics, for G lanes per token: one per
-// compute unit, its LDS (one row of sums per wave) below 64 KiB at every E.
-constexpr int stats_block(int G) { return G == 16 ? 1024 : 512; }
+template <typename F>
+void with_types(int fp32, int sigmoid, F&& f) {
+  if (fp32)
+    sigmoid ? f(float{}, std::true_type{}) : f(float{}, std::false_type{});
+  else
+    sigmoid ? f(uint16_t{}, std::true_type{}) : f(uint16_t{}, std::false_type{});
+}
+
+// Workgroup of the forward with statistics: one per compute unit, its LDS
+// (one row of sums per wave) below 64 KiB and its registers enough at every E.
+constexpr int stats_block(int E) { return E <= 256 ? 1024 : 512; }
+constexpr int lanes_of(int E) { return E <= 512 ? 16 : 64; }
 constexpr int kStatsParts = 256;
 
 }  // namespace
@@ -607,7 +665,7 @@ constexpr int kStatsParts = 256;
 // Workgroups of the forward with statistics, at most: a constant, so the
 // order of the sums does not depend on the device.
 static int64_t router_parts(int64_t T, int64_t E) {
-  const int64_t gpb = E <= 256 ? stats_block(16) / 16 : stats_block(64) / 64;
+  const int64_t gpb = stats_block((int)E) / lanes_of((int)E);
   return std::min<int64_t>((std::max<int64_t>(T, 1) + gpb - 1) / gpb, kStatsParts);
 }
 int64_t router_scratch_words(int64_t T, int64_t E) { return kStatsHead + router_parts(T, E) * 2 * (E + 1); }
@@ -618,25 +676,32 @@ hipError_t launch_router(const RouterArgs& r, int cus, hipStream_t s) {
   const bool stats = r.counts != nullptr;
   if (r.T == 0 && !stats) return hipSuccess;
   const int parts = (int)router_parts(r.T, r.E);
-  auto go = [&](auto tag) {
+  auto go = [&](auto tag, auto sig) {
     using LT = decltype(tag);
+    constexpr bool SIG = decltype(sig)::value;
     with_layout(r.E, [&](auto g, auto v) {
       constexpr int G = decltype(g)::value, V = decltype(v)::value;
       if (stats) {
-        constexpr int B = stats_block(G);
+        constexpr int B = stats_block(G * V);
         const size_t lds = sizeof(float) * (size_t)(r.E + 1) * (1 + B / 64);
-        router_rows<LT, G, V, B, true><<<parts, B, lds, s>>>(a);
+        if (r.k <= 8)
+          router_rows<LT, G, V, B, true, SIG, 8><<<parts, B, lds, s>>>(a);
+        else
+          router_rows<LT, G, V, B, true, SIG, 16><<<parts, B, lds, s>>>(a);
       } else {
         const int64_t gpb = 256 / G;
         const int grid = (int)std::min<int64_t>((r.T + gpb - 1) / gpb, (int64_t)cus * 64);
-        router_rows<LT, G, V, 256, false><<<grid, 256, 0, s>>>(a);
+        if (r.k <= 8)
+          router_rows<LT, G, V, 256, false, SIG, 8><<<grid, 256, 0, s>>>(a);
+        else
+          router_rows<LT, G, V, 256, false, SIG, 16><<<grid, 256, 0, s>>>(a);
       }
     });
   };
-  r.logits_fp32 ? go(float{}) : go(uint16_t{});
+  with_types(r.logits_fp32, r.sigmoid, go);
   MOK_HIP_TRY(hipGetLastError());
   if (stats) {
-    router_stats<<<r.E / 64 + 1, 1024, 0, s>>>(r.part, parts, r.E, r.k, r.sigmoid, r.counts, r.losses);
+    router_stats<<<r.E / 16 + 1, 1024, 0, s>>>(r.part, parts, r.E, r.k, r.sigmoid, r.counts, r.losses);
     MOK_HIP_TRY(hipGetLastError());
   }
   return hipSuccess;
@@ -646,16 +711,17 @@ hipError_t launch_router_bwd(const RouterBwdArgs& r, int cus, hipStream_t s) {
   if (r.T == 0) return hipSuccess;
   RouterBwd a{r.logits, r.T,   r.ld,        r.E,   r.k,      r.bias,     r.mask,    r.sigmoid,
               r.renorm, r.scale, r.d_weights, r.ids, r.counts, r.d_losses, r.d_logits};
-  auto go = [&](auto tag) {
+  auto go = [&](auto tag, auto sig) {
     using LT = decltype(tag);
+    constexpr bool SIG = decltype(sig)::value;
     with_layout(r.E, [&](auto g, auto v) {
       constexpr int G = decltype(g)::value, V = decltype(v)::value;
       const int64_t gpb = 256 / G;
       const int grid = (int)std::min<int64_t>((r.T + gpb - 1) / gpb, (int64_t)cus * 64);
-      router_bwd_rows<LT, G, V, 256><<<grid, 256, 0, s>>>(a);
+      router_bwd_rows<LT, G, V, 256, SIG><<<grid, 256, 0, s>>>(a);
     });
   };
-  r.logits_fp32 ? go(float{}) : go(uint16_t{});
+  with_types(r.logits_fp32, r.sigmoid, go);
   return hipGetLastError();
 }
 

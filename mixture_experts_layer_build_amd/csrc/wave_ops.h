@@ -33,6 +33,14 @@ __device__ __forceinline__ float dpp_movf(float x) {
 constexpr int kRor1 = 0x121, kRor2 = 0x122, kRor4 = 0x124, kRor8 = 0x128;  // row_ror:n
 constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;                          // quad_perm:[1,0,3,2], [2,3,0,1]
 
+// x, as a value the compiler knows nothing of.
+__device__ __forceinline__ int opaque(int x) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(x));
+#endif
+  return x;
+}
+
 // Over the 16 lanes of a row.
 __device__ __forceinline__ float row_sum(float x) {
   x += dpp_movf<kRor8>(x);
@@ -56,6 +64,13 @@ __device__ __forceinline__ int row_min(int x) {
   return x;
 }
 
+__device__ __forceinline__ uint32_t row_umax(uint32_t x) {
+  x = max(x, (uint32_t)dpp_mov<kRor8>((int)x));
+  x = max(x, (uint32_t)dpp_mov<kRor4>((int)x));
+  x = max(x, (uint32_t)dpp_mov<kRor2>((int)x));
+  return max(x, (uint32_t)dpp_mov<kRor1>((int)x));
+}
+
 // Lane l's value in every lane (a scalar register).
 __device__ __forceinline__ int lane_value(int x, int l) { return __builtin_amdgcn_readlane(x, l); }
 __device__ __forceinline__ float lane_valuef(float x, int l) {
@@ -71,6 +86,11 @@ __device__ __forceinline__ float wave_max(float x) {
   x = row_max(x);
   return __builtin_fmaxf(__builtin_fmaxf(lane_valuef(x, 0), lane_valuef(x, 16)),
                          __builtin_fmaxf(lane_valuef(x, 32), lane_valuef(x, 48)));
+}
+__device__ __forceinline__ uint32_t wave_umax(uint32_t x) {
+  x = row_umax(x);
+  return max(max((uint32_t)lane_value((int)x, 0), (uint32_t)lane_value((int)x, 16)),
+             max((uint32_t)lane_value((int)x, 32), (uint32_t)lane_value((int)x, 48)));
 }
 __device__ __forceinline__ int wave_min(int x) {
   x = row_min(x);

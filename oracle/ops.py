@@ -37,7 +37,7 @@ def _keys(logits32, bias, mask):
             key = key + bias.astype(np.float32)  # the definition: one fp32 addition
     T = key.shape[0]
     keep = np.ones(T, bool) if mask is None else mask.astype(bool)
-    broken = keep & (np.isnan(key).any(1) | np.isnan(logits32).any(1) | (logits32 == np.inf).any(1))
+    broken = keep & (np.isnan(key).any(1) | (key == np.inf).any(1))
     live = keep & (broken | (key > -np.inf).any(1))
     return key, keep, broken, live
 
