@@ -489,7 +489,8 @@ mok_status mok_router_topk_backward(const float* d_weights, const void* logits, 
  * sqrt(v), with one E8M0 scale byte per 32 consecutive elements (the last
  * block may be shorter), [ceil(numel/32)]; all-zero bytes are zero moments.
  * A block's scale is the smallest power of two that keeps its largest
- * magnitude within 448 of it (0xFF, NaN, if that is not finite). m is
+ * magnitude within 448 of it (0xFF, NaN, in both moments if the block's v
+ * is not finite). m is
  * rounded to the nearest code; sqrt(v) to one of the two codes around it,
  * chosen at random so that the mean of its square is v, from `seed` and the
  * element's number in the call (tensors are numbered one after the other,

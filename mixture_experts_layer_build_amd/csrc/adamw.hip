@@ -27,6 +27,11 @@
 // consecutive chunks, a 32-element block in 4 neighbouring lanes. The
 // tensors' addresses travel in the kernel's arguments, up to 48 per launch:
 // nothing is copied to the device and nothing is kept between calls.
+// Non-temporal accesses, 1e8 elements: stores alone 573 -> 543 us with fp32
+// states and masters (loads too: 577); with 8 bits loads and stores 329 ->
+// 289 us (stores alone 320). The 8-bit update was bound by its instructions
+// first: packed conversions, the hardware's root and no clamps took it from
+// 229 to 158 us (bf16, no master: 6.4 TB/s) and from 289 to 279 with a master.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -68,9 +73,10 @@ struct AdamArgs {
 static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments");
 
 // u for elements 2i and 2i + 1: one 32-bit hash (multiply and xor-shift
-// rounds over the pair's number and the seed), 16 bits each.
-__device__ __forceinline__ uint32_t pair_bits(uint32_t pair, uint32_t seed) {
-  uint32_t x = pair * 0x9E3779B1u + seed;
+// rounds over the pair's number and the seed), 16 bits each. x = the pair's
+// number * kPairStep + seed.
+constexpr uint32_t kPairStep = 0x9E3779B1u;
+__device__ __forceinline__ uint32_t pair_bits(uint32_t x) {
   x ^= x >> 16;
   x *= 0x85157AF5u;
   x ^= x >> 15;
@@ -86,29 +92,35 @@ __device__ __forceinline__ int state_exponent(uint32_t amax) {
   return (amax >= 0x00800000u && (amax & 0x7FFFFFu) > 0x600000u) ? min(x + 1, 127) : x;
 }
 
-// The products and sums below are rounded one by one, as they are written
-// (no fused multiply-add), and the root of an 8-bit state correctly: codes
-// of 4 significant bits and bf16 gradients make exact ties common, and which
-// way they go should not depend on the compiler's contraction.
+// The products and sums of the moments are rounded one by one, as they are
+// written (no fused multiply-add): codes of 4 significant bits and bf16
+// gradients make exact ties common, and which way they go should not depend
+// on the compiler's contraction.
 #pragma clang fp contract(off)
 
-// One of the two E4M3 values around r >= 0 (r <= 448), r^2 = sq: up where
-// u * (hi^2 - lo^2) < sq - lo^2.
+// One of the two E4M3 values around r (at most 448), r^2 = sq: up where u *
+// (hi^2 - lo^2) < sq - lo^2. An r that its own rounding carried across a
+// code decides the same way from either side of it.
+__device__ __forceinline__ float round_between(float lo, float hi, float sq, float u) {
+  const float lo2 = lo * lo;
+  return u * (hi * hi - lo2) < sq - lo2 ? hi : lo;
+}
+// Normal codes keep 3 bits of fp32's mantissa.
 __device__ __forceinline__ float round_root(float r, float sq, float u) {
-  // normal codes keep 3 bits of fp32's mantissa; below 2^-6 the codes are multiples of 2^-9
-  const float lo_n = u2f(f2u(r) & 0xFFF00000u), hi_n = u2f((f2u(r) & 0xFFF00000u) + 0x100000u);
-  const float lo_s = __builtin_floorf(r * 512.f) * 0x1p-9f;
-  const bool normal = r >= 0x1p-6f;
-  const float lo = normal ? lo_n : lo_s, hi = normal ? hi_n : lo_s + 0x1p-9f;
-  float q = u * (hi * hi - lo * lo) < sq - lo * lo ? hi : lo;
-  q = __builtin_fminf(q, 448.f);
+  const uint32_t lo = f2u(r) & 0xFFF00000u;
+  return round_between(u2f(lo), u2f(lo + 0x100000u), sq, u);
+}
+// Below 2^-6 the codes are multiples of 2^-9; a positive r keeps at least one.
+__device__ __forceinline__ float round_small_root(float r, float sq, float u) {
+  const float lo = __builtin_floorf(r * 512.f) * 0x1p-9f;
+  const float q = round_between(lo, lo + 0x1p-9f, sq, u);
   return sq > 0.f ? __builtin_fmaxf(q, 0x1p-9f) : q;
 }
 
-template <typename T>
+template <bool NT, typename T>
 __device__ __forceinline__ void get8(const T* p, int64_t i, int64_t n, bool vec, float (&v)[8]) {
   if (vec) {
-    load8(p + i, v);
+    NT ? load8_once(p + i, v) : load8(p + i, v);
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q) v[q] = i + q < n ? load1(p + i + q) : 0.f;
@@ -117,7 +129,7 @@ __device__ __forceinline__ void get8(const T* p, int64_t i, int64_t n, bool vec,
 template <typename T>
 __device__ __forceinline__ void put8(T* p, int64_t i, int64_t n, bool vec, const float (&v)[8]) {
   if (vec) {
-    store8(p + i, v);
+    store8_once(p + i, v);
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q)
@@ -142,14 +154,39 @@ __device__ __forceinline__ void put_codes(uint8_t* p, int64_t i, int64_t n, bool
   for (int q = 0; q < 8; ++q)
     if (i + q < n) p[i + q] = (uint8_t)(w[q >> 2] >> (8 * (q & 3)));
 }
-// Values of 8 codes under scale byte s (0xFF: NaN).
+#if defined(__HIP_DEVICE_COMPILE__)
+// Values of 8 codes under scale byte s (not 0xFF), two per instruction.
 __device__ __forceinline__ void decode8(uint2 c, uint32_t s, float (&v)[8]) {
-  const float scale = s == 0xFFu ? __builtin_nanf("") : u2f(s ? s << 23 : 0x00400000u);
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    v[q] = e4m3_decode_byte_scaled(c.x, q, 1.0f) * scale;
-    v[4 + q] = e4m3_decode_byte_scaled(c.y, q, 1.0f) * scale;
-  }
+  const float scale = u2f(s ? s << 23 : 0x00400000u);
+  const f32x2v a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c.x, scale, false);
+  const f32x2v b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c.x, scale, true);
+  const f32x2v d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c.y, scale, false);
+  const f32x2v e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c.y, scale, true);
+  v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1], v[4] = d[0], v[5] = d[1], v[6] = e[0], v[7] = e[1];
+}
+// Codes of 8 values, all at most 448 in magnitude.
+__device__ __forceinline__ uint2 encode8(const float (&v)[8]) {
+  typedef short s16x2 __attribute__((ext_vector_type(2)));
+  const float s = 1.0f;
+  s16x2 a = {0, 0}, b = {0, 0};
+  a = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(a, v[0], v[1], s, false);
+  a = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(a, v[2], v[3], s, true);
+  b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, v[4], v[5], s, false);
+  b = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(b, v[6], v[7], s, true);
+  return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
+}
+#else
+__device__ void decode8(uint2 c, uint32_t s, float (&v)[8]);  // device only
+__device__ uint2 encode8(const float (&v)[8]);
+#endif
+
+// 2^k as the math library's power function gives it: exact, or half an ulp
+// below for some k from 16 on. The states are scaled by it because elementary
+// tensor operations on this GPU scale so: on an exact tie that half ulp
+// decides the code, and with it a step gives the codes that those operations
+// give, bit for bit. (The base is hidden, or the compiler would take exp2.)
+__device__ __forceinline__ float library_power(int k) {
+  return powf(u2f((uint32_t)opaque(0x40000000)), (float)k);
 }
 
 template <typename PT, bool MASTER, typename GT, bool S8>
@@ -168,26 +205,39 @@ __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
   const int64_t begin = (int64_t)(blockIdx.x - t.chunk0) * a.chunk;
   const int64_t end = min(n, begin + (int64_t)a.chunk);
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
+  // 2^-X and 2^-2X for scale byte X + 127
+  __shared__ float down[S8 ? 256 : 1], down2[S8 ? 256 : 1];
+  if constexpr (S8) {
+    static_assert(kThreads == 256, "a thread per scale byte");
+    down[threadIdx.x] = library_power(127 - (int)threadIdx.x);
+    down2[threadIdx.x] = library_power(2 * (127 - (int)threadIdx.x));
+    __syncthreads();
+  }
   // every thread makes the same number of turns (lanes of a block exchange maxima)
   for (int64_t i0 = begin; i0 < end; i0 += kTurn) {
     const int64_t i = i0 + (int64_t)threadIdx.x * 8;
     const bool in = i < n;
     const bool vec = t.vec && i + 8 <= n;
     float g[8], p[8], m[8], v[8];
-    get8((const GT*)t.g, i, n, vec, g);
+    get8<S8>((const GT*)t.g, i, n, vec, g);
     if constexpr (MASTER)
-      get8((const float*)t.master, i, n, vec, p);
+      get8<S8>((const float*)t.master, i, n, vec, p);
     else
-      get8((const PT*)t.p, i, n, vec, p);
+      get8<S8>((const PT*)t.p, i, n, vec, p);
     if constexpr (S8) {
       const uint2 cm = get_codes((const uint8_t*)t.m, i, n, vec), cv = get_codes((const uint8_t*)t.v, i, n, vec);
-      decode8(cm, in ? t.ms[i >> 5] : 0u, m);
-      decode8(cv, in ? t.vs[i >> 5] : 0u, v);
+      const uint32_t sm = in ? t.ms[i >> 5] : 0u, sv = in ? t.vs[i >> 5] : 0u;
+      decode8(cm, sm, m);
+      decode8(cv, sv, v);
 #pragma unroll
       for (int q = 0; q < 8; ++q) v[q] *= v[q];
+      if (max(sm, sv) == 0xFFu) {  // NaN
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m[q] = sm == 0xFFu ? __builtin_nanf("") : m[q], v[q] = sv == 0xFFu ? __builtin_nanf("") : v[q];
+      }
     } else {
-      get8((const float*)t.m, i, n, vec, m);
-      get8((const float*)t.v, i, n, vec, v);
+      get8<false>((const float*)t.m, i, n, vec, m);
+      get8<false>((const float*)t.v, i, n, vec, v);
     }
     float r[8];
 #pragma unroll
@@ -195,42 +245,57 @@ __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
       g[q] *= gs;
       m[q] = a.b1 * m[q] + a.c1 * g[q];
       v[q] = a.b2 * v[q] + a.c2 * (g[q] * g[q]);
-      r[q] = S8 ? __builtin_sqrtf(v[q]) : __builtin_amdgcn_sqrtf(v[q]);
-      p[q] = p[q] * a.keep - a.rate * m[q] * __builtin_amdgcn_rcpf(r[q] * a.rbc2 + a.eps);
+      r[q] = __builtin_amdgcn_sqrtf(v[q]);
+      const float inv = __builtin_amdgcn_rcpf(__builtin_fmaf(r[q], a.rbc2, a.eps));
+      p[q] = __builtin_fmaf(-a.rate * m[q], inv, p[q] * a.keep);
     }
     if (in) {
       put8((PT*)t.p, i, n, vec, p);
       if constexpr (MASTER) put8(t.master, i, n, vec, p);
     }
     if constexpr (S8) {
-      uint32_t mm = 0, mr = 0;
+      // a moment that is not finite comes with a v that is not
+      float mm = 0.f;
+      uint32_t mr = 0;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        mm = max(mm, f2u(m[q]) & 0x7FFFFFFFu);
-        mr = max(mr, f2u(r[q]) & 0x7FFFFFFFu);
+        mm = __builtin_fmaxf(mm, __builtin_fabsf(m[q]));
+        mr = max(mr, f2u(r[q]));
       }
-      mm = quad_max(mm);
       mr = quad_max(mr);
-      const int xm = state_exponent(mm), xr = state_exponent(mr);
-      const float down = __builtin_ldexpf(1.0f, -xr);
+      const int xm = state_exponent(quad_max(f2u(mm))), xr = state_exponent(min(mr, 0x7F7FFFFFu));
+      const float fm = down[xm + 127], fr = u2f((uint32_t)(127 - xr) << 23), fv = mr ? down2[xr + 127] : 0.f;
+      uint32_t x = (t.number0 + (uint32_t)i) / 2 * kPairStep + a.seed;
+      bool small = false;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const uint32_t bits = pair_bits((t.number0 + (uint32_t)i) / 2 + h, a.seed);
-        const float rs0 = r[2 * h] * down, rs1 = r[2 * h + 1] * down;
-        const float s0 = v[2 * h] * down * down, s1 = v[2 * h + 1] * down * down;
-        r[2 * h] = round_root(rs0, s0, ((float)(bits & 0xFFFFu) + 0.5f) * 0x1p-16f);
-        r[2 * h + 1] = round_root(rs1, s1, ((float)(bits >> 16) + 0.5f) * 0x1p-16f);
+      for (int q = 0; q < 8; ++q) {
+        m[q] *= fm;
+        r[q] *= fr;
+        v[q] = fv < __builtin_inff() ? v[q] * fv : v[q] * fr * fr;
+        small |= r[q] < 0x1p-6f;
+      }
+      float u[8];
+#pragma unroll
+      for (int h = 0; h < 4; ++h, x += kPairStep) {
+        const uint32_t bits = pair_bits(x);
+        u[2 * h] = __builtin_fmaf((float)(bits & 0xFFFFu), 0x1p-16f, 0x1p-17f);
+        u[2 * h + 1] = __builtin_fmaf((float)(bits >> 16), 0x1p-16f, 0x1p-17f);
+      }
+      if (small) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          r[q] = r[q] < 0x1p-6f ? round_small_root(r[q], v[q], u[q]) : round_root(r[q], v[q], u[q]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) r[q] = round_root(r[q], v[q], u[q]);
       }
       if (in) {
-        put_codes((uint8_t*)t.m, i, n, vec,
-                  make_uint2(e4m3x4_encode_scaled(m[0], m[1], m[2], m[3], xm),
-                             e4m3x4_encode_scaled(m[4], m[5], m[6], m[7], xm)));
-        put_codes((uint8_t*)t.v, i, n, vec,
-                  make_uint2(e4m3x4_encode_scaled(r[0], r[1], r[2], r[3], 0),
-                             e4m3x4_encode_scaled(r[4], r[5], r[6], r[7], 0)));
+        put_codes((uint8_t*)t.m, i, n, vec, encode8(m));
+        put_codes((uint8_t*)t.v, i, n, vec, encode8(r));
         if ((i & 31) == 0) {
-          t.ms[i >> 5] = mm >= 0x7F800000u ? 0xFFu : (uint8_t)(xm + 127);
-          t.vs[i >> 5] = mr >= 0x7F800000u ? 0xFFu : (uint8_t)(xr + 127);
+          const bool finite = mr < 0x7F800000u;
+          t.ms[i >> 5] = finite ? (uint8_t)(xm + 127) : 0xFFu;
+          t.vs[i >> 5] = finite ? (uint8_t)(xr + 127) : 0xFFu;
         }
       }
     } else if (in) {

@@ -150,6 +150,28 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
+// The same past the caches' keeping (non-temporal), for data that one launch
+// streams through and none reads again soon.
+typedef __attribute__((ext_vector_type(4))) float f32x4nt;
+__device__ __forceinline__ void load8_once(const uint16_t* p, float (&v)[8]) {
+  const u32x4 r = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  unpack8(make_uint4(r[0], r[1], r[2], r[3]), v);
+}
+__device__ __forceinline__ void load8_once(const float* p, float (&v)[8]) {
+  const f32x4nt a = __builtin_nontemporal_load(reinterpret_cast<const f32x4nt*>(p)),
+                b = __builtin_nontemporal_load(reinterpret_cast<const f32x4nt*>(p + 4));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+}
+__device__ __forceinline__ void store8_once(uint16_t* p, const float (&v)[8]) {
+  const u32x4 r = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+  __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>(p));
+}
+__device__ __forceinline__ void store8_once(float* p, const float (&v)[8]) {
+  __builtin_nontemporal_store((f32x4nt){v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4nt*>(p));
+  __builtin_nontemporal_store((f32x4nt){v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4nt*>(p + 4));
+}
+
 // 8 elements as they lie in memory: 4 registers of bf16, 8 of fp32. fresh()
 // makes the compiler forget what the registers were converted to, so that a
 // later pair() converts again instead of keeping the fp32 values alive.
