@@ -14,10 +14,17 @@
 // load, lanes on consecutive chunks; a row belongs to one wave up to 2048
 // columns, whose reduction needs no barrier, and to 256 or 512 threads
 // above (a wave would need more registers than keep enough loads in
-// flight). The grid is persistent: the weights stay in registers from row
-// to row, and the backward adds dw up in registers over a workgroup's rows,
-// writes one partial row per workgroup, and a second launch adds the
-// partials in a fixed order (no atomics: the same bits on every run).
+// flight). The backward holds three streams and dw, so a lane takes at most
+// two chunks of a row (with four it needed 166 registers or spilled: 246 us
+// against 176 at 16384 x 7168). The grid is persistent: the weights stay in
+// registers from row to row, and the backward adds dw up in registers over a
+// workgroup's rows, writes one partial row per workgroup, and a second launch
+// adds the partials in a fixed order (no atomics: the same bits on every
+// run).
+//
+// Measured: forward 8192 x 2048 bf16 with residual 24 us (5.6 TB/s), 16384 x
+// 7168 166 us, to MXFP8 139 us (6.0 TB/s); backward 16384 x 7168 with d_sum
+// 164 us (5.75 TB/s), 8192 x 2048 27 us. A copy of 4 GiB runs at 4.6 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -74,7 +81,7 @@ struct NormFwd {
 };
 
 // RT: the residual's type, void for none.
-template <typename XT, typename RT, int BLOCK, int TPR, int NV>
+template <typename XT, typename RT, bool STREAM, int BLOCK, int TPR, int NV>
 __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
   constexpr bool kRes = !std::is_void<RT>::value;
   using R = typename std::conditional<kRes, RT, float>::type;
@@ -111,10 +118,10 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
     for (int i = 0; i < NV; ++i) {
       const uint32_t c = t + i * TPR;
       if (live && c < nchunk) {
-        load8(x + c * 8, v[i]);
+        load8_as<STREAM>(x + c * 8, v[i]);
         if constexpr (kRes) {
           float r[8];
-          load8(res + c * 8, r);
+          load8_as<STREAM>(res + c * 8, r);
 #pragma unroll
           for (int q = 0; q < 8; ++q) v[i][q] += r[q];
         }
@@ -136,11 +143,18 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
     for (int i = 0; i < NV; ++i) {
       const uint32_t c = t + i * TPR;
       if (c >= nchunk) continue;
-      if constexpr (kRes) store8((R*)a.sum + out + c * 8, v[i]);
+      if constexpr (kRes) {
+        // (an fp32 sum: of a bf16 x past the cache, 5003 x 7168 to MXFP8 80 ->
+        // 76 us; of an fp32 x through it, 32768 x 4096 371 -> 350 us)
+        if constexpr (sizeof(XT) == 2)
+          store8_once((R*)a.sum + out + c * 8, v[i]);
+        else
+          store8((R*)a.sum + out + c * 8, v[i]);
+      }
       float y[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) y[q] = v[i][q] * rstd * w[i][q];
-      if (a.y) store8(a.y + out + c * 8, y);
+      if (a.y) store8_once(a.y + out + c * 8, y);
       if (a.codes) store_mxfp8(y, a.codes + out + c * 8, a.scale + (out >> 5) + (c >> 2), (t & 3) == 0);
     }
   }
@@ -194,7 +208,7 @@ struct NormBwd {
 // A row's dy, s and d_sum stay as they were loaded and are converted twice,
 // in the pass before the row's sum and in the one behind it: in fp32 they
 // would take twice the registers, and half the waves would hide the loads.
-template <typename ST, typename WT, bool DSUM, int BLOCK, int TPR, int NV>
+template <typename ST, typename WT, bool DSUM, bool STREAM, int BLOCK, int TPR, int NV>
 __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(4)))
 rms_norm_bwd_rows(NormBwd a) {
   constexpr int RPB = BLOCK / TPR;
@@ -212,7 +226,7 @@ rms_norm_bwd_rows(NormBwd a) {
     const uint32_t c = t + i * TPR;
 #pragma unroll
     for (int q = 0; q < 8; ++q) dw[i][q] = 0.f;
-    if (c < nchunk) w[i].load((const WT*)a.w + c * 8);
+    if (c < nchunk) w[i].template load<false>((const WT*)a.w + c * 8);
   }
   const float inv_cols = 1.0f / (float)a.cols;
   int parity = 0;
@@ -231,9 +245,9 @@ rms_norm_bwd_rows(NormBwd a) {
     for (int i = 0; i < NV; ++i) {
       const uint32_t c = t + i * TPR;
       if (live && c < nchunk) {
-        dy[i].load(pdy + c * 8);
-        s[i].load(ps + c * 8);
-        if constexpr (DSUM) dsum[i].load(pd + c * 8);
+        dy[i].template load<STREAM>(pdy + c * 8);
+        s[i].template load<STREAM>(ps + c * 8);
+        if constexpr (DSUM) dsum[i].template load<STREAM>(pd + c * 8);
       }
     }
     float along = 0.f;
@@ -277,8 +291,8 @@ rms_norm_bwd_rows(NormBwd a) {
         ds.set(j, d[0], d[1]);
         narrow.set(j, d[0], d[1]);
       }
-      ds.store(pds + c * 8);
-      if (a.dx) narrow.store(pdx + c * 8);
+      ds.template store<STREAM>(pds + c * 8);
+      if (a.dx) narrow.template store<STREAM>(pdx + c * 8);
     }
   }
   // the workgroup's partial row: its row groups one after the other
@@ -368,11 +382,23 @@ __global__ void zero_dw(void* dw, int cols, int w_fp32) {
 
 bool aligned16(const void* p) { return (((uintptr_t)p) & 15) == 0; }
 
+// Inputs larger than the last-level cache are loaded past it: what wrote them
+// left nothing of them there that the first rows would still find. (16384 x
+// 7168 bf16 with residual: 172 -> 166 us, to MXFP8 155 -> 139; 8192 x 2048,
+// whose 67 MB the cache holds: 24 -> 27, so not there. bf16 stores always go
+// past it: 26 -> 24 us at 8192 x 2048, 183 -> 172 at 16384 x 7168.)
+constexpr int64_t kCacheBytes = (int64_t)256 << 20;
+
 template <typename XT, typename RT, int BLOCK, int TPR, int NV>
 void run_fwd(const NormFwd& a, int cus, hipStream_t s) {
   const int64_t need = (a.rows + BLOCK / TPR - 1) / (BLOCK / TPR);
   const int grid = (int)std::min<int64_t>(need, (int64_t)cus * (2048 / BLOCK));
-  rms_norm_rows<XT, RT, BLOCK, TPR, NV><<<grid, BLOCK, 0, s>>>(a);
+  constexpr bool kAllFp32 = sizeof(XT) == 4;  // nothing of it would be streamed
+  constexpr int64_t kBytes = sizeof(XT) + (std::is_void<RT>::value ? 0 : sizeof(typename std::conditional<std::is_void<RT>::value, char, RT>::type));
+  if (!kAllFp32 && a.rows * a.cols * kBytes > kCacheBytes)
+    rms_norm_rows<XT, RT, !kAllFp32, BLOCK, TPR, NV><<<grid, BLOCK, 0, s>>>(a);
+  else
+    rms_norm_rows<XT, RT, false, BLOCK, TPR, NV><<<grid, BLOCK, 0, s>>>(a);
 }
 
 template <typename XT, typename RT>
@@ -408,10 +434,14 @@ int run_bwd(const NormBwd& a, bool vec, hipStream_t s) {
   auto grid = [&](int rows_per_block) {
     return (int)std::min<int64_t>((a.rows + rows_per_block - 1) / rows_per_block, kNormBwdParts);
   };
+  const bool stream = a.rows * a.cols * (int64_t)(2 + (DSUM ? 2 : 1) * sizeof(ST)) > kCacheBytes;
   auto go = [&](auto block, auto tpr, auto nv) {
     constexpr int BLOCK = decltype(block)::value, TPR = decltype(tpr)::value, NV = decltype(nv)::value;
     const int g = grid(BLOCK / TPR);
-    rms_norm_bwd_rows<ST, WT, DSUM, BLOCK, TPR, NV><<<g, BLOCK, 0, s>>>(a);
+    if (stream)
+      rms_norm_bwd_rows<ST, WT, DSUM, true, BLOCK, TPR, NV><<<g, BLOCK, 0, s>>>(a);
+    else
+      rms_norm_bwd_rows<ST, WT, DSUM, false, BLOCK, TPR, NV><<<g, BLOCK, 0, s>>>(a);
     return g;
   };
   using std::integral_constant;

@@ -151,12 +151,18 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 // The same past the caches' keeping (non-temporal), for data that one launch
-// streams through and none reads again soon.
+// streams through and none reads again soon. bf16 lanes fill whole lines per
+// instruction; fp32 ones, at 32 bytes a lane, only with the second, so for
+// them it depends on the rest of the launch and is measured case by case.
 typedef __attribute__((ext_vector_type(4))) float f32x4nt;
-__device__ __forceinline__ void load8_once(const uint16_t* p, float (&v)[8]) {
+__device__ __forceinline__ uint4 load16_once(const void* p) {
   const u32x4 r = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-  unpack8(make_uint4(r[0], r[1], r[2], r[3]), v);
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
+__device__ __forceinline__ void store16_once(void* p, uint4 r) {
+  __builtin_nontemporal_store((u32x4){r.x, r.y, r.z, r.w}, reinterpret_cast<u32x4*>(p));
+}
+__device__ __forceinline__ void load8_once(const uint16_t* p, float (&v)[8]) { unpack8(load16_once(p), v); }
 __device__ __forceinline__ void load8_once(const float* p, float (&v)[8]) {
   const f32x4nt a = __builtin_nontemporal_load(reinterpret_cast<const f32x4nt*>(p)),
                 b = __builtin_nontemporal_load(reinterpret_cast<const f32x4nt*>(p + 4));
@@ -164,12 +170,21 @@ __device__ __forceinline__ void load8_once(const float* p, float (&v)[8]) {
   for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
 }
 __device__ __forceinline__ void store8_once(uint16_t* p, const float (&v)[8]) {
-  const u32x4 r = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-  __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>(p));
+  store16_once(p, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                             pack_bf16x2(v[6], v[7])));
 }
 __device__ __forceinline__ void store8_once(float* p, const float (&v)[8]) {
   __builtin_nontemporal_store((f32x4nt){v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4nt*>(p));
   __builtin_nontemporal_store((f32x4nt){v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4nt*>(p + 4));
+}
+// bf16 past the caches if STREAM, fp32 through them.
+template <bool STREAM>
+__device__ __forceinline__ void load8_as(const uint16_t* p, float (&v)[8]) {
+  STREAM ? load8_once(p, v) : load8(p, v);
+}
+template <bool STREAM>
+__device__ __forceinline__ void load8_as(const float* p, float (&v)[8]) {
+  load8(p, v);
 }
 
 // 8 elements as they lie in memory: 4 registers of bf16, 8 of fp32. fresh()
@@ -180,7 +195,10 @@ struct Raw8;
 template <>
 struct Raw8<uint16_t> {
   uint4 r = make_uint4(0, 0, 0, 0);
-  __device__ __forceinline__ void load(const uint16_t* p) { r = *reinterpret_cast<const uint4*>(p); }
+  template <bool STREAM>
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    r = STREAM ? load16_once(p) : *reinterpret_cast<const uint4*>(p);
+  }
   // elements 2j and 2j + 1
   __device__ __forceinline__ void pair(int j, float& a, float& b) const {
     const uint32_t x = j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w;
@@ -189,7 +207,13 @@ struct Raw8<uint16_t> {
   __device__ __forceinline__ void set(int j, float a, float b) {
     (j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w) = pack_bf16x2(a, b);
   }
-  __device__ __forceinline__ void store(uint16_t* p) const { *reinterpret_cast<uint4*>(p) = r; }
+  template <bool STREAM>
+  __device__ __forceinline__ void store(uint16_t* p) const {
+    if (STREAM)
+      store16_once(p, r);
+    else
+      *reinterpret_cast<uint4*>(p) = r;
+  }
   __device__ __forceinline__ void fresh() {
 #if defined(__HIP_DEVICE_COMPILE__)
     asm volatile("" : "+v"(r.x), "+v"(r.y), "+v"(r.z), "+v"(r.w));
@@ -199,9 +223,11 @@ struct Raw8<uint16_t> {
 template <>
 struct Raw8<float> {
   float v_[8] = {};
+  template <bool STREAM>
   __device__ __forceinline__ void load(const float* p) { load8(p, v_); }
   __device__ __forceinline__ void pair(int j, float& a, float& b) const { a = v_[2 * j], b = v_[2 * j + 1]; }
   __device__ __forceinline__ void set(int j, float a, float b) { v_[2 * j] = a, v_[2 * j + 1] = b; }
+  template <bool STREAM>
   __device__ __forceinline__ void store(float* p) const { store8(p, v_); }
   __device__ __forceinline__ void fresh() {}
 };
