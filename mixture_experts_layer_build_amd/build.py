@@ -1,8 +1,10 @@
-"""Builds the HIP library ``libmok.so`` for gfx950 in-tree.
+"""Builds the HIP library ``libmok.so`` for gfx950 in-tree, and the host-side
+extension module ``_ops.so`` of the calls in ``ops.py``.
 
 Every ``csrc/*.hip`` is compiled to an object with hipcc (in parallel), then
-linked into ``mixture_experts_layer_build_amd/libmok.so``. Always compiles:
-this is also the "does it build" check run on machines without a GPU.
+linked into ``mixture_experts_layer_build_amd/libmok.so``; ``csrc/py_ops.cpp``
+is plain C++ against torch's headers. Always compiles: this is also the "does
+it build" check run on machines without a GPU.
 
 Usage: python -m mixture_experts_layer_build_amd.build [-j N] [--verbose]
 """
@@ -22,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmok.so")
+HOST_MODULE = os.path.join(PKG, "_ops.so")
 
 ARCH = "gfx950"
 
@@ -57,12 +60,37 @@ def compile_one(src: str, verbose: bool) -> str:
     return obj
 
 
+def build_host_module(verbose: bool = False) -> str:
+    """``csrc/py_ops.cpp`` -> ``_ops.so`` (host code only, no HIP)."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = [f"-I{d}" for d in (INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths())]
+    tmp = HOST_MODULE + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
+           os.path.join(CSRC, "py_ops.cpp"), "-o", tmp, f"-L{lib_dir}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on py_ops.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, HOST_MODULE)
+    return HOST_MODULE
+
+
 def build(jobs: int | None = None, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
-    jobs = jobs or min(len(srcs), max(1, min(16, os.cpu_count() or 1)))
+    jobs = jobs or min(len(srcs) + 1, max(1, min(16, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        host = ex.submit(build_host_module, verbose)
         objs = list(ex.map(lambda s: compile_one(s, verbose), srcs))
+        host.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
     if verbose:
