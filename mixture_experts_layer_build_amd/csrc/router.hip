@@ -53,11 +53,19 @@ __device__ __forceinline__ float grp_max(float x) {
   if constexpr (G == 16) return row_max(x);
   return wave_max(x);
 }
+// Whether any lane of the group says so.
 template <int G>
-__device__ __forceinline__ uint32_t grp_umax(uint32_t x) {
-  if constexpr (G == 16) return row_umax(x);
-  return wave_umax(x);
+__device__ __forceinline__ bool grp_any(bool x) {
+  const uint64_t b = __ballot(x);
+  if constexpr (G == 16) return ((uint32_t)(b >> (lane_id() & 48)) & 0xFFFFu) != 0;
+  return b != 0;
 }
+#if defined(__HIP_DEVICE_COMPILE__)
+// NaN or +inf, in one instruction.
+__device__ __forceinline__ bool is_nan_or_inf(float x) { return __builtin_amdgcn_classf(x, 0x203); }
+#else
+__device__ bool is_nan_or_inf(float x);  // device only
+#endif
 template <int G>
 __device__ __forceinline__ int grp_min(int x) {
   if constexpr (G == 16) return row_min(x);
@@ -84,8 +92,8 @@ struct RouterFwd {
 
 // Bits of a key in its order (larger key, larger word); the key is the sum of
 // a logit and a bias or zero, so never -0. -inf is kNone, words of numbers lie
-// above it, +inf and NaN outside [kNone, kBroken).
-constexpr uint32_t kNone = 0x007FFFFFu, kBroken = 0xFF800000u;
+// above it.
+constexpr uint32_t kNone = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t ordered(float key) {
   const uint32_t u = f2u(key);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
@@ -113,35 +121,43 @@ struct Row {
   __device__ __forceinline__ void load(const LT* p, uint32_t off, uint32_t last, const float* bias, int E, int gl,
                                        bool keep) {
     constexpr uint32_t kIds = word_ids(G, VPL);
+    const char* b = (const char*)p;  // (bytes in 32 bits: a scalar base and one register of offset)
+    if (E == G * VPL) {
+      const uint32_t o = (off + (uint32_t)gl) * (uint32_t)sizeof(LT);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      // (bytes in 32 bits: a scalar base and one register of offset)
-      const uint32_t o = min(off + (uint32_t)(i * G + gl), last) * (uint32_t)sizeof(LT);
-      l[i] = load1((const LT*)((const char*)p + o));
-    }
-    top = -kInf;
+      for (int i = 0; i < VPL; ++i) l[i] = load1((const LT*)(b + o) + i * G);
+    } else {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      l[i] = i * G + gl < E ? l[i] : -kInf;
-      top = __builtin_fmaxf(top, l[i]);
+      for (int i = 0; i < VPL; ++i)
+        l[i] = load1((const LT*)(b + min(off + (uint32_t)(i * G + gl), last) * (uint32_t)sizeof(LT)));
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) l[i] = i * G + gl < E ? l[i] : -kInf;
     }
+    top = l[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) top = __builtin_fmaxf(top, l[i]);
     top = grp_max<G>(top);
-    uint32_t most = 0;
+    float most = top;
+    bool odd = false;
     auto see = [&](int i, float key) {
-      const uint32_t w = ordered(key);
-      most = max(most, w - kNone);
-      if constexpr (WORDS) word[i] = (w & ~kIds) | (kIds - (uint32_t)(i * G + gl));
+      odd |= is_nan_or_inf(key);
+      if constexpr (WORDS) word[i] = (ordered(key) & ~kIds) | (kIds - (uint32_t)(i * G + gl));
     };
     if (bias) {
+      most = -kInf;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) see(i, l[i] + bias[min(i * G + gl, E - 1)]);
+      for (int i = 0; i < VPL; ++i) {
+        const float key = l[i] + bias[min(i * G + gl, E - 1)];
+        most = __builtin_fmaxf(most, key);
+        see(i, key);
+      }
+      most = grp_max<G>(most);
     } else {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) see(i, l[i] + 0.0f);
     }
-    most = grp_umax<G>(most);
-    broken = keep && most >= kBroken - kNone;
-    live = keep && most > 0;
+    broken = keep && grp_any<G>(odd);
+    live = keep && (broken || most > -kInf);
   }
 };
 
@@ -173,21 +189,30 @@ __device__ __forceinline__ void merge_desc(uint32_t (&w)[N]) {
         w[i + h] = min(a, b);
       }
 }
-// N words into descending order (bitonic sort).
+// The comparators of Batcher's odd-even merge sort of N words (19 for 8, 63
+// for 16; a bitonic sort has 24 and 80).
+template <int N>
+struct OddEvenSort {
+  int n = 0;
+  signed char lo[80] = {}, hi[80] = {};
+  constexpr OddEvenSort() {
+    for (int p = 1; p < N; p *= 2)
+      for (int d = p; d >= 1; d /= 2)
+        for (int j = d % p; j + d < N; j += 2 * d)
+          for (int i = 0; i < d && i + j + d < N; ++i)
+            if ((i + j) / (2 * p) == (i + j + d) / (2 * p)) lo[n] = (signed char)(i + j), hi[n++] = (signed char)(i + j + d);
+  }
+};
+// N words into descending order.
 template <int N>
 __device__ __forceinline__ void sort_desc(uint32_t (&w)[N]) {
+  constexpr OddEvenSort<N> c{};
 #pragma unroll
-  for (int size = 2; size <= N; size *= 2)
-#pragma unroll
-    for (int h = size / 2; h > 0; h /= 2)
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if ((i & h) == 0) {
-          const bool up = (i & size) != 0;  // this run ascends
-          const uint32_t a = w[i], b = w[i + h];
-          w[i] = up ? min(a, b) : max(a, b);
-          w[i + h] = up ? max(a, b) : min(a, b);
-        }
+  for (int i = 0; i < c.n; ++i) {
+    const uint32_t x = w[c.lo[i]], y = w[c.hi[i]];
+    w[c.lo[i]] = max(x, y);
+    w[c.hi[i]] = min(x, y);
+  }
 }
 // The N largest of a lane's list and another lane's (both descending): the
 // larger of opposite ends is a bitonic list of exactly those.
@@ -271,7 +296,7 @@ __device__ __forceinline__ bool choose_network(const uint32_t (&word)[VPL], int 
 template <typename LT, int G, int VPL, int BLOCK, bool STATS, bool SIGMOID, int NET>
 __global__ void __launch_bounds__(BLOCK) router_rows(RouterFwd a) {
   constexpr int GPB = BLOCK / G;
-  constexpr int KQ = 64 / G;  // choices a lane may hold (k <= 64)
+  constexpr int KQ = NET == 8 ? 1 : 64 / G;  // choices a lane may hold (k <= 8, or <= 64)
   extern __shared__ float lds[];  // STATS: int cnt[E + 1], then float sums[waves][E + 1]
   const int E = a.E, k = a.k;
   const int lane = (int)threadIdx.x % G, group = (int)threadIdx.x / G;
@@ -496,18 +521,27 @@ struct RouterBwd {
 //   sigmoid:        s (1 - s) dw;  renormalised: (1 - s_c) q_c (dw_c - sum q dw), q = s / sum of the chosen s
 //   losses:         a_e = d_balance * E / (k T^2) * count_e:  p_e (a_e - sum p a), for sigmoid times (1 - s_e);
 //                   softmax: + d_z * 2 lse / T * p_e
-template <typename LT, int G, int VPL, int BLOCK, bool SIGMOID>
+// KQ: choices a lane may hold (k <= KQ * G).
+template <typename LT, int G, int VPL, int BLOCK, bool SIGMOID, int KQ>
 __global__ void __launch_bounds__(BLOCK) router_bwd_rows(RouterBwd a) {
   constexpr int GPB = BLOCK / G;
-  constexpr int KQ = 64 / G;
   const int E = a.E, k = a.k;
   const int lane = (int)threadIdx.x % G, group = (int)threadIdx.x / G;
   const bool losses = a.counts != nullptr;
-  float ga = 0.f, gz = 0.f;
+  // a token's row by expert: first its logits, for the chosen ones, then the
+  // gradients to the chosen ones (rows padded so that the four tokens of a
+  // wave meet different banks)
+  __shared__ float by_expert[GPB][G * VPL + 16];
+  float gz = 0.f, ga[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) ga[i] = 0.f;
   if (losses) {
     const float n = (float)max(a.counts[E], 1);
-    ga = a.d_losses[0] * ((float)E / (float)k) / n / n;
+    const float g = a.d_losses[0] * ((float)E / (float)k) / n / n;
     gz = SIGMOID ? 0.f : a.d_losses[1] * 2.f / n;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (i * G + lane < E) ga[i] = g * (float)a.counts[i * G + lane];
   }
   for (int64_t t0 = (int64_t)blockIdx.x * GPB; t0 < a.T; t0 += (int64_t)gridDim.x * GPB) {
     const int64_t t = t0 + group;
@@ -521,29 +555,35 @@ __global__ void __launch_bounds__(BLOCK) router_bwd_rows(RouterBwd a) {
     const LT* rows = (const LT*)a.logits + t0 * a.ld;
     const uint32_t ld = (uint32_t)a.ld, ngrp = (uint32_t)min<int64_t>(GPB, a.T - t0);
     const uint32_t off = min((uint32_t)group, ngrp - 1) * ld, last = (ngrp - 1) * ld + (uint32_t)E - 1;
-    const LT* row = rows + off;
-    Row<LT, G, VPL, false> r;
-    r.load(rows, off, last, a.bias, E, gl, keep);
     // the choices, one or more per lane; an id outside [0, E) has no gradient
     int id[KQ];
     float c[KQ], lc[KQ], ltop = -kInf;
 #pragma unroll
     for (int q = 0; q < KQ; ++q) {
-      id[q] = -1;
-      if (q * G >= k) break;
       const int j = q * G + gl;
+      id[q] = -1;
       c[q] = 0.f;
-      lc[q] = -kInf;
-      if (keep && j < k) {
+      if (q * G < k && keep && j < k) {
         const int64_t v = a.ids[t * k + j];
-        if (v >= 0 && v < E) {
-          id[q] = (int)v;
-          c[q] = a.d_weights[t * k + j] * a.scale;
-          lc[q] = load1(row + v);
-        }
+        id[q] = v >= 0 && v < E ? (int)v : -1;
+        c[q] = a.d_weights[t * k + j] * a.scale;
       }
+    }
+    Row<LT, G, VPL, false> r;
+    r.load(rows, off, last, a.bias, E, gl, keep);
+    float* mine = by_expert[group];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) mine[i * G + gl] = r.l[i];
+    wave_lds_fence();
+#pragma unroll
+    for (int q = 0; q < KQ; ++q) {
+      lc[q] = id[q] >= 0 ? mine[id[q]] : -kInf;
       ltop = __builtin_fmaxf(ltop, lc[q]);
     }
+    wave_lds_fence();
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) mine[i * G + gl] = 0.f;
+    wave_lds_fence();
     const float ptop = SIGMOID ? __builtin_fminf(r.top, 0.f) : r.top;
     const float nan = r.broken ? __builtin_nanf("") : 0.f;
     float p[VPL], den = 0.f;
@@ -566,63 +606,47 @@ __global__ void __launch_bounds__(BLOCK) router_bwd_rows(RouterBwd a) {
       float sc[KQ], sum = 0.f, dot = 0.f;
 #pragma unroll
       for (int q = 0; q < KQ; ++q) {
-        if (q * G >= k) break;
         sc[q] = id[q] < 0 ? 0.f : score_of<SIGMOID>(lc[q], SIGMOID ? __builtin_fminf(wtop, 0.f) : wtop);
         sum += sc[q];
         dot = __builtin_fmaf(sc[q], c[q], dot);
       }
       if (a.renorm) {
         sum = grp_sum<G>(sum);
-        dot = sum > 0.f ? grp_sum<G>(dot) / sum : 0.f;
-      } else if (!SIGMOID) {
-        along = grp_sum<G>(dot) / den;
+        sum = sum > 0.f ? __builtin_amdgcn_rcpf(sum) : 0.f;
+        dot = grp_sum<G>(dot) * sum;
+      } else {
+        sum = SIGMOID ? 1.f : __builtin_amdgcn_rcpf(den);
+        if (!SIGMOID) along = grp_sum<G>(dot) * sum;
+        dot = 0.f;
       }
 #pragma unroll
       for (int q = 0; q < KQ; ++q) {
-        if (q * G >= k) break;
         if (id[q] < 0) continue;
-        c[q] = a.renorm ? sc[q] / sum * (c[q] - dot) : SIGMOID ? sc[q] * c[q] : sc[q] / den * c[q];
-        if (SIGMOID) c[q] *= one_minus(lc[q]);
+        float v = sc[q] * sum * (c[q] - dot);
+        if (SIGMOID) v *= one_minus(lc[q]);
+        atomicAdd(mine + id[q], v);  // (an id is given once, or adds up)
       }
+      wave_lds_fence();
     }
     float dl[VPL];
     if (losses) {
       float pa = 0.f;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = i * G + gl;
-        dl[i] = e < E ? ga * (float)a.counts[e] : 0.f;
-        pa = __builtin_fmaf(p[i], dl[i], pa);
-      }
+      for (int i = 0; i < VPL; ++i) pa = __builtin_fmaf(p[i], ga[i], pa);
       pa = grp_sum<G>(pa);
       const float more = (SIGMOID ? 0.f : gz * (r.top + __logf(den)) - along) - pa;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        dl[i] = p[i] * (dl[i] + more);
+        dl[i] = p[i] * (ga[i] + more);
         if (SIGMOID && r.l[i] > -kInf) dl[i] *= one_minus(r.l[i]);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) dl[i] = full ? -p[i] * along : 0.f;
     }
-    // each choice to the lane that owns its expert (a repeated id adds up)
 #pragma unroll
-    for (int q = 0; q < KQ; ++q)
-#pragma unroll
-      for (int j = 0; j < G; ++j) {
-        if (q * G + j >= k) break;
-        int e;
-        float v;
-        if constexpr (G == 16) {
-          e = row_lane_of(id[q], j);
-          v = u2f((uint32_t)row_lane_of((int)f2u(c[q]), j));
-        } else {
-          e = lane_value(id[q], j);
-          v = lane_valuef(c[q], j);
-        }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) dl[i] += e == i * G + gl ? v : 0.f;
-      }
+    for (int i = 0; i < VPL; ++i) dl[i] += mine[i * G + gl];
+    wave_lds_fence();
     if (!in) continue;
     LT* out = (LT*)a.d_logits + t * E;
 #pragma unroll
@@ -717,8 +741,11 @@ hipError_t launch_router_bwd(const RouterBwdArgs& r, int cus, hipStream_t s) {
     with_layout(r.E, [&](auto g, auto v) {
       constexpr int G = decltype(g)::value, V = decltype(v)::value;
       const int64_t gpb = 256 / G;
-      const int grid = (int)std::min<int64_t>((r.T + gpb - 1) / gpb, (int64_t)cus * 64);
-      router_bwd_rows<LT, G, V, 256, SIG><<<grid, 256, 0, s>>>(a);
+      const int grid = (int)std::min<int64_t>((r.T + gpb - 1) / gpb, (int64_t)cus * 8);
+      if (r.k <= G)
+        router_bwd_rows<LT, G, V, 256, SIG, 1><<<grid, 256, 0, s>>>(a);
+      else if constexpr (G < 64)
+        router_bwd_rows<LT, G, V, 256, SIG, 64 / G><<<grid, 256, 0, s>>>(a);
     });
   };
   with_types(r.logits_fp32, r.sigmoid, go);

@@ -64,13 +64,6 @@ __device__ __forceinline__ int row_min(int x) {
   return x;
 }
 
-__device__ __forceinline__ uint32_t row_umax(uint32_t x) {
-  x = max(x, (uint32_t)dpp_mov<kRor8>((int)x));
-  x = max(x, (uint32_t)dpp_mov<kRor4>((int)x));
-  x = max(x, (uint32_t)dpp_mov<kRor2>((int)x));
-  return max(x, (uint32_t)dpp_mov<kRor1>((int)x));
-}
-
 // Lane l's value in every lane (a scalar register).
 __device__ __forceinline__ int lane_value(int x, int l) { return __builtin_amdgcn_readlane(x, l); }
 __device__ __forceinline__ float lane_valuef(float x, int l) {
@@ -87,36 +80,19 @@ __device__ __forceinline__ float wave_max(float x) {
   return __builtin_fmaxf(__builtin_fmaxf(lane_valuef(x, 0), lane_valuef(x, 16)),
                          __builtin_fmaxf(lane_valuef(x, 32), lane_valuef(x, 48)));
 }
-__device__ __forceinline__ uint32_t wave_umax(uint32_t x) {
-  x = row_umax(x);
-  return max(max((uint32_t)lane_value((int)x, 0), (uint32_t)lane_value((int)x, 16)),
-             max((uint32_t)lane_value((int)x, 32), (uint32_t)lane_value((int)x, 48)));
-}
 __device__ __forceinline__ int wave_min(int x) {
   x = row_min(x);
   return min(min(lane_value(x, 0), lane_value(x, 16)), min(lane_value(x, 32), lane_value(x, 48)));
 }
 
-// Lane j's value (j a constant after unrolling) in every lane of each row of 16.
-__device__ __forceinline__ int row_lane_of(int x, int j) {
-  switch (j) {
-    case 0: return dpp_mov<0x150>(x);
-    case 1: return dpp_mov<0x151>(x);
-    case 2: return dpp_mov<0x152>(x);
-    case 3: return dpp_mov<0x153>(x);
-    case 4: return dpp_mov<0x154>(x);
-    case 5: return dpp_mov<0x155>(x);
-    case 6: return dpp_mov<0x156>(x);
-    case 7: return dpp_mov<0x157>(x);
-    case 8: return dpp_mov<0x158>(x);
-    case 9: return dpp_mov<0x159>(x);
-    case 10: return dpp_mov<0x15A>(x);
-    case 11: return dpp_mov<0x15B>(x);
-    case 12: return dpp_mov<0x15C>(x);
-    case 13: return dpp_mov<0x15D>(x);
-    case 14: return dpp_mov<0x15E>(x);
-    default: return dpp_mov<0x15F>(x);
-  }
+// Orders a wave's LDS accesses before and behind it among its own lanes (LDS
+// serves a wave's instructions in order; this keeps the compiler from moving
+// them).
+__device__ __forceinline__ void wave_lds_fence() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+#endif
 }
 
 // Largest value of 4 consecutive lanes (a 32-element block at 8 per lane).
