@@ -456,7 +456,8 @@ size_t mok_router_scratch_bytes(int64_t T, int32_t experts);
  *         experts and N = max(n, 1): the load-balance loss experts / (k N^2)
  *         * sum_e counts_e * (sum of p_e over live tokens), and the z loss,
  *         the mean over live tokens of logsumexp(logits)^2 (0 for sigmoid).
- * 1 <= k <= min(experts, 64), experts <= 1024, ld <= 2^22 for T > 1.
+ * 1 <= k <= min(experts, 64), experts <= 1024, T * k < 2^31, ld <= 2^22 for
+ * T > 1.
  */
 mok_status mok_router_topk(const void* logits, int logits_is_fp32, int64_t T, int64_t ld, int32_t experts, int32_t k,
                            const float* bias, const uint8_t* token_mask, int32_t scoring, int renormalize, float scale,

@@ -40,6 +40,7 @@ import dataclasses
 import weakref
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import (MOK_MODE_BF16, MOK_MODE_MXFP8, MoKConfig, backward, build_schedule, context_bytes, forward,
                get_workspace, mxfp8_quantize, mxfp8_quantize_transposed, ops)
@@ -265,6 +266,7 @@ class RMSNormFunction(torch.autograd.Function):
         return y, total
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, d_sum):
         s, rstd, weight = ctx.saved_tensors
         need_x, need_w, need_r = ctx.needs_input_grad[:3]
@@ -319,6 +321,7 @@ class RouterFunction(torch.autograd.Function):
         return weights, ids, counts, losses
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_weights, _ids, _counts, d_losses):
         logits, ids, counts, *rest = ctx.saved_tensors
         if d_weights is None and d_losses is None:

@@ -31,7 +31,9 @@
 // states and masters (loads too: 577); with 8 bits loads and stores 329 ->
 // 289 us (stores alone 320). The 8-bit update was bound by its instructions
 // first: packed conversions, the hardware's root and no clamps took it from
-// 229 to 158 us (bf16, no master: 6.4 TB/s) and from 289 to 279 with a master.
+// 229 to 165 us (bf16, no master: 6.1 TB/s) and from 289 to 279 with a master.
+// With workgroups of one turn (kTable): 514 us with fp32 states and masters
+// (5.4 TB/s), 260 us with 8 bits and masters (6.2 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -189,6 +191,15 @@ __device__ __forceinline__ float library_power(int k) {
   return powf(u2f((uint32_t)opaque(0x40000000)), (float)k);
 }
 
+// Whether a workgroup makes a table of the powers first and takes four turns,
+// or takes one turn and finds them as it goes. Workgroups of one turn sweep
+// memory as a closer front: 1e8 elements, bf16 with masters 280 -> 260 us,
+// fp32 287 -> 274, and with fp32 states, which need no powers, 541 -> 514.
+// Where an element moves only 10 bytes the powers' instructions weigh more
+// than that: 165 us with the table, 188 without, 202 with a table per turn.
+template <typename PT, bool MASTER, bool S8>
+constexpr bool kTable = S8 && !MASTER && sizeof(PT) == 2;
+
 template <typename PT, bool MASTER, typename GT, bool S8>
 __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
   // the workgroup's tensor: the last one that begins at or before it
@@ -205,9 +216,10 @@ __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
   const int64_t begin = (int64_t)(blockIdx.x - t.chunk0) * a.chunk;
   const int64_t end = min(n, begin + (int64_t)a.chunk);
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
-  // 2^-X and 2^-2X for scale byte X + 127
-  __shared__ float down[S8 ? 256 : 1], down2[S8 ? 256 : 1];
-  if constexpr (S8) {
+  // 2^-X and 2^-2X for scale byte X + 127 (kTable)
+  constexpr bool kTab = kTable<PT, MASTER, S8>;
+  __shared__ float down[kTab ? 256 : 1], down2[kTab ? 256 : 1];
+  if constexpr (kTab) {
     static_assert(kThreads == 256, "a thread per scale byte");
     down[threadIdx.x] = library_power(127 - (int)threadIdx.x);
     down2[threadIdx.x] = library_power(2 * (127 - (int)threadIdx.x));
@@ -264,7 +276,15 @@ __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
       }
       mr = quad_max(mr);
       const int xm = state_exponent(quad_max(f2u(mm))), xr = state_exponent(min(mr, 0x7F7FFFFFu));
-      const float fm = down[xm + 127], fr = u2f((uint32_t)(127 - xr) << 23), fv = mr ? down2[xr + 127] : 0.f;
+      float fm, fv;  // 2^-X of m, 2^-2X of r
+      if constexpr (kTab) {
+        fm = down[xm + 127], fv = down2[xr + 127];
+      } else {  // even lanes of the block's four find the one, odd ones the other
+        const float power = library_power(threadIdx.x & 1 ? -2 * xr : -xm);
+        fm = dpp_movf<kQuadLane0>(power), fv = dpp_movf<kQuadLane1>(power);
+      }
+      fv = mr ? fv : 0.f;
+      const float fr = u2f((uint32_t)(127 - xr) << 23);
       uint32_t x = (t.number0 + (uint32_t)i) / 2 * kPairStep + a.seed;
       bool small = false;
 #pragma unroll
@@ -321,9 +341,9 @@ hipError_t launch_adamw(const mok_adamw& u, int cus, hipStream_t s) {
   a.eps = (float)u.eps;
   int64_t total = 0;
   for (int i = 0; i < u.count; ++i) total += u.numels[i];
-  // a workgroup takes 4 turns where that still gives every compute unit
-  // several workgroups, else one
-  a.chunk = total >= (int64_t)cus * 4 * 8 * kTurn ? 4 * kTurn : kTurn;
+  // (four turns only where that still gives every compute unit several workgroups)
+  const bool table = u.state_bits == 8 && !u.param_fp32 && !u.masters;
+  a.chunk = table && total >= (int64_t)cus * 4 * 8 * kTurn ? 4 * kTurn : kTurn;
   auto launch = [&](int64_t blocks) -> hipError_t {
     auto go = [&](auto pt, auto master, auto gt, auto s8) {
       adamw_tensors<decltype(pt), decltype(master)::value, decltype(gt), decltype(s8)::value>

@@ -781,7 +781,7 @@ static mok_status check_router(const void* logits, int logits_is_fp32, int64_t T
     return MOK_ERR_INVALID_ARGUMENT;
   if (scoring != MOK_ROUTER_SOFTMAX && scoring != MOK_ROUTER_SIGMOID) return MOK_ERR_INVALID_ARGUMENT;
   if (k > experts) return MOK_ERR_INVALID_ARGUMENT;
-  if (experts > 1024 || k > 64 || T > ((int64_t)1 << 40)) return MOK_ERR_UNSUPPORTED;
+  if (experts > 1024 || k > 64 || T > 0x7FFFFFFF / k) return MOK_ERR_UNSUPPORTED;
   if (T > 1 && ld > ((int64_t)1 << 22)) return MOK_ERR_UNSUPPORTED;  // a workgroup's rows: 32-bit offsets
   if (T > 0 && (!logits || ld < experts)) return MOK_ERR_INVALID_ARGUMENT;
   if (!element_aligned(logits, logits_is_fp32) || !element_aligned(bias, 1)) return MOK_ERR_INVALID_ARGUMENT;

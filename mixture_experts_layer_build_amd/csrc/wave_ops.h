@@ -32,6 +32,7 @@ __device__ __forceinline__ float dpp_movf(float x) {
 
 constexpr int kRor1 = 0x121, kRor2 = 0x122, kRor4 = 0x124, kRor8 = 0x128;  // row_ror:n
 constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;                          // quad_perm:[1,0,3,2], [2,3,0,1]
+constexpr int kQuadLane0 = 0x00, kQuadLane1 = 0x55;                        // quad_perm:[0,0,0,0], [1,1,1,1]
 
 // x, as a value the compiler knows nothing of.
 __device__ __forceinline__ int opaque(int x) {

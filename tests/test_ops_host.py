@@ -76,7 +76,7 @@ def router(logits=P, l32=1, T=4, ld=8, E=8, k=2, bias=None, mask=None, scoring=0
     (INVALID, dict(ld=7)), (INVALID, dict(w=None)), (INVALID, dict(ids=None)), (INVALID, dict(ids=P + 4)),
     (INVALID, dict(counts=P)), (INVALID, dict(losses=P)), (INVALID, dict(counts=P, losses=P)),
     (SMALL, dict(counts=P, losses=P, scratch=P, nbytes=8)), (INVALID, dict(bias=P + 2)), (INVALID, dict(logits=P + 2)),
-    (UNSUPPORTED, dict(E=1025, ld=1025)), (UNSUPPORTED, dict(E=128, ld=128, k=65)),
+    (UNSUPPORTED, dict(E=1025, ld=1025)), (UNSUPPORTED, dict(T=1 << 30)), (UNSUPPORTED, dict(ld=(1 << 22) + 1)), (UNSUPPORTED, dict(E=128, ld=128, k=65)),
     (OK, dict(T=0, logits=None, w=None, ids=None))])
 def test_router_refusals(want, kw):
     assert router(**kw) == want
