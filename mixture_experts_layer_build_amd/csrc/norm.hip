@@ -34,18 +34,22 @@
 namespace mok {
 namespace {
 
-// E4M3 codes and E8M0 scale of a lane's 8 elements of a 32-element block
-// (4 consecutive lanes), by the block rule of the quantizer (X = clamp(floor(
+// E4M3 codes and E8M0 scale of a lane's W elements of a 32-element block (32
+// / W consecutive lanes), by the block rule of the quantizer (X = clamp(floor(
 // log2 amax) - 8, -127, 127)). A block that holds an infinity or a NaN gets
 // the NaN scale 0xFF, so its consumers see it.
-__device__ __forceinline__ void store_mxfp8(const float (&y)[8], uint8_t* codes, uint8_t* scale, bool first) {
+template <int W>
+__device__ __forceinline__ void store_mxfp8(const float (&y)[W], uint8_t* codes, uint8_t* scale, bool first) {
   uint32_t amax = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, f2u(y[i]) & 0x7FFFFFFFu);
-  amax = quad_max(amax);
+  for (int i = 0; i < W; ++i) amax = max(amax, f2u(y[i]) & 0x7FFFFFFFu);
+  amax = W == 8 ? quad_max(amax) : octet_max(amax);
   const int X = mx_block_exponent(amax);
-  *reinterpret_cast<uint2*>(codes) =
-      make_uint2(e4m3x4_encode_scaled(y[0], y[1], y[2], y[3], X), e4m3x4_encode_scaled(y[4], y[5], y[6], y[7], X));
+  const uint32_t lo = e4m3x4_encode_scaled(y[0], y[1], y[2], y[3], X);
+  if constexpr (W == 8)
+    *reinterpret_cast<uint2*>(codes) = make_uint2(lo, e4m3x4_encode_scaled(y[4], y[5], y[6], y[7], X));
+  else
+    *reinterpret_cast<uint32_t*>(codes) = lo;
   if (first) *scale = amax >= 0x7F800000u ? 0xFFu : (uint8_t)(X + 127);
 }
 
@@ -80,28 +84,36 @@ struct NormFwd {
   float* rstd;      // null: not written
 };
 
-// RT: the residual's type, void for none.
+template <typename XT, typename RT>
+constexpr int lane_width = std::is_same<RT, float>::value ? 4 : 8;
+
+// RT: the residual's type, void for none. A lane takes 8 elements per load (16
+// bytes of bf16), or 4 where the residual and the sum are fp32 (16 bytes of
+// them): at 32 bytes a lane an instruction touches every line and fills none
+// (bf16 x, fp32 residual, 16384 x 7168 to MXFP8 250 -> 221 us, 4096 x 2048 22
+// -> 17; fp32 x without a residual only reads fp32, 18 us against 21).
 template <typename XT, typename RT, bool STREAM, int BLOCK, int TPR, int NV>
 __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
   constexpr bool kRes = !std::is_void<RT>::value;
   using R = typename std::conditional<kRes, RT, float>::type;
+  constexpr int W = lane_width<XT, RT>;
   constexpr int RPB = BLOCK / TPR;
   __shared__ float slots[2 * RPB * (TPR / 64)];
   // (a row's waves are whole waves, so its number and addresses are scalars)
   const uint32_t t = threadIdx.x % TPR;
   const int group = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
-  const uint32_t nchunk = (uint32_t)a.cols >> 3;
-  float w[NV][8];
+  const uint32_t nchunk = (uint32_t)a.cols / W;
+  float w[NV][W];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const uint32_t c = t + i * TPR;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) w[i][q] = 0.f;
+    for (int q = 0; q < W; ++q) w[i][q] = 0.f;
     if (c < nchunk) {
       if (a.w_fp32)
-        load8((const float*)a.w + c * 8, w[i]);
+        load_lane<false>((const float*)a.w + c * W, w[i]);
       else
-        load8((const uint16_t*)a.w + c * 8, w[i]);
+        load_lane<false>((const uint16_t*)a.w + c * W, w[i]);
     }
   }
   const float inv_cols = 1.0f / (float)a.cols;
@@ -112,28 +124,28 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
     const bool live = row < a.rows;
     const XT* x = (const XT*)a.x + row * a.ld_x;
     const R* res = (const R*)a.residual + row * a.ld_res;
-    float v[NV][8];
+    float v[NV][W];
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const uint32_t c = t + i * TPR;
       if (live && c < nchunk) {
-        load8_as<STREAM>(x + c * 8, v[i]);
+        load_lane<STREAM>(x + c * W, v[i]);
         if constexpr (kRes) {
-          float r[8];
-          load8_as<STREAM>(res + c * 8, r);
+          float r[W];
+          load_lane<STREAM>(res + c * W, r);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[i][q] += r[q];
+          for (int q = 0; q < W; ++q) v[i][q] += r[q];
         }
       } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[i][q] = 0.f;
+        for (int q = 0; q < W; ++q) v[i][q] = 0.f;
       }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) ss = __builtin_fmaf(v[i][q], v[i][q], ss);
+      for (int q = 0; q < W; ++q) ss = __builtin_fmaf(v[i][q], v[i][q], ss);
     ss = row_threads_sum<TPR>(ss, slots, group, parity);
     const float rstd = 1.0f / __builtin_sqrtf(ss * inv_cols + a.eps);
     if (!live) continue;
@@ -143,19 +155,12 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
     for (int i = 0; i < NV; ++i) {
       const uint32_t c = t + i * TPR;
       if (c >= nchunk) continue;
-      if constexpr (kRes) {
-        // (an fp32 sum: of a bf16 x past the cache, 5003 x 7168 to MXFP8 80 ->
-        // 76 us; of an fp32 x through it, 32768 x 4096 371 -> 350 us)
-        if constexpr (sizeof(XT) == 2)
-          store8_once((R*)a.sum + out + c * 8, v[i]);
-        else
-          store8((R*)a.sum + out + c * 8, v[i]);
-      }
-      float y[8];
+      if constexpr (kRes) store_once((R*)a.sum + out + c * W, v[i]);
+      float y[W];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) y[q] = v[i][q] * rstd * w[i][q];
-      if (a.y) store8_once(a.y + out + c * 8, y);
-      if (a.codes) store_mxfp8(y, a.codes + out + c * 8, a.scale + (out >> 5) + (c >> 2), (t & 3) == 0);
+      for (int q = 0; q < W; ++q) y[q] = v[i][q] * rstd * w[i][q];
+      if (a.y) store_once(a.y + out + c * W, y);
+      if (a.codes) store_mxfp8(y, a.codes + out + c * W, a.scale + (out >> 5) + c / (32 / W), t % (32 / W) == 0);
     }
   }
 }
@@ -393,10 +398,9 @@ template <typename XT, typename RT, int BLOCK, int TPR, int NV>
 void run_fwd(const NormFwd& a, int cus, hipStream_t s) {
   const int64_t need = (a.rows + BLOCK / TPR - 1) / (BLOCK / TPR);
   const int grid = (int)std::min<int64_t>(need, (int64_t)cus * (2048 / BLOCK));
-  constexpr bool kAllFp32 = sizeof(XT) == 4;  // nothing of it would be streamed
-  constexpr int64_t kBytes = sizeof(XT) + (std::is_void<RT>::value ? 0 : sizeof(typename std::conditional<std::is_void<RT>::value, char, RT>::type));
-  if (!kAllFp32 && a.rows * a.cols * kBytes > kCacheBytes)
-    rms_norm_rows<XT, RT, !kAllFp32, BLOCK, TPR, NV><<<grid, BLOCK, 0, s>>>(a);
+  constexpr int64_t kBytes = sizeof(XT) + (std::is_void<RT>::value ? 0 : std::is_same<RT, float>::value ? 4 : 2);
+  if (a.rows * a.cols * kBytes > kCacheBytes)
+    rms_norm_rows<XT, RT, true, BLOCK, TPR, NV><<<grid, BLOCK, 0, s>>>(a);
   else
     rms_norm_rows<XT, RT, false, BLOCK, TPR, NV><<<grid, BLOCK, 0, s>>>(a);
 }
@@ -408,18 +412,19 @@ void pick_fwd(const NormFwd& a, bool vec, int cus, hipStream_t s) {
     return;
   }
   const int c = a.cols;
+  constexpr int M = 8 / lane_width<XT, RT>;  // twice the loads where a lane takes half
   if (c <= 512)
-    run_fwd<XT, RT, 256, 64, 1>(a, cus, s);
+    run_fwd<XT, RT, 256, 64, 1 * M>(a, cus, s);
   else if (c <= 1024)
-    run_fwd<XT, RT, 256, 64, 2>(a, cus, s);
+    run_fwd<XT, RT, 256, 64, 2 * M>(a, cus, s);
   else if (c <= 2048)
-    run_fwd<XT, RT, 256, 64, 4>(a, cus, s);
+    run_fwd<XT, RT, 256, 64, 4 * M>(a, cus, s);
   else if (c <= 4096)
-    run_fwd<XT, RT, 256, 256, 2>(a, cus, s);
+    run_fwd<XT, RT, 256, 256, 2 * M>(a, cus, s);
   else if (c <= 8192)
-    run_fwd<XT, RT, 256, 256, 4>(a, cus, s);
+    run_fwd<XT, RT, 256, 256, 4 * M>(a, cus, s);
   else
-    run_fwd<XT, RT, 512, 512, 4>(a, cus, s);
+    run_fwd<XT, RT, 512, 512, 4 * M>(a, cus, s);
 }
 
 // Workgroups of the backward, at most: two per compute unit, enough to fill

@@ -96,6 +96,13 @@ __device__ __forceinline__ void wave_lds_fence() {
 #endif
 }
 
+// Largest value of 8 consecutive lanes (a block at 4 elements per lane).
+__device__ __forceinline__ uint32_t quad_max(uint32_t x);
+__device__ __forceinline__ uint32_t octet_max(uint32_t x) {
+  x = quad_max(x);
+  return max(x, (uint32_t)dpp_mov<0x141>((int)x));  // row_half_mirror: the other four
+}
+
 // Largest value of 4 consecutive lanes (a 32-element block at 8 per lane).
 __device__ __forceinline__ uint32_t quad_max(uint32_t x) {
   x = max(x, (uint32_t)dpp_mov<kQuadXor1>((int)x));
@@ -154,14 +161,36 @@ __device__ __forceinline__ void store8_once(float* p, const float (&v)[8]) {
   __builtin_nontemporal_store((f32x4nt){v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4nt*>(p));
   __builtin_nontemporal_store((f32x4nt){v[4], v[5], v[6], v[7]}, reinterpret_cast<f32x4nt*>(p + 4));
 }
-// bf16 past the caches if STREAM, fp32 through them.
+// W = 8 or 4 elements per lane, past the caches if STREAM. fp32 takes 4: one
+// 16-byte access, which fills whole lines.
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2nt;
 template <bool STREAM>
-__device__ __forceinline__ void load8_as(const uint16_t* p, float (&v)[8]) {
+__device__ __forceinline__ void load_lane(const uint16_t* p, float (&v)[8]) {
   STREAM ? load8_once(p, v) : load8(p, v);
 }
 template <bool STREAM>
-__device__ __forceinline__ void load8_as(const float* p, float (&v)[8]) {
+__device__ __forceinline__ void load_lane(const uint16_t* p, float (&v)[4]) {
+  const u32x2nt* q = reinterpret_cast<const u32x2nt*>(p);
+  const u32x2nt r = STREAM ? __builtin_nontemporal_load(q) : *q;
+  v[0] = u2f(r[0] << 16), v[1] = u2f(r[0] & 0xFFFF0000u), v[2] = u2f(r[1] << 16), v[3] = u2f(r[1] & 0xFFFF0000u);
+}
+template <bool STREAM>
+__device__ __forceinline__ void load_lane(const float* p, float (&v)[4]) {
+  const f32x4nt* q = reinterpret_cast<const f32x4nt*>(p);
+  const f32x4nt r = STREAM ? __builtin_nontemporal_load(q) : *q;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = r[i];
+}
+template <bool STREAM>
+__device__ __forceinline__ void load_lane(const float* p, float (&v)[8]) {
   load8(p, v);
+}
+__device__ __forceinline__ void store_once(uint16_t* p, const float (&v)[8]) { store8_once(p, v); }
+__device__ __forceinline__ void store_once(uint16_t* p, const float (&v)[4]) {
+  __builtin_nontemporal_store((u32x2nt){pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])}, reinterpret_cast<u32x2nt*>(p));
+}
+__device__ __forceinline__ void store_once(float* p, const float (&v)[4]) {
+  __builtin_nontemporal_store((f32x4nt){v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4nt*>(p));
 }
 
 // 8 elements as they lie in memory: 4 registers of bf16, 8 of fp32. fresh()
