@@ -32,7 +32,7 @@
 // 289 us (stores alone 320). The 8-bit update was bound by its instructions
 // first: packed conversions, the hardware's root and no clamps took it from
 // 229 to 165 us (bf16, no master: 6.1 TB/s) and from 289 to 279 with a master.
-// With workgroups of one turn (kTable): 514 us with fp32 states and masters
+// With workgroups of one turn (TABLE): 514 us with fp32 states and masters
 // (5.4 TB/s), 260 us with 8 bits and masters (6.2 TB/s).
 #include <algorithm>
 #include <cmath>
@@ -191,16 +191,13 @@ __device__ __forceinline__ float library_power(int k) {
   return powf(u2f((uint32_t)opaque(0x40000000)), (float)k);
 }
 
-// Whether a workgroup makes a table of the powers first and takes four turns,
-// or takes one turn and finds them as it goes. Workgroups of one turn sweep
-// memory as a closer front: 1e8 elements, bf16 with masters 280 -> 260 us,
-// fp32 287 -> 274, and with fp32 states, which need no powers, 541 -> 514.
-// Where an element moves only 10 bytes the powers' instructions weigh more
-// than that: 165 us with the table, 188 without, 202 with a table per turn.
-template <typename PT, bool MASTER, bool S8>
-constexpr bool kTable = S8 && !MASTER && sizeof(PT) == 2;
-
-template <typename PT, bool MASTER, typename GT, bool S8>
+// TABLE: the workgroup makes a table of the powers first and takes four turns;
+// else it takes one turn and finds them as it goes. Workgroups of one turn
+// sweep memory as a closer front: 1e8 elements, bf16 with masters 280 -> 260
+// us, fp32 287 -> 274, and with fp32 states, which need no powers, 541 -> 514.
+// Where an element moves only 10 bytes (8 bits, bf16, no masters) the powers'
+// instructions weigh more than that: 165 us with the table, 188 without.
+template <typename PT, bool MASTER, typename GT, bool S8, bool TABLE>
 __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
   // the workgroup's tensor: the last one that begins at or before it
   int lo = 0, hi = a.count - 1;
@@ -216,10 +213,9 @@ __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
   const int64_t begin = (int64_t)(blockIdx.x - t.chunk0) * a.chunk;
   const int64_t end = min(n, begin + (int64_t)a.chunk);
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
-  // 2^-X and 2^-2X for scale byte X + 127 (kTable)
-  constexpr bool kTab = kTable<PT, MASTER, S8>;
-  __shared__ float down[kTab ? 256 : 1], down2[kTab ? 256 : 1];
-  if constexpr (kTab) {
+  // 2^-X and 2^-2X for scale byte X + 127
+  __shared__ float down[TABLE ? 256 : 1], down2[TABLE ? 256 : 1];
+  if constexpr (TABLE) {
     static_assert(kThreads == 256, "a thread per scale byte");
     down[threadIdx.x] = library_power(127 - (int)threadIdx.x);
     down2[threadIdx.x] = library_power(2 * (127 - (int)threadIdx.x));
@@ -277,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
       mr = quad_max(mr);
       const int xm = state_exponent(quad_max(f2u(mm))), xr = state_exponent(min(mr, 0x7F7FFFFFu));
       float fm, fv;  // 2^-X of m, 2^-2X of r
-      if constexpr (kTab) {
+      if constexpr (TABLE) {
         fm = down[xm + 127], fv = down2[xr + 127];
       } else {  // even lanes of the block's four find the one, odd ones the other
         const float power = library_power(threadIdx.x & 1 ? -2 * xr : -xm);
@@ -342,25 +338,31 @@ hipError_t launch_adamw(const mok_adamw& u, int cus, hipStream_t s) {
   int64_t total = 0;
   for (int i = 0; i < u.count; ++i) total += u.numels[i];
   // (four turns only where that still gives every compute unit several workgroups)
-  const bool table = u.state_bits == 8 && !u.param_fp32 && !u.masters;
-  a.chunk = table && total >= (int64_t)cus * 4 * 8 * kTurn ? 4 * kTurn : kTurn;
+  const bool table =
+      u.state_bits == 8 && !u.param_fp32 && !u.masters && total >= (int64_t)cus * 4 * 8 * kTurn;
+  a.chunk = table ? 4 * kTurn : kTurn;
   auto launch = [&](int64_t blocks) -> hipError_t {
-    auto go = [&](auto pt, auto master, auto gt, auto s8) {
-      adamw_tensors<decltype(pt), decltype(master)::value, decltype(gt), decltype(s8)::value>
+    auto go = [&](auto pt, auto master, auto gt, auto s8, auto tab) {
+      adamw_tensors<decltype(pt), decltype(master)::value, decltype(gt), decltype(s8)::value, decltype(tab)::value>
           <<<(unsigned)blocks, kThreads, 0, s>>>(a);
     };
+    const std::true_type yes;
+    const std::false_type no;
     auto with_state = [&](auto pt, auto master, auto gt) {
-      u.state_bits == 8 ? go(pt, master, gt, std::true_type{}) : go(pt, master, gt, std::false_type{});
+      if (u.state_bits != 8) return go(pt, master, gt, no, no);
+      if constexpr (std::is_same<decltype(pt), uint16_t>::value && !decltype(master)::value)
+        if (table) return go(pt, master, gt, yes, yes);
+      go(pt, master, gt, yes, no);
     };
     auto with_grad = [&](auto pt, auto master) {
       u.grad_fp32 ? with_state(pt, master, float{}) : with_state(pt, master, uint16_t{});
     };
     if (u.param_fp32)
-      with_grad(float{}, std::false_type{});
+      with_grad(float{}, no);
     else if (u.masters)
-      with_grad(uint16_t{}, std::true_type{});
+      with_grad(uint16_t{}, yes);
     else
-      with_grad(uint16_t{}, std::false_type{});
+      with_grad(uint16_t{}, no);
     return hipGetLastError();
   };
   uint32_t number = 0;
