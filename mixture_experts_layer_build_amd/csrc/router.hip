@@ -13,17 +13,18 @@
 // A row with a key that is NaN or +inf has no order: its ids are -1 and its
 // weights NaN.
 //
-// Layout: a token belongs to 16 lanes (E <= 512) or to a whole wave, lane l
-// holding experts l, l + 16, ... in registers, so a wave runs four tokens at
-// once and every reduction over a token is four DPP instructions.
+// Layout: a token belongs to 16 lanes (8 where that is faster, see
+// eight_lanes; the wave above 512 experts), lane l of G holding experts l, l +
+// G, ... in registers, so a wave runs four or eight tokens at once and every
+// reduction over a token is three or four DPP instructions.
 //
 // The choice. Per token it costs instructions, not bytes, so it decides the
 // kernel's time beyond about 64 experts. Up to k = 16 it is a sorting
 // network on 32-bit words, the key's order-preserving bits with the lowest 8
 // (9 and 10 above 256 and 512 experts) replaced by the complement of the expert id: a
 // comparator is one max and one min, a lane sorts its experts' words to the
-// 8 or 16 largest, and four merges with the lists of other lanes (max with a
-// DPP operand, then a half-cleaner) leave the token's list in every lane.
+// 8 or 16 largest, and merges with the lists of other lanes (max with a DPP
+// operand, then a half-cleaner) leave the token's list in every lane.
 // For bf16 logits without a bias the words order exactly as the keys do. For
 // fp32 keys two words may agree in the key bits they keep while the keys
 // differ below: that is checked for (neighbours in the list, and the first
@@ -43,21 +44,30 @@ namespace {
 // rounded difference of logits that x is. -inf gives 0.
 __device__ __forceinline__ float exp_neg(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
+// Over a token's group of G lanes (8, 16 or the wave).
 template <int G>
 __device__ __forceinline__ float grp_sum(float x) {
+  if constexpr (G == 8) return octet_sum(x);
   if constexpr (G == 16) return row_sum(x);
   return wave_sum(x);
 }
 template <int G>
 __device__ __forceinline__ float grp_max(float x) {
+  if constexpr (G == 8) return octet_maxf(x);
   if constexpr (G == 16) return row_max(x);
   return wave_max(x);
+}
+template <int G>
+__device__ __forceinline__ int grp_min(int x) {
+  if constexpr (G == 8) return octet_min(x);
+  if constexpr (G == 16) return row_min(x);
+  return wave_min(x);
 }
 // Whether any lane of the group says so.
 template <int G>
 __device__ __forceinline__ bool grp_any(bool x) {
   const uint64_t b = __ballot(x);
-  if constexpr (G == 16) return ((uint32_t)(b >> (lane_id() & 48)) & 0xFFFFu) != 0;
+  if constexpr (G < 64) return ((uint32_t)(b >> (lane_id() & (64 - G))) & ((1u << G) - 1u)) != 0;
   return b != 0;
 }
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -66,12 +76,6 @@ __device__ __forceinline__ bool is_nan_or_inf(float x) { return __builtin_amdgcn
 #else
 __device__ bool is_nan_or_inf(float x);  // device only
 #endif
-template <int G>
-__device__ __forceinline__ int grp_min(int x) {
-  if constexpr (G == 16) return row_min(x);
-  return wave_min(x);
-}
-
 constexpr float kInf = __builtin_inff();
 // words of the statistics' scratch before the partial rows (router_stats)
 constexpr int kStatsHead = 128, kStatsZ = 96;
@@ -261,12 +265,12 @@ __device__ __forceinline__ bool choose_network(const uint32_t (&word)[VPL], int 
       for (int i = 0; i < N; ++i) top[i] = m[i];
     }
   }
-  // rotations by 8, 4, 2, 1 pair lists of different lanes each time: after a
-  // rotation by r, lanes r apart hold the same list
-  merge_dpp<N, kRor8>(top);
-  merge_dpp<N, kRor4>(top);
-  merge_dpp<N, kRor2>(top);
-  merge_dpp<N, kRor1>(top);
+  // each step pairs a lane with one whose list covers other lanes: the next
+  // one, the next two, the mirrored four, the mirrored eight
+  merge_dpp<N, kQuadXor1>(top);
+  merge_dpp<N, kQuadXor2>(top);
+  merge_dpp<N, kHalfMirror>(top);
+  if constexpr (G >= 16) merge_dpp<N, kMirror>(top);
   if constexpr (G == 64) {
     merge_xor<N>(top, 16);
     merge_xor<N>(top, 32);
@@ -412,17 +416,14 @@ __global__ void __launch_bounds__(BLOCK) router_rows(RouterFwd a) {
     }
   }
   if constexpr (STATS) {
-    // a wave's four tokens (or one), then the waves in order
+    // a wave's tokens, then the waves in order
     constexpr int WAVES = BLOCK / 64;
     float* sums = lds + (E + 1);
     const int wave = threadIdx.x >> 6, wl = lane_id();
-    if constexpr (G == 16) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        psum[i] += __shfl_xor(psum[i], 16);
-        psum[i] += __shfl_xor(psum[i], 32);
-      }
-    }
+    for (int d = G; d < 64; d *= 2)
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) psum[i] += __shfl_xor(psum[i], d);
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (wl < G && i * G + wl < E) sums[wave * (E + 1) + i * G + wl] = psum[i];
@@ -657,15 +658,27 @@ __global__ void __launch_bounds__(BLOCK) router_bwd_rows(RouterBwd a) {
   }
 }
 
+// Whether up to 128 experts take 8 lanes per token instead of 16: twice the
+// tokens per wave for one merge less (65536 tokens, k 8: 64 experts 11.2 -> 7.5
+// us, 128 experts 11.8 -> 8.9), once there are enough tokens for four such
+// waves per SIMD (8192 tokens of 128 experts: 6.8 us with 16, 7.8 with 8). A
+// lane then holds one choice, so k is at most 8.
+bool eight_lanes(int64_t T, int k) { return k <= 8 && T >= 32768; }
+
 // Lanes per token and experts per lane for E experts: calls f(G, VPL) with
 // both as compile-time constants.
-template <typename F>
+template <bool EIGHT, typename F>
 void with_layout(int E, F&& f) {
   using std::integral_constant;
   auto go = [&](auto g, auto v) { f(g, v); };
-  if (E <= 64) go(integral_constant<int, 16>{}, integral_constant<int, 4>{});
-  else if (E <= 128) go(integral_constant<int, 16>{}, integral_constant<int, 8>{});
-  else if (E <= 256) go(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+  if constexpr (EIGHT) {
+    if (E <= 64) return go(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+    if (E <= 128) return go(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+  } else {
+    if (E <= 64) return go(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+    if (E <= 128) return go(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+  }
+  if (E <= 256) go(integral_constant<int, 16>{}, integral_constant<int, 16>{});
   else if (E <= 512) go(integral_constant<int, 16>{}, integral_constant<int, 32>{});
   else go(integral_constant<int, 64>{}, integral_constant<int, 16>{});
 }
@@ -681,46 +694,49 @@ void with_types(int fp32, int sigmoid, F&& f) {
 // Workgroup of the forward with statistics: one per compute unit, its LDS
 // (one row of sums per wave) below 64 KiB and its registers enough at every E.
 constexpr int stats_block(int E) { return E <= 256 ? 1024 : 512; }
-constexpr int lanes_of(int E) { return E <= 512 ? 16 : 64; }
+constexpr int lanes_of(int E, bool eight) { return eight && E <= 128 ? 8 : E <= 512 ? 16 : 64; }
 constexpr int kStatsParts = 256;
 
 }  // namespace
 
 // Workgroups of the forward with statistics, at most: a constant, so the
 // order of the sums does not depend on the device.
-static int64_t router_parts(int64_t T, int64_t E) {
-  const int64_t gpb = stats_block((int)E) / lanes_of((int)E);
+static int64_t router_parts(int64_t T, int64_t E, bool eight) {
+  const int64_t gpb = stats_block((int)E) / lanes_of((int)E, eight);
   return std::min<int64_t>((std::max<int64_t>(T, 1) + gpb - 1) / gpb, kStatsParts);
 }
-int64_t router_scratch_words(int64_t T, int64_t E) { return kStatsHead + router_parts(T, E) * 2 * (E + 1); }
+int64_t router_scratch_words(int64_t T, int64_t E) {  // (for every k: more lanes per token, more workgroups)
+  return kStatsHead + router_parts(T, E, false) * 2 * (E + 1);
+}
 
 hipError_t launch_router(const RouterArgs& r, int cus, hipStream_t s) {
   RouterFwd a{r.logits, r.T, r.ld, r.E, r.k, r.bias, r.mask, r.sigmoid, r.renorm,
               !r.logits_fp32 && !r.bias, r.scale, r.weights, r.ids, r.part};
   const bool stats = r.counts != nullptr;
   if (r.T == 0 && !stats) return hipSuccess;
-  const int parts = (int)router_parts(r.T, r.E);
+  const bool eight = eight_lanes(r.T, r.k);
+  const int parts = (int)router_parts(r.T, r.E, eight);
   auto go = [&](auto tag, auto sig) {
     using LT = decltype(tag);
     constexpr bool SIG = decltype(sig)::value;
-    with_layout(r.E, [&](auto g, auto v) {
-      constexpr int G = decltype(g)::value, V = decltype(v)::value;
+    auto run = [&](auto g, auto v, auto net) {
+      constexpr int G = decltype(g)::value, V = decltype(v)::value, NET = decltype(net)::value;
       if (stats) {
         constexpr int B = stats_block(G * V);
         const size_t lds = sizeof(float) * (size_t)(r.E + 1) * (1 + B / 64);
-        if (r.k <= 8)
-          router_rows<LT, G, V, B, true, SIG, 8><<<parts, B, lds, s>>>(a);
-        else
-          router_rows<LT, G, V, B, true, SIG, 16><<<parts, B, lds, s>>>(a);
+        router_rows<LT, G, V, B, true, SIG, NET><<<parts, B, lds, s>>>(a);
       } else {
         const int64_t gpb = 256 / G;
         const int grid = (int)std::min<int64_t>((r.T + gpb - 1) / gpb, (int64_t)cus * 64);
-        if (r.k <= 8)
-          router_rows<LT, G, V, 256, false, SIG, 8><<<grid, 256, 0, s>>>(a);
-        else
-          router_rows<LT, G, V, 256, false, SIG, 16><<<grid, 256, 0, s>>>(a);
+        router_rows<LT, G, V, 256, false, SIG, NET><<<grid, 256, 0, s>>>(a);
       }
-    });
+    };
+    if (eight)
+      with_layout<true>(r.E, [&](auto g, auto v) { run(g, v, std::integral_constant<int, 8>{}); });
+    else if (r.k <= 8)
+      with_layout<false>(r.E, [&](auto g, auto v) { run(g, v, std::integral_constant<int, 8>{}); });
+    else
+      with_layout<false>(r.E, [&](auto g, auto v) { run(g, v, std::integral_constant<int, 16>{}); });
   };
   with_types(r.logits_fp32, r.sigmoid, go);
   MOK_HIP_TRY(hipGetLastError());
@@ -738,7 +754,7 @@ hipError_t launch_router_bwd(const RouterBwdArgs& r, int cus, hipStream_t s) {
   auto go = [&](auto tag, auto sig) {
     using LT = decltype(tag);
     constexpr bool SIG = decltype(sig)::value;
-    with_layout(r.E, [&](auto g, auto v) {
+    with_layout<false>(r.E, [&](auto g, auto v) {
       constexpr int G = decltype(g)::value, V = decltype(v)::value;
       const int64_t gpb = 256 / G;
       const int grid = (int)std::min<int64_t>((r.T + gpb - 1) / gpb, (int64_t)cus * 8);

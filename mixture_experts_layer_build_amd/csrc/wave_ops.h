@@ -30,9 +30,27 @@ __device__ __forceinline__ float dpp_movf(float x) {
   return u2f((uint32_t)dpp_mov<CTRL>((int)f2u(x)));
 }
 
+constexpr int kMirror = 0x140, kHalfMirror = 0x141;                        // row_mirror, row_half_mirror
 constexpr int kRor1 = 0x121, kRor2 = 0x122, kRor4 = 0x124, kRor8 = 0x128;  // row_ror:n
 constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E;                          // quad_perm:[1,0,3,2], [2,3,0,1]
 constexpr int kQuadLane0 = 0x00, kQuadLane1 = 0x55;                        // quad_perm:[0,0,0,0], [1,1,1,1]
+
+// Over 8 consecutive lanes.
+__device__ __forceinline__ float octet_sum(float x) {
+  x += dpp_movf<kQuadXor1>(x);
+  x += dpp_movf<kQuadXor2>(x);
+  return x + dpp_movf<kHalfMirror>(x);
+}
+__device__ __forceinline__ float octet_maxf(float x) {
+  x = __builtin_fmaxf(x, dpp_movf<kQuadXor1>(x));
+  x = __builtin_fmaxf(x, dpp_movf<kQuadXor2>(x));
+  return __builtin_fmaxf(x, dpp_movf<kHalfMirror>(x));
+}
+__device__ __forceinline__ int octet_min(int x) {
+  x = min(x, dpp_mov<kQuadXor1>(x));
+  x = min(x, dpp_mov<kQuadXor2>(x));
+  return min(x, dpp_mov<kHalfMirror>(x));
+}
 
 // x, as a value the compiler knows nothing of.
 __device__ __forceinline__ int opaque(int x) {
@@ -100,7 +118,7 @@ __device__ __forceinline__ void wave_lds_fence() {
 __device__ __forceinline__ uint32_t quad_max(uint32_t x);
 __device__ __forceinline__ uint32_t octet_max(uint32_t x) {
   x = quad_max(x);
-  return max(x, (uint32_t)dpp_mov<0x141>((int)x));  // row_half_mirror: the other four
+  return max(x, (uint32_t)dpp_mov<kHalfMirror>((int)x));
 }
 
 // Largest value of 4 consecutive lanes (a 32-element block at 8 per lane).

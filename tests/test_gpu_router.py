@@ -99,6 +99,38 @@ def test_token_counts(T, dtype):
     check(l, 4, mask=mask, dtype=dtype)
 
 
+@pytest.mark.parametrize("E", [5, 60, 64, 100, 128])
+@pytest.mark.parametrize("scoring,renorm", [("softmax", True), ("sigmoid", False)])
+def test_many_tokens_choose_as_few_do(E, scoring, renorm):
+    """Many tokens may take another layout than few: each part of a large
+    batch, alone, must give the same choices and the same scores within the
+    tolerance, on logits with ties, a mask and a bias."""
+    rng = np.random.default_rng(E)
+    T, k = 40001, min(E, 8)
+    l = (np.round(rng.standard_normal((T, E)) * 64) / 64).astype(np.float32)
+    l[7] = -np.inf
+    l[8, 1] = np.nan
+    lt, bias = dev(l), dev((np.round(rng.standard_normal(E)) / 4).astype(np.float32))
+    mask = dev((rng.random(T) < 0.9).astype(np.uint8))
+    for dtype, b in ((F32, bias), (F32, None), (BF, None)):
+        how = dict(scoring=scoring, renormalize=renorm, bias=b)
+        x = lt.to(dtype)
+        x[8] = 0 if b is not None else x[8]
+        print(f"router {T} x {E} {dtype}", flush=True)
+        w, ids, counts, losses = mok.router_topk(x, k, token_mask=mask, losses=True, **how)
+        assert torch.equal(ids, mok.router_topk(x, k, token_mask=mask, **how)[1])
+        cut = [0, 13, 20000, T - 9, T]
+        for lo, hi in zip(cut[:1] + cut[2:3] + cut[3:4], [13, 20011, T]):
+            w2, ids2 = mok.router_topk(x[lo:hi].contiguous(), k, token_mask=mask[lo:hi].contiguous(), **how)
+            assert torch.equal(ids[lo:hi], ids2)
+            np.testing.assert_allclose(w[lo:hi].cpu().numpy(), w2.cpu().numpy(), rtol=2.0 ** -17)
+        chosen = torch.bincount(ids[ids >= 0], minlength=E)
+        assert torch.equal(counts[:E].long(), chosen)
+        r = oops.router(x[:200].float().cpu().numpy(), k, scoring, renorm, bias=None if b is None else b.cpu().numpy(),
+                        mask=mask[:200].cpu().numpy())
+        np.testing.assert_array_equal(ids[:200].cpu().numpy(), r[1])
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("E", [48, 320])
 def test_selection_bias_and_ties(E, dtype):
