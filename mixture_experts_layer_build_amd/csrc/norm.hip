@@ -4,9 +4,11 @@
 //   backward  xh = s * rstd, g = dy * w:  ds = rstd * (g - xh * mean(g * xh)) + dsum,
 //             dw = sum over rows of dy * xh
 //
-// Everything between a load and a store is fp32. The sum is stored in the
-// residual's type, and y is computed from the fp32 sum before that rounding,
-// so each output is rounded once. The backward starts from the stored sum.
+// Everything between a load and a store is fp32, but for the row's statistics:
+// the threads' sums of squares are added, and rstd is found, in fp64 (a few
+// instructions a row, no slower). The sum is stored in the residual's type,
+// and y is computed from the fp32 sum before that rounding, so each output is
+// rounded once. The backward starts from the stored sum.
 //
 // Both directions are bound by HBM: an element costs a few flops and 4 to 14
 // bytes. A row is held in registers between its statistics and its output,
@@ -22,8 +24,8 @@
 // adds the partials in a fixed order (no atomics: the same bits on every
 // run).
 //
-// Measured: forward 8192 x 2048 bf16 with residual 24 us (5.6 TB/s), 16384 x
-// 7168 166 us, to MXFP8 139 us (6.0 TB/s); backward 16384 x 7168 with d_sum
+// Measured: forward 8192 x 2048 bf16 with residual 23.4 us (5.7 TB/s), 16384 x
+// 7168 160 us, to MXFP8 134 us (6.2 TB/s); backward 16384 x 7168 with d_sum
 // 164 us (5.75 TB/s), 8192 x 2048 27 us. A copy of 4 GiB runs at 4.6 TB/s.
 #include <algorithm>
 #include <type_traits>
@@ -56,20 +58,32 @@ __device__ __forceinline__ void store_mxfp8(const float (&y)[W], uint8_t* codes,
 // Sum over the TPR threads of a row. Waves join through LDS, in two sets of
 // slots used in turn, so that one barrier per row is enough: a set is
 // written again only after the barrier that follows its last read.
-template <int TPR>
-__device__ __forceinline__ float row_threads_sum(float x, float* slots, int group, int parity) {
+template <int TPR, typename T>
+__device__ __forceinline__ T row_threads_sum(T x, T* slots, int group, int parity) {
   x = wave_sum(x);
   if constexpr (TPR == 64) return x;
   constexpr int W = TPR / 64;
-  float* mine = slots + (parity * (int)(blockDim.x / TPR) + group) * W;
+  T* mine = slots + (parity * (int)(blockDim.x / TPR) + group) * W;
   const int wave = (int)(threadIdx.x % TPR) / 64;
   if (lane_id() == 0) mine[wave] = x;
   __syncthreads();
-  float s = 0.f;
+  T s = 0;
 #pragma unroll
   for (int i = 0; i < W; ++i) s += mine[i];
   return s;
 }
+
+#if defined(__HIP_DEVICE_COMPILE__)
+// (sum of squares / cols + eps)^-1/2 to fp64's precision or nearly: the
+// hardware's estimate and one Newton step.
+__device__ __forceinline__ double row_rstd(double ss, int cols, float eps) {
+  const double x = ss / (double)cols + (double)eps;
+  const double r = __builtin_amdgcn_rsq(x);
+  return x > 0.0 && x < __builtin_inf() ? r * (1.5 - 0.5 * x * r * r) : r;
+}
+#else
+__device__ double row_rstd(double ss, int cols, float eps);  // device only
+#endif
 
 struct NormFwd {
   const void *x, *residual, *w;
@@ -98,7 +112,7 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
   using R = typename std::conditional<kRes, RT, float>::type;
   constexpr int W = lane_width<XT, RT>;
   constexpr int RPB = BLOCK / TPR;
-  __shared__ float slots[2 * RPB * (TPR / 64)];
+  __shared__ double slots[2 * RPB * (TPR / 64)];
   // (a row's waves are whole waves, so its number and addresses are scalars)
   const uint32_t t = threadIdx.x % TPR;
   const int group = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
@@ -116,7 +130,6 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
         load_lane<false>((const uint16_t*)a.w + c * W, w[i]);
     }
   }
-  const float inv_cols = 1.0f / (float)a.cols;
   int parity = 0;
   // every thread of the workgroup makes the same number of turns (barrier inside)
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB, parity ^= 1) {
@@ -146,8 +159,8 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int q = 0; q < W; ++q) ss = __builtin_fmaf(v[i][q], v[i][q], ss);
-    ss = row_threads_sum<TPR>(ss, slots, group, parity);
-    const float rstd = 1.0f / __builtin_sqrtf(ss * inv_cols + a.eps);
+    const double exact = row_rstd(row_threads_sum<TPR>((double)ss, slots, group, parity), a.cols, a.eps);
+    const float rstd = (float)exact, rest = (float)(exact - (double)rstd);
     if (!live) continue;
     if (a.rstd && t == 0) a.rstd[row] = rstd;
     const int64_t out = row * a.cols;
@@ -157,8 +170,19 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
       if (c >= nchunk) continue;
       if constexpr (kRes) store_once((R*)a.sum + out + c * W, v[i]);
       float y[W];
+      if (a.codes) {
+        // y rounded once to fp32, so that as few codes as can be fall on the
+        // wrong side of a boundary: rstd and rstd * w in two parts each
 #pragma unroll
-      for (int q = 0; q < W; ++q) y[q] = v[i][q] * rstd * w[i][q];
+        for (int q = 0; q < W; ++q) {
+          const float hi = w[i][q] * rstd;
+          const float lo = __builtin_fmaf(w[i][q], rstd, -hi) + w[i][q] * rest;
+          y[q] = __builtin_fmaf(v[i][q], hi, v[i][q] * lo);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < W; ++q) y[q] = v[i][q] * rstd * w[i][q];
+      }
       if (a.y) store_once(a.y + out + c * W, y);
       if (a.codes) store_mxfp8(y, a.codes + out + c * W, a.scale + (out >> 5) + c / (32 / W), t % (32 / W) == 0);
     }
@@ -171,8 +195,7 @@ template <typename XT, typename RT>
 __global__ void __launch_bounds__(256) rms_norm_any(NormFwd a) {
   constexpr bool kRes = !std::is_void<RT>::value;
   using R = typename std::conditional<kRes, RT, float>::type;
-  __shared__ float slots[2 * 4];
-  const float inv_cols = 1.0f / (float)a.cols;
+  __shared__ double slots[2 * 4];
   int parity = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, parity ^= 1) {
     const XT* x = (const XT*)a.x + row * a.ld_x;
@@ -183,8 +206,7 @@ __global__ void __launch_bounds__(256) rms_norm_any(NormFwd a) {
       if constexpr (kRes) v += load1(res + c);
       ss = __builtin_fmaf(v, v, ss);
     }
-    ss = row_threads_sum<256>(ss, slots, 0, parity);
-    const float rstd = 1.0f / __builtin_sqrtf(ss * inv_cols + a.eps);
+    const float rstd = (float)row_rstd(row_threads_sum<256>((double)ss, slots, 0, parity), a.cols, a.eps);
     if (a.rstd && threadIdx.x == 0) a.rstd[row] = rstd;
     for (int c = threadIdx.x; c < a.cols; c += 256) {
       float v = load1(x + c);

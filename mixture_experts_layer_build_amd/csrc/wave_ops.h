@@ -94,6 +94,25 @@ __device__ __forceinline__ float wave_sum(float x) {
   x = row_sum(x);
   return (lane_valuef(x, 0) + lane_valuef(x, 16)) + (lane_valuef(x, 32) + lane_valuef(x, 48));
 }
+// The same in fp64: a sum whose last additions should not round.
+template <int CTRL>
+__device__ __forceinline__ double dpp_movd(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)dpp_mov<CTRL>((int)(uint32_t)u), hi = (uint32_t)dpp_mov<CTRL>((int)(u >> 32));
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double lane_valued(double x, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = (uint32_t)lane_value((int)(uint32_t)u, l), hi = (uint32_t)lane_value((int)(u >> 32), l);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double x) {
+  x += dpp_movd<kRor8>(x);
+  x += dpp_movd<kRor4>(x);
+  x += dpp_movd<kRor2>(x);
+  x += dpp_movd<kRor1>(x);
+  return (lane_valued(x, 0) + lane_valued(x, 16)) + (lane_valued(x, 32) + lane_valued(x, 48));
+}
 __device__ __forceinline__ float wave_max(float x) {
   x = row_max(x);
   return __builtin_fmaxf(__builtin_fmaxf(lane_valuef(x, 0), lane_valuef(x, 16)),
