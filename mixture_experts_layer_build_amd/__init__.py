@@ -266,6 +266,14 @@ def forward_mxfp8(ws: Workspace, schedule: torch.Tensor, x_codes: torch.Tensor, 
         raise ValueError("x_codes and x_scale must be uint8 and router_weights fp32")
     if x_codes.dim() != 2 or x_codes.shape[1] != H or x_scale.shape != (x_codes.shape[0], H // 32):
         raise ValueError("x_codes must be [T, hidden] and x_scale [T, hidden/32]")
+    T = x_codes.shape[0]
+    if router_weights.numel() != T * ws.cfg.topk or T > ws.cfg.max_tokens:
+        raise ValueError("router_weights must be [T, topk], with T at most max_tokens")
+    if out is not None and (out.dtype != torch.bfloat16 or out.shape != x_codes.shape):
+        raise ValueError("out must be bf16 [T, hidden]")
+    for t in (schedule, x_codes, x_scale, router_weights, out):
+        if t is not None and t.get_device() != ws.device:
+            raise ValueError(f"every tensor must be on the workspace's GPU {ws.device}, got {t.device}")
     if out is None:
         out = torch.empty(x_codes.shape, dtype=torch.bfloat16, device=x_codes.device)
     ws_w = _weights(weights)

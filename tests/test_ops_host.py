@@ -171,3 +171,17 @@ def test_a_loaded_state_keeps_its_types():
     assert got["exp_avg_sq_scale"].dtype == torch.uint8 and got["master"].dtype == torch.float32
     got["exp_avg"].zero_()  # a copy, not the saved tensor
     assert bool((st["exp_avg"] == 200).all())
+
+
+def test_forward_mxfp8_checks_its_tensors_before_it_calls():
+    class Ws:  # (what the checks read of a workspace)
+        cfg = mok.MoKConfig(hidden=64, intermediate=128, num_experts=4, topk=2, max_tokens=8)
+        device, handle = 0, None
+
+    def call(T=4, rw=None, out=None):
+        return mok.forward_mxfp8(Ws, torch.zeros(16, dtype=torch.uint8), torch.zeros(T, 64, dtype=torch.uint8),
+                                 torch.zeros(T, 2, dtype=torch.uint8), torch.zeros(rw or T, 2), {}, out=out)
+    for match, kw in (("topk", dict(rw=3)), ("max_tokens", dict(T=9)), ("out", dict(out=torch.zeros(4, 64))),
+                      ("out", dict(out=torch.zeros(3, 64, dtype=torch.bfloat16))), ("GPU 0", dict())):
+        with pytest.raises(ValueError, match=match):
+            call(**kw)
