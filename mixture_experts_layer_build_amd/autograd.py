@@ -366,7 +366,8 @@ class MoKRouter(torch.nn.Module):
         self.weight.copy_(torch.randn(self.weight.shape, generator=generator, dtype=torch.float32).mul_(init_std))
 
     def forward(self, x, token_mask=None):
-        logits = torch.nn.functional.linear(x.float(), self.weight.float())
+        with torch.autocast(x.device.type, enabled=False):  # (it would make the product bf16)
+            logits = torch.nn.functional.linear(x.float(), self.weight.float())
         bias = None if self.bias is None else self.bias.float()
         return router_topk(logits, self.topk, scoring=self.scoring, renormalize=self.renormalize, scale=self.scale,
                            bias=bias, token_mask=token_mask, losses=self.losses)

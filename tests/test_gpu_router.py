@@ -285,3 +285,14 @@ def test_replayed_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, step())), i
+
+
+def test_module_under_autocast_keeps_its_logits_in_fp32():
+    torch.manual_seed(1)
+    m = MoKRouter(64, 16, 4, device="cuda")
+    m.init_weights(0.5)
+    x = torch.randn(33, 64, device="cuda").bfloat16()
+    w, ids = m(x)
+    with torch.autocast("cuda", dtype=torch.bfloat16):
+        w2, ids2 = m(x)
+    assert torch.equal(ids, ids2) and torch.equal(w, w2)
