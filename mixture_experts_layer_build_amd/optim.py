@@ -70,8 +70,7 @@ class MoKAdamW(torch.optim.Optimizer):
                 st = self.state[p]
                 if not st:
                     st.update(self._init_state(p, group))
-                st["step"] += 1
-                key = (p.device, p.dtype, p.grad.dtype, "master" in st, st["step"])
+                key = (p.device, p.dtype, p.grad.dtype, "master" in st, st["step"] + 1)
                 kinds.setdefault(key, []).append((p, p.grad.contiguous(), st))
             for (_, _, _, master, step), items in kinds.items():
                 states = [st for _, _, st in items]
@@ -82,6 +81,8 @@ class MoKAdamW(torch.optim.Optimizer):
                                lr=float(group["lr"]), betas=group["betas"], eps=group["eps"],
                                weight_decay=group["weight_decay"], grad_scale=grad_scale,
                                seed=step * 0xD1B54A35 + call * 0x85EBCA77)
+                for st in states:  # (only now: a refused call leaves its tensors and their step as they were)
+                    st["step"] = step
                 call += 1
         return loss
 

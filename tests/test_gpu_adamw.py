@@ -305,3 +305,14 @@ def test_optimizer_refuses_capture():
             opt.step()
     torch.cuda.synchronize()
     opt.step()
+
+
+def test_a_refused_step_is_not_counted():
+    p = torch.nn.Parameter(torch.ones(64, device="cuda"))
+    p.grad = torch.ones(64, device="cuda")
+    opt = MoKAdamW([p])
+    with pytest.raises(ValueError):
+        opt.step(grad_scale=torch.ones(2, device="cuda"))
+    assert opt.state[p]["step"] == 0 and torch.equal(p.detach(), torch.ones(64, device="cuda"))
+    opt.step()
+    assert opt.state[p]["step"] == 1

@@ -185,3 +185,12 @@ def test_forward_mxfp8_checks_its_tensors_before_it_calls():
                       ("out", dict(out=torch.zeros(3, 64, dtype=torch.bfloat16))), ("GPU 0", dict())):
         with pytest.raises(ValueError, match=match):
             call(**kw)
+
+
+def test_a_refused_step_is_not_counted():
+    p = torch.nn.Parameter(torch.zeros(4))
+    p.grad = torch.ones(4)
+    opt = MoKAdamW([p])
+    with pytest.raises(ValueError, match="CUDA"):
+        opt.step()
+    assert opt.state[p]["step"] == 0
