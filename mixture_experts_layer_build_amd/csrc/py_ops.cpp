@@ -323,7 +323,11 @@ struct Items {
 struct Step {
   int n = 0;
   std::vector<int64_t> numels;
-  std::vector<void*> written;  // addresses of what the step writes
+  struct Bytes {
+    uintptr_t begin, end;
+    bool written;
+  };
+  std::vector<Bytes> touched;  // what the step reads and writes
   const Tensor* first = nullptr;
 
   // Adds one tensor of a list: all of one type of `types`, dense, on one GPU.
@@ -337,7 +341,7 @@ struct Step {
     if (!t.is_contiguous()) bad("every tensor of " + name + " must be contiguous");
     void* p = t.data_ptr();
     to->push_back(p);
-    if (writes && numel > 0) written.push_back(p);
+    if (numel > 0) touched.push_back({(uintptr_t)p, (uintptr_t)p + numel * t.element_size(), writes});
   }
   void length(const char* name, const Items& l) const {
     if (l.size() != n)
@@ -361,6 +365,9 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t nargs) {
   constexpr auto kNone = at::ScalarType::Undefined;
   at::ScalarType pt = kNone, gt = kNone, wt = kNone, mt[2] = {kNone, kNone}, st[2] = {kNone, kNone};
   std::vector<void*> pp, pg, pw, pm[2], psc[2];
+  for (auto* v : {&pp, &pg, &pw, &pm[0], &pm[1], &psc[0], &psc[1]}) v->reserve(s.n);
+  s.numels.reserve(s.n);
+  s.touched.reserve((size_t)s.n * 7);
   for (int i = 0; i < s.n; ++i) {
     const Tensor& p = tensor("params", params[i]);
     const int64_t n = p.numel();
@@ -385,9 +392,15 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t nargs) {
             (n + 31) / 32, &st[k], &psc[k], true);
     }
   }
-  std::sort(s.written.begin(), s.written.end());
-  if (std::adjacent_find(s.written.begin(), s.written.end()) != s.written.end())
-    bad("a tensor that the step writes is given twice");
+  std::sort(s.touched.begin(), s.touched.end(),
+            [](const Step::Bytes& x, const Step::Bytes& y) { return x.begin < y.begin; });
+  uintptr_t any_end = 0, written_end = 0;
+  for (const Step::Bytes& b : s.touched) {
+    if (b.begin < (b.written ? any_end : written_end))
+      bad("a tensor that the step writes is given twice, or overlaps another");
+    any_end = std::max(any_end, b.end);
+    if (b.written) written_end = std::max(written_end, b.end);
+  }
   const Tensor* scale = maybe("grad_scale", a[11]);
   if (scale) {
     check("grad_scale", *scale, *s.first, {kF32});

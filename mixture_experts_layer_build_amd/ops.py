@@ -119,8 +119,8 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, masters=None, *, step: int,
     for 8-bit states pairs (codes, scale): E4M3 codes [numel] of m (of
     sqrt(v)) and E8M0 scales [ceil(numel/32)], zeros at the start. grad_scale:
     a device fp32 tensor of one element that multiplies every gradient. seed
-    (default: the step) chooses the 8-bit states' roundings. No two tensors
-    may overlap."""
+    (default: the step) chooses the 8-bit states' roundings. What the step
+    writes may overlap no other tensor of the call."""
     if len(params) == 0 and not (len(grads) or len(exp_avgs) or len(exp_avg_sqs) or masters):
         return
     if len(params) == 0:

@@ -316,3 +316,16 @@ def test_a_refused_step_is_not_counted():
     assert opt.state[p]["step"] == 0 and torch.equal(p.detach(), torch.ones(64, device="cuda"))
     opt.step()
     assert opt.state[p]["step"] == 1
+
+
+def test_overlapping_tensors_are_refused():
+    buf = torch.zeros(400, device="cuda")
+    p, g, m, v = (torch.zeros(64, device="cuda") for _ in range(4))
+    for args in (([buf[:64]], [g], [buf[32:96]], [v]), ([p], [buf[:64]], [m], [buf[63:127]]),
+                 ([buf[:64], buf[16:80]], [g, g], [m, buf[100:164]], [v, buf[200:264]]),
+                 ([buf[:300], buf[8:72]], [torch.zeros(300, device="cuda"), g], [torch.zeros(300, device="cuda"), m],
+                  [torch.zeros(300, device="cuda"), v])):
+        with pytest.raises(ValueError, match="overlaps"):
+            mok.adamw_step(*args, step=1, lr=1e-3)
+    # neighbours in one buffer, and one gradient for two tensors, are no overlap
+    mok.adamw_step([buf[:64], buf[64:128]], [g, g], [buf[128:192], m], [buf[192:256], v], step=1, lr=1e-3)
