@@ -43,8 +43,11 @@ def _load():
 def _call(name: str, first: torch.Tensor, *args):
     """One call on the GPU of `first` and its current stream."""
     f = getattr(_host or _load(), name)
-    index = first.get_device()
-    if index < 0:  # not on a GPU: the call refuses it
+    try:
+        index = first.get_device()
+    except AttributeError:
+        index = -1
+    if index < 0:  # no tensor, or not on a GPU: the call refuses it
         out = f(*args, 0)
     elif index == torch._C._cuda_getDevice():
         out = f(*args, torch._C._cuda_getCurrentRawStream(index))

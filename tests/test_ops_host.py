@@ -194,3 +194,12 @@ def test_a_refused_step_is_not_counted():
     with pytest.raises(ValueError, match="CUDA"):
         opt.step()
     assert opt.state[p]["step"] == 0
+
+
+def test_what_is_no_tensor_is_refused():
+    w = torch.ones(64, dtype=torch.bfloat16)
+    for call in (lambda: mok.rms_norm(None, w), lambda: mok.rms_norm_mxfp8([1.0], w), lambda: mok.router_topk(None, 2),
+                 lambda: mok.rms_norm_backward(None, w, w, w), lambda: mok.router_topk_backward(w, None, w),
+                 lambda: mok.adamw_step([None], [w], [w], [w], step=1, lr=1e-3)):
+        with pytest.raises(ValueError, match="must be a tensor"):
+            call()
