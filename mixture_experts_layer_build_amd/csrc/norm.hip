@@ -17,7 +17,7 @@
 // columns, whose reduction needs no barrier, and to 256 or 512 threads
 // above (a wave would need more registers than keep enough loads in
 // flight). The backward holds three streams and dw, so a lane takes at most
-// two chunks of a row (with four it needed 166 registers or spilled: 246 us
+// two such chunks of a row (with four it needed 166 registers or spilled: 246 us
 // against 176 at 16384 x 7168). The grid is persistent: the weights stay in
 // registers from row to row, and the backward adds dw up in registers over a
 // workgroup's rows, writes one partial row per workgroup, and a second launch
@@ -26,7 +26,7 @@
 //
 // Measured: forward 8192 x 2048 bf16 with residual 23.4 us (5.7 TB/s), 16384 x
 // 7168 160 us, to MXFP8 134 us (6.2 TB/s); backward 16384 x 7168 with d_sum
-// 164 us (5.75 TB/s), 8192 x 2048 27 us. A copy of 4 GiB runs at 4.6 TB/s.
+// 162 us (5.8 TB/s), of fp32 rows 285 us, 8192 x 2048 27 us. A copy of 4 GiB runs at 4.6 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -235,25 +235,37 @@ struct NormBwd {
 // A row's dy, s and d_sum stay as they were loaded and are converted twice,
 // in the pass before the row's sum and in the one behind it: in fp32 they
 // would take twice the registers, and half the waves would hide the loads.
+// fp32 rows take 4 elements per lane, as in the forward, and go past the caches
+// where the launch exceeds them (16384 x 7168 with d_sum 305 -> 285 us, without
+// 216 -> 204; 8192 x 4096 90 -> 84; 4096 x 512, which the cache holds, 9.8 ->
+// 10.1).
+template <typename ST>
+constexpr int bwd_width = std::is_same<ST, float>::value ? 4 : 8;
+__device__ __forceinline__ void store_floats(float* p, const float (&v)[8]) { store8(p, v); }
+__device__ __forceinline__ void store_floats(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+
 template <typename ST, typename WT, bool DSUM, bool STREAM, int BLOCK, int TPR, int NV>
 __global__ void __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(4)))
 rms_norm_bwd_rows(NormBwd a) {
+  constexpr int W = bwd_width<ST>;
   constexpr int RPB = BLOCK / TPR;
   static_assert(BLOCK % TPR == 0, "whole rows");
   __shared__ float slots[2 * RPB * (TPR / 64)];
-  __shared__ float dw_lds[RPB > 1 ? TPR * NV * 8 : 1];
+  __shared__ float dw_lds[RPB > 1 ? TPR * NV * W : 1];
   // (a row's waves are whole waves, so its number and addresses are scalars)
   const uint32_t t = threadIdx.x % TPR;
   const int group = __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPR);
-  const uint32_t nchunk = (uint32_t)a.cols >> 3;
-  Raw8<WT> w[NV];
-  float dw[NV][8];
+  const uint32_t nchunk = (uint32_t)a.cols / W;
+  Raw<WT, W> w[NV];
+  float dw[NV][W];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const uint32_t c = t + i * TPR;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) dw[i][q] = 0.f;
-    if (c < nchunk) w[i].template load<false>((const WT*)a.w + c * 8);
+    for (int q = 0; q < W; ++q) dw[i][q] = 0.f;
+    if (c < nchunk) w[i].template load<false>((const WT*)a.w + c * W);
   }
   const float inv_cols = 1.0f / (float)a.cols;
   int parity = 0;
@@ -266,15 +278,15 @@ rms_norm_bwd_rows(NormBwd a) {
     const ST* pd = (const ST*)a.dsum + row * a.ld_dsum;
     ST* pds = (ST*)a.ds + row * a.cols;
     uint16_t* pdx = a.dx + row * a.cols;
-    Raw8<uint16_t> dy[NV];
-    Raw8<ST> s[NV], dsum[DSUM ? NV : 1];
+    Raw<uint16_t, W> dy[NV];
+    Raw<ST, W> s[NV], dsum[DSUM ? NV : 1];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const uint32_t c = t + i * TPR;
       if (live && c < nchunk) {
-        dy[i].template load<STREAM>(pdy + c * 8);
-        s[i].template load<STREAM>(ps + c * 8);
-        if constexpr (DSUM) dsum[i].template load<STREAM>(pd + c * 8);
+        dy[i].template load<STREAM>(pdy + c * W);
+        s[i].template load<STREAM>(ps + c * W);
+        if constexpr (DSUM) dsum[i].template load<STREAM>(pd + c * W);
       }
     }
     float along = 0.f;
@@ -282,7 +294,7 @@ rms_norm_bwd_rows(NormBwd a) {
     for (int i = 0; i < NV; ++i) {
       w[i].fresh();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < W / 2; ++j) {
         float d[2], x[2], wv[2];
         dy[i].pair(j, d[0], d[1]);
         s[i].pair(j, x[0], x[1]);
@@ -304,10 +316,10 @@ rms_norm_bwd_rows(NormBwd a) {
       w[i].fresh();
       dy[i].fresh();
       s[i].fresh();
-      Raw8<ST> ds;
-      Raw8<uint16_t> narrow;
+      Raw<ST, W> ds;
+      Raw<uint16_t, W> narrow;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < W / 2; ++j) {
         float d[2], x[2], wv[2], more[2] = {0.f, 0.f};
         dy[i].pair(j, d[0], d[1]);
         s[i].pair(j, x[0], x[1]);
@@ -318,8 +330,8 @@ rms_norm_bwd_rows(NormBwd a) {
         ds.set(j, d[0], d[1]);
         narrow.set(j, d[0], d[1]);
       }
-      ds.template store<STREAM>(pds + c * 8);
-      if (a.dx) narrow.template store<STREAM>(pdx + c * 8);
+      ds.template store<STREAM>(pds + c * W);
+      if (a.dx) narrow.template store<STREAM>(pdx + c * W);
     }
   }
   // the workgroup's partial row: its row groups one after the other
@@ -332,14 +344,14 @@ rms_norm_bwd_rows(NormBwd a) {
       if (c >= nchunk) continue;
       if constexpr (RPB > 1) {
         if (g > 0) {
-          float have[8];
-          load8(dw_lds + c * 8, have);
+          float have[W];
+          load_lane<false>(dw_lds + c * W, have);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) dw[i][q] += have[q];
+          for (int q = 0; q < W; ++q) dw[i][q] += have[q];
         }
-        if (g < RPB - 1) store8(dw_lds + c * 8, dw[i]);
+        if (g < RPB - 1) store_floats(dw_lds + c * W, dw[i]);
       }
-      if (g == RPB - 1) store8(a.dw_part + (int64_t)blockIdx.x * a.cols + c * 8, dw[i]);
+      if (g == RPB - 1) store_floats(a.dw_part + (int64_t)blockIdx.x * a.cols + c * W, dw[i]);
     }
   }
 }
@@ -476,12 +488,13 @@ int run_bwd(const NormBwd& a, bool vec, hipStream_t s) {
     rms_norm_bwd_any<ST><<<grid(1), 256, 0, s>>>(a);
     return grid(1);
   }
-  if (c <= 512) return go(integral_constant<int, 512>{}, integral_constant<int, 64>{}, integral_constant<int, 1>{});
-  if (c <= 1024) return go(integral_constant<int, 512>{}, integral_constant<int, 64>{}, integral_constant<int, 2>{});
-  if (c <= 2048) return go(integral_constant<int, 512>{}, integral_constant<int, 256>{}, integral_constant<int, 1>{});
-  if (c <= 4096) return go(integral_constant<int, 512>{}, integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  if (c <= 8192) return go(integral_constant<int, 512>{}, integral_constant<int, 512>{}, integral_constant<int, 2>{});
-  return go(integral_constant<int, 1024>{}, integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+  constexpr int M = 8 / bwd_width<ST>;  // twice the chunks where a lane takes half
+  if (c <= 512) return go(integral_constant<int, 512>{}, integral_constant<int, 64>{}, integral_constant<int, 1 * M>{});
+  if (c <= 1024) return go(integral_constant<int, 512>{}, integral_constant<int, 64>{}, integral_constant<int, 2 * M>{});
+  if (c <= 2048) return go(integral_constant<int, 512>{}, integral_constant<int, 256>{}, integral_constant<int, 1 * M>{});
+  if (c <= 4096) return go(integral_constant<int, 512>{}, integral_constant<int, 256>{}, integral_constant<int, 2 * M>{});
+  if (c <= 8192) return go(integral_constant<int, 512>{}, integral_constant<int, 512>{}, integral_constant<int, 2 * M>{});
+  return go(integral_constant<int, 1024>{}, integral_constant<int, 1024>{}, integral_constant<int, 2 * M>{});
 }
 
 }  // namespace

@@ -230,13 +230,14 @@ __device__ __forceinline__ void store_once(float* p, const float (&v)[4]) {
   __builtin_nontemporal_store((f32x4nt){v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4nt*>(p));
 }
 
-// 8 elements as they lie in memory: 4 registers of bf16, 8 of fp32. fresh()
-// makes the compiler forget what the registers were converted to, so that a
-// later pair() converts again instead of keeping the fp32 values alive.
-template <typename T>
-struct Raw8;
+// A lane's elements as they lie in memory, 16 bytes of the wider type beside
+// them: 8 of bf16, or 4 with fp32 rows. fresh() makes the compiler forget what
+// the registers were converted to, so that a later pair() converts again
+// instead of keeping the fp32 values alive.
+template <typename T, int W>
+struct Raw;
 template <>
-struct Raw8<uint16_t> {
+struct Raw<uint16_t, 8> {
   uint4 r = make_uint4(0, 0, 0, 0);
   template <bool STREAM>
   __device__ __forceinline__ void load(const uint16_t* p) {
@@ -264,14 +265,61 @@ struct Raw8<uint16_t> {
   }
 };
 template <>
-struct Raw8<float> {
-  float v_[8] = {};
+struct Raw<uint16_t, 4> {
+  uint32_t r[2] = {};
   template <bool STREAM>
-  __device__ __forceinline__ void load(const float* p) { load8(p, v_); }
-  __device__ __forceinline__ void pair(int j, float& a, float& b) const { a = v_[2 * j], b = v_[2 * j + 1]; }
-  __device__ __forceinline__ void set(int j, float a, float b) { v_[2 * j] = a, v_[2 * j + 1] = b; }
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    const u32x2nt* q = reinterpret_cast<const u32x2nt*>(p);
+    const u32x2nt x = STREAM ? __builtin_nontemporal_load(q) : *q;
+    r[0] = x[0], r[1] = x[1];
+  }
+  __device__ __forceinline__ void pair(int j, float& a, float& b) const {
+    a = u2f(r[j] << 16), b = u2f(r[j] & 0xFFFF0000u);
+  }
+  __device__ __forceinline__ void set(int j, float a, float b) { r[j] = pack_bf16x2(a, b); }
   template <bool STREAM>
-  __device__ __forceinline__ void store(float* p) const { store8(p, v_); }
+  __device__ __forceinline__ void store(uint16_t* p) const {
+    u32x2nt* q = reinterpret_cast<u32x2nt*>(p);
+    const u32x2nt x = {r[0], r[1]};
+    if (STREAM)
+      __builtin_nontemporal_store(x, q);
+    else
+      *q = x;
+  }
+  __device__ __forceinline__ void fresh() {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+v"(r[0]), "+v"(r[1]));
+#endif
+  }
+};
+template <int W>
+struct Raw<float, W> {
+  f32x4nt v_[W / 4] = {};
+  template <bool STREAM>
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      const f32x4nt* q = reinterpret_cast<const f32x4nt*>(p) + i;
+      v_[i] = STREAM && W == 4 ? __builtin_nontemporal_load(q) : *q;
+    }
+  }
+  __device__ __forceinline__ void pair(int j, float& a, float& b) const {
+    a = v_[j / 2][2 * (j & 1)], b = v_[j / 2][2 * (j & 1) + 1];
+  }
+  __device__ __forceinline__ void set(int j, float a, float b) {
+    v_[j / 2][2 * (j & 1)] = a, v_[j / 2][2 * (j & 1) + 1] = b;
+  }
+  template <bool STREAM>
+  __device__ __forceinline__ void store(float* p) const {
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i) {
+      f32x4nt* q = reinterpret_cast<f32x4nt*>(p) + i;
+      if (STREAM && W == 4)
+        __builtin_nontemporal_store(v_[i], q);
+      else
+        *q = v_[i];
+    }
+  }
   __device__ __forceinline__ void fresh() {}
 };
 __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
