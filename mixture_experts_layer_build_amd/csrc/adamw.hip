@@ -23,17 +23,24 @@
 // next update through undivided.
 //
 // Bound by HBM: 10 (bf16, 8 bits, no master) to 28 (bf16, fp32 states and
-// master) bytes per element. 8 elements per lane and turn, lanes on
-// consecutive chunks, a 32-element block in 4 neighbouring lanes. The
-// tensors' addresses travel in the kernel's arguments, up to 48 per launch:
-// nothing is copied to the device and nothing is kept between calls.
-// Non-temporal accesses, 1e8 elements: stores alone 573 -> 543 us with fp32
-// states and masters (loads too: 577); with 8 bits loads and stores 329 ->
-// 289 us (stores alone 320). The 8-bit update was bound by its instructions
+// master) bytes per element. 8 elements per lane and turn. With 8-bit states
+// they are neighbours, so that a 32-element block lies in 4 lanes; with fp32
+// states, whose 32 bytes per lane would touch every line and fill none, they
+// are two groups of 4, each of which fills lines with every instruction.
+// The tensors' addresses travel in the kernel's arguments, up to 48 per
+// launch: nothing is copied to the device and nothing is kept between calls.
+//
+// Stores go past the caches, and loads too (STREAM) where the tensors exceed
+// the last-level cache. Groups of 4, fp32 states: 1e8 elements with masters 515
+// us -> 517 with plain loads, 473 with loads past the caches; 1e7, which the
+// cache holds, 43 -> 41 and 46. 8 bits with masters: 1.6e7 elements 45.3 -> 41.5
+// with plain loads; 1e8 329 -> 289 with loads past the caches (before the
+// following). The 8-bit update was bound by its instructions
 // first: packed conversions, the hardware's root and no clamps took it from
 // 229 to 165 us (bf16, no master: 6.1 TB/s) and from 289 to 279 with a master.
-// With workgroups of one turn (TABLE): 514 us with fp32 states and masters
-// (5.4 TB/s), 260 us with 8 bits and masters (6.2 TB/s).
+//
+// Measured, 1e8 bf16 elements with masters: 473 us with fp32 states (5.9
+// TB/s), 260 us with 8 bits (6.2 TB/s).
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -138,6 +145,38 @@ __device__ __forceinline__ void put8(T* p, int64_t i, int64_t n, bool vec, const
       if (i + q < n) store1(p + i + q, v[q]);
   }
 }
+// The same for a lane's two groups of 4 elements, kHalf apart.
+constexpr int kHalf = kThreads * 4;
+template <bool NT, typename T>
+__device__ __forceinline__ void get4x2(const T* p, int64_t i, int64_t n, bool vec, float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h, i += kHalf) {
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (vec && i + 4 <= n) {
+      load_lane<NT>(p + i, x);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (i + q < n) x[q] = load1(p + i + q);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[4 * h + q] = x[q];
+  }
+}
+template <typename T>
+__device__ __forceinline__ void put4x2(T* p, int64_t i, int64_t n, bool vec, const float (&v)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h, i += kHalf) {
+    const float x[4] = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+    if (vec && i + 4 <= n) {
+      store_once(p + i, x);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (i + q < n) store1(p + i + q, x[q]);
+    }
+  }
+}
 __device__ __forceinline__ uint2 get_codes(const uint8_t* p, int64_t i, int64_t n, bool vec) {
   if (vec) return *reinterpret_cast<const uint2*>(p + i);
   uint32_t w[2] = {0, 0};
@@ -194,10 +233,11 @@ __device__ __forceinline__ float library_power(int k) {
 // TABLE: the workgroup makes a table of the powers first and takes four turns;
 // else it takes one turn and finds them as it goes. Workgroups of one turn
 // sweep memory as a closer front: 1e8 elements, bf16 with masters 280 -> 260
-// us, fp32 287 -> 274, and with fp32 states, which need no powers, 541 -> 514.
+// us, fp32 287 -> 274, and with fp32 states, which need no powers, 541 -> 514
+// (8 neighbouring elements per lane then).
 // Where an element moves only 10 bytes (8 bits, bf16, no masters) the powers'
 // instructions weigh more than that: 165 us with the table, 188 without.
-template <typename PT, bool MASTER, typename GT, bool S8, bool TABLE>
+template <typename PT, bool MASTER, typename GT, bool S8, bool TABLE, bool STREAM>
 __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
   // the workgroup's tensor: the last one that begins at or before it
   int lo = 0, hi = a.count - 1;
@@ -223,15 +263,27 @@ __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
   }
   // every thread makes the same number of turns (lanes of a block exchange maxima)
   for (int64_t i0 = begin; i0 < end; i0 += kTurn) {
-    const int64_t i = i0 + (int64_t)threadIdx.x * 8;
+    const int64_t i = i0 + (int64_t)threadIdx.x * (S8 ? 8 : 4);
     const bool in = i < n;
-    const bool vec = t.vec && i + 8 <= n;
+    const bool vec = t.vec && (!S8 || i + 8 <= n);
+    auto get = [&](auto* p, float(&v)[8]) {
+      if constexpr (S8)
+        get8<STREAM>(p, i, n, vec, v);
+      else
+        get4x2<STREAM>(p, i, n, vec, v);
+    };
+    auto put = [&](auto* p, const float(&v)[8]) {
+      if constexpr (!S8)
+        put4x2(p, i, n, vec, v);
+      else if (in)
+        put8(p, i, n, vec, v);
+    };
     float g[8], p[8], m[8], v[8];
-    get8<S8>((const GT*)t.g, i, n, vec, g);
+    get((const GT*)t.g, g);
     if constexpr (MASTER)
-      get8<S8>((const float*)t.master, i, n, vec, p);
+      get((const float*)t.master, p);
     else
-      get8<S8>((const PT*)t.p, i, n, vec, p);
+      get((const PT*)t.p, p);
     if constexpr (S8) {
       const uint2 cm = get_codes((const uint8_t*)t.m, i, n, vec), cv = get_codes((const uint8_t*)t.v, i, n, vec);
       const uint32_t sm = in ? t.ms[i >> 5] : 0u, sv = in ? t.vs[i >> 5] : 0u;
@@ -244,8 +296,8 @@ __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
         for (int q = 0; q < 8; ++q) m[q] = sm == 0xFFu ? __builtin_nanf("") : m[q], v[q] = sv == 0xFFu ? __builtin_nanf("") : v[q];
       }
     } else {
-      get8<false>((const float*)t.m, i, n, vec, m);
-      get8<false>((const float*)t.v, i, n, vec, v);
+      get((const float*)t.m, m);
+      get((const float*)t.v, v);
     }
     float r[8];
 #pragma unroll
@@ -257,10 +309,8 @@ __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
       const float inv = __builtin_amdgcn_rcpf(__builtin_fmaf(r[q], a.rbc2, a.eps));
       p[q] = __builtin_fmaf(-a.rate * m[q], inv, p[q] * a.keep);
     }
-    if (in) {
-      put8((PT*)t.p, i, n, vec, p);
-      if constexpr (MASTER) put8(t.master, i, n, vec, p);
-    }
+    put((PT*)t.p, p);
+    if constexpr (MASTER) put(t.master, p);
     if constexpr (S8) {
       // a moment that is not finite comes with a v that is not
       float mm = 0.f;
@@ -314,12 +364,15 @@ __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
           t.vs[i >> 5] = finite ? (uint8_t)(xr + 127) : 0xFFu;
         }
       }
-    } else if (in) {
-      put8((float*)t.m, i, n, vec, m);
-      put8((float*)t.v, i, n, vec, v);
+    } else {
+      put((float*)t.m, m);
+      put((float*)t.v, v);
     }
   }
 }
+
+// the last-level cache (what each side of it measured stands above)
+constexpr int64_t kCacheBytes = (int64_t)256 << 20;
 
 bool aligned(const void* p, uintptr_t to) { return (((uintptr_t)p) & (to - 1)) == 0; }
 
@@ -341,10 +394,17 @@ hipError_t launch_adamw(const mok_adamw& u, int cus, hipStream_t s) {
   const bool table =
       u.state_bits == 8 && !u.param_fp32 && !u.masters && total >= (int64_t)cus * 4 * 8 * kTurn;
   a.chunk = table ? 4 * kTurn : kTurn;
+  const int64_t each = (u.param_fp32 ? 4 : u.masters ? 6 : 2) + (u.grad_fp32 ? 4 : 2) + (u.state_bits == 8 ? 2 : 8);
+  const bool stream = total * each > kCacheBytes;
   auto launch = [&](int64_t blocks) -> hipError_t {
     auto go = [&](auto pt, auto master, auto gt, auto s8, auto tab) {
-      adamw_tensors<decltype(pt), decltype(master)::value, decltype(gt), decltype(s8)::value, decltype(tab)::value>
-          <<<(unsigned)blocks, kThreads, 0, s>>>(a);
+      using PT = decltype(pt);
+      using GT = decltype(gt);
+      constexpr bool M = decltype(master)::value, S8 = decltype(s8)::value, TABLE = decltype(tab)::value;
+      if (stream)
+        adamw_tensors<PT, M, GT, S8, TABLE, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+      else
+        adamw_tensors<PT, M, GT, S8, TABLE, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
     };
     const std::true_type yes;
     const std::false_type no;
