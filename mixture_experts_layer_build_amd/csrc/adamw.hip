@@ -371,9 +371,6 @@ __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
   }
 }
 
-// the last-level cache (what each side of it measured stands above)
-constexpr int64_t kCacheBytes = (int64_t)256 << 20;
-
 bool aligned(const void* p, uintptr_t to) { return (((uintptr_t)p) & (to - 1)) == 0; }
 
 }  // namespace

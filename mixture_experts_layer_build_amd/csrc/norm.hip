@@ -26,7 +26,8 @@
 //
 // Measured: forward 8192 x 2048 bf16 with residual 23.4 us (5.7 TB/s), 16384 x
 // 7168 160 us, to MXFP8 134 us (6.2 TB/s); backward 16384 x 7168 with d_sum
-// 162 us (5.8 TB/s), of fp32 rows 285 us, 8192 x 2048 27 us. A copy of 4 GiB runs at 4.6 TB/s.
+// 162 us (5.8 TB/s), of fp32 rows 285 us, 8192 x 2048 27 us. A copy of 4 GiB
+// runs at 4.6 TB/s.
 #include <algorithm>
 #include <type_traits>
 
@@ -421,13 +422,13 @@ __global__ void zero_dw(void* dw, int cols, int w_fp32) {
 
 bool aligned16(const void* p) { return (((uintptr_t)p) & 15) == 0; }
 
-// Inputs larger than the last-level cache are loaded past it: what wrote them
-// left nothing of them there that the first rows would still find. (16384 x
-// 7168 bf16 with residual: 172 -> 166 us, to MXFP8 155 -> 139; 8192 x 2048,
-// whose 67 MB the cache holds: 24 -> 27, so not there. bf16 stores always go
-// past it: 26 -> 24 us at 8192 x 2048, 183 -> 172 at 16384 x 7168.)
-constexpr int64_t kCacheBytes = (int64_t)256 << 20;
-
+// Inputs larger than the last-level cache (kCacheBytes) are loaded past it:
+// what wrote them left nothing of them there that the first rows would still
+// find. (16384 x 7168 bf16 with residual: 172 -> 166 us, to MXFP8 155 -> 139.
+// Below, inputs that the cache still holds are worth more than that costs:
+// 5003 x 7168 with an fp32 residual, 215 MB, past it 79 us for 64 if they are
+// there, 80 for 82 if not. bf16 stores always go past it: 26 -> 24 us at 8192
+// x 2048, 183 -> 172 at 16384 x 7168.)
 template <typename XT, typename RT, int BLOCK, int TPR, int NV>
 void run_fwd(const NormFwd& a, int cus, hipStream_t s) {
   const int64_t need = (a.rows + BLOCK / TPR - 1) / (BLOCK / TPR);

@@ -171,6 +171,9 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
+// The last-level cache: launches that touch more load past it where that
+// measured faster.
+constexpr int64_t kCacheBytes = (int64_t)256 << 20;
 // The same past the caches' keeping (non-temporal), for data that one launch
 // streams through and none reads again soon. bf16 lanes fill whole lines per
 // instruction; fp32 ones, at 32 bytes a lane, only with the second, so for
