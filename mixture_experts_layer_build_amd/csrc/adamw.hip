@@ -196,6 +196,7 @@ __device__ __forceinline__ void put_codes(uint8_t* p, int64_t i, int64_t n, bool
     if (i + q < n) p[i + q] = (uint8_t)(w[q >> 2] >> (8 * (q & 3)));
 }
 #if defined(__HIP_DEVICE_COMPILE__)
+__device__ __forceinline__ bool is_subnormal(float x) { return __builtin_amdgcn_classf(x, 0x90); }
 // Values of 8 codes under scale byte s (not 0xFF), two per instruction.
 __device__ __forceinline__ void decode8(uint2 c, uint32_t s, float (&v)[8]) {
   const float scale = u2f(s ? s << 23 : 0x00400000u);
@@ -217,7 +218,8 @@ __device__ __forceinline__ uint2 encode8(const float (&v)[8]) {
   return make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
 }
 #else
-__device__ void decode8(uint2 c, uint32_t s, float (&v)[8]);  // device only
+__device__ bool is_subnormal(float x);  // device only
+__device__ void decode8(uint2 c, uint32_t s, float (&v)[8]);
 __device__ uint2 encode8(const float (&v)[8]);
 #endif
 
@@ -300,12 +302,22 @@ __global__ void __launch_bounds__(kThreads) adamw_tensors(AdamArgs a) {
       get((const float*)t.v, v);
     }
     float r[8];
+    bool tiny = false;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       g[q] *= gs;
       m[q] = a.b1 * m[q] + a.c1 * g[q];
       v[q] = a.b2 * v[q] + a.c2 * (g[q] * g[q]);
       r[q] = __builtin_amdgcn_sqrtf(v[q]);
+      tiny |= is_subnormal(v[q]);
+    }
+    if (tiny) {  // the hardware's root takes a subnormal v for 0
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (is_subnormal(v[q])) r[q] = __builtin_amdgcn_sqrtf(v[q] * 0x1p64f) * 0x1p-32f;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
       const float inv = __builtin_amdgcn_rcpf(__builtin_fmaf(r[q], a.rbc2, a.eps));
       p[q] = __builtin_fmaf(-a.rate * m[q], inv, p[q] * a.keep);
     }

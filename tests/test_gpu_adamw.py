@@ -329,3 +329,19 @@ def test_overlapping_tensors_are_refused():
             mok.adamw_step(*args, step=1, lr=1e-3)
     # neighbours in one buffer, and one gradient for two tensors, are no overlap
     mok.adamw_step([buf[:64], buf[64:128]], [g, g], [buf[128:192], m], [buf[192:256], v], step=1, lr=1e-3)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [0.0, 1e-30])
+def test_second_moments_below_the_normal_range(bits, eps):
+    """Gradients of 1e-19: v is subnormal, its root is not. The first update
+    is -lr * sign(g); g^2 and v are rounded to multiples of 2^-149, by at most
+    2^-150 / 1e-38 and 2^-150 / 5e-40 (1.5e-6 together, half of it in the
+    root), and four roundings of 2^-23 follow: below 2^-19."""
+    g = (torch.rand(4000, device="cuda") * 2e-19 + 1e-19) * torch.randn(4000, device="cuda").sign()
+    p = torch.zeros(4000, device="cuda")
+    st = [torch.zeros(4000, device="cuda") for _ in range(2)] if bits == 32 else \
+        [(torch.zeros(4000, dtype=torch.uint8, device="cuda"), torch.zeros(125, dtype=torch.uint8, device="cuda"))
+         for _ in range(2)]
+    mok.adamw_step([p], [g], [st[0]], [st[1]], step=1, lr=0.5, betas=(B1, B2), eps=eps)
+    assert ((p + 0.5 * g.sign()).abs() <= 0.5 * 2.0 ** -19).all()
