@@ -398,7 +398,8 @@ mok_status mok_mxfp8_quantize_transposed(const void* src, int64_t batches, int64
  * At least one output must be asked for. Without codes every width, stride
  * and alignment is accepted; cols % 8 == 0, cols <= 16384, strides % 8 == 0
  * and 16-byte alignment run the fast kernel. The sum of squares is an fp32
- * sum: rows with |s| above about 1e18 overflow it (rstd 0).
+ * sum: rows with |s| above about 1e18 overflow it (rstd 0), and rows with all
+ * |s| below about 1e-18 leave it inexact, which shows only with eps near 0.
  */
 mok_status mok_rms_norm(const void* x, int x_is_fp32, int64_t ld_x, const void* residual, int residual_is_fp32,
                         int64_t ld_residual, const void* weight, int weight_is_fp32, int64_t rows, int64_t cols,
