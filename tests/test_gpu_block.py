@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 import mixture_experts_layer_build_amd as mok  # noqa: E402
-from mixture_experts_layer_build_amd.autograd import MoKExperts, MoKRMSNorm, MoKRouter  # noqa: E402
+from mixture_experts_layer_build_amd.autograd import MoKExperts, MoKRMSNorm, MoKRouter, rms_norm, router_topk  # noqa: E402
 from mixture_experts_layer_build_amd.optim import MoKAdamW  # noqa: E402
 
 BF = torch.bfloat16
@@ -165,3 +165,33 @@ def test_serving_step_in_mxfp8():
         rw, ids = mok.router_topk(torch.randn(1, E, device="cuda"), K, token_mask=m1)
         o = mok.forward_mxfp8(ws, mok.build_schedule(ws, ids), codes, scale, rw, w)
         assert o.shape == (1, H) and torch.isfinite(o.float()).all()
+
+
+def test_captured_forward_and_backward():
+    """Norm, router and both backward passes in one graph, replayed on new
+    values between eager calls."""
+    torch.manual_seed(4)
+    x, w = bf((65, H)).requires_grad_(), bf(H).requires_grad_()
+    r, gate = bf((65, H)), torch.randn(E, H, device="cuda", requires_grad=True)
+
+    def step():
+        y, s = rms_norm(x, w, r)
+        wt, _, _, losses = router_topk(y.float() @ gate.t(), K, losses=True)
+        return torch.autograd.grad((wt ** 2).sum() + losses.sum() + s.float().mean(), [x, w, gate])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(3):
+        with torch.no_grad():
+            x.copy_(bf((65, H)))
+            gate.copy_(torch.randn(E, H, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, step()))
