@@ -274,12 +274,15 @@ def forward_mxfp8(ws: Workspace, schedule: torch.Tensor, x_codes: torch.Tensor, 
     for t in (schedule, x_codes, x_scale, router_weights, out):
         if t is not None and t.get_device() != ws.device:
             raise ValueError(f"every tensor must be on the workspace's GPU {ws.device}, got {t.device}")
+    given = [t for t in (out, context) if t is not None]
     if out is None:
         out = torch.empty(x_codes.shape, dtype=torch.bfloat16, device=x_codes.device)
     ws_w = _weights(weights)
     _lib.check("mok_forward_mxfp8", lib().mok_forward_mxfp8(
         ws.handle, _ptr(schedule), schedule.numel(), _ptr(x_codes), _ptr(x_scale), _ptr(router_weights),
         C.byref(ws_w), _ptr(out), _ptr(context), 0 if context is None else context.numel(), _stream()))
+    if given:  # (written through their addresses)
+        torch.autograd.graph.increment_version(given)
     return out
 
 

@@ -144,6 +144,18 @@ PyObject* result(mok_status st, std::initializer_list<Tensor> ts) {
   return r;
 }
 
+// Moves the in-place version counter of a tensor that a call wrote through its
+// address: autograd's check of saved tensors and the layer's quantized weights
+// go by it. (Tensors made in inference mode have none.)
+void written(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+void written(const Tensor* t) {
+  if (t) written(*t);
+}
+// Whether a call may have enqueued work: not if its arguments were refused.
+bool ran(mok_status st) { return st == MOK_OK || st == MOK_ERR_HIP; }
+
 // ---- RMS norm ----
 
 struct Norm {
@@ -195,6 +207,7 @@ PyObject* rms_norm_mxfp8(PyObject* const* a, Py_ssize_t n) {
   blocks.push_back(k.cols / 32);
   Tensor codes = make(k.x.sizes(), k.x, kU8), scale = make(blocks, k.x, kU8);
   const mok_status st = k.run(number(a[3]), ptr(y), codes.data_ptr(), scale.data_ptr(), ptr(rstd), stream_of(a[6]));
+  if (ran(st)) written(y), written(rstd);
   return result(st, {codes, scale, k.sum});
 }
 
@@ -230,6 +243,7 @@ PyObject* rms_norm_backward(PyObject* const* a, Py_ssize_t n) {
   const mok_status st = f_rms_norm_backward(dy.data_ptr(), lddy, s.data_ptr(), fp32(s), lds, (const float*)pr, pw,
                                             fp32(w), ptr(dsum), ldd, rows, cols, ds.data_ptr(), ptr(dx), dw.data_ptr(),
                                             scratch.data_ptr(), bytes, stream_of(a[6]));
+  if (ran(st)) written(dx);
   return result(st, {ds, dw});
 }
 
@@ -328,6 +342,7 @@ struct Step {
     bool written;
   };
   std::vector<Bytes> touched;  // what the step reads and writes
+  std::vector<const Tensor*> outputs;
   const Tensor* first = nullptr;
 
   // Adds one tensor of a list: all of one type of `types`, dense, on one GPU.
@@ -341,6 +356,7 @@ struct Step {
     if (!t.is_contiguous()) bad("every tensor of " + name + " must be contiguous");
     void* p = t.data_ptr();
     to->push_back(p);
+    if (writes) outputs.push_back(&t);
     if (numel > 0) touched.push_back({(uintptr_t)p, (uintptr_t)p + numel * t.element_size(), writes});
   }
   void length(const char* name, const Items& l) const {
@@ -368,6 +384,7 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t nargs) {
   for (auto* v : {&pp, &pg, &pw, &pm[0], &pm[1], &psc[0], &psc[1]}) v->reserve(s.n);
   s.numels.reserve(s.n);
   s.touched.reserve((size_t)s.n * 7);
+  s.outputs.reserve((size_t)s.n * 6);
   for (int i = 0; i < s.n; ++i) {
     const Tensor& p = tensor("params", params[i]);
     const int64_t n = p.numel();
@@ -422,7 +439,10 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t nargs) {
   u.param_fp32 = pt == kF32, u.grad_fp32 = gt == kF32, u.state_bits = small ? 8 : 32;
   u.seed = (uint32_t)PyLong_AsUnsignedLongMask(a[12]);
   if (PyErr_Occurred()) throw python_error();
-  return PyLong_FromLong(f_adamw_step(&u, stream_of(a[13])));
+  const mok_status status = f_adamw_step(&u, stream_of(a[13]));
+  if (ran(status))
+    for (const Tensor* t : s.outputs) written(*t);
+  return PyLong_FromLong(status);
 }
 
 // bind(addresses of the C ABI's functions, in the order below)

@@ -3,7 +3,9 @@
 Direct calls over the C ABI (``include/mok.h`` states formulas, types and
 refusals); the package re-exports them. They allocate their outputs with
 torch, enqueue on the current stream of the tensors' device, and need no
-workspace. Tensors on the CPU are rejected: there is no fallback.
+workspace. Tensors on the CPU are rejected: there is no fallback. What a call
+writes into tensors that it was given (``adamw_step``; the outputs handed to a
+norm) moves their in-place version counters.
 
 The checks and allocations of these calls are compiled (``csrc/py_ops.cpp``,
 built with the library): at a few tokens the host's share decides their time.
