@@ -470,8 +470,9 @@ mok_status mok_router_topk(const void* logits, int logits_is_fp32, int64_t T, in
  * every element written, from d_weights fp32 [T, k], the forward's ids and,
  * if the losses have a gradient, d_losses fp32 [2] with the forward's counts
  * (both or neither). The choice itself and counts are constants. Choices
- * with an id outside [0, experts) get no gradient; tokens that are masked
- * out or have no key above -inf get zeros, a row without an order NaN.
+ * with an id outside [0, experts) get no gradient, whatever their d_weights
+ * hold; tokens that are masked out or have no key above -inf get zeros, a row
+ * without an order NaN.
  */
 mok_status mok_router_topk_backward(const float* d_weights, const void* logits, int logits_is_fp32, int64_t T,
                                     int64_t ld, int32_t experts, int32_t k, const float* bias,

@@ -567,7 +567,8 @@ __global__ void __launch_bounds__(BLOCK) router_bwd_rows(RouterBwd a) {
       if (q * G < k && keep && j < k) {
         const int64_t v = a.ids[t * k + j];
         id[q] = v >= 0 && v < E ? (int)v : -1;
-        c[q] = a.d_weights[t * k + j] * a.scale;
+        // (its d_weights may be anything: a weight of 0 has an infinite logarithm)
+        c[q] = id[q] >= 0 ? a.d_weights[t * k + j] * a.scale : 0.f;
       }
     }
     Row<LT, G, VPL, false> r;
