@@ -442,7 +442,7 @@ size_t mok_router_scratch_bytes(int64_t T, int32_t experts);
  *   key   = logit + bias, one fp32 addition (bias fp32 [experts], nullable:
  *           it selects only, the weights do not see it)
  *   ids   int64 [T, k]: the k largest keys in descending order, ties to the
- *         lowest expert id. A key of -inf is never chosen: where fewer than
+ *         lowest expert id (-0 and +0 tie). A key of -inf is never chosen: where fewer than
  *         k are left, id -1 and weight 0 (mok_build_schedule does not
  *         dispatch such an assignment).
  *   weights fp32 [T, k]: the scores of the chosen, divided by their sum if

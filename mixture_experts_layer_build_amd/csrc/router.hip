@@ -94,9 +94,9 @@ struct RouterFwd {
   float* part;            // statistics (router_stats)
 };
 
-// Bits of a key in its order (larger key, larger word); the key is the sum of
-// a logit and a bias or zero, so never -0. -inf is kNone, words of numbers lie
-// above it.
+// Bits of a key in its order (larger key, larger word). The key must not be
+// -0, which is equal to +0: callers add +0. -inf is kNone, words of numbers
+// lie above it.
 constexpr uint32_t kNone = 0x007FFFFFu;
 __device__ __forceinline__ uint32_t ordered(float key) {
   const uint32_t u = f2u(key);
@@ -151,7 +151,7 @@ struct Row {
       most = -kInf;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        const float key = l[i] + bias[min(i * G + gl, E - 1)];
+        const float key = l[i] + bias[min(i * G + gl, E - 1)] + 0.0f;  // (-0 + -0 is -0)
         most = __builtin_fmaxf(most, key);
         see(i, key);
       }

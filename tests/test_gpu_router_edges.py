@@ -1,4 +1,5 @@
-"""The router where its rules decide: choices that have no expert.
+"""The router where its rules decide: keys of both zeros, and choices that
+have no expert.
 
 Tolerances as in test_gpu_router.py: a gradient's element is off by 2^-16 of
 M, the row's largest |dw| (finite ones) times scale plus the losses' terms."""
@@ -12,6 +13,27 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 import mixture_experts_layer_build_amd as mok  # noqa: E402
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("E,k", [(16, 1), (16, 8), (64, 8), (128, 8), (128, 16), (128, 17), (300, 8), (600, 8), (600, 16)])
+def test_keys_of_both_zeros_are_equal(E, k, dtype):
+    """Each row has one logit of -0 and, at a higher id, one of +0, all others
+    are distinct and below, and the bias is -0: the keys are -0 + -0 = -0 and
+    +0 + -0 = +0, which are equal, so the lower id comes first. (No other
+    keys are equal, so nothing else sends a row down another path.)"""
+    rng = np.random.default_rng([E, k])
+    for T in (9, 33000) if E == 64 else (9,):
+        l = -1.0 - np.argsort(rng.random((T, E)), 1).astype(np.float32)
+        for t in range(T):
+            low, high = np.sort(rng.choice(E, 2, replace=False))
+            l[t, low], l[t, high] = -0.0, 0.0
+        bias = np.full(E, -0.0, np.float32)
+        print(f"zeros T={T} E={E} k={k} {dtype}", flush=True)
+        _, ids = mok.router_topk(torch.from_numpy(l).cuda().to(dtype), k, bias=torch.from_numpy(bias).cuda())
+        np.testing.assert_array_equal(ids[:9].cpu().numpy(), oops.router(l[:9], k, bias=bias)[1])
 
 
 @pytest.mark.parametrize("scoring,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
