@@ -94,11 +94,10 @@ __device__ __forceinline__ uint32_t pair_bits(uint32_t x) {
   return x;
 }
 
-// Smallest X with amax <= 448 * 2^X, from amax's bits; -127 for 0.
+// Smallest X >= -127 with amax <= 448 * 2^X, from amax's bits: 448 is 1.75 *
+// 2^8. (At most 120, for the largest fp32 values.)
 __device__ __forceinline__ int state_exponent(uint32_t amax) {
-  if (amax == 0) return -127;
-  const int x = mx_block_exponent(amax);
-  return (amax >= 0x00800000u && (amax & 0x7FFFFFu) > 0x600000u) ? min(x + 1, 127) : x;
+  return max((int)(amax >> 23) - (127 + 8) + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0), -127);
 }
 
 // The products and sums of the moments are rounded one by one, as they are
