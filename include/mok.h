@@ -491,14 +491,17 @@ mok_status mok_router_topk_backward(const float* d_weights, const void* logits, 
  * fp32 (state_bits 32), or (state_bits 8) as E4M3 codes [numel] of m and of
  * sqrt(v), with one E8M0 scale byte per 32 consecutive elements (the last
  * block may be shorter), [ceil(numel/32)]; all-zero bytes are zero moments.
- * A block's scale is the smallest power of two that keeps its largest
- * magnitude within 448 of it (0xFF, NaN, in both moments if the block's v
- * is not finite). m is
- * rounded to the nearest code; sqrt(v) to one of the two codes around it,
- * chosen at random so that the mean of its square is v, from `seed` and the
- * element's number in the call (tensors are numbered one after the other,
- * each from a multiple of 32, modulo 2^32): the same seed gives the same
- * bits, and each step should have its own.
+ * A block's scale 2^X is the smallest power of two that keeps its largest
+ * magnitude within 448 of it (0xFF, NaN, in both moments if the block's v is
+ * not finite). m is rounded to the nearest code, and an m half way between
+ * two codes to the even one, or to the smaller one under those scales whose
+ * 2^-X the math library's power function gives half a unit low (X = -16 to
+ * -20 and some below): the codes are those of the elementary tensor
+ * operations on the same GPU, bit for bit. sqrt(v) is rounded to one of the
+ * two codes around it, chosen at random so that the mean of its square is v,
+ * from `seed` and the element's number in the call (tensors are numbered one
+ * after the other, each from a multiple of 32, modulo 2^32): the same seed
+ * gives the same bits, and each step should have its own.
  * Tensors of the call must not overlap. grad_scale (nullable): a device
  * fp32, read when the kernel runs. lr, step and seed are values of the call:
  * a captured graph repeats them.

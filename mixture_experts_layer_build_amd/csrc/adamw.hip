@@ -223,10 +223,15 @@ __device__ uint2 encode8(const float (&v)[8]);
 #endif
 
 // 2^k as the math library's power function gives it: exact, or half an ulp
-// below for some k from 16 on. The states are scaled by it because elementary
-// tensor operations on this GPU scale so: on an exact tie that half ulp
-// decides the code, and with it a step gives the codes that those operations
-// give, bit for bit. (The base is hidden, or the compiler would take exp2.)
+// below (k = 16 to 20, 22, 24, 25, 28, 29, 32, ...). The states are scaled by
+// it because elementary tensor operations on this GPU scale so, and a step
+// gives the codes that those operations give, bit for bit. The half ulp shows
+// only where m is half way between two codes, both equally near: then the
+// smaller one is taken, not the even one. That is no rare case: a bf16 gradient
+// and a code of 4 bits often add up to few bits (0.25 % of the codes of a step
+// on gradients of a normal distribution), and with the exact power two steps'
+// parameters differ from those of the elementary operations by 5e-5 of them.
+// (The base is hidden, or the compiler would take exp2.)
 __device__ __forceinline__ float library_power(int k) {
   return powf(u2f((uint32_t)opaque(0x40000000)), (float)k);
 }

@@ -62,3 +62,41 @@ def test_scales_at_the_low_end():
         half = (oops.decode8(m[0].cpu().numpy(), m[1].cpu().numpy()) * 0.5).astype(np.float32)
         step(torch.zeros(g.size, device="cuda"), m, v, b1=0.5)
         check_m(m, half + np.float32(0))
+
+
+def blocks_of(values, exponents):
+    """Blocks of 448 and 31 of `values`, times 2^x for x in `exponents`."""
+    out = []
+    for x in exponents:
+        for i in range(0, values.size, 31):
+            b = np.zeros(32)
+            b[0] = 448.0
+            b[1:1 + values[i:i + 31].size] = values[i:i + 31]
+            out.append(b * 2.0 ** x)
+    return np.concatenate(out).astype(np.float32)
+
+
+@pytest.mark.parametrize("pt,master", [(F32, False), (torch.bfloat16, False), (torch.bfloat16, True)])
+@pytest.mark.parametrize("copies", [1, 600])
+def test_moments_half_way_between_two_codes(pt, master, copies):
+    """Every pair of neighbouring codes under every scale from 2^-60 to 2^49.
+    (Many copies: sizes that fill each compute unit several times.)"""
+    code = oops.E4M3  # 0, 2^-9, ... 448
+    mid = (code[:-1] + code[1:]) / 2
+    g = blocks_of(np.concatenate([mid, -mid]), range(-60, 50))
+    t = torch.from_numpy(g).cuda().repeat(copies)
+    m, v = zeros8(t.numel()), zeros8(t.numel())
+    print(f"half way {pt} {master} {t.numel()}", flush=True)
+    step(t, m, v, pt, master)
+    for i in {0, copies - 1}:
+        check_m([a.view(copies, -1)[i] for a in m], g)
+
+
+def test_a_root_that_is_a_code_is_kept():
+    """v = r^2 with r on a code (times 2^x): the random choice has nothing to
+    choose, whatever the scale. (From x = -53 on: below, the smallest squares
+    are no normal numbers and are rounded.)"""
+    g = blocks_of(oops.E4M3[1:], range(-53, 50))
+    m, v = zeros8(g.size), zeros8(g.size)
+    step(torch.from_numpy(g).cuda(), m, v)
+    check_m(v, g)
