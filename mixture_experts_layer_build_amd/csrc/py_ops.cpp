@@ -383,7 +383,7 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t nargs) {
   std::vector<void*> pp, pg, pw, pm[2], psc[2];
   for (auto* v : {&pp, &pg, &pw, &pm[0], &pm[1], &psc[0], &psc[1]}) v->reserve(s.n);
   s.numels.reserve(s.n);
-  s.touched.reserve((size_t)s.n * 7);
+  s.touched.reserve((size_t)s.n * 7 + 1);
   s.outputs.reserve((size_t)s.n * 6);
   for (int i = 0; i < s.n; ++i) {
     const Tensor& p = tensor("params", params[i]);
@@ -409,6 +409,12 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t nargs) {
             (n + 31) / 32, &st[k], &psc[k], true);
     }
   }
+  const Tensor* scale = maybe("grad_scale", a[11]);
+  if (scale) {
+    check("grad_scale", *scale, *s.first, {kF32});
+    if (scale->numel() != 1) bad("grad_scale must have one element");
+    s.touched.push_back({(uintptr_t)scale->data_ptr(), (uintptr_t)scale->data_ptr() + sizeof(float), false});
+  }
   std::sort(s.touched.begin(), s.touched.end(),
             [](const Step::Bytes& x, const Step::Bytes& y) { return x.begin < y.begin; });
   uintptr_t any_end = 0, written_end = 0;
@@ -417,11 +423,6 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t nargs) {
       bad("a tensor that the step writes is given twice, or overlaps another");
     any_end = std::max(any_end, b.end);
     if (b.written) written_end = std::max(written_end, b.end);
-  }
-  const Tensor* scale = maybe("grad_scale", a[11]);
-  if (scale) {
-    check("grad_scale", *scale, *s.first, {kF32});
-    if (scale->numel() != 1) bad("grad_scale must have one element");
   }
   mok_adamw u{};
   u.struct_size = sizeof(u);
