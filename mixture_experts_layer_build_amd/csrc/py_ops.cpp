@@ -20,6 +20,7 @@
 #include <cmath>
 #include <stdexcept>
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "mok.h"
@@ -156,6 +157,24 @@ void written(const Tensor* t) {
 // Whether a call may have enqueued work: not if its arguments were refused.
 bool ran(mok_status st) { return st == MOK_OK || st == MOK_ERR_HIP; }
 
+// The memory between a tensor's first and last element.
+std::pair<uintptr_t, uintptr_t> span(const Tensor& t) {
+  const uintptr_t p = (uintptr_t)t.data_ptr();
+  int64_t last = 0;
+  for (int64_t i = 0; i < t.dim(); ++i) last += (t.size(i) - 1) * t.stride(i);
+  return {p, t.numel() ? p + (last + 1) * t.element_size() : p};
+}
+// Refuses a given output that overlaps `other` (null: none): another row's
+// threads would read what one has written. `in_place`: where `other` is the
+// same memory, element by element, a row is read before it is written.
+void apart(const char* name, const Tensor& out, const char* other_name, const Tensor* other, bool in_place) {
+  if (!other) return;
+  const auto a = span(out), b = span(*other);
+  if (a.first >= b.second || b.first >= a.second) return;
+  if (in_place && a == b && out.element_size() == other->element_size() && other->is_contiguous()) return;
+  bad(std::string(name) + " overlaps " + other_name);
+}
+
 // ---- RMS norm ----
 
 struct Norm {
@@ -203,6 +222,11 @@ PyObject* rms_norm_mxfp8(PyObject* const* a, Py_ssize_t n) {
   const Tensor *y = maybe("y", a[4]), *rstd = maybe("rstd", a[5]);
   if (y) check("y", *y, k.x, {kBf16}), shaped("y", *y, k.x.sizes()), dense("y", *y);
   if (rstd) check("rstd", *rstd, k.x, {kF32}), shaped("rstd", *rstd, lead), dense("rstd", *rstd);
+  if (y) apart("y", *y, "x", &k.x, true), apart("y", *y, "residual", k.res, true), apart("y", *y, "weight", &k.w, false);
+  if (rstd) {
+    apart("rstd", *rstd, "x", &k.x, false), apart("rstd", *rstd, "residual", k.res, false);
+    apart("rstd", *rstd, "weight", &k.w, false), apart("rstd", *rstd, "y", y, false);
+  }
   auto blocks = lead.vec();
   blocks.push_back(k.cols / 32);
   Tensor codes = make(k.x.sizes(), k.x, kU8), scale = make(blocks, k.x, kU8);
@@ -234,6 +258,10 @@ PyObject* rms_norm_backward(PyObject* const* a, Py_ssize_t n) {
     ldd = row_stride("d_sum", *dsum);
   }
   if (dx) check("dx", *dx, dy, {kBf16}), shaped("dx", *dx, dy.sizes()), dense("dx", *dx);
+  if (dx) {
+    apart("dx", *dx, "dy", &dy, true), apart("dx", *dx, "s", &s, true), apart("dx", *dx, "d_sum", dsum, true);
+    apart("dx", *dx, "rstd", &rstd, false), apart("dx", *dx, "weight", &w, false);
+  }
   const void* pr = dense("rstd", rstd);
   const void* pw = dense("weight", w);
   const int64_t rows = dy.numel() / cols;

@@ -73,7 +73,8 @@ def rms_norm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor
     """The norm with its output in MXFP8, as ``forward_mxfp8`` takes it.
     Returns (codes uint8 [..., cols], scale uint8 [..., cols/32], sum). Give
     ``y`` (bf16, x's shape) and ``rstd`` (fp32, one per row) to have them
-    filled too, for a backward."""
+    filled too, for a backward. y may be x's or the residual's own tensor
+    (dense, bf16); else they overlap no other tensor of the call."""
     return _call("rms_norm_mxfp8", x, x, weight, residual, eps, y, rstd)
 
 
@@ -82,7 +83,8 @@ def rms_norm_backward(dy: torch.Tensor, s: torch.Tensor, rstd: torch.Tensor, wei
     """(ds, d_weight) from dy (bf16), the saved s (the forward's sum, or x
     without a residual) and rstd; ``d_sum`` is the gradient that arrives
     through the sum. ds is the gradient of x and of the residual, in s's
-    type; ``dx`` (bf16) receives it in bf16 as well."""
+    type; ``dx`` (bf16) receives it in bf16 as well, and may be a dense bf16
+    dy, s or d_sum itself, but overlaps no other tensor of the call."""
     return _call("rms_norm_backward", dy, dy, s, rstd, weight, d_sum, dx)
 
 
