@@ -230,9 +230,12 @@ def schedule_fields(ws: Workspace, schedule: torch.Tensor) -> dict:
                 tiles=f(L.tiles, len(TILE_BMS) * (E + 2)))
 
 
+_WEIGHTS = ("routed_gate", "routed_up", "routed_down", "shared_gate", "shared_up", "shared_down")
+
+
 def _weights(w: dict) -> _lib.MokWeights:
     s = _lib.MokWeights()
-    for name in ("routed_gate", "routed_up", "routed_down", "shared_gate", "shared_up", "shared_down"):
+    for name in _WEIGHTS:
         setattr(s, name, _ptr(w.get(name)))
         setattr(s, name + "_scale", _ptr(w.get(name + "_scale")))
     return s
@@ -271,7 +274,8 @@ def forward_mxfp8(ws: Workspace, schedule: torch.Tensor, x_codes: torch.Tensor, 
         raise ValueError("router_weights must be [T, topk], with T at most max_tokens")
     if out is not None and (out.dtype != torch.bfloat16 or out.shape != x_codes.shape):
         raise ValueError("out must be bf16 [T, hidden]")
-    for t in (schedule, x_codes, x_scale, router_weights, out):
+    for t in (schedule, x_codes, x_scale, router_weights, out, context,
+              *(weights.get(n + s) for n in _WEIGHTS for s in ("", "_scale"))):
         if t is not None and t.get_device() != ws.device:
             raise ValueError(f"every tensor must be on the workspace's GPU {ws.device}, got {t.device}")
     given = [t for t in (out, context) if t is not None]
