@@ -26,12 +26,21 @@ class MoKAdamW(torch.optim.Optimizer):
 
     def __init__(self, params, lr: float = 1e-3, betas: tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, state_bits: int = 32, master_weights: bool = True):
-        if state_bits not in (32, 8):
+        defaults = dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay, state_bits=state_bits,
+                        master_weights=master_weights)
+        self._check_group(defaults)
+        super().__init__(params, defaults)
+
+    @staticmethod
+    def _check_group(g: dict) -> None:
+        if g["state_bits"] not in (32, 8):
             raise ValueError("state_bits must be 32 or 8")
-        if lr < 0 or eps < 0 or weight_decay < 0 or not all(0 <= b < 1 for b in betas):
+        if g["lr"] < 0 or g["eps"] < 0 or g["weight_decay"] < 0 or not all(0 <= b < 1 for b in g["betas"]):
             raise ValueError("lr, eps and weight_decay must not be negative, betas must lie in [0, 1)")
-        super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps, weight_decay=weight_decay,
-                                      state_bits=state_bits, master_weights=master_weights))
+
+    def add_param_group(self, param_group: dict) -> None:
+        self._check_group({**self.defaults, **param_group})
+        super().add_param_group(param_group)
 
     def _init_state(self, p: torch.Tensor, group: dict) -> dict:
         if p.dtype not in (torch.bfloat16, torch.float32):

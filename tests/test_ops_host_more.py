@@ -1,10 +1,12 @@
-"""More refusals on the CPU: tensors of another GPU in a forward on codes."""
+"""More refusals on the CPU: tensors of another GPU in a forward on codes, and
+the options of an optimizer's groups."""
 import pytest
 
 from mokutil import ROOT  # noqa: F401
 
 torch = pytest.importorskip("torch")
 import mixture_experts_layer_build_amd as mok  # noqa: E402
+from mixture_experts_layer_build_amd.optim import MoKAdamW  # noqa: E402
 
 
 class On:
@@ -35,3 +37,16 @@ def test_forward_mxfp8_refuses_a_context_or_weights_of_another_gpu():
             call(**kw)
     with pytest.raises(ValueError, match="must live on the GPU"):  # (the next check, on the tensors behind)
         call()
+
+
+def test_optimizer_checks_each_group():
+    p, q = torch.nn.Parameter(torch.zeros(4)), torch.nn.Parameter(torch.zeros(4))
+    for bad in (dict(state_bits=16), dict(lr=-1.0), dict(betas=(0.9, 1.0)), dict(eps=-1.0), dict(weight_decay=-0.1)):
+        with pytest.raises(ValueError):
+            MoKAdamW([{"params": [p], **bad}])
+        opt = MoKAdamW([p])
+        with pytest.raises(ValueError):
+            opt.add_param_group({"params": [q], **bad})
+        assert len(opt.param_groups) == 1
+    opt.add_param_group({"params": [q], "state_bits": 8, "lr": 0.5})
+    assert opt.param_groups[1]["state_bits"] == 8 and opt.param_groups[1]["eps"] == 1e-8
