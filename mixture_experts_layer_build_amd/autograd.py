@@ -24,7 +24,8 @@ read for one GPU:
   before production": MXFP8 takes pre-quantized weights). Each quantized
   copy is kept per parameter and made again whenever the parameter's
   in-place version counter moves (an optimizer step, a ``copy_``), so a
-  step never runs on stale codes.
+  step never runs on stale codes; a captured training step makes them at
+  every replay.
 
 Around the layer: ``rms_norm`` and ``MoKRMSNorm`` (the norm in front of it,
 with the residual's addition) and ``router_topk`` and ``MoKRouter`` (the
@@ -72,14 +73,19 @@ class MoKRuntime:
             raise ValueError("the MoE layer runs on the GPU only: inputs must be CUDA tensors")
         return get_workspace(self.cfg, device.index if device.index is not None else torch.cuda.current_device())
 
-    def quantized(self, name: str, w: torch.Tensor, transposed: bool = False) -> tuple[torch.Tensor, torch.Tensor]:
+    def quantized(self, name: str, w: torch.Tensor, transposed: bool = False, trained: bool = False
+                  ) -> tuple[torch.Tensor, torch.Tensor]:
         """MXFP8 codes and scales of a BF16 weight along its last dimension
         (the forward's form), or transposed and quantized along its
         second-to-last (the backward's form), made again when the weight
-        changed since they were made."""
+        changed since they were made. A graph does not ask at its replays: in
+        a capture the codes of a weight in training are made in the graph,
+        and what a capture made is not kept (it holds nothing before the
+        first replay)."""
         key = (name, transposed)
+        capturing = torch.cuda.is_current_stream_capturing()
         hit = self._q.get(key)
-        if hit is not None:
+        if hit is not None and not (capturing and trained):
             ref, version, ptr, codes, sc = hit
             if ref() is w and version == w._version and ptr == w.data_ptr():
                 return codes, sc
@@ -88,17 +94,18 @@ class MoKRuntime:
         else:
             codes, sc = mxfp8_quantize(w.detach().reshape(-1, w.shape[-1]), axis=1)
             codes = codes.view(w.shape)
-        self._q[key] = (weakref.ref(w), w._version, w.data_ptr(), codes, sc)
+        if not capturing:
+            self._q[key] = (weakref.ref(w), w._version, w.data_ptr(), codes, sc)
         return codes, sc
 
-    def forward_weights(self, w: dict) -> dict:
+    def forward_weights(self, w: dict, trained: bool = False) -> dict:
         if self.mode == MOK_MODE_BF16:
             return w
         q = {}
         for name, t in w.items():
             if t is None:
                 continue
-            q[name], q[name + "_scale"] = self.quantized(name, t)
+            q[name], q[name + "_scale"] = self.quantized(name, t, trained=trained and t.requires_grad)
         return q
 
     def backward_weights(self, w: dict) -> dict:
@@ -110,7 +117,7 @@ class MoKRuntime:
         for name, t in w.items():
             if t is None:
                 continue
-            q[name], q[name + "_scale"] = self.quantized(name, t, transposed=True)
+            q[name], q[name + "_scale"] = self.quantized(name, t, transposed=True, trained=t.requires_grad)
         return q
 
 
@@ -157,7 +164,8 @@ def _run_forward(runtime: MoKRuntime, keep: bool, x, router_weights, top_experts
     ws = runtime.workspace(x.device)
     sched = build_schedule(ws, top_experts)
     context = torch.empty(context_bytes(cfg, runtime.mode), dtype=torch.uint8, device=x.device) if keep else None
-    out = forward(ws, sched, x, router_weights, runtime.forward_weights(w), mode=runtime.mode, context=context)
+    out = forward(ws, sched, x, router_weights, runtime.forward_weights(w, trained=keep), mode=runtime.mode,
+                  context=context)
     return out, sched, context, w
 
 
