@@ -566,9 +566,9 @@ __global__ void __launch_bounds__(BLOCK) router_bwd_rows(RouterBwd a) {
       c[q] = 0.f;
       if (q * G < k && keep && j < k) {
         const int64_t v = a.ids[t * k + j];
+        const float d = a.d_weights[t * k + j];  // (without an expert anything: a weight of 0 has an infinite logarithm)
         id[q] = v >= 0 && v < E ? (int)v : -1;
-        // (its d_weights may be anything: a weight of 0 has an infinite logarithm)
-        c[q] = id[q] >= 0 ? a.d_weights[t * k + j] * a.scale : 0.f;
+        c[q] = d * a.scale;
       }
     }
     Row<LT, G, VPL, false> r;
@@ -580,6 +580,7 @@ __global__ void __launch_bounds__(BLOCK) router_bwd_rows(RouterBwd a) {
 #pragma unroll
     for (int q = 0; q < KQ; ++q) {
       lc[q] = id[q] >= 0 ? mine[id[q]] : -kInf;
+      c[q] = id[q] >= 0 ? c[q] : 0.f;
       ltop = __builtin_fmaxf(ltop, lc[q]);
     }
     wave_lds_fence();
