@@ -369,23 +369,67 @@ struct Step {
     uintptr_t begin, end;
     bool written;
   };
-  std::vector<Bytes> touched;  // what the step reads and writes
+  std::vector<Bytes> touched;  // what the step reads and writes, tensor by tensor, one of each list
+  size_t lists = 0;
+  Bytes scale{0, 0, false};
   std::vector<const Tensor*> outputs;
   const Tensor* first = nullptr;
 
   // Adds one tensor of a list: all of one type of `types`, dense, on one GPU.
-  void add(const std::string& name, const Tensor& t, Types types, int64_t numel, at::ScalarType* type,
+  void add(const char* name, const Tensor& t, Types types, int64_t numel, at::ScalarType* type,
            std::vector<void*>* to, bool writes) {
     if (t.device() != first->device()) bad("every tensor must be on " + first->device().str() + ": " + name);
-    if (t.numel() != numel) bad("the tensors of " + name + " must have the sizes of the params");
+    if (t.numel() != numel) bad(std::string("the tensors of ") + name + " must have the sizes of the params");
     if (to->empty() && one_of(t.scalar_type(), types)) *type = t.scalar_type();
     if (t.scalar_type() != *type)
-      bad(name + " must all be " + text(types) + ", got " + name_of(t.scalar_type()));
-    if (!t.is_contiguous()) bad("every tensor of " + name + " must be contiguous");
+      bad(std::string(name) + " must all be " + text(types) + ", got " + name_of(t.scalar_type()));
+    if (!t.is_contiguous()) bad(std::string("every tensor of ") + name + " must be contiguous");
     void* p = t.data_ptr();
     to->push_back(p);
     if (writes) outputs.push_back(&t);
     if (numel > 0) touched.push_back({(uintptr_t)p, (uintptr_t)p + numel * t.element_size(), writes});
+  }
+  // Whether a range that is written overlaps another. A list's tensors mostly
+  // lie in memory in their order: the lists are a few ascending runs, which are
+  // merged (36 tensors, 4 lists: 0.4 us; a sort takes 1.5).
+  bool overlaps() const {
+    const auto before = [](const Bytes& x, const Bytes& y) { return x.begin < y.begin; };
+    constexpr size_t kRuns = 16;
+    size_t run[kRuns + 1], runs = 0;  // where each begins, and the end
+    const size_t n = touched.size() + (scale.end ? 1 : 0);
+    std::vector<Bytes> both(2 * n);
+    Bytes *a = both.data(), *b = a + n, *to = a;
+    const auto next = [&](const Bytes& x) {
+      if (to == a || before(x, to[-1])) {
+        if (runs < kRuns) run[runs] = to - a;
+        ++runs;
+      }
+      *to++ = x;
+    };
+    for (size_t l = 0; l < lists; ++l)
+      for (size_t i = l; i < touched.size(); i += lists) next(touched[i]);
+    if (scale.end) next(scale);
+    if (runs > kRuns) {
+      std::sort(a, a + n, before);
+    } else {
+      run[runs] = n;
+      for (size_t left = runs; left > 1; left = (left + 1) / 2, std::swap(a, b)) {
+        for (size_t i = 0; i < left; i += 2) {
+          const size_t mid = run[i + 1], end = i + 1 < left ? run[i + 2] : mid;
+          std::merge(a + run[i], a + mid, a + mid, a + end, b + run[i], before);
+          run[i / 2] = run[i];
+        }
+        run[(left + 1) / 2] = n;
+      }
+    }
+    uintptr_t any_end = 0, written_end = 0;
+    for (size_t i = 0; i < n; ++i) {
+      const Bytes& x = a[i];
+      if (x.begin < (x.written ? any_end : written_end)) return true;
+      any_end = std::max(any_end, x.end);
+      if (x.written) written_end = std::max(written_end, x.end);
+    }
+    return false;
   }
   void length(const char* name, const Items& l) const {
     if (l.size() != n)
@@ -411,7 +455,8 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t nargs) {
   std::vector<void*> pp, pg, pw, pm[2], psc[2];
   for (auto* v : {&pp, &pg, &pw, &pm[0], &pm[1], &psc[0], &psc[1]}) v->reserve(s.n);
   s.numels.reserve(s.n);
-  s.touched.reserve((size_t)s.n * 7 + 1);
+  s.touched.reserve((size_t)s.n * 7);
+  s.lists = (small ? 6 : 4) + (with_masters ? 1 : 0);
   s.outputs.reserve((size_t)s.n * 6);
   for (int i = 0; i < s.n; ++i) {
     const Tensor& p = tensor("params", params[i]);
@@ -433,7 +478,7 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t nargs) {
       if (!(PyTuple_Check(o) || PyList_Check(o)) || PySequence_Fast_GET_SIZE(o) != 2)
         bad(std::string(name) + " must be pairs (codes, scale)");
       s.add(name, tensor(name, PySequence_Fast_GET_ITEM(o, 0)), {kU8, at::kFloat8_e4m3fn}, n, &mt[k], &pm[k], true);
-      s.add(std::string(name) + " scales", tensor(name, PySequence_Fast_GET_ITEM(o, 1)), {kU8, at::kFloat8_e8m0fnu},
+      s.add(k ? "exp_avg_sqs scales" : "exp_avgs scales", tensor(name, PySequence_Fast_GET_ITEM(o, 1)), {kU8, at::kFloat8_e8m0fnu},
             (n + 31) / 32, &st[k], &psc[k], true);
     }
   }
@@ -441,17 +486,9 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t nargs) {
   if (scale) {
     check("grad_scale", *scale, *s.first, {kF32});
     if (scale->numel() != 1) bad("grad_scale must have one element");
-    s.touched.push_back({(uintptr_t)scale->data_ptr(), (uintptr_t)scale->data_ptr() + sizeof(float), false});
+    s.scale = {(uintptr_t)scale->data_ptr(), (uintptr_t)scale->data_ptr() + sizeof(float), false};
   }
-  std::sort(s.touched.begin(), s.touched.end(),
-            [](const Step::Bytes& x, const Step::Bytes& y) { return x.begin < y.begin; });
-  uintptr_t any_end = 0, written_end = 0;
-  for (const Step::Bytes& b : s.touched) {
-    if (b.begin < (b.written ? any_end : written_end))
-      bad("a tensor that the step writes is given twice, or overlaps another");
-    any_end = std::max(any_end, b.end);
-    if (b.written) written_end = std::max(written_end, b.end);
-  }
+  if (s.overlaps()) bad("a tensor that the step writes is given twice, or overlaps another");
   mok_adamw u{};
   u.struct_size = sizeof(u);
   u.count = s.n;
