@@ -271,7 +271,9 @@ mok_status mok_forward(mok_workspace* ws, mok_mode mode, const void* schedule, s
  * everything else, arguments and results, is as in mok_forward with
  * MOK_MODE_MXFP8, and with the codes that mok_mxfp8_quantize(axis = 1) gives
  * for a bf16 x the output bits are those of mok_forward on that x. A
- * backward on the context still takes x in bf16.
+ * backward on the context still takes x in bf16. A token with a NaN scale
+ * (0xFF) gets a row of NaN and reaches no other token; with a swiglu_limit,
+ * which clamps a NaN like any value, its row may be finite and means nothing.
  */
 mok_status mok_forward_mxfp8(mok_workspace* ws, const void* schedule, size_t schedule_bytes, const uint8_t* x_codes,
                              const uint8_t* x_scale, const float* router_weights, const mok_weights* weights,
@@ -442,11 +444,13 @@ size_t mok_router_scratch_bytes(int64_t T, int32_t experts);
  *   key   = logit + bias, one fp32 addition (bias fp32 [experts], nullable:
  *           it selects only, the weights do not see it)
  *   ids   int64 [T, k]: the k largest keys in descending order, ties to the
- *         lowest expert id (-0 and +0 tie). A key of -inf is never chosen: where fewer than
- *         k are left, id -1 and weight 0 (mok_build_schedule does not
- *         dispatch such an assignment).
+ *         lowest expert id (-0 and +0 tie). A key of -inf is never chosen:
+ *         where fewer than k are left, id -1 and weight 0 (mok_build_schedule
+ *         does not dispatch such an assignment).
  *   weights fp32 [T, k]: the scores of the chosen, divided by their sum if
- *         `renormalize`, times `scale`.
+ *         `renormalize`, times `scale`. A batch of 32768 tokens or more may
+ *         add a token's scores in another order than a smaller one: its ids
+ *         are the same, its weights up to 2^-17 of them apart.
  * token_mask (nullable, one byte per token): tokens with a 0 get ids -1 and
  * weights 0, whatever their logits hold. A row with a key that is NaN or
  * +inf has no order: ids -1 and weights NaN.

@@ -81,7 +81,8 @@ class MoKRuntime:
         changed since they were made. A graph does not ask at its replays: in
         a capture the codes of a weight in training are made in the graph,
         and what a capture made is not kept (it holds nothing before the
-        first replay)."""
+        first replay). A captured inference forward reads the codes that were
+        kept at its capture: capture again after the weights change."""
         key = (name, transposed)
         capturing = torch.cuda.is_current_stream_capturing()
         hit = self._q.get(key)
@@ -359,7 +360,8 @@ class MoKRouter(torch.nn.Module):
     ``router_topk``. forward(x [T, H], token_mask) -> (weights fp32 [T, k],
     ids int64 [T, k]), and with ``losses`` also (counts, losses). With
     ``selection_bias`` the module keeps an fp32 buffer that shifts the choice
-    alone, for balancing without a loss: move it by the counts."""
+    alone, for balancing without a loss: move it by the counts, after the
+    backward pass (which reads it, so autograd refuses an earlier change)."""
 
     def __init__(self, hidden: int, num_experts: int, topk: int, scoring: str = "softmax", renormalize: bool = True,
                  scale: float = 1.0, selection_bias: bool = False, losses: bool = False, device=None):

@@ -30,17 +30,19 @@
 // The tensors' addresses travel in the kernel's arguments, up to 48 per
 // launch: nothing is copied to the device and nothing is kept between calls.
 //
-// Stores go past the caches, and loads too (STREAM) where the tensors exceed
-// the last-level cache. Groups of 4, fp32 states: 1e8 elements with masters 515
-// us -> 517 with plain loads, 473 with loads past the caches; 1e7, which the
-// cache holds, 43 -> 41 and 46. 8 bits with masters: 1.6e7 elements 45.3 -> 41.5
-// with plain loads; 1e8 329 -> 289 with loads past the caches (before the
-// following). The 8-bit update was bound by its instructions
-// first: packed conversions, the hardware's root and no clamps took it from
-// 229 to 165 us (bf16, no master: 6.1 TB/s) and from 289 to 279 with a master.
+// Measured now: 1e8 bf16 elements with masters 464-473 us with fp32 states
+// (5.9-6.0 TB/s), 260 with 8 bits (6.2 TB/s), 165-170 with 8 bits and no masters
+// (6.0-6.1 TB/s); 1e8 fp32 elements 470 with fp32 states, 274 with 8 bits.
 //
-// Measured, 1e8 bf16 elements with masters: 473 us with fp32 states (5.9
-// TB/s), 260 us with 8 bits (6.2 TB/s).
+// What led there, each pair timed in turn on the code of its time (1e8 bf16
+// elements unless a number is given):
+//   8-bit update with packed conversions, the hardware's root and no clamps (it
+//     was bound by its instructions): no masters 229 -> 165 us
+//   stores past the caches always, loads only where the tensors exceed the
+//     last-level cache (STREAM): 8 bits with masters 329 -> 289, fp32 states with
+//     masters 517 with loads through the caches, 473 past them; 1e7 elements, which
+//     the cache holds, 41 and 46, so there they go through it
+//   one turn per workgroup instead of four: see TABLE below
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -83,7 +85,10 @@ static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments");
 
 // u for elements 2i and 2i + 1: one 32-bit hash (multiply and xor-shift
 // rounds over the pair's number and the seed), 16 bits each. x = the pair's
-// number * kPairStep + seed.
+// number * kPairStep + seed. Of the odd multipliers this asks only that any
+// flipped bit of x flips each bit of the hash about every other time (between
+// 49.1 and 50.9 % over 2^20 draws) and that the two halves, and neighbouring
+// pairs, are not correlated (below 0.2 %). The oracle holds the same ones.
 constexpr uint32_t kPairStep = 0x9E3779B1u;
 __device__ __forceinline__ uint32_t pair_bits(uint32_t x) {
   x ^= x >> 16;
@@ -238,9 +243,9 @@ __device__ __forceinline__ float library_power(int k) {
 
 // TABLE: the workgroup makes a table of the powers first and takes four turns;
 // else it takes one turn and finds them as it goes. Workgroups of one turn
-// sweep memory as a closer front: 1e8 elements, bf16 with masters 280 -> 260
-// us, fp32 287 -> 274, and with fp32 states, which need no powers, 541 -> 514
-// (8 neighbouring elements per lane then).
+// sweep memory as a closer front: with fp32 states, which need no powers, 541
+// -> 514 us against four turns (1e8 bf16 elements with masters, 8 neighbouring
+// elements per lane then), with 8 bits 280 -> 260 (fp32 parameters 287 -> 274).
 // Where an element moves only 10 bytes (8 bits, bf16, no masters) the powers'
 // instructions weigh more than that: 165 us with the table, 188 without.
 template <typename PT, bool MASTER, typename GT, bool S8, bool TABLE, bool STREAM>

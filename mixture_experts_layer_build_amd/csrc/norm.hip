@@ -40,7 +40,7 @@ namespace {
 // E4M3 codes and E8M0 scale of a lane's W elements of a 32-element block (32
 // / W consecutive lanes), by the block rule of the quantizer (X = clamp(floor(
 // log2 amax) - 8, -127, 127)). A block that holds an infinity or a NaN gets
-// the NaN scale 0xFF, so its consumers see it.
+// the NaN scale 0xFF, and the layer's products with it are NaN.
 template <int W>
 __device__ __forceinline__ void store_mxfp8(const float (&y)[W], uint8_t* codes, uint8_t* scale, bool first) {
   uint32_t amax = 0;
@@ -191,7 +191,10 @@ __global__ void __launch_bounds__(BLOCK) rms_norm_rows(NormFwd a) {
 }
 
 // Any width, stride and alignment: one workgroup per row, one element per
-// lane and load, the row read twice (the second time from cache).
+// lane and load, the row read twice (the second time from cache). Two-byte
+// loads and the second pass are what it costs: 4096 x 5003 bf16 with residual 63
+// us, 4096 x 20480 287 (floors 35 and 145); the backward, which also adds dw up
+// in memory, 188 and 1250. Widths of models take the other kernel.
 template <typename XT, typename RT>
 __global__ void __launch_bounds__(256) rms_norm_any(NormFwd a) {
   constexpr bool kRes = !std::is_void<RT>::value;

@@ -4,7 +4,10 @@ Every parameter of one type is updated by one kernel launch per 48 tensors
 (``ops.adamw_step``). The moments are kept in fp32, or in 8 bits (E4M3 codes
 with one scale per 32 elements: about a quarter of the memory). bf16
 parameters get an fp32 master by default: an update smaller than half a bf16
-step would otherwise be lost.
+step would otherwise be lost. The master is taken from the parameter at its
+first step; a parameter changed by others afterwards (a checkpoint loaded into
+the model alone) is written from the master again at the next one, so load the
+optimizer's state with the model's, or delete the parameter's state.
 """
 from __future__ import annotations
 
