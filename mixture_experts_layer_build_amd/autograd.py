@@ -67,6 +67,8 @@ class MoKRuntime:
         self.mode = mode
         # name -> (weak reference to the weight, its version, its address, codes, scales)
         self._q: dict = {}
+        # address -> (codes, scales) that a captured graph reads: kept when the weight's are made again
+        self._in_graphs: dict = {}
 
     def workspace(self, device: torch.device):
         if device.type != "cuda":
@@ -82,13 +84,16 @@ class MoKRuntime:
         a capture the codes of a weight in training are made in the graph,
         and what a capture made is not kept (it holds nothing before the
         first replay). A captured inference forward reads the codes that were
-        kept at its capture: capture again after the weights change."""
+        kept at its capture, which then live as long as this object: capture
+        again after the weights change."""
         key = (name, transposed)
         capturing = torch.cuda.is_current_stream_capturing()
         hit = self._q.get(key)
         if hit is not None and not (capturing and trained):
             ref, version, ptr, codes, sc = hit
             if ref() is w and version == w._version and ptr == w.data_ptr():
+                if capturing:
+                    self._in_graphs[codes.data_ptr()] = (codes, sc)
                 return codes, sc
         if transposed:
             codes, sc = mxfp8_quantize_transposed(w.detach())

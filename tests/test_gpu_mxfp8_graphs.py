@@ -73,3 +73,23 @@ def test_a_capture_leaves_no_codes_behind():
             torch.cuda.synchronize()
             assert torch.equal(got, want)
             assert torch.equal(moe_layer(rt, x, rw, ids, *w), want)
+
+
+def test_a_captured_inference_forward_keeps_the_codes_it_reads():
+    x, rw, ids, _, w = inputs()
+    rt = runtime()
+    with torch.no_grad():
+        want = moe_layer(rt, x, rw, ids, *w)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = moe_layer(rt, x, rw, ids, *w)
+        for p in w:
+            p.mul_(2)
+        assert not torch.equal(moe_layer(rt, x, rw, ids, *w), want)  # codes made again
+        others = [torch.full((n,), 0x55, dtype=torch.uint8, device="cuda")  # would lie where the first codes were
+                  for p in w for n in (p.numel(), p.numel() // 32) for _ in range(3)]
+        for _ in range(2):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+        assert all((t == 0x55).all() for t in others)
