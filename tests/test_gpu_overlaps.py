@@ -76,3 +76,29 @@ def test_a_backward_of_any_width_runs_in_place(cols):
         t = [dy.clone(), s.clone(), d.clone()]
         got = mok.rms_norm_backward(t[0], t[1], rstd, w, t[2], dx=t[k])
         assert torch.equal(t[k], dx) and torch.equal(got[0], ds) and torch.equal(got[1], dw)
+
+
+@pytest.mark.parametrize("shuffled", [False, True])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_one_overlap_among_many_tensors_is_found(shuffled, bits):
+    """40 tensors in one buffer per list, in their order or in none: no
+    overlap, then one shifted into its neighbour, in each list in turn."""
+    n, size = 40, 64
+    order = torch.randperm(n, generator=torch.Generator().manual_seed(2)).tolist() if shuffled else range(n)
+    buf = torch.zeros(4, n * size, device="cuda")
+    codes = torch.zeros(2, n * size, dtype=torch.uint8, device="cuda")
+    scales = torch.zeros(2, n * 2, dtype=torch.uint8, device="cuda")
+
+    def lists(which, at):
+        cut = lambda b, l, w: [b[i * w - (1 if (l, i) == (which, at) else 0):][:w] for i in order]  # noqa: E731
+        p, g = cut(buf[0], 0, size), cut(buf[1], 1, size)
+        if bits == 32:
+            return p, g, cut(buf[2], 2, size), cut(buf[3], 3, size)
+        return (p, g, *(list(zip(cut(codes[k], 2 + k, size), cut(scales[k], 4 + k, 2))) for k in range(2)))
+
+    mok.adamw_step(*lists(None, None), step=1, lr=1e-3)
+    mok.adamw_step(*lists(1, 7), step=1, lr=1e-3)  # gradients are only read
+    for which in (0, 2, 3) if bits == 32 else (0, 2, 3, 4, 5):
+        for at in (1, 23, n - 1):
+            with pytest.raises(ValueError, match="overlaps"):
+                mok.adamw_step(*lists(which, at), step=1, lr=1e-3)
