@@ -531,6 +531,124 @@ typedef struct mok_adamw {
 
 mok_status mok_adamw_step(const mok_adamw* step, void* stream);
 
+/* ---- the experts' products outside the fused layer --------------------
+ *
+ * The matrix products of experts by themselves: ragged ones for training and
+ * prompts (any other expert function stands on these), and 4-bit weights with
+ * their product and the layer on them, for decoding. The conventions of the
+ * operators around the layer hold here too. */
+
+/*
+ * Matrix product grouped by expert: y[r] = W_e x[r] for the rows r of expert
+ * e, offsets[e] <= r < offsets[e + 1]. x bf16 [rows, k] with row stride ld_x,
+ * weight bf16 [experts, n, k] dense, offsets device int32 or int64 (flag
+ * offsets_int64) [experts + 1], not decreasing, y bf16 [rows, n] with row
+ * stride ld_y; sums in fp32, rounded once. Rows before offsets[0] and from
+ * offsets[experts] on belong to no expert: with zero_rest = 1 they get zeros,
+ * with 0 they are left as they were. What such rows of x hold reaches
+ * nothing. Each bound is taken as if clamped to [0, rows]: offsets that
+ * decrease give unspecified rows of y, and no access outside the tensors.
+ * Every width, stride and alignment is accepted; n and k, ld_x and ld_y that
+ * are multiples of 8, with 16-byte aligned tensors, run the fast kernels.
+ * 1 <= experts <= 1024, n and k at most 2^20, ld at most 2^21, rows at
+ * most 2^30.
+ */
+mok_status mok_grouped_matmul(const void* x, int64_t ld_x, const void* weight, const void* offsets, int offsets_int64,
+                              int64_t rows, int32_t experts, int64_t n, int64_t k, void* y, int64_t ld_y,
+                              int zero_rest, void* stream);
+
+/*
+ * Its gradients. dx[r] = W_e^T dy[r], bf16 [rows, k], rows of no expert as
+ * above. d_weight[e] = sum over e's rows of dy[r] x[r]^T, [experts, n, k] in
+ * bf16 or fp32, written in full: zeros for an expert without rows.
+ */
+mok_status mok_grouped_matmul_dx(const void* dy, int64_t ld_dy, const void* weight, const void* offsets,
+                                 int offsets_int64, int64_t rows, int32_t experts, int64_t n, int64_t k, void* dx,
+                                 int64_t ld_dx, int zero_rest, void* stream);
+mok_status mok_grouped_matmul_dw(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, const void* offsets,
+                                 int offsets_int64, int64_t rows, int32_t experts, int64_t n, int64_t k,
+                                 void* d_weight, int d_weight_fp32, void* stream);
+
+/* Formats of 4-bit weights: a code for every element, two to a byte along a
+ * row (the even column in the low half), and a scale for every group of
+ * consecutive elements of a row. */
+typedef enum mok_w4_format {
+  MOK_W4_INT4 = 0, /* value (code - zero) * scale; codes 0..15, scale bf16, zero one byte per group, or 8 for all;
+                      groups of 32, 64 or 128 */
+  MOK_W4_MXFP4 = 1 /* code E2M1 (sign in bit 3), scale E8M0, groups of 32 (OCP MXFP4) */
+} mok_w4_format;
+
+/* One weight: codes [.., n, k/2], scale and zero (nullable) [.., n, k/group]. */
+typedef struct mok_w4 {
+  const uint8_t* codes;
+  const void* scale;
+  const uint8_t* zero;
+} mok_w4;
+
+/*
+ * Quantizes src [rows, cols] (bf16 or fp32, row stride ld_src). Per group:
+ *   int4, zero == NULL: scale = bf16(amax / 7), code = clamp(rint(v / scale),
+ *     -8, 7) + 8 (8 where the scale is 0)
+ *   int4 with zero: lo = min(0, min v), hi = max(0, max v), scale =
+ *     bf16((hi - lo) / 15), zero = clamp(rint(-lo / scale), 0, 15), code =
+ *     clamp(rint(v / scale) + zero, 0, 15) (both 0 where the scale is 0)
+ *   MXFP4: X = clamp(floor(log2 amax) - 2, -127, 127), -127 for zeros; scale
+ *     byte X + 127, code = v / 2^X to the nearest, ties to even, at most 6
+ * in fp32, divisions and roundings as IEEE has them (rint: ties to even), so
+ * that codes and scales are those of the elementary tensor operations. Inputs
+ * must be finite, hi - lo within fp32. cols a multiple of `group`, ld_src of
+ * 8, src 16-byte and codes 4-byte aligned (MOK_ERR_UNSUPPORTED otherwise).
+ */
+mok_status mok_w4_quantize(const void* src, int src_is_fp32, int64_t rows, int64_t cols, int64_t ld_src,
+                           int32_t format, int32_t group, uint8_t* codes, void* scale, uint8_t* zero, void* stream);
+
+/* The values of 4-bit weights, rounded to bf16: dst [rows, cols] dense,
+ * 16-byte aligned, codes 4-byte aligned. */
+mok_status mok_w4_dequantize(const mok_w4* weight, int64_t rows, int64_t cols, int32_t format, int32_t group,
+                             void* dst, void* stream);
+
+/*
+ * y[t] = W x[t] for T rows of x bf16 [T, k] and one 4-bit weight [n, k]: the
+ * products are exact, sums in fp32, y bf16 [T, n] rounded once. Made for few
+ * rows (each 64 of them read the weight once); for a prompt, dequantize. k a
+ * multiple of the group, ld_x of 8, x and codes 16-byte aligned
+ * (MOK_ERR_UNSUPPORTED otherwise); T at most 65535, n < 2^31 / 16, k at most
+ * 2^20.
+ */
+mok_status mok_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, int64_t k, int32_t format, int32_t group,
+                         const mok_w4* weight, void* y, int64_t ld_y, void* stream);
+
+/*
+ * The layer on 4-bit experts, for few tokens, without schedule or workspace:
+ *   out[t] = sum over j of w[t, j] * Wd_e h,  h = silu(g) * u, g = Wg_e x[t],
+ *   u = Wu_e x[t], e = ids[t, j], plus the shared expert's with weight 1.
+ * Ids outside [0, experts) are no choice; nothing is dropped. A token without
+ * a choice gets the shared expert's output, or zeros. h is rounded to bf16 as
+ * in mok_forward (the matrix instructions take bf16), every other step is
+ * fp32. swiglu_limit as in mok_config. All six weights have one format and
+ * group, which divides hidden, intermediate and shared_intermediate; zero
+ * points in all of them or in none. gate and up [experts, intermediate,
+ * hidden], down [experts, hidden, intermediate], shared ones without the
+ * first dimension. T * topk <= 8192, T <= 8192, topk <= 64, experts <= 1024,
+ * sizes at most 2^16; codes, x and scratch 16-byte aligned
+ * (MOK_ERR_UNSUPPORTED otherwise). scratch: the call's own until its work has
+ * run.
+ */
+typedef struct mok_w4_layer {
+  uint32_t struct_size;
+  int32_t hidden, intermediate, num_experts, topk, shared_intermediate; /* 0: no shared expert */
+  int32_t format, group;
+  float swiglu_limit; /* 0: none */
+  mok_w4 routed_gate, routed_up, routed_down, shared_gate, shared_up, shared_down;
+} mok_w4_layer;
+
+/* Bytes of mok_forward_w4's scratch; 0 if the layer or T is invalid. */
+size_t mok_forward_w4_scratch_bytes(const mok_w4_layer* layer, int64_t T);
+
+mok_status mok_forward_w4(const mok_w4_layer* layer, const void* x, const float* router_weights,
+                          const int64_t* top_experts, int64_t T, void* out, void* scratch, size_t scratch_bytes,
+                          void* stream);
+
 /* ---- diagnostics (these synchronise; never on the hot path) ---------- */
 
 /* Per-kernel event timing inside a workspace: when enabled, every launch

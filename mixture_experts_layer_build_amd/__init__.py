@@ -22,14 +22,16 @@ import torch
 
 from . import _lib
 from ._lib import (MOK_MODE_BF16, MOK_MODE_MXFP8, HDR_FIELDS, TILE_BMS, MokError)
-from .ops import adamw_step, rms_norm, rms_norm_backward, rms_norm_mxfp8, router_topk, router_topk_backward
+from .ops import (adamw_step, forward_w4, grouped_matmul, grouped_matmul_backward, rms_norm, rms_norm_backward,
+                  rms_norm_mxfp8, router_topk, router_topk_backward, w4_dequantize, w4_matmul, w4_quantize)
 
 __all__ = ["MoKConfig", "Workspace", "create_workspace", "get_workspace", "clear_workspace_cache",
            "build_schedule", "forward", "forward_static", "backward", "mxfp8_quantize",
            "mxfp8_quantize_transposed", "mxfp8_backward_weights", "schedule_fields",
            "schedule_bytes", "context_bytes", "workspace_bytes", "MokError", "MOK_MODE_BF16", "MOK_MODE_MXFP8", "lib",
            "forward_mxfp8", "rms_norm", "rms_norm_mxfp8", "rms_norm_backward", "router_topk", "router_topk_backward",
-           "adamw_step"]
+           "adamw_step", "grouped_matmul", "grouped_matmul_backward", "w4_quantize", "w4_dequantize", "w4_matmul",
+           "forward_w4"]
 
 
 def lib():

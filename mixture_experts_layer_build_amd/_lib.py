@@ -22,6 +22,9 @@ MOK_MODE_MXFP8 = 1
 MOK_ROUTER_SOFTMAX = 0
 MOK_ROUTER_SIGMOID = 1
 
+MOK_W4_INT4 = 0
+MOK_W4_MXFP4 = 1
+
 # Every symbol include/mok.h declares (checked by the CPU tests).
 EXPORTS = (
     "mok_status_string", "mok_validate_config", "mok_schedule_bytes", "mok_schedule_layout_query",
@@ -30,7 +33,8 @@ EXPORTS = (
     "mok_workspace_set_timing", "mok_workspace_set_timing_mask", "mok_workspace_read_timing",
     "mok_workspace_read_status", "mok_forward_mxfp8", "mok_rms_norm", "mok_rms_norm_scratch_bytes",
     "mok_rms_norm_backward", "mok_router_scratch_bytes", "mok_router_topk", "mok_router_topk_backward",
-    "mok_adamw_step",
+    "mok_adamw_step", "mok_grouped_matmul", "mok_grouped_matmul_dx", "mok_grouped_matmul_dw", "mok_w4_quantize",
+    "mok_w4_dequantize", "mok_w4_matmul", "mok_forward_w4_scratch_bytes", "mok_forward_w4",
 )
 
 HDR_FIELDS = ("T", "k", "E", "C", "P", "rows_cap", "n_mb", "minibatch", "dropped", "invalid",
@@ -85,6 +89,17 @@ class MokAdamW(C.Structure):
         ("seed", C.c_uint32)]
 
 
+class MokW4(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("codes", "scale", "zero")]
+
+
+class MokW4Layer(C.Structure):
+    _fields_ = [("struct_size", C.c_uint32)] + [(n, C.c_int32) for n in (
+        "hidden", "intermediate", "num_experts", "topk", "shared_intermediate", "format", "group")] + [
+        ("swiglu_limit", C.c_float)] + [(n, MokW4) for n in (
+            "routed_gate", "routed_up", "routed_down", "shared_gate", "shared_up", "shared_down")]
+
+
 _lib = None
 
 
@@ -134,6 +149,14 @@ def load() -> C.CDLL:
         "mok_router_topk_backward": (i32, [vp, vp, i32, i64, i64, C.c_int32, C.c_int32, vp, vp, C.c_int32, i32, f32,
                                            vp, vp, vp, vp, vp]),
         "mok_adamw_step": (i32, [C.POINTER(MokAdamW), vp]),
+        "mok_grouped_matmul": (i32, [vp, i64, vp, vp, i32, i64, C.c_int32, i64, i64, vp, i64, i32, vp]),
+        "mok_grouped_matmul_dx": (i32, [vp, i64, vp, vp, i32, i64, C.c_int32, i64, i64, vp, i64, i32, vp]),
+        "mok_grouped_matmul_dw": (i32, [vp, i64, vp, i64, vp, i32, i64, C.c_int32, i64, i64, vp, i32, vp]),
+        "mok_w4_quantize": (i32, [vp, i32, i64, i64, i64, C.c_int32, C.c_int32, vp, vp, vp, vp]),
+        "mok_w4_dequantize": (i32, [C.POINTER(MokW4), i64, i64, C.c_int32, C.c_int32, vp, vp]),
+        "mok_w4_matmul": (i32, [vp, i64, i64, i64, i64, C.c_int32, C.c_int32, C.POINTER(MokW4), vp, i64, vp]),
+        "mok_forward_w4_scratch_bytes": (sz, [C.POINTER(MokW4Layer), i64]),
+        "mok_forward_w4": (i32, [C.POINTER(MokW4Layer), vp, vp, vp, i64, vp, vp, sz, vp]),
     })
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

@@ -47,7 +47,7 @@ from . import (MOK_MODE_BF16, MOK_MODE_MXFP8, MoKConfig, backward, build_schedul
                get_workspace, mxfp8_quantize, mxfp8_quantize_transposed, ops)
 
 __all__ = ["MoKRuntime", "MoKAutogradFunction", "MoKExperts", "moe_layer", "rms_norm", "MoKRMSNorm", "router_topk",
-           "MoKRouter"]
+           "MoKRouter", "grouped_matmul", "MoKGroupedLinear"]
 
 _WEIGHT_NAMES = ("shared_gate", "shared_up", "shared_down", "routed_gate", "routed_up", "routed_down")
 
@@ -390,3 +390,49 @@ class MoKRouter(torch.nn.Module):
     def extra_repr(self) -> str:
         return (f"hidden={self.weight.shape[1]}, experts={self.weight.shape[0]}, topk={self.topk}, "
                 f"scoring={self.scoring}, renormalize={self.renormalize}, scale={self.scale}")
+
+
+class GroupedMatmulFunction(torch.autograd.Function):
+    """The grouped product, differentiable in x and the weight."""
+
+    @staticmethod
+    def forward(ctx, x, weight, offsets):
+        ctx.save_for_backward(x, weight, offsets)
+        return ops.grouped_matmul(x, weight, offsets)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, offsets = ctx.saved_tensors
+        need_x, need_w = ctx.needs_input_grad[:2]
+        dx, dw = ops.grouped_matmul_backward(dy.contiguous(), x, weight, offsets, need_dx=need_x, need_dw=need_w)
+        return dx, dw, None
+
+
+def grouped_matmul(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor) -> torch.Tensor:
+    """Differentiable ``ops.grouped_matmul``: y[r] = weight[e] @ x[r] for the
+    rows of expert e, zeros for rows of none."""
+    return GroupedMatmulFunction.apply(x, weight, offsets)
+
+
+class MoKGroupedLinear(torch.nn.Module):
+    """A linear map per expert (bf16 [experts, out, in], no bias), for expert
+    functions other than the layer's: forward(x [rows, in], offsets [experts +
+    1]) -> [rows, out], the rows sorted by expert."""
+
+    def __init__(self, num_experts: int, in_features: int, out_features: int, device=None):
+        super().__init__()
+        self.weight = torch.nn.Parameter(
+            torch.empty(num_experts, out_features, in_features, dtype=torch.bfloat16, device=device))
+
+    @torch.no_grad()
+    def init_weights(self, init_std: float = 0.02, generator: torch.Generator | None = None) -> None:
+        """Normal(0, init_std) draws, rounded to bf16."""
+        self.weight.copy_(torch.randn(self.weight.shape, generator=generator, dtype=torch.float32).mul_(init_std))
+
+    def forward(self, x, offsets):
+        return grouped_matmul(x, self.weight, offsets)
+
+    def extra_repr(self) -> str:
+        e, n, k = self.weight.shape
+        return f"experts={e}, in_features={k}, out_features={n}"

@@ -877,6 +877,157 @@ extern "C" mok_status mok_adamw_step(const mok_adamw* u, void* stream) {
 }
 
 // ------------------------------------------------------------------------
+// The experts' products outside the layer
+// ------------------------------------------------------------------------
+namespace {
+bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+
+// Checks and launches one of the grouped products; cols_*: the shortest row
+// of a, of b (0: b is the weight) and of the output (0: it is the weight's).
+mok_status run_grouped(GroupedOp op, const GroupedArgs& g, int64_t cols_a, int64_t cols_b, int64_t cols_out,
+                       void* stream) {
+  if (g.rows < 0 || g.E < 1 || g.n < 1 || g.k < 1 || !flag(g.offsets64) || !flag(g.zero_rest) || !flag(g.out_fp32))
+    return MOK_ERR_INVALID_ARGUMENT;
+  constexpr int64_t kMaxCols = 1 << 20, kMaxLd = 1 << 21;
+  if (g.E > kGroupedMaxExperts || g.n > kMaxCols || g.k > kMaxCols || g.rows > (1 << 30)) return MOK_ERR_UNSUPPORTED;
+  if (g.rows == 0 && op != GROUPED_DW) return MOK_OK;
+  if (!g.out || !g.offsets) return MOK_ERR_INVALID_ARGUMENT;
+  if (g.rows > 0) {
+    if (!g.a || !g.b || g.ld_a < cols_a || g.ld_b < cols_b || g.ld_out < cols_out) return MOK_ERR_INVALID_ARGUMENT;
+    if (g.ld_a > kMaxLd || g.ld_b > kMaxLd || g.ld_out > kMaxLd) return MOK_ERR_UNSUPPORTED;
+  }
+  if (!element_aligned(g.a, 0) || !element_aligned(g.b, 0) || !element_aligned(g.out, g.out_fp32) ||
+      !aligned(g.offsets, g.offsets64 ? 8 : 4))
+    return MOK_ERR_INVALID_ARGUMENT;
+  const int cus = current_cus();
+  if (cus <= 0) return MOK_ERR_HIP;
+  return to_status(launch_grouped(op, g, cus, (hipStream_t)stream));
+}
+
+// Format and group of 4-bit weights whose rows have `k` elements.
+mok_status check_w4(int32_t format, int32_t group, int64_t k) {
+  if (format != MOK_W4_INT4 && format != MOK_W4_MXFP4) return MOK_ERR_INVALID_ARGUMENT;
+  if (group != 32 && (format == MOK_W4_MXFP4 || (group != 64 && group != 128))) return MOK_ERR_UNSUPPORTED;
+  return k % group == 0 ? MOK_OK : MOK_ERR_UNSUPPORTED;
+}
+// One weight's pointers: codes at a multiple of `align` bytes.
+mok_status check_w4(const mok_w4& w, int32_t format, int align) {
+  if (!w.codes || !w.scale || (format == MOK_W4_MXFP4 && w.zero)) return MOK_ERR_INVALID_ARGUMENT;
+  if (format == MOK_W4_INT4 && !aligned(w.scale, 2)) return MOK_ERR_INVALID_ARGUMENT;
+  return aligned(w.codes, align) ? MOK_OK : MOK_ERR_UNSUPPORTED;
+}
+}  // namespace
+
+extern "C" mok_status mok_grouped_matmul(const void* x, int64_t ld_x, const void* weight, const void* offsets,
+                                         int offsets_int64, int64_t rows, int32_t experts, int64_t n, int64_t k,
+                                         void* y, int64_t ld_y, int zero_rest, void* stream) {
+  GroupedArgs g{};
+  g.a = x, g.ld_a = ld_x, g.b = weight, g.offsets = offsets, g.offsets64 = offsets_int64;
+  g.rows = rows, g.E = experts, g.n = n, g.k = k, g.out = y, g.ld_out = ld_y, g.zero_rest = zero_rest;
+  return run_grouped(GROUPED_Y, g, k, 0, n, stream);
+}
+
+extern "C" mok_status mok_grouped_matmul_dx(const void* dy, int64_t ld_dy, const void* weight, const void* offsets,
+                                            int offsets_int64, int64_t rows, int32_t experts, int64_t n, int64_t k,
+                                            void* dx, int64_t ld_dx, int zero_rest, void* stream) {
+  GroupedArgs g{};
+  g.a = dy, g.ld_a = ld_dy, g.b = weight, g.offsets = offsets, g.offsets64 = offsets_int64;
+  g.rows = rows, g.E = experts, g.n = n, g.k = k, g.out = dx, g.ld_out = ld_dx, g.zero_rest = zero_rest;
+  return run_grouped(GROUPED_DX, g, n, 0, k, stream);
+}
+
+extern "C" mok_status mok_grouped_matmul_dw(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
+                                            const void* offsets, int offsets_int64, int64_t rows, int32_t experts,
+                                            int64_t n, int64_t k, void* d_weight, int d_weight_fp32, void* stream) {
+  GroupedArgs g{};
+  g.a = dy, g.ld_a = ld_dy, g.b = x, g.ld_b = ld_x, g.offsets = offsets, g.offsets64 = offsets_int64;
+  g.rows = rows, g.E = experts, g.n = n, g.k = k, g.out = d_weight, g.out_fp32 = d_weight_fp32;
+  return run_grouped(GROUPED_DW, g, n, k, 0, stream);
+}
+
+extern "C" mok_status mok_w4_quantize(const void* src, int src_is_fp32, int64_t rows, int64_t cols, int64_t ld_src,
+                                      int32_t format, int32_t group, uint8_t* codes, void* scale, uint8_t* zero,
+                                      void* stream) {
+  if (rows < 0 || cols < 0 || !flag(src_is_fp32)) return MOK_ERR_INVALID_ARGUMENT;
+  const mok_status st = check_w4(format, group, cols);
+  if (st != MOK_OK || rows == 0 || cols == 0) return st;
+  if (!src || ld_src < cols) return MOK_ERR_INVALID_ARGUMENT;
+  const mok_status sw = check_w4(mok_w4{codes, scale, zero}, format, 4);
+  if (sw != MOK_OK) return sw;
+  if (!aligned(src, 16) || ld_src % 8 != 0) return MOK_ERR_UNSUPPORTED;
+  if (rows > kW4MaxElements / cols || ld_src > kW4MaxElements / rows) return MOK_ERR_UNSUPPORTED;
+  return to_status(
+      launch_w4_quantize(src, src_is_fp32, rows, cols, ld_src, format, group, codes, scale, zero, (hipStream_t)stream));
+}
+
+extern "C" mok_status mok_w4_dequantize(const mok_w4* weight, int64_t rows, int64_t cols, int32_t format,
+                                        int32_t group, void* dst, void* stream) {
+  if (rows < 0 || cols < 0 || !weight) return MOK_ERR_INVALID_ARGUMENT;
+  const mok_status st = check_w4(format, group, cols);
+  if (st != MOK_OK || rows == 0 || cols == 0) return st;
+  if (!dst) return MOK_ERR_INVALID_ARGUMENT;
+  const mok_status sw = check_w4(*weight, format, 4);
+  if (sw != MOK_OK) return sw;
+  if (!aligned(dst, 16) || rows > kW4MaxElements / cols) return MOK_ERR_UNSUPPORTED;
+  return to_status(launch_w4_dequantize(*weight, rows, cols, format, group, dst, (hipStream_t)stream));
+}
+
+extern "C" mok_status mok_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, int64_t k, int32_t format,
+                                    int32_t group, const mok_w4* weight, void* y, int64_t ld_y, void* stream) {
+  if (T < 0 || n < 1 || k < 1 || !weight) return MOK_ERR_INVALID_ARGUMENT;
+  const mok_status st = check_w4(format, group, k);
+  if (st != MOK_OK) return st;
+  if (T > 65535 || n >= (1 << 27) || k > (1 << 20)) return MOK_ERR_UNSUPPORTED;
+  if (T == 0) return MOK_OK;
+  if (!x || !y || ld_x < k || ld_y < n || !element_aligned(y, 0)) return MOK_ERR_INVALID_ARGUMENT;
+  const mok_status sw = check_w4(*weight, format, 16);
+  if (sw != MOK_OK) return sw;
+  if (!aligned(x, 16) || ld_x % 8 != 0 || ld_x > (1LL << 40) || ld_y > (1LL << 40)) return MOK_ERR_UNSUPPORTED;
+  return to_status(launch_w4_matmul(x, ld_x, T, n, k, format, group, *weight, y, ld_y, (hipStream_t)stream));
+}
+
+// The layer's sizes (its pointers are checked by the call alone).
+static mok_status check_w4_layer(const mok_w4_layer* l, int64_t T) {
+  if (!l || l->struct_size != sizeof(mok_w4_layer) || T < 0) return MOK_ERR_INVALID_ARGUMENT;
+  if (l->hidden < 1 || l->intermediate < 1 || l->num_experts < 1 || l->topk < 1 || l->shared_intermediate < 0)
+    return MOK_ERR_INVALID_ARGUMENT;
+  if (!(l->swiglu_limit >= 0.0f) || !std::isfinite(l->swiglu_limit)) return MOK_ERR_INVALID_ARGUMENT;
+  constexpr int32_t kMax = 1 << 16;
+  if (l->hidden > kMax || l->intermediate > kMax || l->shared_intermediate > kMax) return MOK_ERR_UNSUPPORTED;
+  if (l->num_experts > 1024 || l->topk > 64 || T > 8192 || T * l->topk > 8192) return MOK_ERR_UNSUPPORTED;
+  for (const int32_t width : {l->hidden, l->intermediate, l->shared_intermediate}) {
+    const mok_status st = check_w4(l->format, l->group, width);
+    if (st != MOK_OK) return st;
+  }
+  return MOK_OK;
+}
+
+extern "C" size_t mok_forward_w4_scratch_bytes(const mok_w4_layer* layer, int64_t T) {
+  return check_w4_layer(layer, T) == MOK_OK ? w4_layer_scratch(*layer, T) : 0;
+}
+
+extern "C" mok_status mok_forward_w4(const mok_w4_layer* layer, const void* x, const float* router_weights,
+                                     const int64_t* top_experts, int64_t T, void* out, void* scratch,
+                                     size_t scratch_bytes, void* stream) {
+  const mok_status st = check_w4_layer(layer, T);
+  if (st != MOK_OK || T == 0) return st;
+  const mok_w4_layer& l = *layer;
+  if (!x || !router_weights || !top_experts || !out || !scratch) return MOK_ERR_INVALID_ARGUMENT;
+  if (!element_aligned(router_weights, 1) || !aligned(top_experts, 8) || !element_aligned(out, 0))
+    return MOK_ERR_INVALID_ARGUMENT;
+  const bool zero = l.routed_gate.zero != nullptr;
+  for (const mok_w4* w : {&l.routed_gate, &l.routed_up, &l.routed_down, &l.shared_gate, &l.shared_up, &l.shared_down}) {
+    if (w == &l.shared_gate && l.shared_intermediate == 0) break;
+    const mok_status sw = check_w4(*w, l.format, 16);
+    if (sw != MOK_OK) return sw;
+    if ((w->zero != nullptr) != zero) return MOK_ERR_INVALID_ARGUMENT;
+  }
+  if (!aligned(x, 16) || !aligned(scratch, 16)) return MOK_ERR_UNSUPPORTED;
+  if (scratch_bytes < w4_layer_scratch(l, T)) return MOK_ERR_BUFFER_TOO_SMALL;
+  return to_status(launch_w4_layer(l, x, router_weights, top_experts, T, out, scratch, (hipStream_t)stream));
+}
+
+// ------------------------------------------------------------------------
 // Diagnostics
 // ------------------------------------------------------------------------
 extern "C" const char* mok_kernel_name(int id) {

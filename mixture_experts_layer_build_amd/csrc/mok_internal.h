@@ -295,6 +295,38 @@ hipError_t launch_router_bwd(const RouterBwdArgs& r, int cus, hipStream_t s);
 
 hipError_t launch_adamw(const mok_adamw& u, int cus, hipStream_t s);
 
+// ---------------------------------------------------------------------------
+// The experts' products outside the layer
+// ---------------------------------------------------------------------------
+constexpr int kGroupedMaxExperts = 1024;         // whose tile table a workgroup holds
+constexpr int64_t kW4MaxElements = (int64_t)1 << 40;
+enum GroupedOp : int { GROUPED_Y = 0, GROUPED_DX = 1, GROUPED_DW = 2 };
+
+struct GroupedArgs {
+  const void* a;      // x (Y) or dy (DX, DW)
+  const void* b;      // weight (Y, DX) or x (DW)
+  const void* offsets;
+  int offsets64;
+  int64_t ld_a, ld_b;  // ld_b: DW only
+  int64_t rows, n, k;
+  int E;
+  void* out;
+  int64_t ld_out;      // Y, DX
+  int zero_rest;       // Y, DX
+  int out_fp32;        // DW
+};
+hipError_t launch_grouped(GroupedOp op, const GroupedArgs& g, int cus, hipStream_t s);
+
+hipError_t launch_w4_quantize(const void* src, int src_fp32, int64_t rows, int64_t cols, int64_t ld, int format,
+                              int group, uint8_t* codes, void* scale, uint8_t* zero, hipStream_t s);
+hipError_t launch_w4_dequantize(const mok_w4& w, int64_t rows, int64_t cols, int format, int group, void* dst,
+                                hipStream_t s);
+hipError_t launch_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, int64_t k, int format, int group,
+                            const mok_w4& w, void* y, int64_t ld_y, hipStream_t s);
+size_t w4_layer_scratch(const mok_w4_layer& l, int64_t T);
+hipError_t launch_w4_layer(const mok_w4_layer& l, const void* x, const float* router_w, const int64_t* ids, int64_t T,
+                           void* out, void* scratch, hipStream_t s);
+
 // The SwiGLU input limit the kernels apply: +inf (no clamp) unless the
 // configuration sets a positive finite limit.
 inline float swiglu_lim(const mok_config& c) {

@@ -34,6 +34,14 @@ decltype(&mok_router_scratch_bytes) f_router_scratch_bytes;
 decltype(&mok_router_topk) f_router_topk;
 decltype(&mok_router_topk_backward) f_router_topk_backward;
 decltype(&mok_adamw_step) f_adamw_step;
+decltype(&mok_grouped_matmul) f_grouped_matmul;
+decltype(&mok_grouped_matmul_dx) f_grouped_matmul_dx;
+decltype(&mok_grouped_matmul_dw) f_grouped_matmul_dw;
+decltype(&mok_w4_quantize) f_w4_quantize;
+decltype(&mok_w4_dequantize) f_w4_dequantize;
+decltype(&mok_w4_matmul) f_w4_matmul;
+decltype(&mok_forward_w4_scratch_bytes) f_forward_w4_scratch_bytes;
+decltype(&mok_forward_w4) f_forward_w4;
 
 using at::Tensor;
 constexpr auto kBf16 = at::kBFloat16;
@@ -511,9 +519,232 @@ PyObject* adamw_step(PyObject* const* a, Py_ssize_t nargs) {
   return PyLong_FromLong(status);
 }
 
+// ---- grouped products ----
+
+// The weight [experts, n, k], the offsets [experts + 1] and rows [rows, cols] of a grouped product.
+struct Grouped {
+  const Tensor &w, &offsets;
+  int64_t E, n, k;
+  Grouped(PyObject* weight, PyObject* off, const Tensor& first) : w(tensor("weight", weight)), offsets(tensor("offsets", off)) {
+    check("weight", w, first, {kBf16});
+    if (w.dim() != 3 || w.size(0) < 1 || w.size(1) < 1 || w.size(2) < 1) bad("weight must be [experts, n, k], none of them 0");
+    dense("weight", w);
+    E = w.size(0), n = w.size(1), k = w.size(2);
+    if (E > 1024) bad("at most 1024 experts");
+    check("offsets", offsets, first, {at::kInt, at::kLong});
+    shaped("offsets", offsets, {E + 1});
+    dense("offsets", offsets);
+  }
+  int wide() const { return offsets.scalar_type() == at::kLong; }
+};
+int64_t rows_of(const char* name, const Tensor& t, const Tensor& first, int64_t cols) {
+  check(name, t, first, {kBf16});
+  if (t.dim() != 2 || t.size(1) != cols) bad(std::string(name) + " must be [rows, " + std::to_string(cols) + "], got " + text(t.sizes()));
+  return t.size(0);
+}
+
+// grouped_matmul(x, weight, offsets, out, stream) -> (y,)
+PyObject* grouped_matmul(PyObject* const* a, Py_ssize_t nargs) {
+  count("grouped_matmul", nargs, 5);
+  const Tensor& x = on_gpu("x", tensor("x", a[0]));
+  const Grouped g(a[1], a[2], x);
+  const int64_t rows = rows_of("x", x, x, g.k), ldx = row_stride("x", x);
+  const Tensor* out = maybe("out", a[3]);
+  if (out) {
+    if (rows_of("out", *out, x, g.n) != rows) bad("out must have x's rows");
+    apart("out", *out, "x", &x, false), apart("out", *out, "weight", &g.w, false);
+    apart("out", *out, "offsets", &g.offsets, false);
+  }
+  Tensor y = out ? *out : make({rows, g.n}, x, kBf16);
+  const int64_t ldy = row_stride("out", y);
+  const mok_status st = f_grouped_matmul(x.data_ptr(), ldx, g.w.data_ptr(), g.offsets.data_ptr(), g.wide(), rows,
+                                         (int32_t)g.E, g.n, g.k, y.data_ptr(), ldy, !out, stream_of(a[4]));
+  if (ran(st)) written(out);
+  return result(st, {y});
+}
+
+// grouped_matmul_backward(dy, x, weight, offsets, need_dx, need_dw, dw_fp32, stream) -> (dx, dw)
+PyObject* grouped_matmul_backward(PyObject* const* a, Py_ssize_t nargs) {
+  count("grouped_matmul_backward", nargs, 8);
+  const Tensor &dy = on_gpu("dy", tensor("dy", a[0])), &x = tensor("x", a[1]);
+  const Grouped g(a[2], a[3], dy);
+  const int64_t rows = rows_of("dy", dy, dy, g.n), lddy = row_stride("dy", dy);
+  if (rows_of("x", x, dy, g.k) != rows) bad("x must have dy's rows");
+  const int64_t ldx = row_stride("x", x);
+  const bool wide = a[6] == Py_True;
+  Tensor dx, dw;
+  mok_status st = MOK_OK;
+  if (a[4] == Py_True) {
+    dx = make({rows, g.k}, dy, kBf16);
+    st = f_grouped_matmul_dx(dy.data_ptr(), lddy, g.w.data_ptr(), g.offsets.data_ptr(), g.wide(), rows, (int32_t)g.E,
+                             g.n, g.k, dx.data_ptr(), g.k, 1, stream_of(a[7]));
+  }
+  if (st == MOK_OK && a[5] == Py_True) {
+    dw = make({g.E, g.n, g.k}, dy, wide ? kF32 : kBf16);
+    st = f_grouped_matmul_dw(dy.data_ptr(), lddy, x.data_ptr(), ldx, g.offsets.data_ptr(), g.wide(), rows, (int32_t)g.E,
+                             g.n, g.k, dw.data_ptr(), wide, stream_of(a[7]));
+  }
+  return result(st, {dx, dw});
+}
+
+// ---- 4-bit weights ----
+
+struct Weight4 {
+  const Tensor &codes, &scale;
+  const Tensor* zero;
+  int32_t format, group = 0;
+  int64_t k = 0;
+  // Checks types, devices and that the three fit each other. `name`: the weight's.
+  Weight4(const char* name, PyObject* c, PyObject* s, PyObject* z, const Tensor& first)
+      : codes(tensor(name, c)), scale(tensor((std::string(name) + "'s scale").c_str(), s)), zero(maybe("a zero point", z)) {
+    const std::string n(name);
+    check(name, codes, first, {kU8});
+    check((n + "'s scale").c_str(), scale, first, {kBf16, kU8, at::kFloat8_e8m0fnu});
+    format = scale.scalar_type() == kBf16 ? MOK_W4_INT4 : MOK_W4_MXFP4;
+    if (codes.dim() < 1 || codes.size(-1) < 1) bad(n + " must have a last dimension of at least 1");
+    k = codes.size(-1) * 2;
+    if (scale.dim() != codes.dim() || scale.sizes().slice(0, codes.dim() - 1) != codes.sizes().slice(0, codes.dim() - 1))
+      bad(n + "'s scale must have its rows: codes " + text(codes.sizes()) + ", scale " + text(scale.sizes()));
+    const int64_t groups = scale.size(-1);
+    if (groups < 1 || k % groups != 0 || (k / groups != 32 && (format == MOK_W4_MXFP4 || (k / groups != 64 && k / groups != 128))))
+      bad(n + ": " + std::to_string(groups) + " scales for " + std::to_string(k) + " columns are no groups of 32" +
+          (format == MOK_W4_MXFP4 ? "" : ", 64 or 128"));
+    group = (int32_t)(k / groups);
+    dense(name, codes), dense((n + "'s scale").c_str(), scale);
+    if (zero) {
+      if (format == MOK_W4_MXFP4) bad("MXFP4 weights have no zero points");
+      check((n + "'s zero point").c_str(), *zero, first, {kU8});
+      shaped((n + "'s zero point").c_str(), *zero, scale.sizes());
+      dense((n + "'s zero point").c_str(), *zero);
+    }
+  }
+  mok_w4 c() const { return mok_w4{(const uint8_t*)codes.data_ptr(), scale.data_ptr(), (const uint8_t*)ptr(zero)}; }
+  int64_t rows() const { return codes.numel() / codes.size(-1); }
+};
+
+// w4_quantize(weight, mxfp4, group, zero_point, stream) -> (codes, scale, zero)
+PyObject* w4_quantize(PyObject* const* a, Py_ssize_t nargs) {
+  count("w4_quantize", nargs, 5);
+  const Tensor& w = on_gpu("weight", tensor("weight", a[0]));
+  check("weight", w, w, {kBf16, kF32});
+  const bool mx = a[1] == Py_True, with_zero = a[3] == Py_True;
+  const int32_t group = small_integer("group", a[2]);
+  if (mx && (with_zero || group != 32)) bad("MXFP4 has groups of 32 and no zero points");
+  if (group != 32 && group != 64 && group != 128) bad("group must be 32, 64 or 128");
+  if (w.dim() < 1 || w.size(-1) < 1 || w.size(-1) % group != 0) bad("the last dimension must be a multiple of the group, " + std::to_string(group));
+  const int64_t cols = w.size(-1), ld = row_stride("weight", w);
+  auto size = w.sizes().vec();
+  size.back() = cols / 2;
+  Tensor codes = make(size, w, kU8), zero;
+  size.back() = cols / group;
+  Tensor scale = make(size, w, mx ? kU8 : kBf16);
+  if (with_zero) zero = make(size, w, kU8);
+  const mok_status st = f_w4_quantize(w.data_ptr(), fp32(w), w.numel() / cols, cols, ld, mx ? MOK_W4_MXFP4 : MOK_W4_INT4,
+                                      group, (uint8_t*)codes.data_ptr(), scale.data_ptr(),
+                                      with_zero ? (uint8_t*)zero.data_ptr() : nullptr, stream_of(a[4]));
+  return result(st, {codes, scale, zero});
+}
+
+// w4_dequantize(codes, scale, zero, stream) -> (values,)
+PyObject* w4_dequantize(PyObject* const* a, Py_ssize_t nargs) {
+  count("w4_dequantize", nargs, 4);
+  const Weight4 w("codes", a[0], a[1], a[2], on_gpu("codes", tensor("codes", a[0])));
+  auto size = w.codes.sizes().vec();
+  size.back() = w.k;
+  Tensor out = make(size, w.codes, kBf16);
+  const mok_w4 c = w.c();
+  const mok_status st = f_w4_dequantize(&c, w.rows(), w.k, w.format, w.group, out.data_ptr(), stream_of(a[3]));
+  return result(st, {out});
+}
+
+// w4_matmul(x, codes, scale, zero, stream) -> (y,)
+PyObject* w4_matmul(PyObject* const* a, Py_ssize_t nargs) {
+  count("w4_matmul", nargs, 5);
+  const Tensor& x = on_gpu("x", tensor("x", a[0]));
+  check("x", x, x, {kBf16});
+  const Weight4 w("codes", a[1], a[2], a[3], x);
+  if (w.codes.dim() != 2 || w.codes.size(0) < 1) bad("codes must be [n, k/2]");
+  if (x.dim() < 1 || x.size(-1) != w.k) bad("x must have a last dimension of " + std::to_string(w.k));
+  const int64_t n = w.codes.size(0), T = x.numel() / w.k, ldx = row_stride("x", x);
+  auto size = x.sizes().vec();
+  size.back() = n;
+  Tensor y = make(size, x, kBf16);
+  const mok_w4 c = w.c();
+  const mok_status st = f_w4_matmul(x.data_ptr(), ldx, T, n, w.k, w.format, w.group, &c, y.data_ptr(), n, stream_of(a[4]));
+  return result(st, {y});
+}
+
+// forward_w4(x, router_weights, top_experts, weights, limit, out, stream) -> (y,); weights: codes, scale and zero (or
+// None) of routed gate, up, down and of shared gate, up, down (or None)
+PyObject* forward_w4(PyObject* const* a, Py_ssize_t nargs) {
+  count("forward_w4", nargs, 7);
+  const Tensor &x = on_gpu("x", tensor("x", a[0])), &rw = tensor("router_weights", a[1]), &ids = tensor("top_experts", a[2]);
+  check("x", x, x, {kBf16});
+  if (x.dim() != 2 || x.size(1) < 1) bad("x must be [tokens, hidden]");
+  const int64_t T = x.size(0), H = x.size(1);
+  check("router_weights", rw, x, {kF32});
+  check("top_experts", ids, x, {at::kLong});
+  if (ids.dim() != 2 || ids.size(0) != T || ids.size(1) < 1 || ids.size(1) > 64)
+    bad("top_experts must be [tokens, topk], topk between 1 and 64, got " + text(ids.sizes()));
+  shaped("router_weights", rw, ids.sizes());
+  if (!PyTuple_Check(a[3]) || PyTuple_GET_SIZE(a[3]) != 18) bad("weights must be 18 entries");
+  static const char* const names[6] = {"routed_gate", "routed_up", "routed_down", "shared_gate", "shared_up", "shared_down"};
+  mok_w4_layer l{};
+  l.struct_size = sizeof(l);
+  mok_w4* to[6] = {&l.routed_gate, &l.routed_up, &l.routed_down, &l.shared_gate, &l.shared_up, &l.shared_down};
+  int64_t E = 0, I = 0, Is = 0;
+  bool with_zero = false;
+  const Tensor* out = maybe("out", a[5]);
+  for (int i = 0; i < 6; ++i) {
+    PyObject* const* part = &PyTuple_GET_ITEM(a[3], 3 * i);
+    if (i >= 3 && part[0] == Py_None) {
+      if (i > 3 && Is) bad("the shared expert needs all of shared_gate, shared_up and shared_down");
+      if (part[1] != Py_None || part[2] != Py_None) bad(std::string(names[i]) + "'s codes are missing");
+      continue;
+    }
+    if (i > 3 && !Is) bad("the shared expert needs all of shared_gate, shared_up and shared_down");
+    const Weight4 w(names[i], part[0], part[1], part[2], x);
+    if (i == 0) {
+      if (w.codes.dim() != 3 || w.codes.size(0) < 1 || w.codes.size(0) > 1024 || w.codes.size(1) < 1)
+        bad("routed_gate must be [experts, intermediate, hidden/2], at most 1024 experts");
+      E = w.codes.size(0), I = w.codes.size(1);
+      l.format = w.format, l.group = w.group, with_zero = w.zero != nullptr;
+    }
+    if (i == 3) {
+      if (w.codes.dim() != 2 || w.codes.size(0) < 1) bad("shared_gate must be [shared_intermediate, hidden/2]");
+      Is = w.codes.size(0);
+    }
+    const int64_t wide = i < 3 ? I : Is, n = i % 3 == 2 ? H : wide, k = i % 3 == 2 ? wide : H;
+    if (k % 2 != 0) bad("hidden and intermediate must be even");
+    if (i < 3)
+      shaped(names[i], w.codes, {E, n, k / 2});
+    else
+      shaped(names[i], w.codes, {n, k / 2});
+    if (w.format != l.format || w.group != l.group || (w.zero != nullptr) != with_zero)
+      bad("all weights must have one format and group, and zero points in all of them or in none");
+    *to[i] = w.c();
+    if (out) apart("out", *out, names[i], &w.codes, false), apart("out", *out, names[i], &w.scale, false), apart("out", *out, names[i], w.zero, false);
+  }
+  if (H > 1 << 16 || I > 1 << 16 || Is > 1 << 16) bad("hidden and intermediate sizes are at most 65536");
+  l.hidden = (int32_t)H, l.intermediate = (int32_t)I, l.num_experts = (int32_t)E, l.topk = (int32_t)ids.size(1);
+  l.shared_intermediate = (int32_t)Is;
+  l.swiglu_limit = (float)number(a[4]);
+  if (out) {
+    check("out", *out, x, {kBf16}), shaped("out", *out, x.sizes()), dense("out", *out);
+    apart("out", *out, "x", &x, false), apart("out", *out, "router_weights", &rw, false), apart("out", *out, "top_experts", &ids, false);
+  }
+  const void *px = dense("x", x), *prw = dense("router_weights", rw), *pid = dense("top_experts", ids);
+  Tensor y = out ? *out : make({T, H}, x, kBf16);
+  const size_t bytes = f_forward_w4_scratch_bytes(&l, T);
+  Tensor scratch = make({(int64_t)bytes}, x, kU8);
+  const mok_status st = f_forward_w4(&l, px, (const float*)prw, (const int64_t*)pid, T, y.data_ptr(), scratch.data_ptr(), bytes, stream_of(a[6]));
+  if (ran(st)) written(out);
+  return result(st, {y});
+}
+
 // bind(addresses of the C ABI's functions, in the order below)
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  count("bind", n, 7);
+  count("bind", n, 15);
   f_rms_norm = (decltype(f_rms_norm))stream_of(a[0]);
   f_rms_norm_scratch_bytes = (decltype(f_rms_norm_scratch_bytes))stream_of(a[1]);
   f_rms_norm_backward = (decltype(f_rms_norm_backward))stream_of(a[2]);
@@ -521,6 +752,14 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   f_router_topk = (decltype(f_router_topk))stream_of(a[4]);
   f_router_topk_backward = (decltype(f_router_topk_backward))stream_of(a[5]);
   f_adamw_step = (decltype(f_adamw_step))stream_of(a[6]);
+  f_grouped_matmul = (decltype(f_grouped_matmul))stream_of(a[7]);
+  f_grouped_matmul_dx = (decltype(f_grouped_matmul_dx))stream_of(a[8]);
+  f_grouped_matmul_dw = (decltype(f_grouped_matmul_dw))stream_of(a[9]);
+  f_w4_quantize = (decltype(f_w4_quantize))stream_of(a[10]);
+  f_w4_dequantize = (decltype(f_w4_dequantize))stream_of(a[11]);
+  f_w4_matmul = (decltype(f_w4_matmul))stream_of(a[12]);
+  f_forward_w4_scratch_bytes = (decltype(f_forward_w4_scratch_bytes))stream_of(a[13]);
+  f_forward_w4 = (decltype(f_forward_w4))stream_of(a[14]);
   Py_RETURN_NONE;
 }
 
@@ -549,6 +788,12 @@ PyMethodDef methods[] = {method<bind>("bind"),
                          method<router_topk>("router_topk"),
                          method<router_topk_backward>("router_topk_backward"),
                          method<adamw_step>("adamw_step"),
+                         method<grouped_matmul>("grouped_matmul"),
+                         method<grouped_matmul_backward>("grouped_matmul_backward"),
+                         method<w4_quantize>("w4_quantize"),
+                         method<w4_dequantize>("w4_dequantize"),
+                         method<w4_matmul>("w4_matmul"),
+                         method<forward_w4>("forward_w4"),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_ops", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,11 +1,12 @@
-"""The operators around the layer: RMS norm, top-k router, AdamW step.
+"""The operators around the layer: RMS norm, top-k router, AdamW step, and the
+experts' products outside it: grouped by expert, and with 4-bit weights.
 
 Direct calls over the C ABI (``include/mok.h`` states formulas, types and
 refusals); the package re-exports them. They allocate their outputs with
 torch, enqueue on the current stream of the tensors' device, and need no
 workspace. Tensors on the CPU are rejected: there is no fallback. What a call
 writes into tensors that it was given (``adamw_step``; the outputs handed to a
-norm) moves their in-place version counters.
+norm, a product or the 4-bit layer) moves their in-place version counters.
 
 The checks and allocations of these calls are compiled (``csrc/py_ops.cpp``,
 built with the library): at a few tokens the host's share decides their time.
@@ -18,11 +19,14 @@ import torch
 
 from . import _lib
 
-__all__ = ["rms_norm", "rms_norm_mxfp8", "rms_norm_backward", "router_topk", "router_topk_backward", "adamw_step"]
+__all__ = ["rms_norm", "rms_norm_mxfp8", "rms_norm_backward", "router_topk", "router_topk_backward", "adamw_step",
+           "grouped_matmul", "grouped_matmul_backward", "w4_quantize", "w4_dequantize", "w4_matmul", "forward_w4"]
 
 _SCORING = {"softmax": _lib.MOK_ROUTER_SOFTMAX, "sigmoid": _lib.MOK_ROUTER_SIGMOID}
 _BOUND = ("mok_rms_norm", "mok_rms_norm_scratch_bytes", "mok_rms_norm_backward", "mok_router_scratch_bytes",
-          "mok_router_topk", "mok_router_topk_backward", "mok_adamw_step")
+          "mok_router_topk", "mok_router_topk_backward", "mok_adamw_step", "mok_grouped_matmul",
+          "mok_grouped_matmul_dx", "mok_grouped_matmul_dw", "mok_w4_quantize", "mok_w4_dequantize", "mok_w4_matmul",
+          "mok_forward_w4_scratch_bytes", "mok_forward_w4")
 
 _host = None
 
@@ -134,3 +138,69 @@ def adamw_step(params, grads, exp_avgs, exp_avg_sqs, masters=None, *, step: int,
         raise ValueError("there are no params, but other tensors")
     _call("adamw_step", params[0], params, grads, exp_avgs, exp_avg_sqs, masters, step, lr, betas[0], betas[1], eps,
           weight_decay, grad_scale, step if seed is None else seed)
+
+
+def grouped_matmul(x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """Matrix product grouped by expert: y[r] = weight[e] @ x[r] for the rows
+    offsets[e] <= r < offsets[e + 1]. x bf16 [rows, k] (dense rows), weight bf16
+    [experts, n, k], offsets int32 or int64 [experts + 1], not decreasing.
+    Returns y bf16 [rows, n]; rows of no expert get zeros, or are left as they
+    were in a given ``out``, which overlaps no other tensor of the call."""
+    return _call("grouped_matmul", x, x, weight, offsets, out)[0]
+
+
+def grouped_matmul_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, offsets: torch.Tensor, *,
+                            need_dx: bool = True, need_dw: bool = True, dw_dtype: torch.dtype = torch.bfloat16):
+    """(dx bf16 [rows, k], dweight [experts, n, k]) from dy bf16 [rows, n];
+    None for one that is not needed. Rows of no expert get zeros in dx and
+    count in no dweight; an expert without rows gets zeros. ``dw_dtype``: bf16
+    or fp32."""
+    if dw_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"dw_dtype must be bfloat16 or float32, got {dw_dtype}")
+    return _call("grouped_matmul_backward", dy, dy, x, weight, offsets, bool(need_dx), bool(need_dw),
+                 dw_dtype == torch.float32)
+
+
+_W4_FORMATS = {"int4": False, "mxfp4": True}
+
+
+def w4_quantize(weight: torch.Tensor, format: str = "int4", group: int | None = None, zero_point: bool = False):
+    """A weight [..., k] (bf16 or fp32) in 4 bits: (codes uint8 [..., k/2],
+    scale [..., k/group], zero). "int4": groups of 32, 64 or 128 (the default)
+    along k, scale bf16, and with ``zero_point`` zero uint8 (else None, and the
+    zero point is 8). "mxfp4": groups of 32, scale uint8 (E8M0), zero None."""
+    if format not in _W4_FORMATS:
+        raise ValueError(f"format must be one of {sorted(_W4_FORMATS)}, got {format!r}")
+    mx = _W4_FORMATS[format]
+    return _call("w4_quantize", weight, weight, mx, (32 if mx else 128) if group is None else group, bool(zero_point))
+
+
+def w4_dequantize(codes: torch.Tensor, scale: torch.Tensor, zero: torch.Tensor | None = None) -> torch.Tensor:
+    """The values of a 4-bit weight in bf16 [..., k], as ``forward`` and
+    ``grouped_matmul`` take them (for a prompt). The scale's type tells the
+    format."""
+    return _call("w4_dequantize", codes, codes, scale, zero)[0]
+
+
+def w4_matmul(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor,
+              zero: torch.Tensor | None = None) -> torch.Tensor:
+    """y bf16 [..., n] = x bf16 [..., k] times a 4-bit weight [n, k],
+    transposed. Made for few rows of x (decoding)."""
+    return _call("w4_matmul", x, x, codes, scale, zero)[0]
+
+
+_W4_PARTS = tuple(kind + name + end for kind in ("routed_", "shared_") for name in ("gate", "up", "down")
+                  for end in ("", "_scale", "_zero"))
+
+
+def forward_w4(x: torch.Tensor, router_weights: torch.Tensor, top_experts: torch.Tensor, weights: dict,
+               swiglu_limit: float = 0.0, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The layer's forward for few tokens on 4-bit experts: out bf16 [T, H]
+    from x bf16 [T, H], the router's weights fp32 [T, k] and ids int64 [T, k]
+    (an id outside the experts is no choice). ``weights``: routed_gate/up
+    [E, I, H/2], routed_down [E, H, I/2] and optionally shared_* as
+    ``w4_quantize`` gives their codes, with *_scale (and *_zero) entries, all of
+    one format and group. Needs no schedule and no workspace; T * k <= 8192."""
+    return _call("forward_w4", x, x, router_weights, top_experts, tuple(map(weights.get, _W4_PARTS)), swiglu_limit,
+                 out)[0]

@@ -1,0 +1,224 @@
+"""The matrix product grouped by expert and its gradients against float64, at
+the sizes where they can go wrong: empty experts, rows of no expert, one row,
+odd widths, strides, alignments, both offset types, and captured calls.
+
+Tolerance, per element: a rounding to bf16 is at most 2^-8 of the value (half a
+step, 2^-24 for fp32), and an fp32 sum of n products is off by at most n 2^-24
+of the sum of their magnitudes."""
+import numpy as np
+import pytest
+
+from mokutil import ROOT  # noqa: F401
+from oracle import products as op
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import mixture_experts_layer_build_amd as mok  # noqa: E402
+from mixture_experts_layer_build_amd import autograd as ag  # noqa: E402
+
+
+def normal(seed, *shape, std=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=gen) * std).to(torch.bfloat16)
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def close(got, want, mags, terms, half_step=2.0 ** -8, what=""):
+    """|got - want| <= half_step |want| + terms 2^-24 mags, mags: the same product of magnitudes."""
+    got = f64(got)
+    assert got.shape == want.shape
+    lim = half_step * np.abs(want) + terms * 2.0 ** -24 * mags
+    bad = ~(np.abs(got - want) <= lim)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, first at {np.argwhere(bad)[0]}"
+
+
+def check(x, w, off, dy, dw_dtype=torch.bfloat16, y=None, grads=None):
+    """The three products (made here unless given) against the oracle."""
+    X, W, DY, o = f64(x), f64(w), f64(dy), off.cpu().long().numpy()
+    inside = np.zeros(X.shape[0], bool)
+    inside[o[0]:o[-1]] = True
+    X, DY = X * 1.0, DY * 1.0
+    X[~inside], DY[~inside] = 0, 0  # (they may hold anything)
+    n, k = W.shape[1:]
+    y = mok.grouped_matmul(x, w, off) if y is None else y
+    dx, dw = mok.grouped_matmul_backward(dy, x, w, off, dw_dtype=dw_dtype) if grads is None else grads
+    assert y.dtype == dx.dtype == torch.bfloat16 and dw.dtype == dw_dtype
+    close(y, op.grouped(X, W, o), op.grouped(np.abs(X), np.abs(W), o), k, what="y")
+    want, mags = op.grouped_backward(DY, X, W, o), op.grouped_backward(np.abs(DY), np.abs(X), np.abs(W), o)
+    close(dx, want[0], mags[0], n, what="dx")
+    longest = int(np.diff(o).max())
+    close(dw, want[1], mags[1], longest + 1, 2.0 ** -8 if dw_dtype == torch.bfloat16 else 2.0 ** -24, what="dw")
+
+
+def case(seed, sizes, n, k, lead=0, tail=0):
+    off = np.cumsum([lead] + list(sizes))
+    rows = int(off[-1]) + tail
+    x, dy = normal(seed, rows, k).cuda(), normal(seed + 1, rows, n).cuda()
+    for t in (x, dy):  # rows of no expert hold what must reach nothing
+        t[:lead] = float("nan")
+        t[rows - tail:] = float("inf")
+    return x, normal(seed + 2, len(sizes), n, k, std=k ** -0.5).cuda(), torch.tensor(off, dtype=torch.int32).cuda(), dy
+
+
+SIZES = {
+    "one_row": [1], "one_expert": [70], "empty_ends": [0, 3, 0, 0, 130, 1, 0], "ragged": [33, 1, 0, 257, 64, 31, 100],
+    "full_tiles": [256, 512, 64], "many": [i % 5 for i in range(200)], "long": [700, 0, 2],
+}
+
+
+@pytest.mark.parametrize("name", SIZES)
+@pytest.mark.parametrize("n,k", [(64, 64), (256, 320), (768, 128), (72, 200), (8, 8), (264, 1000)])
+def test_widths_of_eight(name, n, k):
+    check(*case(n + k, SIZES[name], n, k, lead=3, tail=5))
+
+
+@pytest.mark.parametrize("n,k", [(1, 1), (7, 64), (64, 7), (65, 129), (255, 33), (129, 514)])
+@pytest.mark.parametrize("name", ["one_row", "empty_ends", "ragged"])
+def test_odd_widths(name, n, k):
+    check(*case(n + k, SIZES[name], n, k, tail=2))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("offsets", [torch.int32, torch.int64])
+def test_types(dtype, offsets):
+    x, w, off, dy = case(5, SIZES["ragged"], 136, 264, lead=1, tail=40)
+    check(x, w, off.to(offsets), dy, dtype)
+
+
+@pytest.mark.parametrize("rows", [0, 5])
+def test_no_rows(rows):
+    x, dy = normal(0, rows, 64).cuda(), normal(1, rows, 32).cuda()
+    w, off = normal(2, 3, 32, 64).cuda(), torch.zeros(4, dtype=torch.int32, device="cuda")
+    y = mok.grouped_matmul(x, w, off)
+    dx, dw = mok.grouped_matmul_backward(dy, x, w, off, dw_dtype=torch.float32)
+    assert y.shape == (rows, 32) and dx.shape == (rows, 64)
+    assert not y.any() and not dx.any() and not dw.any()
+
+
+def test_the_rows_of_no_expert_in_a_given_out():
+    x, w, off, dy = case(7, [5, 0, 40], 96, 64, lead=4, tail=9)
+    out = torch.full((58, 96), 7.0, dtype=torch.bfloat16, device="cuda")
+    before = out._version
+    y = mok.grouped_matmul(x, w, off, out=out)
+    assert y.data_ptr() == out.data_ptr() and out._version > before
+    assert bool((out[:4] == 7).all()) and bool((out[49:] == 7).all())
+    assert torch.equal(out[4:49], mok.grouped_matmul(x, w, off)[4:49])
+
+
+@pytest.mark.parametrize("shift", [0, 1, 8])
+@pytest.mark.parametrize("extra", [8, 3])
+def test_strides_and_alignments(shift, extra):
+    x, w, off, dy = case(11, SIZES["ragged"], 72, 136, tail=1)
+    rows = x.shape[0]
+    xs = torch.full((rows, 136 + shift + extra), float("nan"), dtype=torch.bfloat16, device="cuda")
+    xs[:, shift:shift + 136] = x
+    ds = torch.full((rows, 72 + shift + extra), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ds[:, shift:shift + 72] = dy
+    xv, dv = xs[:, shift:shift + 136], ds[:, shift:shift + 72]
+    ws = torch.empty(w.numel() + shift, dtype=torch.bfloat16, device="cuda")[shift:].view(w.shape)
+    ws.copy_(w)
+    check(xv, ws, off, dv)
+    out = torch.zeros(rows, 72 + shift + extra, dtype=torch.bfloat16, device="cuda")
+    y = mok.grouped_matmul(xv, ws, off, out=out[:, shift:shift + 72])
+    check(xv, ws, off, dv, y=y)
+    assert not out[:, :shift].any() and not out[:, shift + 72:].any()
+
+
+def test_rows_and_experts_do_not_mix():
+    """An infinity or a NaN stays in its row of y and dx, and in its expert's dw."""
+    x, w, off, dy = case(13, [40, 30, 50], 64, 96)
+    x[45, 3], dy[46, 5] = float("inf"), float("nan")
+    y = mok.grouped_matmul(x, w, off).float()
+    dx, dw = mok.grouped_matmul_backward(dy, x, w, off)
+    assert not torch.isfinite(y[45]).any() and torch.isfinite(y[torch.arange(120) != 45]).all()
+    assert torch.isnan(dx[46]).all() and torch.isfinite(dx[torch.arange(120) != 46].float()).all()
+    assert torch.isfinite(dw[0].float()).all() and torch.isfinite(dw[2].float()).all()
+    assert not torch.isfinite(dw[1, :, 3].float()).any() and torch.isnan(dw[1, 5].float()).all()
+
+
+def test_bad_offsets_stay_inside():
+    """Offsets below 0, beyond the rows and decreasing: no access outside, and good experts are right."""
+    x, w, _, dy = case(17, [64, 64, 64], 64, 64)
+    off = torch.tensor([-5, 64, 30, 1000], dtype=torch.int32, device="cuda")
+    y = mok.grouped_matmul(x, w, off)
+    mok.grouped_matmul_backward(dy, x, w, off)
+    assert torch.equal(y[:30], mok.grouped_matmul(x, w, torch.tensor([0, 64, 64, 64]).cuda())[:30])
+
+
+def test_same_bits_every_time():
+    x, w, off, dy = case(19, SIZES["ragged"], 256, 320)
+    first = (mok.grouped_matmul(x, w, off), *mok.grouped_matmul_backward(dy, x, w, off))
+    for _ in range(3):
+        again = (mok.grouped_matmul(x, w, off), *mok.grouped_matmul_backward(dy, x, w, off))
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_gradients_through_autograd_and_by_differences():
+    """The product is linear in x and in the weight, so <dy, f(d)> is the exact difference quotient along d."""
+    x, w, off, dy = case(23, [20, 0, 45, 7], 48, 80, lead=2, tail=3)
+    x, dy = x.nan_to_num(0, 0, 0), dy.nan_to_num(0, 0, 0)
+    lin = ag.MoKGroupedLinear(4, 80, 48, device="cuda")
+    with torch.no_grad():
+        lin.weight.copy_(w)
+    xg = x.clone().requires_grad_()
+    y = lin(xg, off)
+    y.backward(dy)
+    check(x, w, off, dy, y=y, grads=(xg.grad, lin.weight.grad))
+    d, dwt = normal(24, *x.shape).cuda(), normal(25, *w.shape).cuda()
+    inside = torch.zeros(x.shape[0], 1, device="cuda")
+    inside[2:74] = 1
+    DY = (dy.float() * inside).double()
+    for direction, grad, f in ((d, xg.grad, lambda v: mok.grouped_matmul(v, w, off)),
+                               (dwt, lin.weight.grad, lambda v: mok.grouped_matmul(x, v, off))):
+        got, want = (grad.double() * direction.double()).sum(), (DY * f(direction).double()).sum()
+        # each side: every term off by 2^-8 of itself (the rounding of the bf16 outputs)
+        lim = 2.0 ** -8 * ((grad.double() * direction.double()).abs().sum() + (DY * f(direction).double()).abs().sum())
+        assert abs(float(got - want)) <= float(lim)
+    # only what is asked for
+    xg.grad = None
+    lin.weight.requires_grad_(False)
+    lin(xg, off).backward(dy)
+    assert lin.weight.grad is not None and xg.grad is not None
+    assert mok.grouped_matmul_backward(dy, x, w, off, need_dx=False)[0] is None
+    assert mok.grouped_matmul_backward(dy, x, w, off, need_dw=False)[1] is None
+
+
+def test_captured_and_replayed_with_new_inputs():
+    x, w, off, dy = case(29, SIZES["ragged"], 128, 192, tail=4)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        mok.grouped_matmul(x, w, off)
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = mok.grouped_matmul(x, w, off)
+        dx, dw = mok.grouped_matmul_backward(dy, x, w, off)
+    for seed, sizes in ((31, SIZES["ragged"]), (37, [0, 86, 400, 0, 0, 0, 0]), (41, [69, 69, 69, 69, 69, 70, 71])):
+        x2, w2, off2, dy2 = case(seed, sizes, 128, 192, tail=4)
+        for a, b in ((x, x2), (w, w2), (off, off2), (dy, dy2)):
+            a.copy_(b)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, mok.grouped_matmul(x2, w2, off2))
+        for a, b in zip((dx, dw), mok.grouped_matmul_backward(dy2, x2, w2, off2)):
+            assert torch.equal(a, b)
+
+
+def test_two_streams_at_once():
+    a, b = case(43, SIZES["ragged"], 256, 192), case(47, SIZES["long"], 200, 136)
+    want = [(mok.grouped_matmul(*c[:3]), *mok.grouped_matmul_backward(c[3], *c[:3])) for c in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(3):
+        for i, c in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i] = (mok.grouped_matmul(*c[:3]), *mok.grouped_matmul_backward(c[3], *c[:3]))
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(p, q) for p, q in zip(w, g))
