@@ -7,8 +7,10 @@
 //   dx    e's rows         W's columns   W's rows        dy         W_e^T
 //   dW    W's rows         W's columns   e's rows        dy^T       x^T
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
+#include "gemm_common.h"
 #include "mok_internal.h"
 
 namespace mok {
@@ -181,9 +183,291 @@ __global__ void __launch_bounds__(kAnyThreads) grouped_any(GroupedArgs g) {
   if (OP != GROUPED_DW && g.zero_rest) zero_rest(g, N);
 }
 
+// ---------------------------------------------------------------------------
+// Widths of 8: 256 x 256 output tiles, eight waves of 128 x 64 (4 x 2 MFMA
+// tiles of 32 x 32), operands by LDS-DMA into a ring of four stages of 32
+// contraction steps.
+//
+// A stage holds an operand either as 256 rows of 32 dense contraction elements
+// ("rows", 64 bytes each; x, dy, W of y) or as 32 contraction rows of 256 dense
+// elements ("columns", 512 bytes each; W of dx, both operands of dW), as it lies
+// in memory; columns are turned on the way to the registers by the transposing
+// LDS read. 16-byte chunks are swizzled so that the reads of a wave's quarter
+// hit every bank once: rows by (row / 4) % 4 within 64 bytes, columns by
+// 4 (row % 4) within 512.
+//
+// One barrier per stage, in the middle of its products: the fragments of the
+// second half are in registers by then, so the products go on while the waves
+// meet, and the loads issued behind it have two stages' time to land.
+// ---------------------------------------------------------------------------
+constexpr int kTile = 256, kStep = 32, kThreads = 512, kRing = 4;
+constexpr int kOperandBytes = kTile * kStep * 2, kStageBytes = 2 * kOperandBytes;
+constexpr int kNumXcd = 8;
+constexpr int kGroupM = 4;               // M tiles that run together with all N tiles
+constexpr uint32_t kOff = 0x80000000u;   // past every resource: loads return 0
+
+struct alignas(16) TileLds {
+  uint8_t ring[kRing][kStageBytes];
+  int32_t tiles[kGroupedMaxExperts + 1];
+  int32_t part[kThreads / 64];
+};
+
+// An operand of the current tile.
+template <bool COLUMNS>
+struct Operand {
+  const uint8_t* base;  // its first row (rows) or its first contraction row (columns) at the tile
+  int64_t ld;           // bytes from row to row
+  uint32_t off[2];      // this lane's two loads of a stage, kOff if outside
+  int chunk[2];         // rows: the contraction chunk of each
+
+  // `have`: rows (columns: elements) of the tile that exist.
+  __device__ __forceinline__ void init(const void* p, int64_t ld_elements, int have, int wave, int lane) {
+    base = (const uint8_t*)p;
+    ld = ld_elements * 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (COLUMNS) {
+        const int row = (2 * wave + i) * 2 + (lane >> 5), c = (lane & 31) ^ (4 * (row & 3));
+        chunk[i] = 0;
+        off[i] = c * 8 < have ? (uint32_t)(row * ld) + 16u * c : kOff;
+      } else {
+        const int row = (2 * wave + i) * 16 + (lane >> 2), c = (lane & 3) ^ ((row >> 2) & 3);
+        chunk[i] = c;
+        off[i] = row < have ? (uint32_t)(row * ld) + 16u * c : kOff;
+      }
+    }
+  }
+  // Loads contraction elements k0 .. k0 + 31 of K to LDS at `to`.
+  __device__ __forceinline__ void load(int k0, int K, uint32_t to, int wave) const {
+    if (COLUMNS) {
+      // rows past K lie behind the resource's end
+      const i32x4v rs = rsrc(base + (int64_t)k0 * ld, (uint32_t)(min(K - k0, kStep) * ld));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) lds_dma16(rs, off[i], 0, to + (uint32_t)(2 * wave + i) * 1024u);
+    } else {
+      const i32x4v rs = rsrc(base + (int64_t)k0 * 2, 0x7FFFFFFFu);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        lds_dma16(rs, k0 + 8 * chunk[i] < K ? off[i] : kOff, 0, to + (uint32_t)(2 * wave + i) * 1024u);
+    }
+  }
+  // The fragment of 32 rows from `row0`, contraction elements 16 ks + 8 lh + 0..7 of row row0 + lr.
+  static __device__ __forceinline__ bf16x8 fragment(const uint8_t* st, int row0, int ks, int lane) {
+    const int lr = lane & 31, lh = lane >> 5;
+    if (COLUMNS) {
+      typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+      typedef __attribute__((address_space(3))) bf16x4 lds4;
+      const int i = lane & 15, m = row0 + (lr & 16) + 4 * (i & 3), k = 16 * ks + 8 * lh + (i >> 2);
+      // (k % 4 is i / 4 in both reads)
+      const uint8_t* at = st + k * 512 + ((m >> 3) ^ (4 * (i >> 2))) * 16 + (m & 7) * 2;
+#if defined(__HIP_DEVICE_COMPILE__)
+      const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)at);
+      const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(at + 4 * 512));
+      return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+#else
+      return bf16x8{};
+#endif
+    } else {
+      const int row = row0 + lr;
+      return *reinterpret_cast<const bf16x8*>(st + row * 64 + (((2 * ks + lh) ^ (lr >> 2)) & 3) * 16);
+    }
+  }
+};
+
+// Writes a wave's 128 x 64 results through its 16 KiB of LDS, whole lines of a
+// row per store. T: uint16_t (bf16) or float.
+template <typename T>
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[4][2], uint8_t* lds, T* out, int64_t ld, int rows,
+                                           int cols, int lane) {
+  constexpr int RB = 64 * sizeof(T), CH = RB / 16, HALF = 16384 / RB;  // bytes, chunks of a row; rows at a time
+  const int lr = lane & 31, lh = lane >> 5;
+#pragma unroll
+  for (int h = 0; h < 128 / HALF; ++h) {
+#pragma unroll
+    for (int i = 0; i < HALF / 32; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16& a = acc[h * (HALF / 32) + i][j];
+          const int row = i * 32 + lr, col = j * 32 + 8 * q + 4 * lh;
+          uint8_t* at = lds + row * RB + ((col * sizeof(T) / 16) ^ (row & (CH - 1))) * 16 + (col * sizeof(T) & 15);
+          if constexpr (sizeof(T) == 2)
+            *reinterpret_cast<uint2*>(at) =
+                make_uint2(pack_bf16x2(a[4 * q], a[4 * q + 1]), pack_bf16x2(a[4 * q + 2], a[4 * q + 3]));
+          else
+            *reinterpret_cast<f32x4*>(at) = f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+        }
+    const int c = lane & (CH - 1);
+#pragma unroll
+    for (int r0 = 0; r0 < HALF; r0 += 64 / CH) {
+      const int row = r0 + lane / CH;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * RB + (c ^ (row & (CH - 1))) * 16);
+      if (h * HALF + row < rows && c * (int)(16 / sizeof(T)) < cols)
+        *reinterpret_cast<u32x4*>((uint8_t*)(out + (int64_t)(h * HALF + row) * ld) + c * 16) = v;
+    }
+  }
+}
+
+template <int OP, bool F32>
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) grouped_tiles(GroupedArgs g) {
+  __shared__ TileLds L;
+  constexpr bool ACOL = OP == GROUPED_DW, BCOL = OP != GROUPED_Y;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int N = (int)(OP == GROUPED_Y ? g.n : g.k), nt = (N + kTile - 1) / kTile;
+  const int mts = (int)((g.n + kTile - 1) / kTile);  // dW: M tiles of an expert
+  if (OP != GROUPED_DW) scan_tiles<kThreads>(g, kTile, L.tiles, L.part);
+  const int64_t all = OP == GROUPED_DW ? (int64_t)g.E * mts * nt : (int64_t)L.tiles[g.E] * nt;
+  // Workgroup b runs on XCD b % 8; runs of as many tiles as an XCD has
+  // workgroups go to the XCDs in turn, so that the tiles that share operands
+  // run together on one L2.
+  const int nq = gridDim.x % kNumXcd == 0 ? kNumXcd : 1;
+  const int slots = gridDim.x / nq;
+  for (int64_t id = (int64_t)(blockIdx.x % nq) * slots + blockIdx.x / nq; id < all; id += gridDim.x) {
+    // ---- the tile ----
+    int e, local, nm;
+    if (OP == GROUPED_DW) {
+      e = (int)(id / (mts * nt));
+      local = (int)(id - (int64_t)e * mts * nt);
+      nm = mts;
+    } else {
+      e = expert_of(L.tiles, g.E, (int)(id / nt));
+      local = (int)(id - (int64_t)L.tiles[e] * nt);
+      nm = L.tiles[e + 1] - L.tiles[e];
+    }
+    const int first = local / (kGroupM * nt) * kGroupM, gm = min(kGroupM, nm - first), r = local - first * nt;
+    const int m0 = __builtin_amdgcn_readfirstlane((first + r % gm) * kTile);
+    const int n0 = __builtin_amdgcn_readfirstlane(r / gm * kTile);
+    int lo, hi;
+    segment(g, e, lo, hi);
+    lo = __builtin_amdgcn_readfirstlane(lo), hi = __builtin_amdgcn_readfirstlane(hi);
+    const int rows = (OP == GROUPED_DW ? (int)g.n : hi - lo) - m0, cols = N - n0;
+    const int K = (int)(OP == GROUPED_Y ? g.k : OP == GROUPED_DX ? g.n : hi - lo);
+    Operand<ACOL> A;
+    Operand<BCOL> B;
+    const uint16_t* a = (const uint16_t*)g.a;
+    const uint16_t* b = (const uint16_t*)g.b;
+    if (OP == GROUPED_DW) {
+      A.init(a + lo * g.ld_a + m0, g.ld_a, rows, wave, lane);
+      B.init(b + lo * g.ld_b + n0, g.ld_b, cols, wave, lane);
+    } else {
+      A.init(a + (lo + m0) * g.ld_a, g.ld_a, rows, wave, lane);
+      B.init(b + (int64_t)e * g.n * g.k + (OP == GROUPED_Y ? n0 * g.k : n0), g.k, cols, wave, lane);
+    }
+    const uint32_t ring = lds_addr(&L.ring[0][0]);
+    auto issue = [&](int kt) {
+      const uint32_t to = ring + (uint32_t)(kt % kRing) * kStageBytes;
+      A.load(kt * kStep, K, to, wave);
+      B.load(kt * kStep, K, to + kOperandBytes, wave);
+    };
+    f32x16 acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+    const int nk = (K + kStep - 1) / kStep;
+    // NI: 32-row blocks of this wave that hold rows, rounded up to 0, 1, 2 or 4 (at compile time, so that a ragged
+    // tile leaves out reads and products without branches between them)
+    auto run = [&](auto ni_c) {
+      constexpr int NI = decltype(ni_c)::value;
+      bf16x8 fa[2][NI > 0 ? NI : 1], fb[2][2];
+      auto fragments = [&](int kt, int ks) {
+        const uint8_t* st = &L.ring[kt % kRing][0];
+        if constexpr (NI > 0) {
+#pragma unroll
+          for (int i = 0; i < NI; ++i) fa[ks][i] = Operand<ACOL>::fragment(st, wm * 128 + i * 32, ks, lane);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) fb[ks][j] = Operand<BCOL>::fragment(st + kOperandBytes, wn * 64 + j * 32, ks, lane);
+        }
+      };
+      auto products = [&](int ks) {
+        if constexpr (NI > 0) {
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[ks][j], fa[ks][i], acc[i][j], 0, 0, 0);
+        }
+      };
+      if (nk > 2)
+        wait_vmcnt<8>();
+      else
+        wait_vmcnt<0>();
+      __syncthreads();  // stage 0 has landed for every wave
+      fragments(0, 0);
+      for (int kt = 0; kt < nk; ++kt) {
+        fragments(kt, 1);
+        __builtin_amdgcn_sched_barrier(0);
+        products(0);
+        __builtin_amdgcn_sched_barrier(0);
+        if (kt + 1 < nk) {
+          if (kt + 2 < nk)
+            wait_vmcnt<4>();
+          else
+            wait_vmcnt<0>();
+          __syncthreads();  // stage kt + 1 has landed, and nobody reads stage kt - 1 any more
+          if (kt + 3 < nk) issue(kt + 3);
+          fragments(kt + 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        products(1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    wait_vmcnt<0>();   // the stores of the tile before
+    __syncthreads();   // its LDS is free
+    for (int kt = 0; kt < min(nk, 3); ++kt) issue(kt);
+    const int live = min(4, max(0, (rows - wm * 128 + 31) / 32));
+    if (nk > 0) {
+      if (live > 2)
+        run(std::integral_constant<int, 4>{});
+      else if (live == 2)
+        run(std::integral_constant<int, 2>{});
+      else if (live == 1)
+        run(std::integral_constant<int, 1>{});
+      else
+        run(std::integral_constant<int, 0>{});
+    }
+    // ---- results ----
+    __syncthreads();  // nobody reads the ring any more
+    uint8_t* stage = &L.ring[0][0] + wave * 16384;
+    const int mr = rows - wm * 128, nc = cols - wn * 64;
+    if (OP == GROUPED_DW) {
+      const int64_t at = ((int64_t)e * g.n + m0 + wm * 128) * g.k + n0 + wn * 64;
+      if (F32)
+        store_tile(acc, stage, (float*)g.out + at, g.k, mr, nc, lane);
+      else
+        store_tile(acc, stage, (uint16_t*)g.out + at, g.k, mr, nc, lane);
+    } else {
+      store_tile(acc, stage, (uint16_t*)g.out + (lo + m0 + wm * 128) * g.ld_out + n0 + wn * 64, g.ld_out, mr, nc, lane);
+    }
+  }
+  if (OP != GROUPED_DW && g.zero_rest) zero_rest(g, N);
+}
+
+bool by_eight(const GroupedArgs& g) {
+  return ((g.n | g.k | g.ld_a | g.ld_b | g.ld_out) & 7) == 0 &&
+         (((uintptr_t)g.a | (uintptr_t)g.b | (uintptr_t)g.out) & 15) == 0;
+}
+
 }  // namespace
 
 hipError_t launch_grouped(GroupedOp op, const GroupedArgs& g, int cus, hipStream_t s) {
+  if (by_eight(g)) {
+    switch (op) {
+      case GROUPED_Y: grouped_tiles<GROUPED_Y, false><<<cus, kThreads, 0, s>>>(g); break;
+      case GROUPED_DX: grouped_tiles<GROUPED_DX, false><<<cus, kThreads, 0, s>>>(g); break;
+      default:
+        if (g.out_fp32)
+          grouped_tiles<GROUPED_DW, true><<<cus, kThreads, 0, s>>>(g);
+        else
+          grouped_tiles<GROUPED_DW, false><<<cus, kThreads, 0, s>>>(g);
+    }
+    return hipGetLastError();
+  }
   const int grid = cus * 4;
   switch (op) {
     case GROUPED_Y: grouped_any<GROUPED_Y><<<grid, kAnyThreads, 0, s>>>(g); break;
