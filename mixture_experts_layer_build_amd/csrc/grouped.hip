@@ -274,67 +274,60 @@ struct Operand {
   }
 };
 
-// Writes a wave's 128 x 64 results through its 16 KiB of LDS, whole lines of a
-// row per store. T: uint16_t (bf16) or float.
+// Writes a wave's 128 x 64 results through its 4 KiB of LDS, 32 rows of 128
+// bytes at a time, whole lines of a row per store.
 template <typename T>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[4][2], uint8_t* lds, T* out, int64_t ld, int rows,
                                            int cols, int lane) {
-  constexpr int RB = 64 * sizeof(T), CH = RB / 16, HALF = 16384 / RB;  // bytes, chunks of a row; rows at a time
+  constexpr int PART = sizeof(T) == 4 ? 2 : 1;  // passes over the 64 columns
   const int lr = lane & 31, lh = lane >> 5;
 #pragma unroll
-  for (int h = 0; h < 128 / HALF; ++h) {
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int i = 0; i < HALF / 32; ++i)
+    for (int h = 0; h < PART; ++h) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2 / PART; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const f32x16& a = acc[h * (HALF / 32) + i][j];
-          const int row = i * 32 + lr, col = j * 32 + 8 * q + 4 * lh;
-          uint8_t* at = lds + row * RB + ((col * sizeof(T) / 16) ^ (row & (CH - 1))) * 16 + (col * sizeof(T) & 15);
+          const f32x16& a = acc[i][h + j];
+          uint8_t* row = lds + lr * 128;
           if constexpr (sizeof(T) == 2)
-            *reinterpret_cast<uint2*>(at) =
+            *reinterpret_cast<uint2*>(row + ((j * 4 + q) ^ (lr & 7)) * 16 + lh * 8) =
                 make_uint2(pack_bf16x2(a[4 * q], a[4 * q + 1]), pack_bf16x2(a[4 * q + 2], a[4 * q + 3]));
           else
-            *reinterpret_cast<f32x4*>(at) = f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
+            *reinterpret_cast<f32x4*>(row + ((2 * q + lh) ^ (lr & 7)) * 16) =
+                f32x4{a[4 * q], a[4 * q + 1], a[4 * q + 2], a[4 * q + 3]};
         }
-    const int c = lane & (CH - 1);
+      const int c = lane & 7, col = (h * 8 + c) * (int)(16 / sizeof(T));
 #pragma unroll
-    for (int r0 = 0; r0 < HALF; r0 += 64 / CH) {
-      const int row = r0 + lane / CH;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(lds + row * RB + (c ^ (row & (CH - 1))) * 16);
-      if (h * HALF + row < rows && c * (int)(16 / sizeof(T)) < cols)
-        *reinterpret_cast<u32x4*>((uint8_t*)(out + (int64_t)(h * HALF + row) * ld) + c * 16) = v;
+      for (int r0 = 0; r0 < 32; r0 += 8) {
+        const int r = r0 + (lane >> 3);
+        const u32x4 v = *reinterpret_cast<const u32x4*>(lds + r * 128 + (c ^ (r & 7)) * 16);
+        if (i * 32 + r < rows && col < cols) *reinterpret_cast<u32x4*>(out + (int64_t)(i * 32 + r) * ld + col) = v;
+      }
     }
-  }
 }
 
-template <int OP, bool F32>
-__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) grouped_tiles(GroupedArgs g) {
-  __shared__ TileLds L;
-  constexpr bool ACOL = OP == GROUPED_DW, BCOL = OP != GROUPED_Y;
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
-  const int N = (int)(OP == GROUPED_Y ? g.n : g.k), nt = (N + kTile - 1) / kTile;
-  const int mts = (int)((g.n + kTile - 1) / kTile);  // dW: M tiles of an expert
-  if (OP != GROUPED_DW) scan_tiles<kThreads>(g, kTile, L.tiles, L.part);
-  const int64_t all = OP == GROUPED_DW ? (int64_t)g.E * mts * nt : (int64_t)L.tiles[g.E] * nt;
-  // Workgroup b runs on XCD b % 8; runs of as many tiles as an XCD has
-  // workgroups go to the XCDs in turn, so that the tiles that share operands
-  // run together on one L2.
-  const int nq = gridDim.x % kNumXcd == 0 ? kNumXcd : 1;
-  const int slots = gridDim.x / nq;
-  for (int64_t id = (int64_t)(blockIdx.x % nq) * slots + blockIdx.x / nq; id < all; id += gridDim.x) {
-    // ---- the tile ----
+// A tile of the output: its operands, and where a wave's results go.
+template <int OP>
+struct Tile {
+  static constexpr bool ACOL = OP == GROUPED_DW, BCOL = OP != GROUPED_Y;
+  Operand<ACOL> A;
+  Operand<BCOL> B;
+  int K, rows, cols;  // contraction length; rows and columns of the output from the tile's corner on
+  int64_t out;        // element of its corner
+
+  __device__ __forceinline__ void init(const GroupedArgs& g, const int32_t* tiles, int64_t id, int wave, int lane) {
+    const int N = (int)(OP == GROUPED_Y ? g.n : g.k), nt = (N + kTile - 1) / kTile;
     int e, local, nm;
     if (OP == GROUPED_DW) {
-      e = (int)(id / (mts * nt));
-      local = (int)(id - (int64_t)e * mts * nt);
-      nm = mts;
+      nm = (int)((g.n + kTile - 1) / kTile);
+      e = (int)(id / (nm * nt));
+      local = (int)(id - (int64_t)e * nm * nt);
     } else {
-      e = expert_of(L.tiles, g.E, (int)(id / nt));
-      local = (int)(id - (int64_t)L.tiles[e] * nt);
-      nm = L.tiles[e + 1] - L.tiles[e];
+      e = expert_of(tiles, g.E, (int)(id / nt));
+      local = (int)(id - (int64_t)tiles[e] * nt);
+      nm = tiles[e + 1] - tiles[e];
     }
     const int first = local / (kGroupM * nt) * kGroupM, gm = min(kGroupM, nm - first), r = local - first * nt;
     const int m0 = __builtin_amdgcn_readfirstlane((first + r % gm) * kTile);
@@ -342,25 +335,51 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
     int lo, hi;
     segment(g, e, lo, hi);
     lo = __builtin_amdgcn_readfirstlane(lo), hi = __builtin_amdgcn_readfirstlane(hi);
-    const int rows = (OP == GROUPED_DW ? (int)g.n : hi - lo) - m0, cols = N - n0;
-    const int K = (int)(OP == GROUPED_Y ? g.k : OP == GROUPED_DX ? g.n : hi - lo);
-    Operand<ACOL> A;
-    Operand<BCOL> B;
+    rows = (OP == GROUPED_DW ? (int)g.n : hi - lo) - m0, cols = N - n0;
+    K = (int)(OP == GROUPED_Y ? g.k : OP == GROUPED_DX ? g.n : hi - lo);
     const uint16_t* a = (const uint16_t*)g.a;
     const uint16_t* b = (const uint16_t*)g.b;
     if (OP == GROUPED_DW) {
       A.init(a + lo * g.ld_a + m0, g.ld_a, rows, wave, lane);
       B.init(b + lo * g.ld_b + n0, g.ld_b, cols, wave, lane);
+      out = ((int64_t)e * g.n + m0) * g.k + n0;
     } else {
       A.init(a + (lo + m0) * g.ld_a, g.ld_a, rows, wave, lane);
       B.init(b + (int64_t)e * g.n * g.k + (OP == GROUPED_Y ? n0 * g.k : n0), g.k, cols, wave, lane);
+      out = (lo + m0) * g.ld_out + n0;
     }
-    const uint32_t ring = lds_addr(&L.ring[0][0]);
-    auto issue = [&](int kt) {
-      const uint32_t to = ring + (uint32_t)(kt % kRing) * kStageBytes;
-      A.load(kt * kStep, K, to, wave);
-      B.load(kt * kStep, K, to + kOperandBytes, wave);
-    };
+  }
+  __device__ __forceinline__ int steps() const { return (K + kStep - 1) / kStep; }
+  // Loads stage kt.
+  __device__ __forceinline__ void issue(int kt, uint32_t ring, int wave) const {
+    const uint32_t to = ring + (uint32_t)(kt % kRing) * kStageBytes;
+    A.load(kt * kStep, K, to, wave);
+    B.load(kt * kStep, K, to + kOperandBytes, wave);
+  }
+};
+
+template <int OP, bool F32>
+__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) grouped_tiles(GroupedArgs g) {
+  __shared__ TileLds L;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int N = (int)(OP == GROUPED_Y ? g.n : g.k), nt = (N + kTile - 1) / kTile;
+  if (OP != GROUPED_DW) scan_tiles<kThreads>(g, kTile, L.tiles, L.part);
+  const int64_t all =
+      OP == GROUPED_DW ? (int64_t)g.E * ((g.n + kTile - 1) / kTile) * nt : (int64_t)L.tiles[g.E] * nt;
+  // Workgroup b runs on XCD b % 8; runs of as many tiles as an XCD has
+  // workgroups go to the XCDs in turn, so that the tiles that share operands
+  // run together on one L2.
+  const int nq = gridDim.x % kNumXcd == 0 ? kNumXcd : 1;
+  const int slots = gridDim.x / nq;
+  int64_t id = (int64_t)(blockIdx.x % nq) * slots + blockIdx.x / nq;
+  const uint32_t ring = lds_addr(&L.ring[0][0]);
+  Tile<OP> t;
+  if (id < all) {
+    t.init(g, L.tiles, id, wave, lane);
+    for (int kt = 0; kt < min(t.steps(), 3); ++kt) t.issue(kt, ring, wave);
+  }
+  while (id < all) {
     f32x16 acc[4][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -368,7 +387,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
-    const int nk = (K + kStep - 1) / kStep;
+    const int nk = t.steps();
     // NI: 32-row blocks of this wave that hold rows, rounded up to 0, 1, 2 or 4 (at compile time, so that a ragged
     // tile leaves out reads and products without branches between them)
     auto run = [&](auto ni_c) {
@@ -378,12 +397,15 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
         const uint8_t* st = &L.ring[kt % kRing][0];
         if constexpr (NI > 0) {
 #pragma unroll
-          for (int i = 0; i < NI; ++i) fa[ks][i] = Operand<ACOL>::fragment(st, wm * 128 + i * 32, ks, lane);
+          for (int i = 0; i < NI; ++i)
+            fa[ks][i] = Operand<Tile<OP>::ACOL>::fragment(st, wm * 128 + i * 32, ks, lane);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) fb[ks][j] = Operand<BCOL>::fragment(st + kOperandBytes, wn * 64 + j * 32, ks, lane);
+          for (int j = 0; j < 2; ++j)
+            fb[ks][j] = Operand<Tile<OP>::BCOL>::fragment(st + kOperandBytes, wn * 64 + j * 32, ks, lane);
         }
       };
       auto products = [&](int ks) {
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (NI > 0) {
 #pragma unroll
           for (int i = 0; i < NI; ++i)
@@ -391,36 +413,37 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
             for (int j = 0; j < 2; ++j)
               acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[ks][j], fa[ks][i], acc[i][j], 0, 0, 0);
         }
+        __builtin_amdgcn_sched_barrier(0);
       };
+      // One stage; AFTER: how many of this wave's loads behind stage kt + 1's may be in flight (-1: there is no such
+      // stage). Kept free of branches: where paths meet, the compiler waits for the reads of either.
+      auto step = [&](int kt, auto after, bool more) {
+        constexpr int AFTER = decltype(after)::value;
+        fragments(kt, 1);
+        products(0);
+        if constexpr (AFTER >= 0) {
+          wait_vmcnt<(AFTER < 0 ? 0 : AFTER)>();
+          __syncthreads();  // stage kt + 1 has landed, and nobody reads stage kt - 1 any more
+          if (more) t.issue(kt + 3, ring, wave);
+          fragments(kt + 1, 0);
+        }
+        products(1);
+      };
+      using std::integral_constant;
+      // (the stores of the tile before are younger than the first stages' loads)
       if (nk > 2)
         wait_vmcnt<8>();
       else
         wait_vmcnt<0>();
       __syncthreads();  // stage 0 has landed for every wave
       fragments(0, 0);
-      for (int kt = 0; kt < nk; ++kt) {
-        fragments(kt, 1);
-        __builtin_amdgcn_sched_barrier(0);
-        products(0);
-        __builtin_amdgcn_sched_barrier(0);
-        if (kt + 1 < nk) {
-          if (kt + 2 < nk)
-            wait_vmcnt<4>();
-          else
-            wait_vmcnt<0>();
-          __syncthreads();  // stage kt + 1 has landed, and nobody reads stage kt - 1 any more
-          if (kt + 3 < nk) issue(kt + 3);
-          fragments(kt + 1, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        products(1);
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      int kt = 0;
+      for (; kt < nk - 3; ++kt) step(kt, integral_constant<int, 4>{}, true);
+      if (nk > 2) step(kt++, integral_constant<int, 4>{}, false);
+      if (nk > 1) step(kt++, integral_constant<int, 0>{}, false);
+      step(kt, integral_constant<int, -1>{}, false);
     };
-    wait_vmcnt<0>();   // the stores of the tile before
-    __syncthreads();   // its LDS is free
-    for (int kt = 0; kt < min(nk, 3); ++kt) issue(kt);
-    const int live = min(4, max(0, (rows - wm * 128 + 31) / 32));
+    const int live = min(4, max(0, (t.rows - wm * 128 + 31) / 32));
     if (nk > 0) {
       if (live > 2)
         run(std::integral_constant<int, 4>{});
@@ -431,19 +454,23 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
       else
         run(std::integral_constant<int, 0>{});
     }
-    // ---- results ----
+    // ---- results, while the next tile's first stages are loaded ----
     __syncthreads();  // nobody reads the ring any more
-    uint8_t* stage = &L.ring[0][0] + wave * 16384;
-    const int mr = rows - wm * 128, nc = cols - wn * 64;
-    if (OP == GROUPED_DW) {
-      const int64_t at = ((int64_t)e * g.n + m0 + wm * 128) * g.k + n0 + wn * 64;
-      if (F32)
-        store_tile(acc, stage, (float*)g.out + at, g.k, mr, nc, lane);
-      else
-        store_tile(acc, stage, (uint16_t*)g.out + at, g.k, mr, nc, lane);
-    } else {
-      store_tile(acc, stage, (uint16_t*)g.out + (lo + m0 + wm * 128) * g.ld_out + n0 + wn * 64, g.ld_out, mr, nc, lane);
+    const int64_t out = t.out;
+    const int rows = t.rows - wm * 128, cols = t.cols - wn * 64;
+    id += gridDim.x;
+    if (id < all) {
+      t.init(g, L.tiles, id, wave, lane);
+      for (int kt = 0; kt < min(t.steps(), 3); ++kt) t.issue(kt, ring, wave);
     }
+    // the fourth stage is not in use before every wave has passed the next tile's first barrier
+    uint8_t* part = &L.ring[3][0] + wave * 4096;
+    const int64_t ld = OP == GROUPED_DW ? g.k : g.ld_out;
+    const int64_t at = out + (int64_t)(wm * 128) * ld + wn * 64;
+    if constexpr (F32)
+      store_tile(acc, part, (float*)g.out + at, ld, rows, cols, lane);
+    else
+      store_tile(acc, part, (uint16_t*)g.out + at, ld, rows, cols, lane);
   }
   if (OP != GROUPED_DW && g.zero_rest) zero_rest(g, N);
 }
