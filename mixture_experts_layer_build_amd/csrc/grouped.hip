@@ -237,19 +237,13 @@ struct Operand {
       }
     }
   }
-  // Loads contraction elements k0 .. k0 + 31 of K to LDS at `to`.
-  __device__ __forceinline__ void load(int k0, int K, uint32_t to, int wave) const {
-    if (COLUMNS) {
-      // rows past K lie behind the resource's end
-      const i32x4v rs = rsrc(base + (int64_t)k0 * ld, (uint32_t)(min(K - k0, kStep) * ld));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) lds_dma16(rs, off[i], 0, to + (uint32_t)(2 * wave + i) * 1024u);
-    } else {
-      const i32x4v rs = rsrc(base + (int64_t)k0 * 2, 0x7FFFFFFFu);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        lds_dma16(rs, k0 + 8 * chunk[i] < K ? off[i] : kOff, 0, to + (uint32_t)(2 * wave + i) * 1024u);
-    }
+  // Load i of the two for contraction elements k0 .. k0 + 31 of K, to LDS at `to`.
+  __device__ __forceinline__ void load(int k0, int K, uint32_t to, int wave, int i) const {
+    to += (uint32_t)(2 * wave + i) * 1024u;
+    if (COLUMNS)  // rows past K lie behind the resource's end
+      lds_dma16(rsrc(base + (int64_t)k0 * ld, (uint32_t)(min(K - k0, kStep) * ld)), off[i], 0, to);
+    else
+      lds_dma16(rsrc(base + (int64_t)k0 * 2, 0x7FFFFFFFu), k0 + 8 * chunk[i] < K ? off[i] : kOff, 0, to);
   }
   // The fragment of 32 rows from `row0`, contraction elements 16 ks + 8 lh + 0..7 of row row0 + lr.
   static __device__ __forceinline__ bf16x8 fragment(const uint8_t* st, int row0, int ks, int lane) {
@@ -353,8 +347,16 @@ struct Tile {
   // Loads stage kt.
   __device__ __forceinline__ void issue(int kt, uint32_t ring, int wave) const {
     const uint32_t to = ring + (uint32_t)(kt % kRing) * kStageBytes;
-    A.load(kt * kStep, K, to, wave);
-    B.load(kt * kStep, K, to + kOperandBytes, wave);
+    A.load(kt * kStep, K, to, wave, 0), A.load(kt * kStep, K, to, wave, 1);
+    B.load(kt * kStep, K, to + kOperandBytes, wave, 0), B.load(kt * kStep, K, to + kOperandBytes, wave, 1);
+  }
+  // One of the four loads of a wave for stage kt.
+  __device__ __forceinline__ void issue_part(int kt, int part, uint32_t ring, int wave) const {
+    const uint32_t to = ring + (uint32_t)(kt % kRing) * kStageBytes;
+    if (part < 2)
+      A.load(kt * kStep, K, to, wave, part);
+    else
+      B.load(kt * kStep, K, to + kOperandBytes, wave, part - 2);
   }
 };
 
@@ -393,41 +395,52 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
     auto run = [&](auto ni_c) {
       constexpr int NI = decltype(ni_c)::value;
       bf16x8 fa[2][NI > 0 ? NI : 1], fb[2][2];
-      auto fragments = [&](int kt, int ks) {
-        const uint8_t* st = &L.ring[kt % kRing][0];
-        if constexpr (NI > 0) {
-#pragma unroll
-          for (int i = 0; i < NI; ++i)
+      // read(st, ks, r): the r-th of the fragments of half ks, in the order of their use
+      auto read = [&](const uint8_t* st, int ks, int r) {
+        if (NI > 0 && r < 6) {
+          if (r == 0 || r == 2)
+            fb[ks][r / 2] = Operand<Tile<OP>::BCOL>::fragment(st + kOperandBytes, wn * 64 + r / 2 * 32, ks, lane);
+          else if (const int i = r == 1 ? 0 : r - 2; i < NI)
             fa[ks][i] = Operand<Tile<OP>::ACOL>::fragment(st, wm * 128 + i * 32, ks, lane);
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            fb[ks][j] = Operand<Tile<OP>::BCOL>::fragment(st + kOperandBytes, wn * 64 + j * 32, ks, lane);
         }
       };
-      auto products = [&](int ks) {
-        __builtin_amdgcn_sched_barrier(0);
-        if constexpr (NI > 0) {
+      auto stage = [&](int kt) { return (const uint8_t*)&L.ring[kt % kRing][0]; };
+      // The products of half ks, between them the reads of the other half's
+      // fragments and a stage's loads: while a product occupies the matrix
+      // pipe, the wave's next instructions go to the other units, so none of
+      // them may queue up in front of the products.
+      auto half = [&](int ks, auto read_next, auto&& load) {
 #pragma unroll
-          for (int i = 0; i < NI; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[ks][j], fa[ks][i], acc[i][j], 0, 0, 0);
+        for (int m = 0; m < 8; ++m) {
+          if constexpr (NI > 0) if (m / 2 < NI) {
+            __builtin_amdgcn_sched_barrier(0);
+            acc[m / 2][m % 2] =
+                __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[ks][m % 2], fa[ks][m / 2], acc[m / 2][m % 2], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          read_next(m);
+          load(m);
         }
         __builtin_amdgcn_sched_barrier(0);
       };
       // One stage; AFTER: how many of this wave's loads behind stage kt + 1's may be in flight (-1: there is no such
       // stage). Kept free of branches: where paths meet, the compiler waits for the reads of either.
-      auto step = [&](int kt, auto after, bool more) {
+      auto step = [&](int kt, auto after, auto more) {
         constexpr int AFTER = decltype(after)::value;
-        fragments(kt, 1);
-        products(0);
+        constexpr bool MORE = decltype(more)::value;
+        half(0, [&](int m) { read(stage(kt), 1, m); }, [](int) {});
         if constexpr (AFTER >= 0) {
           wait_vmcnt<(AFTER < 0 ? 0 : AFTER)>();
-          __syncthreads();  // stage kt + 1 has landed, and nobody reads stage kt - 1 any more
-          if (more) t.issue(kt + 3, ring, wave);
-          fragments(kt + 1, 0);
+          // stage kt + 1 has landed, and nobody reads stage kt - 1 any more (its last fragments went into products
+          // that this wave has issued; the reads in flight are of stage kt)
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          half(1, [&](int m) { read(stage(kt + 1), 0, m); }, [&](int m) {
+            if (MORE && m % 2 == 1) t.issue_part(kt + 3, m / 2, ring, wave);
+          });
+        } else {
+          half(1, [](int) {}, [](int) {});
         }
-        products(1);
       };
       using std::integral_constant;
       // (the stores of the tile before are younger than the first stages' loads)
@@ -436,12 +449,12 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
       else
         wait_vmcnt<0>();
       __syncthreads();  // stage 0 has landed for every wave
-      fragments(0, 0);
+      for (int r = 0; r < 6; ++r) read(stage(0), 0, r);
       int kt = 0;
-      for (; kt < nk - 3; ++kt) step(kt, integral_constant<int, 4>{}, true);
-      if (nk > 2) step(kt++, integral_constant<int, 4>{}, false);
-      if (nk > 1) step(kt++, integral_constant<int, 0>{}, false);
-      step(kt, integral_constant<int, -1>{}, false);
+      for (; kt < nk - 3; ++kt) step(kt, integral_constant<int, 4>{}, std::true_type{});
+      if (nk > 2) step(kt++, integral_constant<int, 4>{}, std::false_type{});
+      if (nk > 1) step(kt++, integral_constant<int, 0>{}, std::false_type{});
+      step(kt, integral_constant<int, -1>{}, std::false_type{});
     };
     const int live = min(4, max(0, (t.rows - wm * 128 + 31) / 32));
     if (nk > 0) {
