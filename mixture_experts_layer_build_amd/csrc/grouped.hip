@@ -92,101 +92,8 @@ __device__ __forceinline__ void zero_rest(const GroupedArgs& g, int cols) {
 }
 
 // ---------------------------------------------------------------------------
-// Every width, stride and alignment: 64 x 64 output tiles, operands loaded
-// element by element along whichever index is dense, four waves of one 32 x 32
-// MFMA tile each.
-// ---------------------------------------------------------------------------
-constexpr int kAnyTile = 64, kAnyK = 32, kAnyThreads = 256;
-
-template <int OP>
-__global__ void __launch_bounds__(kAnyThreads) grouped_any(GroupedArgs g) {
-  constexpr int LD = kAnyK + 8;  // 80-byte rows: 16-byte reads of 32 rows without bank conflicts
-  __shared__ alignas(16) uint16_t As[kAnyTile * LD], Bs[kAnyTile * LD];
-  __shared__ int32_t tiles[kGroupedMaxExperts + 1], part[kAnyThreads / 64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int lr = lane & 31, lh = lane >> 5, wm = wave >> 1, wn = wave & 1;
-  const int M = OP == GROUPED_DW ? (int)g.n : 0;
-  const int N = (int)(OP == GROUPED_Y ? g.n : g.k);
-  const int nt = (N + kAnyTile - 1) / kAnyTile;
-  int64_t all;
-  if (OP == GROUPED_DW) {
-    all = (int64_t)g.E * ((M + kAnyTile - 1) / kAnyTile) * nt;
-  } else {
-    scan_tiles<kAnyThreads>(g, kAnyTile, tiles, part);
-    all = (int64_t)tiles[g.E] * nt;
-  }
-  for (int64_t t = blockIdx.x; t < all; t += gridDim.x) {
-    const int ni = (int)(t % nt), mt = (int)(t / nt);
-    const int mts = (M + kAnyTile - 1) / kAnyTile;
-    const int e = OP == GROUPED_DW ? mt / mts : expert_of(tiles, g.E, mt);
-    int lo, hi;
-    segment(g, e, lo, hi);
-    const int m0 = (OP == GROUPED_DW ? mt - e * mts : mt - tiles[e]) * kAnyTile, n0 = ni * kAnyTile;
-    const int mrows = OP == GROUPED_DW ? M : hi - lo;
-    const int K = (int)(OP == GROUPED_Y ? g.k : OP == GROUPED_DX ? g.n : hi - lo);
-    const uint16_t* A = (const uint16_t*)g.a + (int64_t)lo * g.ld_a;
-    const uint16_t* B = (const uint16_t*)g.b + (OP == GROUPED_DW ? (int64_t)lo * g.ld_b : (int64_t)e * g.n * g.k);
-    f32x16 acc;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] = 0.f;
-    for (int k0 = 0; k0 < K; k0 += kAnyK) {
-#pragma unroll
-      for (int i = 0; i < kAnyTile * kAnyK / kAnyThreads; ++i) {
-        const int at = i * kAnyThreads + tid;
-        {  // A
-          const int m = OP == GROUPED_DW ? at % kAnyTile : at / kAnyK;
-          const int k = OP == GROUPED_DW ? at / kAnyTile : at % kAnyK;
-          uint16_t v = 0;
-          if (m0 + m < mrows && k0 + k < K)
-            v = OP == GROUPED_DW ? A[(int64_t)(k0 + k) * g.ld_a + m0 + m] : A[(int64_t)(m0 + m) * g.ld_a + k0 + k];
-          As[m * LD + k] = v;
-        }
-        {  // B
-          const int n = OP == GROUPED_Y ? at / kAnyK : at % kAnyTile;
-          const int k = OP == GROUPED_Y ? at % kAnyK : at / kAnyTile;
-          uint16_t v = 0;
-          if (n0 + n < N && k0 + k < K)
-            v = OP == GROUPED_Y    ? B[(int64_t)(n0 + n) * g.k + k0 + k]
-                : OP == GROUPED_DX ? B[(int64_t)(k0 + k) * g.k + n0 + n]
-                                   : B[(int64_t)(k0 + k) * g.ld_b + n0 + n];
-          Bs[n * LD + k] = v;
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int ks = 0; ks < kAnyK / 16; ++ks) {
-        const bf16x8 fa = *reinterpret_cast<const bf16x8*>(As + (wm * 32 + lr) * LD + ks * 16 + lh * 8);
-        const bf16x8 fb = *reinterpret_cast<const bf16x8*>(Bs + (wn * 32 + lr) * LD + ks * 16 + lh * 8);
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb, fa, acc, 0, 0, 0);
-      }
-      __syncthreads();
-    }
-    // accumulator r of a lane: row lr, column 8 (r / 4) + 4 lh + r % 4 of its 32 x 32 tile
-    const int m = m0 + wm * 32 + lr;
-    if (m < mrows) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int n = n0 + wn * 32 + 8 * (r / 4) + 4 * lh + r % 4;
-        if (n >= N) continue;
-        if (OP == GROUPED_DW) {
-          const int64_t at = ((int64_t)e * g.n + m) * g.k + n;
-          if (g.out_fp32)
-            ((float*)g.out)[at] = acc[r];
-          else
-            ((uint16_t*)g.out)[at] = f32_to_bf16(acc[r]);
-        } else {
-          ((uint16_t*)g.out)[(int64_t)(lo + m) * g.ld_out + n] = f32_to_bf16(acc[r]);
-        }
-      }
-    }
-  }
-  if (OP != GROUPED_DW && g.zero_rest) zero_rest(g, N);
-}
-
-// ---------------------------------------------------------------------------
-// Widths of 8: 256 x 256 output tiles, eight waves of 128 x 64 (4 x 2 MFMA
-// tiles of 32 x 32), operands by LDS-DMA into a ring of four stages of 32
-// contraction steps.
+// 256 x 256 output tiles, eight waves of 128 x 64 (4 x 2 MFMA tiles of 32 x
+// 32), operands in a ring of four LDS stages of 32 contraction steps.
 //
 // A stage holds an operand either as 256 rows of 32 dense contraction elements
 // ("rows", 64 bytes each; x, dy, W of y) or as 32 contraction rows of 256 dense
@@ -199,6 +106,12 @@ __global__ void __launch_bounds__(kAnyThreads) grouped_any(GroupedArgs g) {
 // One barrier per stage, in the middle of its products: the fragments of the
 // second half are in registers by then, so the products go on while the waves
 // meet, and the loads issued behind it have two stages' time to land.
+//
+// DMA: widths and strides that are multiples of 8 elements in 16-byte aligned
+// tensors are loaded straight to LDS, three stages ahead. Others go through
+// registers, one stage ahead: 16-byte loads at the elements' own alignment
+// (which the memory takes), and single elements where a chunk of 8 ends beyond
+// the tile.
 // ---------------------------------------------------------------------------
 constexpr int kTile = 256, kStep = 32, kThreads = 512, kRing = 4;
 constexpr int kOperandBytes = kTile * kStep * 2, kStageBytes = 2 * kOperandBytes;
@@ -212,13 +125,32 @@ struct alignas(16) TileLds {
   int32_t part[kThreads / 64];
 };
 
+// 16 bytes at an element's alignment.
+struct __attribute__((packed, aligned(2))) Unaligned16 {
+  u32x4 v;
+};
+
+// Elements p[0..n) of eight, zeros behind them.
+__device__ __forceinline__ u32x4 load_some(const uint8_t* p, int n) {
+  u32x4 v{0, 0, 0, 0};
+  if (n >= 8) {
+    v = ((const Unaligned16*)p)->v;
+  } else if (n > 0) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (j < n) v[j / 2] |= (uint32_t)((const uint16_t*)p)[j] << (16 * (j % 2));
+  }
+  return v;
+}
+
 // An operand of the current tile.
 template <bool COLUMNS>
 struct Operand {
   const uint8_t* base;  // its first row (rows) or its first contraction row (columns) at the tile
   int64_t ld;           // bytes from row to row
   uint32_t off[2];      // this lane's two loads of a stage, kOff if outside
-  int chunk[2];         // rows: the contraction chunk of each
+  int chunk[2];         // rows: the contraction chunk of each; columns: its contraction row
+  int width[2];         // columns: elements from its first one to the tile's end (not for DMA)
 
   // `have`: rows (columns: elements) of the tile that exist.
   __device__ __forceinline__ void init(const void* p, int64_t ld_elements, int have, int wave, int lane) {
@@ -228,7 +160,8 @@ struct Operand {
     for (int i = 0; i < 2; ++i) {
       if (COLUMNS) {
         const int row = (2 * wave + i) * 2 + (lane >> 5), c = (lane & 31) ^ (4 * (row & 3));
-        chunk[i] = 0;
+        chunk[i] = row;
+        width[i] = have - c * 8;
         off[i] = c * 8 < have ? (uint32_t)(row * ld) + 16u * c : kOff;
       } else {
         const int row = (2 * wave + i) * 16 + (lane >> 2), c = (lane & 3) ^ ((row >> 2) & 3);
@@ -244,6 +177,14 @@ struct Operand {
       lds_dma16(rsrc(base + (int64_t)k0 * ld, (uint32_t)(min(K - k0, kStep) * ld)), off[i], 0, to);
     else
       lds_dma16(rsrc(base + (int64_t)k0 * 2, 0x7FFFFFFFu), k0 + 8 * chunk[i] < K ? off[i] : kOff, 0, to);
+  }
+  // The same through registers: at the element's alignment, then to LDS.
+  __device__ __forceinline__ u32x4 fetch(int k0, int K, int i) const {
+    if (COLUMNS) return load_some(base + (int64_t)k0 * ld + off[i], k0 + chunk[i] < K ? width[i] : 0);
+    return load_some(base + (int64_t)k0 * 2 + off[i], off[i] != kOff ? K - k0 - 8 * chunk[i] : 0);
+  }
+  static __device__ __forceinline__ void put(u32x4 v, uint8_t* to, int wave, int lane, int i) {
+    *reinterpret_cast<u32x4*>(to + (2 * wave + i) * 1024 + lane * 16) = v;
   }
   // The fragment of 32 rows from `row0`, contraction elements 16 ks + 8 lh + 0..7 of row row0 + lr.
   static __device__ __forceinline__ bf16x8 fragment(const uint8_t* st, int row0, int ks, int lane) {
@@ -270,7 +211,7 @@ struct Operand {
 
 // Writes a wave's 128 x 64 results through its 4 KiB of LDS, 32 rows of 128
 // bytes at a time, whole lines of a row per store.
-template <typename T>
+template <typename T, bool DMA>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[4][2], uint8_t* lds, T* out, int64_t ld, int rows,
                                            int cols, int lane) {
   constexpr int PART = sizeof(T) == 4 ? 2 : 1;  // passes over the 64 columns
@@ -297,7 +238,23 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[4][2], uint8_t* l
       for (int r0 = 0; r0 < 32; r0 += 8) {
         const int r = r0 + (lane >> 3);
         const u32x4 v = *reinterpret_cast<const u32x4*>(lds + r * 128 + (c ^ (r & 7)) * 16);
-        if (i * 32 + r < rows && col < cols) *reinterpret_cast<u32x4*>(out + (int64_t)(i * 32 + r) * ld + col) = v;
+        T* to = out + (int64_t)(i * 32 + r) * ld + col;
+        constexpr int PER = 16 / sizeof(T);
+        if (i * 32 + r >= rows) continue;
+        if constexpr (DMA) {
+          if (col < cols) *reinterpret_cast<u32x4*>(to) = v;
+        } else if (col + PER <= cols) {
+          ((Unaligned16*)to)->v = v;
+        } else {
+#pragma unroll
+          for (int j = 0; j < PER - 1; ++j) {
+            if (col + j >= cols) break;
+            if constexpr (sizeof(T) == 4)
+              to[j] = u2f(v[j]);
+            else
+              to[j] = (T)(v[j / 2] >> (16 * (j % 2)));
+          }
+        }
       }
     }
 }
@@ -350,6 +307,18 @@ struct Tile {
     A.load(kt * kStep, K, to, wave, 0), A.load(kt * kStep, K, to, wave, 1);
     B.load(kt * kStep, K, to + kOperandBytes, wave, 0), B.load(kt * kStep, K, to + kOperandBytes, wave, 1);
   }
+  // The four loads of a wave for stage kt, and their way to LDS (without DMA).
+  __device__ __forceinline__ void fetch(int kt, u32x4 (&v)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[i] = A.fetch(kt * kStep, K, i), v[2 + i] = B.fetch(kt * kStep, K, i);
+  }
+  static __device__ __forceinline__ void put(const u32x4 (&v)[4], uint8_t* stage, int wave, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      Operand<ACOL>::put(v[i], stage, wave, lane, i);
+      Operand<BCOL>::put(v[2 + i], stage + kOperandBytes, wave, lane, i);
+    }
+  }
   // One of the four loads of a wave for stage kt.
   __device__ __forceinline__ void issue_part(int kt, int part, uint32_t ring, int wave) const {
     const uint32_t to = ring + (uint32_t)(kt % kRing) * kStageBytes;
@@ -360,7 +329,7 @@ struct Tile {
   }
 };
 
-template <int OP, bool F32>
+template <int OP, bool F32, bool DMA>
 __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) grouped_tiles(GroupedArgs g) {
   __shared__ TileLds L;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -377,10 +346,13 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
   int64_t id = (int64_t)(blockIdx.x % nq) * slots + blockIdx.x / nq;
   const uint32_t ring = lds_addr(&L.ring[0][0]);
   Tile<OP> t;
-  if (id < all) {
+  // The first stages of the tile `id`.
+  auto begin = [&] {
     t.init(g, L.tiles, id, wave, lane);
-    for (int kt = 0; kt < min(t.steps(), 3); ++kt) t.issue(kt, ring, wave);
-  }
+    if (DMA)
+      for (int kt = 0; kt < min(t.steps(), 3); ++kt) t.issue(kt, ring, wave);
+  };
+  if (id < all) begin();
   while (id < all) {
     f32x16 acc[4][2];
 #pragma unroll
@@ -395,6 +367,7 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
     auto run = [&](auto ni_c) {
       constexpr int NI = decltype(ni_c)::value;
       bf16x8 fa[2][NI > 0 ? NI : 1], fb[2][2];
+      u32x4 v[4];  // without DMA: a stage on its way
       // read(st, ks, r): the r-th of the fragments of half ks, in the order of their use
       auto read = [&](const uint8_t* st, int ks, int r) {
         if (NI > 0 && r < 6) {
@@ -430,29 +403,40 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
         constexpr bool MORE = decltype(more)::value;
         half(0, [&](int m) { read(stage(kt), 1, m); }, [](int) {});
         if constexpr (AFTER >= 0) {
-          wait_vmcnt<(AFTER < 0 ? 0 : AFTER)>();
+          if (DMA) {
+            wait_vmcnt<(AFTER < 0 ? 0 : AFTER)>();
+          } else {
+            t.put(v, &L.ring[(kt + 1) % kRing][0], wave, lane);
+            if (MORE) t.fetch(kt + 2, v);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          }
           // stage kt + 1 has landed, and nobody reads stage kt - 1 any more (its last fragments went into products
           // that this wave has issued; the reads in flight are of stage kt)
           __builtin_amdgcn_s_barrier();
           asm volatile("" ::: "memory");
           half(1, [&](int m) { read(stage(kt + 1), 0, m); }, [&](int m) {
-            if (MORE && m % 2 == 1) t.issue_part(kt + 3, m / 2, ring, wave);
+            if (DMA && MORE && m % 2 == 1) t.issue_part(kt + 3, m / 2, ring, wave);
           });
         } else {
           half(1, [](int) {}, [](int) {});
         }
       };
       using std::integral_constant;
-      // (the stores of the tile before are younger than the first stages' loads)
-      if (nk > 2)
-        wait_vmcnt<8>();
-      else
+      if (!DMA) {
+        t.fetch(0, v);
+        t.put(v, &L.ring[0][0], wave, lane);
+        if (nk > 1) t.fetch(1, v);
+      } else if (nk > 2) {
+        wait_vmcnt<8>();  // (the stores of the tile before are younger than the first stages' loads)
+      } else {
         wait_vmcnt<0>();
+      }
       __syncthreads();  // stage 0 has landed for every wave
       for (int r = 0; r < 6; ++r) read(stage(0), 0, r);
       int kt = 0;
-      for (; kt < nk - 3; ++kt) step(kt, integral_constant<int, 4>{}, std::true_type{});
-      if (nk > 2) step(kt++, integral_constant<int, 4>{}, std::false_type{});
+      constexpr int AHEAD = DMA ? 3 : 2;  // stages from a load to its use
+      for (; kt < nk - AHEAD; ++kt) step(kt, integral_constant<int, 4>{}, std::true_type{});
+      if (DMA && nk > 2) step(kt++, integral_constant<int, 4>{}, std::false_type{});
       if (nk > 1) step(kt++, integral_constant<int, 0>{}, std::false_type{});
       step(kt, integral_constant<int, -1>{}, std::false_type{});
     };
@@ -472,18 +456,15 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
     const int64_t out = t.out;
     const int rows = t.rows - wm * 128, cols = t.cols - wn * 64;
     id += gridDim.x;
-    if (id < all) {
-      t.init(g, L.tiles, id, wave, lane);
-      for (int kt = 0; kt < min(t.steps(), 3); ++kt) t.issue(kt, ring, wave);
-    }
+    if (id < all) begin();
     // the fourth stage is not in use before every wave has passed the next tile's first barrier
     uint8_t* part = &L.ring[3][0] + wave * 4096;
     const int64_t ld = OP == GROUPED_DW ? g.k : g.ld_out;
     const int64_t at = out + (int64_t)(wm * 128) * ld + wn * 64;
     if constexpr (F32)
-      store_tile(acc, part, (float*)g.out + at, ld, rows, cols, lane);
+      store_tile<float, DMA>(acc, part, (float*)g.out + at, ld, rows, cols, lane);
     else
-      store_tile(acc, part, (uint16_t*)g.out + at, ld, rows, cols, lane);
+      store_tile<uint16_t, DMA>(acc, part, (uint16_t*)g.out + at, ld, rows, cols, lane);
   }
   if (OP != GROUPED_DW && g.zero_rest) zero_rest(g, N);
 }
@@ -495,25 +476,24 @@ bool by_eight(const GroupedArgs& g) {
 
 }  // namespace
 
-hipError_t launch_grouped(GroupedOp op, const GroupedArgs& g, int cus, hipStream_t s) {
-  if (by_eight(g)) {
-    switch (op) {
-      case GROUPED_Y: grouped_tiles<GROUPED_Y, false><<<cus, kThreads, 0, s>>>(g); break;
-      case GROUPED_DX: grouped_tiles<GROUPED_DX, false><<<cus, kThreads, 0, s>>>(g); break;
-      default:
-        if (g.out_fp32)
-          grouped_tiles<GROUPED_DW, true><<<cus, kThreads, 0, s>>>(g);
-        else
-          grouped_tiles<GROUPED_DW, false><<<cus, kThreads, 0, s>>>(g);
-    }
-    return hipGetLastError();
-  }
-  const int grid = cus * 4;
+template <bool DMA>
+static void launch_tiles(GroupedOp op, const GroupedArgs& g, int cus, hipStream_t s) {
   switch (op) {
-    case GROUPED_Y: grouped_any<GROUPED_Y><<<grid, kAnyThreads, 0, s>>>(g); break;
-    case GROUPED_DX: grouped_any<GROUPED_DX><<<grid, kAnyThreads, 0, s>>>(g); break;
-    default: grouped_any<GROUPED_DW><<<grid, kAnyThreads, 0, s>>>(g); break;
+    case GROUPED_Y: grouped_tiles<GROUPED_Y, false, DMA><<<cus, kThreads, 0, s>>>(g); break;
+    case GROUPED_DX: grouped_tiles<GROUPED_DX, false, DMA><<<cus, kThreads, 0, s>>>(g); break;
+    default:
+      if (g.out_fp32)
+        grouped_tiles<GROUPED_DW, true, DMA><<<cus, kThreads, 0, s>>>(g);
+      else
+        grouped_tiles<GROUPED_DW, false, DMA><<<cus, kThreads, 0, s>>>(g);
   }
+}
+
+hipError_t launch_grouped(GroupedOp op, const GroupedArgs& g, int cus, hipStream_t s) {
+  if (by_eight(g))
+    launch_tiles<true>(op, g, cus, s);
+  else
+    launch_tiles<false>(op, g, cus, s);
   return hipGetLastError();
 }
 
