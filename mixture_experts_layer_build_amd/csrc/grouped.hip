@@ -113,16 +113,26 @@ __device__ __forceinline__ void zero_rest(const GroupedArgs& g, int cols) {
 // (which the memory takes), and single elements where a chunk of 8 ends beyond
 // the tile.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 256, kStep = 32, kThreads = 512, kRing = 4;
-constexpr int kOperandBytes = kTile * kStep * 2, kStageBytes = 2 * kOperandBytes;
+constexpr int kStep = 32, kRing = 4;
 constexpr int kNumXcd = 8;
 constexpr int kGroupM = 4;               // M tiles that run together with all N tiles
 constexpr uint32_t kOff = 0x80000000u;   // past every resource: loads return 0
 
+// S: rows and columns of a tile.
+template <int S>
+struct Shape {
+  static constexpr int kThreads = S == 256 ? 512 : 256, kWaves = kThreads / 64;
+  static constexpr int kWaveRows = S / 2, kWavesN = S / 64;  // a wave has S / 2 rows and 64 columns
+  static constexpr int kBlocks = kWaveRows / 32;             // its MFMA tiles along the rows
+  static constexpr int kOperandBytes = S * kStep * 2, kStageBytes = 2 * kOperandBytes;
+  static_assert(kOperandBytes == kWaves * 2 * 1024, "two loads of a wave per operand and stage");
+};
+
+template <int S>
 struct alignas(16) TileLds {
-  uint8_t ring[kRing][kStageBytes];
+  uint8_t ring[kRing][Shape<S>::kStageBytes];
   int32_t tiles[kGroupedMaxExperts + 1];
-  int32_t part[kThreads / 64];
+  int32_t part[Shape<S>::kWaves];
 };
 
 // 16 bytes at an element's alignment.
@@ -130,11 +140,19 @@ struct __attribute__((packed, aligned(2))) Unaligned16 {
   u32x4 v;
 };
 
-// Elements p[0..n) of eight, zeros behind them.
-__device__ __forceinline__ u32x4 load_some(const uint8_t* p, int n) {
+// Elements p[0..n) of eight, zeros behind them; `before`: elements of the same
+// row in front of p.
+__device__ __forceinline__ u32x4 load_some(const uint8_t* p, int n, int before) {
   u32x4 v{0, 0, 0, 0};
   if (n >= 8) {
     v = ((const Unaligned16*)p)->v;
+  } else if (n > 0 && before >= 8) {
+    // the eight that end with the last one, shifted down
+    typedef __attribute__((ext_vector_type(2))) uint64_t u64x2;
+    const u64x2 w = __builtin_bit_cast(u64x2, ((const Unaligned16*)(p - 2 * (8 - n)))->v);
+    const int s = 16 * (8 - n);
+    const uint64_t low = s >= 64 ? w[1] >> (s - 64) : (w[0] >> s) | (w[1] << (64 - s));
+    v = __builtin_bit_cast(u32x4, u64x2{low, s >= 64 ? 0 : w[1] >> s});
   } else if (n > 0) {
 #pragma unroll
     for (int j = 0; j < 7; ++j)
@@ -144,24 +162,27 @@ __device__ __forceinline__ u32x4 load_some(const uint8_t* p, int n) {
 }
 
 // An operand of the current tile.
-template <bool COLUMNS>
+template <bool COLUMNS, int S>
 struct Operand {
+  static constexpr int kRowChunks = S / 8, kLoadRows = 64 / kRowChunks;  // columns: chunks of a row, rows of a load
+
   const uint8_t* base;  // its first row (rows) or its first contraction row (columns) at the tile
   int64_t ld;           // bytes from row to row
   uint32_t off[2];      // this lane's two loads of a stage, kOff if outside
   int chunk[2];         // rows: the contraction chunk of each; columns: its contraction row
-  int width[2];         // columns: elements from its first one to the tile's end (not for DMA)
+  int width[2];         // columns: elements from its first one to the row's end (not for DMA)
+  int before[2];        // columns: elements of the row in front of its first one
 
-  // `have`: rows (columns: elements) of the tile that exist.
-  __device__ __forceinline__ void init(const void* p, int64_t ld_elements, int have, int wave, int lane) {
+  // `have`: rows (columns: elements) from the tile's first one on that exist; `front`: columns in front of it.
+  __device__ __forceinline__ void init(const void* p, int64_t ld_elements, int have, int front, int wave, int lane) {
     base = (const uint8_t*)p;
     ld = ld_elements * 2;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (COLUMNS) {
-        const int row = (2 * wave + i) * 2 + (lane >> 5), c = (lane & 31) ^ (4 * (row & 3));
+        const int row = (2 * wave + i) * kLoadRows + lane / kRowChunks, c = lane % kRowChunks ^ (4 * (row & 3));
         chunk[i] = row;
-        width[i] = have - c * 8;
+        width[i] = have - c * 8, before[i] = front + c * 8;
         off[i] = c * 8 < have ? (uint32_t)(row * ld) + 16u * c : kOff;
       } else {
         const int row = (2 * wave + i) * 16 + (lane >> 2), c = (lane & 3) ^ ((row >> 2) & 3);
@@ -180,8 +201,9 @@ struct Operand {
   }
   // The same through registers: at the element's alignment, then to LDS.
   __device__ __forceinline__ u32x4 fetch(int k0, int K, int i) const {
-    if (COLUMNS) return load_some(base + (int64_t)k0 * ld + off[i], k0 + chunk[i] < K ? width[i] : 0);
-    return load_some(base + (int64_t)k0 * 2 + off[i], off[i] != kOff ? K - k0 - 8 * chunk[i] : 0);
+    if (COLUMNS)
+      return load_some(base + (int64_t)k0 * ld + off[i], k0 + chunk[i] < K ? width[i] : 0, before[i]);
+    return load_some(base + (int64_t)k0 * 2 + off[i], off[i] != kOff ? K - k0 - 8 * chunk[i] : 0, k0 + 8 * chunk[i]);
   }
   static __device__ __forceinline__ void put(u32x4 v, uint8_t* to, int wave, int lane, int i) {
     *reinterpret_cast<u32x4*>(to + (2 * wave + i) * 1024 + lane * 16) = v;
@@ -194,10 +216,10 @@ struct Operand {
       typedef __attribute__((address_space(3))) bf16x4 lds4;
       const int i = lane & 15, m = row0 + (lr & 16) + 4 * (i & 3), k = 16 * ks + 8 * lh + (i >> 2);
       // (k % 4 is i / 4 in both reads)
-      const uint8_t* at = st + k * 512 + ((m >> 3) ^ (4 * (i >> 2))) * 16 + (m & 7) * 2;
+      const uint8_t* at = st + k * (S * 2) + ((m >> 3) ^ (4 * (i >> 2))) * 16 + (m & 7) * 2;
 #if defined(__HIP_DEVICE_COMPILE__)
       const bf16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)at);
-      const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(at + 4 * 512));
+      const bf16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds4*)(at + 4 * S * 2));
       return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 #else
       return bf16x8{};
@@ -209,15 +231,15 @@ struct Operand {
   }
 };
 
-// Writes a wave's 128 x 64 results through its 4 KiB of LDS, 32 rows of 128
+// Writes a wave's results (BLOCKS x 32 rows of 64) through its 4 KiB of LDS, 32 rows of 128
 // bytes at a time, whole lines of a row per store.
-template <typename T, bool DMA>
-__device__ __forceinline__ void store_tile(const f32x16 (&acc)[4][2], uint8_t* lds, T* out, int64_t ld, int rows,
+template <typename T, bool DMA, int BLOCKS>
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[BLOCKS][2], uint8_t* lds, T* out, int64_t ld, int rows,
                                            int cols, int lane) {
   constexpr int PART = sizeof(T) == 4 ? 2 : 1;  // passes over the 64 columns
   const int lr = lane & 31, lh = lane >> 5;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < BLOCKS; ++i)
 #pragma unroll
     for (int h = 0; h < PART; ++h) {
 #pragma unroll
@@ -260,19 +282,22 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[4][2], uint8_t* l
 }
 
 // A tile of the output: its operands, and where a wave's results go.
-template <int OP>
+template <int OP, int S>
 struct Tile {
-  static constexpr bool ACOL = OP == GROUPED_DW, BCOL = OP != GROUPED_Y;
-  Operand<ACOL> A;
-  Operand<BCOL> B;
+  using OpA = Operand<OP == GROUPED_DW, S>;
+  using OpB = Operand<OP != GROUPED_Y, S>;
+  static constexpr int kOperandBytes = Shape<S>::kOperandBytes, kStageBytes = Shape<S>::kStageBytes;
+  OpA A;
+  OpB B;
   int K, rows, cols;  // contraction length; rows and columns of the output from the tile's corner on
   int64_t out;        // element of its corner
+  int turn;           // the stage that its contraction begins with
 
   __device__ __forceinline__ void init(const GroupedArgs& g, const int32_t* tiles, int64_t id, int wave, int lane) {
-    const int N = (int)(OP == GROUPED_Y ? g.n : g.k), nt = (N + kTile - 1) / kTile;
+    const int N = (int)(OP == GROUPED_Y ? g.n : g.k), nt = (N + S - 1) / S;
     int e, local, nm;
     if (OP == GROUPED_DW) {
-      nm = (int)((g.n + kTile - 1) / kTile);
+      nm = (int)((g.n + S - 1) / S);
       e = (int)(id / (nm * nt));
       local = (int)(id - (int64_t)e * nm * nt);
     } else {
@@ -281,88 +306,113 @@ struct Tile {
       nm = tiles[e + 1] - tiles[e];
     }
     const int first = local / (kGroupM * nt) * kGroupM, gm = min(kGroupM, nm - first), r = local - first * nt;
-    const int m0 = __builtin_amdgcn_readfirstlane((first + r % gm) * kTile);
-    const int n0 = __builtin_amdgcn_readfirstlane(r / gm * kTile);
+    const int m0 = __builtin_amdgcn_readfirstlane((first + r % gm) * S);
+    const int n0 = __builtin_amdgcn_readfirstlane(r / gm * S);
     int lo, hi;
     segment(g, e, lo, hi);
     lo = __builtin_amdgcn_readfirstlane(lo), hi = __builtin_amdgcn_readfirstlane(hi);
     rows = (OP == GROUPED_DW ? (int)g.n : hi - lo) - m0, cols = N - n0;
     K = (int)(OP == GROUPED_Y ? g.k : OP == GROUPED_DX ? g.n : hi - lo);
+    // Rows that lie a multiple of 4 KiB apart have the same columns in the same
+    // memory channels: tiles start at different columns, spread over the range
+    // between the XCDs and the experts, and by a few stages between tiles that
+    // share operands (which stay near each other for the cache's sake).
+    const int n = steps();
+    turn = 0;
+    if (OP != GROUPED_DW && n > 0) {
+      const int apart = OP == GROUPED_Y ? 2 * ((m0 / S + n0 / S) % 4) : 0;
+      turn = ((int)(blockIdx.x % kNumXcd) * n / kNumXcd + 3 * e + apart) % n;
+    }
     const uint16_t* a = (const uint16_t*)g.a;
     const uint16_t* b = (const uint16_t*)g.b;
     if (OP == GROUPED_DW) {
-      A.init(a + lo * g.ld_a + m0, g.ld_a, rows, wave, lane);
-      B.init(b + lo * g.ld_b + n0, g.ld_b, cols, wave, lane);
+      A.init(a + lo * g.ld_a + m0, g.ld_a, rows, m0, wave, lane);
+      B.init(b + lo * g.ld_b + n0, g.ld_b, cols, n0, wave, lane);
       out = ((int64_t)e * g.n + m0) * g.k + n0;
     } else {
-      A.init(a + (lo + m0) * g.ld_a, g.ld_a, rows, wave, lane);
-      B.init(b + (int64_t)e * g.n * g.k + (OP == GROUPED_Y ? n0 * g.k : n0), g.k, cols, wave, lane);
+      A.init(a + (lo + m0) * g.ld_a, g.ld_a, rows, 0, wave, lane);
+      B.init(b + (int64_t)e * g.n * g.k + (OP == GROUPED_Y ? n0 * g.k : n0), g.k, cols, n0, wave, lane);
       out = (lo + m0) * g.ld_out + n0;
     }
   }
   __device__ __forceinline__ int steps() const { return (K + kStep - 1) / kStep; }
+  // First contraction element of the kt-th stage.
+  __device__ __forceinline__ int at(int kt) const {
+    const int n = steps(), k = kt + turn;
+    return (k < n ? k : k - n) * kStep;
+  }
   // Loads stage kt.
   __device__ __forceinline__ void issue(int kt, uint32_t ring, int wave) const {
     const uint32_t to = ring + (uint32_t)(kt % kRing) * kStageBytes;
-    A.load(kt * kStep, K, to, wave, 0), A.load(kt * kStep, K, to, wave, 1);
-    B.load(kt * kStep, K, to + kOperandBytes, wave, 0), B.load(kt * kStep, K, to + kOperandBytes, wave, 1);
+    A.load(at(kt), K, to, wave, 0), A.load(at(kt), K, to, wave, 1);
+    B.load(at(kt), K, to + kOperandBytes, wave, 0), B.load(at(kt), K, to + kOperandBytes, wave, 1);
   }
   // The four loads of a wave for stage kt, and their way to LDS (without DMA).
   __device__ __forceinline__ void fetch(int kt, u32x4 (&v)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) v[i] = A.fetch(kt * kStep, K, i), v[2 + i] = B.fetch(kt * kStep, K, i);
+    for (int i = 0; i < 2; ++i) v[i] = A.fetch(at(kt), K, i), v[2 + i] = B.fetch(at(kt), K, i);
   }
   static __device__ __forceinline__ void put(const u32x4 (&v)[4], uint8_t* stage, int wave, int lane) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      Operand<ACOL>::put(v[i], stage, wave, lane, i);
-      Operand<BCOL>::put(v[2 + i], stage + kOperandBytes, wave, lane, i);
+      OpA::put(v[i], stage, wave, lane, i);
+      OpB::put(v[2 + i], stage + kOperandBytes, wave, lane, i);
     }
   }
   // One of the four loads of a wave for stage kt.
   __device__ __forceinline__ void issue_part(int kt, int part, uint32_t ring, int wave) const {
     const uint32_t to = ring + (uint32_t)(kt % kRing) * kStageBytes;
     if (part < 2)
-      A.load(kt * kStep, K, to, wave, part);
+      A.load(at(kt), K, to, wave, part);
     else
-      B.load(kt * kStep, K, to + kOperandBytes, wave, part - 2);
+      B.load(at(kt), K, to + kOperandBytes, wave, part - 2);
   }
 };
 
-template <int OP, bool F32, bool DMA>
-__global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2, 2))) grouped_tiles(GroupedArgs g) {
-  __shared__ TileLds L;
+template <int OP, bool F32, bool DMA, int S>
+__global__ void __launch_bounds__(Shape<S>::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
+grouped_tiles(GroupedArgs g) {
+  using H = Shape<S>;
+  using T = Tile<OP, S>;
+  __shared__ TileLds<S> L;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
-  const int N = (int)(OP == GROUPED_Y ? g.n : g.k), nt = (N + kTile - 1) / kTile;
-  if (OP != GROUPED_DW) scan_tiles<kThreads>(g, kTile, L.tiles, L.part);
+  const int wm = wave / H::kWavesN, wn = wave % H::kWavesN;
+  const int N = (int)(OP == GROUPED_Y ? g.n : g.k), nt = (N + S - 1) / S;
+  if (OP != GROUPED_DW) scan_tiles<H::kThreads>(g, S, L.tiles, L.part);
   const int64_t all =
-      OP == GROUPED_DW ? (int64_t)g.E * ((g.n + kTile - 1) / kTile) * nt : (int64_t)L.tiles[g.E] * nt;
-  // Workgroup b runs on XCD b % 8; runs of as many tiles as an XCD has
-  // workgroups go to the XCDs in turn, so that the tiles that share operands
-  // run together on one L2.
-  const int nq = gridDim.x % kNumXcd == 0 ? kNumXcd : 1;
-  const int slots = gridDim.x / nq;
-  int64_t id = (int64_t)(blockIdx.x % nq) * slots + blockIdx.x / nq;
+      OP == GROUPED_DW ? (int64_t)g.E * ((g.n + S - 1) / S) * nt : (int64_t)L.tiles[g.E] * nt;
+  // Workgroup b runs on XCD b % 8. Runs of neighbouring tiles, which share
+  // operands, go to the XCDs in turn: as many as an XCD has workgroups, but in
+  // the last round the XCDs share what is left evenly.
+  const int nq = gridDim.x % kNumXcd == 0 ? kNumXcd : 1, slots = gridDim.x / nq;
+  const int xcd = blockIdx.x % nq, slot = blockIdx.x / nq;
+  const int64_t full = all - all % gridDim.x;
+  const int last = (int)(all - full + nq - 1) / nq;
+  // the tile behind `at`, this workgroup's first one of a round
+  auto tile_of = [&](int64_t at) {
+    if (at + gridDim.x <= all) return at + (int64_t)xcd * slots + slot;
+    return slot < last ? at + (int64_t)xcd * last + slot : all;
+  };
+  int64_t round = 0, id = tile_of(0);
   const uint32_t ring = lds_addr(&L.ring[0][0]);
-  Tile<OP> t;
+  T t;
   // The first stages of the tile `id`.
   auto begin = [&] {
     t.init(g, L.tiles, id, wave, lane);
     if (DMA)
-      for (int kt = 0; kt < min(t.steps(), 3); ++kt) t.issue(kt, ring, wave);
+      for (int kt = 0; kt < min(t.steps(), kRing - 1); ++kt) t.issue(kt, ring, wave);
   };
   if (id < all) begin();
   while (id < all) {
-    f32x16 acc[4][2];
+    f32x16 acc[H::kBlocks][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < H::kBlocks; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
     const int nk = t.steps();
-    // NI: 32-row blocks of this wave that hold rows, rounded up to 0, 1, 2 or 4 (at compile time, so that a ragged
+    // NI: 32-row blocks of this wave that hold rows, rounded up to 0, 1, 2 or all (at compile time, so that a ragged
     // tile leaves out reads and products without branches between them)
     auto run = [&](auto ni_c) {
       constexpr int NI = decltype(ni_c)::value;
@@ -370,11 +420,11 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
       u32x4 v[4];  // without DMA: a stage on its way
       // read(st, ks, r): the r-th of the fragments of half ks, in the order of their use
       auto read = [&](const uint8_t* st, int ks, int r) {
-        if (NI > 0 && r < 6) {
+        if (NI > 0 && r < NI + 2) {
           if (r == 0 || r == 2)
-            fb[ks][r / 2] = Operand<Tile<OP>::BCOL>::fragment(st + kOperandBytes, wn * 64 + r / 2 * 32, ks, lane);
+            fb[ks][r / 2] = T::OpB::fragment(st + T::kOperandBytes, wn * 64 + r / 2 * 32, ks, lane);
           else if (const int i = r == 1 ? 0 : r - 2; i < NI)
-            fa[ks][i] = Operand<Tile<OP>::ACOL>::fragment(st, wm * 128 + i * 32, ks, lane);
+            fa[ks][i] = T::OpA::fragment(st, wm * H::kWaveRows + i * 32, ks, lane);
         }
       };
       auto stage = [&](int kt) { return (const uint8_t*)&L.ring[kt % kRing][0]; };
@@ -382,9 +432,10 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
       // fragments and a stage's loads: while a product occupies the matrix
       // pipe, the wave's next instructions go to the other units, so none of
       // them may queue up in front of the products.
+      constexpr int kMost = 2 * H::kBlocks;
       auto half = [&](int ks, auto read_next, auto&& load) {
 #pragma unroll
-        for (int m = 0; m < 8; ++m) {
+        for (int m = 0; m < kMost; ++m) {
           if constexpr (NI > 0) if (m / 2 < NI) {
             __builtin_amdgcn_sched_barrier(0);
             acc[m / 2][m % 2] =
@@ -415,7 +466,8 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
           __builtin_amdgcn_s_barrier();
           asm volatile("" ::: "memory");
           half(1, [&](int m) { read(stage(kt + 1), 0, m); }, [&](int m) {
-            if (DMA && MORE && m % 2 == 1) t.issue_part(kt + 3, m / 2, ring, wave);
+            constexpr int EVERY = kMost / 4;
+            if (DMA && MORE && m % EVERY == EVERY - 1) t.issue_part(kt + kRing - 1, m / EVERY, ring, wave);
           });
         } else {
           half(1, [](int) {}, [](int) {});
@@ -426,24 +478,31 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
         t.fetch(0, v);
         t.put(v, &L.ring[0][0], wave, lane);
         if (nk > 1) t.fetch(1, v);
-      } else if (nk > 2) {
-        wait_vmcnt<8>();  // (the stores of the tile before are younger than the first stages' loads)
+      } else if (nk > kRing - 2) {
+        wait_vmcnt<4 * (kRing - 2)>();  // (the stores of the tile before are younger than the first stages' loads)
       } else {
         wait_vmcnt<0>();
       }
       __syncthreads();  // stage 0 has landed for every wave
-      for (int r = 0; r < 6; ++r) read(stage(0), 0, r);
+      for (int r = 0; r < NI + 2; ++r) read(stage(0), 0, r);
       int kt = 0;
-      constexpr int AHEAD = DMA ? 3 : 2;  // stages from a load to its use
-      for (; kt < nk - AHEAD; ++kt) step(kt, integral_constant<int, 4>{}, std::true_type{});
-      if (DMA && nk > 2) step(kt++, integral_constant<int, 4>{}, std::false_type{});
-      if (nk > 1) step(kt++, integral_constant<int, 0>{}, std::false_type{});
+      constexpr int AHEAD = DMA ? kRing - 1 : 2;  // stages from a load to its use
+      for (; kt < nk - AHEAD; ++kt) step(kt, integral_constant<int, 4 * (kRing - 3)>{}, std::true_type{});
+      // the last stages: one fewer in flight from step to step
+      auto drain = [&](auto self, auto left) {
+        constexpr int LEFT = decltype(left)::value;
+        if constexpr (LEFT > 1) {
+          if (nk >= LEFT) step(kt++, integral_constant<int, 4 * (LEFT - 2)>{}, std::false_type{});
+          self(self, integral_constant<int, LEFT - 1>{});
+        }
+      };
+      drain(drain, integral_constant<int, AHEAD>{});
       step(kt, integral_constant<int, -1>{}, std::false_type{});
     };
-    const int live = min(4, max(0, (t.rows - wm * 128 + 31) / 32));
+    const int live = min(H::kBlocks, max(0, (t.rows - wm * H::kWaveRows + 31) / 32));
     if (nk > 0) {
       if (live > 2)
-        run(std::integral_constant<int, 4>{});
+        run(std::integral_constant<int, H::kBlocks>{});
       else if (live == 2)
         run(std::integral_constant<int, 2>{});
       else if (live == 1)
@@ -454,19 +513,93 @@ __global__ void __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2
     // ---- results, while the next tile's first stages are loaded ----
     __syncthreads();  // nobody reads the ring any more
     const int64_t out = t.out;
-    const int rows = t.rows - wm * 128, cols = t.cols - wn * 64;
-    id += gridDim.x;
+    const int rows = t.rows - wm * H::kWaveRows, cols = t.cols - wn * 64;
+    round += gridDim.x;
+    id = tile_of(round);
     if (id < all) begin();
-    // the fourth stage is not in use before every wave has passed the next tile's first barrier
-    uint8_t* part = &L.ring[3][0] + wave * 4096;
+    // the last stage is not in use before every wave has passed the next tile's first barrier
+    static_assert(H::kWaves * 4096 == H::kStageBytes, "4 KiB for each wave");
+    uint8_t* part = &L.ring[kRing - 1][0] + wave * 4096;
     const int64_t ld = OP == GROUPED_DW ? g.k : g.ld_out;
-    const int64_t at = out + (int64_t)(wm * 128) * ld + wn * 64;
+    const int64_t at = out + (int64_t)(wm * H::kWaveRows) * ld + wn * 64;
     if constexpr (F32)
-      store_tile<float, DMA>(acc, part, (float*)g.out + at, ld, rows, cols, lane);
+      store_tile<float, DMA, H::kBlocks>(acc, part, (float*)g.out + at, ld, rows, cols, lane);
     else
-      store_tile<uint16_t, DMA>(acc, part, (uint16_t*)g.out + at, ld, rows, cols, lane);
+      store_tile<uint16_t, DMA, H::kBlocks>(acc, part, (uint16_t*)g.out + at, ld, rows, cols, lane);
   }
   if (OP != GROUPED_DW && g.zero_rest) zero_rest(g, N);
+}
+
+// ---------------------------------------------------------------------------
+// y for few rows per expert (decoding, small batches): bound by reading the
+// weights of the experts that have rows. A workgroup takes 16 rows of one
+// expert's weight and all its rows of x, 16 at a time; its waves take
+// chunks of 128 columns in turn and their sums are joined through LDS. Weights
+// and x go from memory straight into the operands of the 16 x 16 x 32 matrix
+// instruction (lane % 16 is the row of x, or of the weight, lane / 16 the
+// eighth of 32 columns).
+// ---------------------------------------------------------------------------
+constexpr int kFewWaves = 8, kFewChunk = 128;
+
+__global__ void __launch_bounds__(kFewWaves * 64) grouped_few(GroupedArgs g) {
+  __shared__ f32x4 part[kFewWaves][64];
+  __shared__ uint64_t busy[kGroupedMaxExperts / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kg = lane >> 4, li = lane & 15;
+  if (g.zero_rest && blockIdx.y == 0) zero_rest(g, (int)g.n);
+  // the blockIdx.y-th expert with rows
+  for (int e0 = 0; e0 < g.E; e0 += kFewWaves * 64) {
+    int lo = 0, hi = 0;
+    if (e0 + tid < g.E) segment(g, e0 + tid, lo, hi);
+    const uint64_t m = __ballot(hi > lo);
+    if (lane == 0 && e0 + wave * 64 < g.E) busy[e0 / 64 + wave] = m;
+  }
+  __syncthreads();
+  int e = -1, left = blockIdx.y;
+  for (int q = 0; q * 64 < g.E; ++q) {
+    uint64_t m = busy[q];
+    const int c = __popcll(m);
+    if (left < c) {
+      for (; left > 0; --left) m &= m - 1;
+      e = 64 * q + __ffsll((unsigned long long)m) - 1;
+      break;
+    }
+    left -= c;
+  }
+  e = __builtin_amdgcn_readfirstlane(e);
+  if (e < 0) return;  // fewer experts than workgroups: all of it
+  int lo, hi;
+  segment(g, e, lo, hi);
+  const int K = (int)g.k, n0 = blockIdx.x * 16;
+  const uint16_t* w = (const uint16_t*)g.b + ((int64_t)e * g.n + min(n0 + li, (int)g.n - 1)) * K;
+  for (int r0 = lo; r0 < hi; r0 += 16) {
+    f32x4 sum{0.f, 0.f, 0.f, 0.f};
+    // (rows past the end repeat the last one: their results are not stored)
+    const uint16_t* x = (const uint16_t*)g.a + (int64_t)min(r0 + li, hi - 1) * g.ld_a;
+    for (int k0 = wave * kFewChunk; k0 < K; k0 += kFewWaves * kFewChunk) {
+      bf16x8 a[4], b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = k0 + 32 * j + 8 * kg;
+        const bf16x8 none{};
+        b[j] = k < K ? *(const bf16x8*)(w + k) : none;
+        a[j] = k < K ? *(const bf16x8*)(x + k) : none;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], b[j], sum, 0, 0, 0);
+    }
+    part[wave][lane] = sum;
+    __syncthreads();
+    if (tid < 256) {  // row tid / 16, column tid % 16
+      const int r = tid >> 4, at = (r >> 2) * 16 + (tid & 15);
+      float v = 0.f;
+#pragma unroll
+      for (int q = 0; q < kFewWaves; ++q) v += part[q][at][r & 3];
+      const int row = r0 + r, col = n0 + (tid & 15);
+      if (row < hi && col < g.n) ((uint16_t*)g.out)[(int64_t)row * g.ld_out + col] = f32_to_bf16(v);
+    }
+    __syncthreads();
+  }
 }
 
 bool by_eight(const GroupedArgs& g) {
@@ -476,24 +609,50 @@ bool by_eight(const GroupedArgs& g) {
 
 }  // namespace
 
-template <bool DMA>
+template <bool DMA, int S>
 static void launch_tiles(GroupedOp op, const GroupedArgs& g, int cus, hipStream_t s) {
+  constexpr int THR = Shape<S>::kThreads;
+  const int grid = cus * (512 / THR);  // two waves per SIMD
   switch (op) {
-    case GROUPED_Y: grouped_tiles<GROUPED_Y, false, DMA><<<cus, kThreads, 0, s>>>(g); break;
-    case GROUPED_DX: grouped_tiles<GROUPED_DX, false, DMA><<<cus, kThreads, 0, s>>>(g); break;
+    case GROUPED_Y: grouped_tiles<GROUPED_Y, false, DMA, S><<<grid, THR, 0, s>>>(g); break;
+    case GROUPED_DX: grouped_tiles<GROUPED_DX, false, DMA, S><<<grid, THR, 0, s>>>(g); break;
     default:
       if (g.out_fp32)
-        grouped_tiles<GROUPED_DW, true, DMA><<<cus, kThreads, 0, s>>>(g);
+        grouped_tiles<GROUPED_DW, true, DMA, S><<<grid, THR, 0, s>>>(g);
       else
-        grouped_tiles<GROUPED_DW, false, DMA><<<cus, kThreads, 0, s>>>(g);
+        grouped_tiles<GROUPED_DW, false, DMA, S><<<grid, THR, 0, s>>>(g);
   }
 }
 
+// Whether 128 x 128 tiles are faster than 256 x 256. They read each operand
+// twice as often (65536 rows, 32 experts of 2048 x 7168: 2536 us against
+// 1731), but there are four times as many of them, and a batch wastes less of
+// them at the experts' ends. So: few rows per expert, where reading the weights
+// is the work (4096 rows, 128 experts of 768 x 2048: 87 us against 101; 1024 rows, 32 experts of
+// 2048 x 7168: 192 against 185), or fewer tiles than would occupy the card (2048 rows, 8
+// experts of 2048 x 2048: 34 us against 42; 8192 rows: 96 against 92).
+static bool small_tiles(GroupedOp op, const GroupedArgs& g, int cus) {
+  if (g.rows <= 32 * (int64_t)g.E) return true;
+  auto tiles = [](int64_t n, int64_t s) { return (n + s - 1) / s; };
+  if (op == GROUPED_DW) return g.E * tiles(g.n, 256) * tiles(g.k, 256) < cus;
+  // half a tile per expert is lost at its end, about
+  const int64_t n = op == GROUPED_Y ? g.n : g.k;
+  return (std::min<int64_t>(g.E, g.rows) + tiles(g.rows, 64)) * tiles(n, 128) <= cus * 7 / 2;
+}
+
 hipError_t launch_grouped(GroupedOp op, const GroupedArgs& g, int cus, hipStream_t s) {
-  if (by_eight(g))
-    launch_tiles<true>(op, g, cus, s);
-  else
-    launch_tiles<false>(op, g, cus, s);
+  const bool eight = by_eight(g), small = small_tiles(op, g, cus);
+  // A few rows per expert: every weight is used for 16 rows at most (8 rows,
+  // 128 experts of 768 x 2048: 9 us against 28 with tiles; 256 rows 67 against 69,
+  // 1024 rows 96 against 79).
+  if (op == GROUPED_Y && eight && g.rows <= 2 * (int64_t)g.E) {
+    const dim3 grid((unsigned)((g.n + 15) / 16), (unsigned)std::min<int64_t>(g.E, g.rows));
+    grouped_few<<<grid, kFewWaves * 64, 0, s>>>(g);
+  } else if (eight) {
+    small ? launch_tiles<true, 128>(op, g, cus, s) : launch_tiles<true, 256>(op, g, cus, s);
+  } else {
+    small ? launch_tiles<false, 128>(op, g, cus, s) : launch_tiles<false, 256>(op, g, cus, s);
+  }
   return hipGetLastError();
 }
 
