@@ -264,7 +264,7 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[BLOCKS][2], uint8
         constexpr int PER = 16 / sizeof(T);
         if (i * 32 + r >= rows) continue;
         if constexpr (DMA) {
-          if (col < cols) *reinterpret_cast<u32x4*>(to) = v;
+          if (col < cols) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(to));
         } else if (col + PER <= cols) {
           ((Unaligned16*)to)->v = v;
         } else {
