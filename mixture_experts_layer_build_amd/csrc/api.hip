@@ -1024,7 +1024,9 @@ extern "C" mok_status mok_forward_w4(const mok_w4_layer* layer, const void* x, c
   }
   if (!aligned(x, 16) || !aligned(scratch, 16)) return MOK_ERR_UNSUPPORTED;
   if (scratch_bytes < w4_layer_scratch(l, T)) return MOK_ERR_BUFFER_TOO_SMALL;
-  return to_status(launch_w4_layer(l, x, router_weights, top_experts, T, out, scratch, (hipStream_t)stream));
+  const int cus = current_cus();
+  if (cus <= 0) return MOK_ERR_HIP;
+  return to_status(launch_w4_layer(l, x, router_weights, top_experts, T, out, scratch, cus, (hipStream_t)stream));
 }
 
 // ------------------------------------------------------------------------

@@ -325,7 +325,7 @@ hipError_t launch_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, i
                             const mok_w4& w, void* y, int64_t ld_y, hipStream_t s);
 size_t w4_layer_scratch(const mok_w4_layer& l, int64_t T);
 hipError_t launch_w4_layer(const mok_w4_layer& l, const void* x, const float* router_w, const int64_t* ids, int64_t T,
-                           void* out, void* scratch, hipStream_t s);
+                           void* out, void* scratch, int cus, hipStream_t s);
 
 // The SwiGLU input limit the kernels apply: +inf (no clamp) unless the
 // configuration sets a positive finite limit.

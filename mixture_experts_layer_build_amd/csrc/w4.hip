@@ -98,53 +98,86 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// One lane's part of a chunk of 16 weight rows: codes, and the scales and zero
-// points of the groups (MXFP4: of its own block).
+// One lane's part of a chunk of 16 weight rows, as loaded: codes, and the scales
+// and zero points of the chunk's groups (MXFP4: the scale of its own block).
 template <int FMT, int G>
 struct Chunk {
   static constexpr int NG = FMT == kMx ? 1 : kChunk / G;
   u32v4 codes;
-  float scale[NG], zero[NG];
+  uint32_t sc[(NG + 1) / 2], z;
 
-  // Row `row` of a weight of K columns at columns k0..; columns past K count as zeros (whatever the codes, x is 0).
-  __device__ __forceinline__ void load(const W4& w, int64_t row, int k0, int K, int kg) {
+  // Row `row` of a weight of K columns at columns k0..; `whole`: K is a multiple of the chunk and the scales and zero
+  // points are aligned to a chunk's. Columns past K stand for zeros.
+  __device__ __forceinline__ void load(const W4& w, int64_t row, int k0, int K, int kg, bool whole) {
     const int k = k0 + 32 * kg;
     const bool in = k < K;
     codes = u32v4{0, 0, 0, 0};
     if (in) codes = *reinterpret_cast<const u32v4*>(w.codes + row * (K / 2) + k / 2);
+    z = 0;
     if constexpr (FMT == kMx) {
-      scale[0] = in ? e8m0(((const uint8_t*)w.scale)[row * (K / 32) + k / 32]) : 1.f;
+      sc[0] = in ? ((const uint8_t*)w.scale)[row * (K / 32) + k / 32] : 127;
     } else {
-      const int groups = K / G;
+      const int groups = K / G, at = k0 / G;
+      const uint16_t* s = (const uint16_t*)w.scale + row * groups + at;
+      const uint8_t* zp = FMT == kZero ? w.zero + row * groups + at : nullptr;
+      if (NG > 1 && whole) {
+        if constexpr (NG == 4) {
+          const u32v2 v = *reinterpret_cast<const u32v2*>(s);
+          sc[0] = v[0], sc[1] = v[1];
+          if (FMT == kZero) z = *reinterpret_cast<const uint32_t*>(zp);
+        } else if constexpr (NG == 2) {
+          sc[0] = *reinterpret_cast<const uint32_t*>(s);
+          if (FMT == kZero) z = *reinterpret_cast<const uint16_t*>(zp);
+        }
+      } else {
 #pragma unroll
-      for (int i = 0; i < NG; ++i) {
-        const int at = k0 / G + i;
-        scale[i] = 0.f, zero[i] = 8.f;
-        if (at < groups) {
-          scale[i] = bf16_to_f32(((const uint16_t*)w.scale)[row * groups + at]);
-          if (FMT == kZero) zero[i] = (float)w.zero[row * groups + at];
+        for (int i = 0; i < NG; ++i) {
+          if (i % 2 == 0) sc[i / 2] = 0;
+          if (at + i < groups) {
+            sc[i / 2] |= (uint32_t)s[i] << (16 * (i % 2));
+            if (FMT == kZero) z |= (uint32_t)zp[i] << (8 * i);
+          }
         }
       }
     }
   }
+  __device__ __forceinline__ float scale(int i) const {
+    return i % 2 ? u2f(sc[i / 2] & 0xFFFF0000u) : u2f(sc[i / 2] << 16);
+  }
+  // 128 + the zero point of group i
+  __device__ __forceinline__ float offset(int i) const {
+    return FMT == kZero ? 128.f + (float)(z >> (8 * i) & 255) : 136.f;
+  }
 };
 
-// One lane's x of a chunk: 16 tokens, four operands. In int4's order for int4,
-// with the groups' sums of x; token `row` is null where there is none.
+// One lane's x of a chunk, as loaded: four operands of a row (null: zeros).
+// ORDERED: the row is stored in the order of int4_values.
+struct TokenChunk {
+  u32v4 v[4];
+  template <int FMT>
+  __device__ __forceinline__ void load(const uint16_t* row, int k0, int K, int kg) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = k0 + (FMT == kMx ? 32 * kg + 8 * j : 32 * j + 8 * kg);
+      v[j] = u32v4{0, 0, 0, 0};
+      if (row && k < K) v[j] = *reinterpret_cast<const u32v4*>(row + k);
+    }
+  }
+};
+
+// x of a chunk as the products take it: the operands in int4's order, and for
+// int4 the groups' sums of x.
 template <int FMT, int G>
 struct Tokens {
   static constexpr int NG = FMT == kMx ? 1 : kChunk / G;
   bf16x8 v[4];
   f32x4 sum[NG];
 
-  __device__ __forceinline__ void load(const uint16_t* row, int k0, int K, int kg) {
+  template <bool ORDERED>
+  __device__ __forceinline__ void set(const TokenChunk& x) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = k0 + (FMT == kMx ? 32 * kg + 8 * j : 32 * j + 8 * kg);
-      u32v4 x{0, 0, 0, 0};
-      if (row && k < K) x = *reinterpret_cast<const u32v4*>(row + k);
-      v[j] = FMT == kMx ? __builtin_bit_cast(bf16x8, x) : int4_order(x);
-    }
+    for (int j = 0; j < 4; ++j)
+      v[j] = FMT == kMx || ORDERED ? __builtin_bit_cast(bf16x8, x.v[j]) : int4_order(x.v[j]);
     if constexpr (FMT != kMx) {
       const u32v4 ones{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
@@ -158,20 +191,19 @@ struct Tokens {
   }
 };
 
-// The chunk's products out[t] = x_t . w for TT tiles of 16 tokens; tiles
-// without their bit in `live` (the same in every lane) are left out.
-template <int FMT, int G, int TT>
-__device__ __forceinline__ void multiply(Chunk<FMT, G>& w, const Tokens<FMT, G> (&x)[TT], uint32_t live,
-                                         f32x4 (&out)[TT]) {
-#pragma unroll
-  for (int t = 0; t < TT; ++t) out[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+// The chunk's products x_t . w for TT tiles of 16 rows of x in P parts each
+// (whose sum x is), added to out.
+template <int FMT, int G, int TT, int P>
+__device__ __forceinline__ void multiply(Chunk<FMT, G> w, const Tokens<FMT, G> (&x)[TT][P], f32x4 (&out)[TT]) {
   if constexpr (FMT == kMx) {
+    const float scale = e8m0(w.sc[0]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bf16x8 b = mx_values(w.codes[j], w.scale[0]);
+      const bf16x8 b = mx_values(w.codes[j], scale);
 #pragma unroll
       for (int t = 0; t < TT; ++t)
-        if (TT == 1 || (live >> t & 1)) out[t] = mfma16(x[t].v[j], b, out[t]);
+#pragma unroll
+        for (int q = 0; q < P; ++q) out[t] = mfma16(x[t][q].v[j], b, out[t]);
     }
   } else {
     constexpr int NG = kChunk / G, PER = 4 / NG;
@@ -186,69 +218,96 @@ __device__ __forceinline__ void multiply(Chunk<FMT, G>& w, const Tokens<FMT, G> 
         const bf16x8 b = int4_values(w.codes[i * PER + j]);
 #pragma unroll
         for (int t = 0; t < TT; ++t)
-          if (TT == 1 || (live >> t & 1)) acc[t] = mfma16(x[t].v[i * PER + j], b, acc[t]);
+#pragma unroll
+          for (int q = 0; q < P; ++q) acc[t] = mfma16(x[t][q].v[i * PER + j], b, acc[t]);
       }
-      const float off = 128.f + w.zero[i];
+      const float scale = w.scale(i), off = w.offset(i);
 #pragma unroll
       for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) out[t][r] += w.scale[i] * (acc[t][r] - off * x[t].sum[i][r]);
+        for (int r = 0; r < 4; ++r) {
+          float sum = x[t][0].sum[i][r];
+#pragma unroll
+          for (int q = 1; q < P; ++q) sum += x[t][q].sum[i][r];
+          out[t][r] += scale * (acc[t][r] - off * sum);
+        }
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// y = x W^T: a workgroup takes 16 rows of the weight and 16 TT tokens, its
-// waves the chunks in turn.
+// y = x W^T: a workgroup takes 16 NS rows of the weight and 16 TT rows of x,
+// its waves the chunks in turn; the next chunk's weights are loaded before a
+// chunk is multiplied.
 // ---------------------------------------------------------------------------
-template <int FMT, int G, int TT, int NW>
+template <int FMT, int G, int TT, int NS, int NW>
 __global__ void __launch_bounds__(NW * 64)
-w4_product(const uint16_t* x, int64_t ld_x, int T, int64_t n, int K, W4 w, uint16_t* y, int64_t ld_y) {
-  __shared__ f32x4 part[NW][TT][64];
+w4_product(const uint16_t* x, int64_t ld_x, int T, int64_t n, int K, W4 w, bool whole, uint16_t* y, int64_t ld_y) {
+  __shared__ f32x4 part[NW][NS][TT][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, kg = lane >> 4, li = lane & 15;
-  const int64_t row = min((int64_t)blockIdx.x * 16 + li, n - 1);
   const int t0 = blockIdx.y * (16 * TT);
-  f32x4 sum[TT];
+  int64_t row[NS];
+  const uint16_t* xr[TT];
 #pragma unroll
-  for (int t = 0; t < TT; ++t) sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int k0 = wave * kChunk; k0 < K; k0 += NW * kChunk) {
-    Chunk<FMT, G> c;
-    c.load(w, row, k0, K, kg);
-    Tokens<FMT, G> xs[TT];
+  for (int s = 0; s < NS; ++s) row[s] = min((int64_t)blockIdx.x * (16 * NS) + 16 * s + li, n - 1);
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const int tok = t0 + 16 * t + li;
-      xs[t].load(tok < T ? x + tok * ld_x : nullptr, k0, K, kg);
-    }
-    f32x4 v[TT];
-    multiply<FMT, G, TT>(c, xs, ~0u, v);
+  for (int t = 0; t < TT; ++t) xr[t] = t0 + 16 * t + li < T ? x + (t0 + 16 * t + li) * ld_x : nullptr;
+  f32x4 sum[NS][TT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) sum[t] += v[t];
+  for (int s = 0; s < NS; ++s)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) sum[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  int k0 = wave * kChunk;
+  Chunk<FMT, G> c[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) c[s].load(w, row[s], k0, K, kg, whole && k0 < K);
+  for (; k0 < K; k0 += NW * kChunk) {
+    TokenChunk xc[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) xc[t].template load<FMT>(xr[t], k0, K, kg);
+    Chunk<FMT, G> next[NS];
+    const int k1 = k0 + NW * kChunk;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) next[s].load(w, row[s], k1, K, kg, whole && k1 < K);
+    Tokens<FMT, G> xs[TT][1];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) xs[t][0].template set<false>(xc[t]);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) multiply<FMT, G, TT, 1>(c[s], xs, sum[s]);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) c[s] = next[s];
   }
 #pragma unroll
-  for (int t = 0; t < TT; ++t) part[wave][t][lane] = sum[t];
+  for (int s = 0; s < NS; ++s)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) part[wave][s][t][lane] = sum[s][t];
   __syncthreads();
-  for (int i = threadIdx.x; i < TT * 256; i += NW * 64) {  // token i / 16, weight row i % 16
-    const int t = i >> 8, tok = (i >> 4) & 15, at = (tok >> 2) * 16 + (i & 15);
+  for (int i = threadIdx.x; i < NS * TT * 256; i += NW * 64) {  // weight row i % 16 of its sixteen, row of x i / 16
+    const int s = i / (TT * 256), at16 = i % (TT * 256), t = at16 >> 8, tok = (at16 >> 4) & 15;
+    const int at = (tok >> 2) * 16 + (i & 15);
     float v = 0.f;
 #pragma unroll
-    for (int q = 0; q < NW; ++q) v += part[q][t][at][tok & 3];
-    const int64_t col = (int64_t)blockIdx.x * 16 + (i & 15);
-    if (t0 + (i >> 4) < T && col < n) y[(t0 + (i >> 4)) * ld_y + col] = f32_to_bf16(v);
+    for (int q = 0; q < NW; ++q) v += part[q][s][t][at][tok & 3];
+    const int64_t col = (int64_t)blockIdx.x * (16 * NS) + 16 * s + (i & 15);
+    if (t0 + (at16 >> 4) < T && col < n) y[(t0 + (at16 >> 4)) * ld_y + col] = f32_to_bf16(v);
   }
 }
 
 // ---------------------------------------------------------------------------
-// The layer
+// The layer: h of every choice, then the output. h is kept as two bf16 that add
+// up to it (16 bits of it): the matrix instructions take bf16, and one alone
+// would double the output's error. It is stored in the order of int4_values.
 // ---------------------------------------------------------------------------
 struct Layer {
   int H, I, Is, E, k, T;
   float limit;
   W4 gate, up, down, sgate, sup, sdown;
+  bool whole_h, whole_i, whole_s;  // whole chunks along hidden, intermediate, shared intermediate
   const uint16_t* x;
   const float* rw;
   const int64_t* ids;
-  uint16_t* h;   // [T k, I], then [T, Is]
+  uint16_t* h;  // [T k][2][I], then [T][2][Is]
+  float* y;     // [T k + T][H]
   uint16_t* out;
 };
 
@@ -257,220 +316,277 @@ __device__ __forceinline__ int choice(const Layer& p, int pair) {
   return e >= 0 && e < p.E ? (int)e : -1;
 }
 
-// h of one expert's rows: 16 columns of I per workgroup. blockIdx.y numbers the
-// distinct experts among the ids (in order), the shared expert behind them.
-template <int FMT, int G, int TT, int NW>
+// LDS of the choices sorted by expert, in row tiles of 16.
+size_t plan_lds(const Layer& p) {
+  const size_t pairs = (size_t)p.T * p.k, tiles = std::min<size_t>(p.E, pairs) + pairs / 16;
+  return (p.E + tiles) * 4 + pairs * 4;
+}
+
+struct Plan {
+  int routed, tiles;   // row tiles of the routed experts; with the shared expert's behind them
+  const int* tile;     // expert << 18 | (rows - 1) << 14 | first choice in the list
+  const uint16_t* list;
+
+  // The same list in every workgroup: an expert's choices in their own order, since which of them share a row tile
+  // must not depend on who asks.
+  template <int NTHR>
+  __device__ __forceinline__ void build(const Layer& p, uint8_t* lds, int (&part)[NTHR / 64 + 1]) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, pairs = p.T * p.k;
+    int* cursor = (int*)lds;  // [E]: count, then where the expert's next choice goes, then its end
+    int* to = cursor + p.E;
+    uint16_t* any = (uint16_t*)(to + min(p.E, pairs) + pairs / 16);
+    uint16_t* out = any + pairs;
+    for (int e = tid; e < p.E; e += NTHR) cursor[e] = 0;
+    __syncthreads();
+    for (int i = tid; i < pairs; i += NTHR) {
+      const int e = choice(p, i);
+      if (e >= 0) atomicAdd(&cursor[e], 1);
+    }
+    int base = 0;  // rows | tiles << 16 of the experts before
+    for (int e0 = 0; e0 < p.E; e0 += NTHR) {
+      __syncthreads();
+      const int e = e0 + tid, rows = e < p.E ? cursor[e] : 0, tiles_e = (rows + 15) / 16;
+      const int mine = rows | tiles_e << 16;
+      int s = mine;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(s, d);
+        if (lane >= d) s += v;
+      }
+      if (lane == 63) part[wave] = s;
+      __syncthreads();
+      int before = base, all = base;
+      for (int w = 0; w < NTHR / 64; ++w) {
+        if (w < wave) before += part[w];
+        all += part[w];
+      }
+      before += s - mine;
+      const int r0 = before & 0xFFFF, t0 = before >> 16;
+      if (e < p.E) cursor[e] = r0;
+      for (int q = 0; q < tiles_e; ++q) to[t0 + q] = e << 18 | (min(16, rows - 16 * q) - 1) << 14 | (r0 + 16 * q);
+      base = all;
+    }
+    __syncthreads();
+    for (int i = tid; i < pairs; i += NTHR) {
+      const int e = choice(p, i);
+      if (e >= 0) any[atomicAdd(&cursor[e], 1)] = (uint16_t)i;
+    }
+    __syncthreads();
+    for (int i = tid; i < pairs; i += NTHR) {
+      const int e = choice(p, i);
+      if (e < 0) continue;
+      const int first = e > 0 ? cursor[e - 1] : 0, end = cursor[e];
+      int at = first;
+      for (int q = first; q < end; ++q) at += any[q] < i;
+      out[at] = (uint16_t)i;
+    }
+    __syncthreads();
+    routed = base >> 16;
+    tiles = routed + (p.Is > 0 ? (p.T + 15) / 16 : 0);
+    tile = to, list = out;
+  }
+};
+
+// A row tile: its expert (-1: the shared one) and this lane's choice (T k + the
+// token for the shared expert), -1 past its rows.
+struct RowTile {
+  int e, rows, first;
+  bool shared;
+  __device__ __forceinline__ void get(const Plan& l, int i, int T) {
+    shared = i >= l.routed;
+    if (shared) {
+      e = 0, first = 16 * (i - l.routed), rows = min(16, T - first);
+    } else {
+      const int v = __builtin_amdgcn_readfirstlane(l.tile[i]);
+      e = v >> 18, rows = (v >> 14 & 15) + 1, first = v & 0x3FFF;
+    }
+  }
+  __device__ __forceinline__ int pair(const Plan& l, int r, int pairs) const {
+    return r >= rows ? -1 : shared ? pairs + first + r : l.list[first + r];
+  }
+};
+
+// The element of int4_values' order that element i of eight goes to.
+__device__ __forceinline__ int ordered(int i) { return (i & 3) * 2 + (i >> 2); }
+
+// h: items of one row tile and 16 columns of I, taken in turn by the
+// workgroups; a workgroup's waves take the item's chunks in turn, the next
+// step's weights and x on their way while one is multiplied.
+template <int FMT, int G, int NW>
 __global__ void __launch_bounds__(NW * 64) w4_gate_up(Layer p) {
-  __shared__ f32x4 part[2][NW][TT][64];
-  __shared__ uint32_t seen[32];
-  __shared__ int count;
-  extern __shared__ uint8_t dyn[];
-  uint16_t* list = (uint16_t*)dyn;  // [T k] the expert's pairs
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, kg = lane >> 4, li = lane & 15;
-  const int pairs = p.T * p.k;
-  const int slots = min(p.E, pairs);
-  const bool shared = (int)blockIdx.y == slots;
-  int e = 0, rows = p.T;
-  if (!shared) {
-    if (tid < 32) seen[tid] = 0;
-    if (tid == 0) count = 0;
-    __syncthreads();
-    for (int i = tid; i < pairs; i += NW * 64) {
-      const int c = choice(p, i);
-      if (c >= 0) atomicOr(&seen[c >> 5], 1u << (c & 31));
-    }
-    __syncthreads();
-    // the blockIdx.y-th expert seen
-    int left = blockIdx.y;
-    e = -1;
-    for (int q = 0; q < 32; ++q) {
-      uint32_t bits = seen[q];
-      const int c = __popc(bits);
-      if (left < c) {
-        for (; left > 0; --left) bits &= bits - 1;
-        e = 32 * q + __ffs(bits) - 1;
-        break;
-      }
-      left -= c;
-    }
-    if (e < 0) return;  // fewer experts than slots: the whole workgroup
-    // its pairs, in any order: a row's h does not depend on its place
-    for (int i = tid; i < pairs; i += NW * 64)
-      if (choice(p, i) == e) list[atomicAdd(&count, 1)] = (uint16_t)i;
-    __syncthreads();
-    rows = count;
-  }
-  const int I = shared ? p.Is : p.I, K = p.H;
-  const int n0 = blockIdx.x * 16;
-  if (n0 >= I) return;
-  const int64_t row = (shared ? 0 : (int64_t)e * I) + min(n0 + li, I - 1);
-  const W4 wg = shared ? p.sgate : p.gate, wu = shared ? p.sup : p.up;
-  for (int r0 = 0; r0 < rows; r0 += 16 * TT) {
-    f32x4 g[TT], u[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) g[t] = u[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const uint16_t* xr[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-      const int r = r0 + 16 * t + li;
-      xr[t] = r < rows ? p.x + (int64_t)(shared ? r : list[r] / p.k) * K : nullptr;
-    }
-    for (int k0 = wave * kChunk; k0 < K; k0 += NW * kChunk) {
-      Chunk<FMT, G> cg, cu;
-      cg.load(wg, row, k0, K, kg);
-      cu.load(wu, row, k0, K, kg);
-      Tokens<FMT, G> xs[TT];
-#pragma unroll
-      for (int t = 0; t < TT; ++t) xs[t].load(xr[t], k0, K, kg);
-      f32x4 v[TT];
-      multiply<FMT, G, TT>(cg, xs, ~0u, v);
-#pragma unroll
-      for (int t = 0; t < TT; ++t) g[t] += v[t];
-      multiply<FMT, G, TT>(cu, xs, ~0u, v);
-#pragma unroll
-      for (int t = 0; t < TT; ++t) u[t] += v[t];
-    }
-#pragma unroll
-    for (int t = 0; t < TT; ++t) part[0][wave][t][lane] = g[t], part[1][wave][t][lane] = u[t];
-    __syncthreads();
-    for (int i = tid; i < TT * 256; i += NW * 64) {
-      const int t = i >> 8, tok = (i >> 4) & 15, at = (tok >> 2) * 16 + (i & 15);
-      float vg = 0.f, vu = 0.f;
-#pragma unroll
-      for (int q = 0; q < NW; ++q) vg += part[0][q][t][at][tok & 3], vu += part[1][q][t][at][tok & 3];
-      const int r = r0 + (i >> 4), col = n0 + (i & 15);
-      if (r < rows && col < I) {
-        const float lg = fminf(vg, p.limit), lu = fminf(fmaxf(vu, -p.limit), p.limit);
-        const float v = lg / (1.f + __expf(-lg)) * lu;
-        uint16_t* h = shared ? p.h + (int64_t)pairs * p.I + (int64_t)r * I : p.h + (int64_t)list[r] * I;
-        h[col] = f32_to_bf16(v);
-      }
-    }
-    __syncthreads();
-  }
-}
-
-// LDS of the output kernel besides its partial sums: weights and coefficients
-// [NT][k] fp32, ids [NT][k], and a byte for every (distinct expert, token).
-size_t down_lds(int nt, int k, int E) {
-  return (size_t)nt * k * (4 + 4 + 2) + (size_t)std::min(E, nt * k) * nt;
-}
-
-// The output: 16 columns of H for 16 TT tokens per workgroup. Its work is every
-// chunk of every distinct expert of these tokens, and of the shared expert,
-// taken by the waves in turn. A token's row of h is that of its first choice of
-// the expert (zeros if it has none), and the chunk's result goes to the token's
-// sum times the router weight of its choices of the expert. So a token's sums
-// are added in a fixed order, and no other launch joins them.
-template <int FMT, int G, int TT, int NW>
-__global__ void __launch_bounds__(NW * 64) w4_down(Layer p) {
-  constexpr int NT = 16 * TT;
-  __shared__ f32x4 part[NW][TT][64];
-  __shared__ uint32_t seen[32];
-  __shared__ int before[33];
-  __shared__ int16_t expert[1024];
+  __shared__ f32x4 part[2][NW][64];
+  __shared__ int scan[NW + 1];
   extern __shared__ uint8_t dyn[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), kg = lane >> 4,
             li = lane & 15;
-  const int t0 = blockIdx.y * NT, nt = min(NT, p.T - t0), pairs = nt * p.k;
-  float* given = (float*)dyn;
-  float* coef = given + NT * p.k;
-  int16_t* id = (int16_t*)(coef + NT * p.k);
-  uint8_t* slot = (uint8_t*)(id + NT * p.k);  // 1 + the token's first choice of the expert, 0: none
-  if (tid < 32) seen[tid] = 0;
-  __syncthreads();
-  for (int i = tid; i < pairs; i += NW * 64) {
-    const int c = choice(p, t0 * p.k + i);
-    id[i] = (int16_t)c;
-    given[i] = p.rw[t0 * p.k + i];
-    if (c >= 0) atomicOr(&seen[c >> 5], 1u << (c & 31));
-  }
-  __syncthreads();
-  if (tid == 0) {
-    int n = 0;
-    for (int q = 0; q < 32; ++q) before[q] = n, n += __popc(seen[q]);
-    before[32] = n;
-  }
-  __syncthreads();
-  const int distinct = before[32];
-  auto place = [&](int e) { return before[e >> 5] + __popc(seen[e >> 5] & ((1u << (e & 31)) - 1)); };
-  for (int i = tid; i < distinct * NT / 4; i += NW * 64) ((uint32_t*)slot)[i] = 0;
-  for (int e = tid; e < p.E; e += NW * 64)
-    if (seen[e >> 5] >> (e & 31) & 1) expert[place(e)] = (int16_t)e;
-  __syncthreads();
-  for (int i = tid; i < pairs; i += NW * 64) {
-    const int e = id[i], t = i / p.k, b = t * p.k;
-    if (e < 0) continue;
-    float sum = 0.f;
-    bool first = true;
-    for (int j = b; j < b + p.k; ++j)
-      if (id[j] == e) {
-        sum += given[j];
-        first = first && j >= i;
-      }
-    if (first) {
-      coef[i] = sum;
-      slot[place(e) * NT + t] = (uint8_t)(i - b + 1);
-    }
-  }
-  __syncthreads();
+  Plan l;
+  l.build<NW * 64>(p, dyn, scan);
+  const int pairs = p.T * p.k, K = p.H;
+  const int slabs_r = (p.I + 15) / 16, slabs_s = (p.Is + 15) / 16;
+  const int items_r = l.routed * slabs_r, items = items_r + (l.tiles - l.routed) * slabs_s;
+  const int steps = (K + NW * kChunk - 1) / (NW * kChunk);  // of an item, for each wave
 
-  const int64_t col = min((int)blockIdx.x * 16 + li, p.H - 1);
-  const int C = (p.I + kChunk - 1) / kChunk, routed = distinct * C;
-  const int units = routed + (p.Is + kChunk - 1) / kChunk;
-  f32x4 sum[TT];
-#pragma unroll
-  for (int t = 0; t < TT; ++t) sum[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int q = wave; q < units; q += NW) {
-    Chunk<FMT, G> c;
-    Tokens<FMT, G> xs[TT];
-    f32x4 v[TT];
-    if (q < routed) {
-      const int at = q / C, k0 = (q - at * C) * kChunk, e = expert[at];
-      c.load(p.down, (int64_t)e * p.H + col, k0, p.I, kg);
-      uint32_t live = 0;
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const int tok = 16 * t + li, s = slot[at * NT + tok];
-        if (__ballot(s != 0) != 0) live |= 1u << t;
-        const int64_t pair = (int64_t)(t0 + tok) * p.k + s - 1;
-        xs[t].load(s ? p.h + pair * p.I : nullptr, k0, p.I, kg);
+  struct Step {
+    Chunk<FMT, G> g, u;
+    TokenChunk x;
+  };
+  RowTile t;
+  int n0 = 0;
+  auto item = [&](int i) {
+    const bool sh = i >= items_r;
+    const int v = sh ? i - items_r : i, slabs = sh ? slabs_s : slabs_r;
+    t.get(l, (sh ? l.routed : 0) + v / slabs, p.T);
+    n0 = v % slabs * 16;
+  };
+  const uint16_t* xr = nullptr;
+  int64_t row = 0;
+  auto begin = [&] {
+    const int pr = t.pair(l, li, pairs), wide = t.shared ? p.Is : p.I;
+    xr = pr < 0 ? nullptr : p.x + (int64_t)(t.shared ? pr - pairs : pr / p.k) * K;
+    row = (int64_t)t.e * wide + min(n0 + li, wide - 1);
+  };
+  auto load = [&](Step& s, int st) {
+    const int k0 = (st * NW + wave) * kChunk;
+    const bool whole = p.whole_h && k0 < K;
+    const W4 wg = t.shared ? p.sgate : p.gate, wu = t.shared ? p.sup : p.up;
+    s.g.load(wg, row, k0, K, kg, whole);
+    s.u.load(wu, row, k0, K, kg, whole);
+    s.x.template load<FMT>(xr, k0, K, kg);
+  };
+  int i = blockIdx.x;
+  if (i >= items) return;
+  Step cur;
+  item(i);
+  begin();
+  load(cur, 0);
+  while (true) {
+    f32x4 g[1]{f32x4{0.f, 0.f, 0.f, 0.f}}, u[1]{f32x4{0.f, 0.f, 0.f, 0.f}};
+    const RowTile done = t;
+    const int col0 = n0, following = i + gridDim.x;
+    for (int st = 0; st < steps; ++st) {
+      Step next;
+      if (st + 1 < steps) {
+        load(next, st + 1);
+      } else if (following < items) {
+        item(following);
+        begin();
+        load(next, 0);
       }
-      multiply<FMT, G, TT>(c, xs, live, v);
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const uint32_t s4 = *(const uint32_t*)(slot + at * NT + 16 * t + 4 * kg);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int s = s4 >> (8 * r) & 255;
-          // (not 0 times v: another token's expert may hold what is not finite)
-          if (s) sum[t][r] += coef[(16 * t + 4 * kg + r) * p.k + s - 1] * v[t][r];
-        }
-      }
-    } else {
-      const int k0 = (q - routed) * kChunk;
-      c.load(p.sdown, col, k0, p.Is, kg);
-      const uint16_t* hs = p.h + (int64_t)p.T * p.k * p.I;
-#pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        const int tok = 16 * t + li;
-        xs[t].load(tok < nt ? hs + (int64_t)(t0 + tok) * p.Is : nullptr, k0, p.Is, kg);
-      }
-      multiply<FMT, G, TT>(c, xs, ~0u, v);
-#pragma unroll
-      for (int t = 0; t < TT; ++t) sum[t] += v[t];
+      Tokens<FMT, G> xs[1][1];
+      xs[0][0].template set<false>(cur.x);
+      multiply<FMT, G, 1, 1>(cur.g, xs, g);
+      multiply<FMT, G, 1, 1>(cur.u, xs, u);
+      cur = next;
     }
+    part[0][wave][lane] = g[0], part[1][wave][lane] = u[0];
+    __syncthreads();
+    if (tid < 256) {  // row tid / 16, column tid % 16
+      const int r = tid >> 4, c = tid & 15, at = (r >> 2) * 16 + c;
+      float vg = 0.f, vu = 0.f;
+#pragma unroll
+      for (int q = 0; q < NW; ++q) vg += part[0][q][at][r & 3], vu += part[1][q][at][r & 3];
+      const int pr = done.pair(l, r, pairs), wide = done.shared ? p.Is : p.I, col = col0 + c;
+      if (pr >= 0 && col < wide) {
+        const float lg = fminf(vg, p.limit), lu = fminf(fmaxf(vu, -p.limit), p.limit);
+        const float v = lg / (1.f + __expf(-lg)) * lu;
+        const uint16_t hi = f32_to_bf16(v), lo = f32_to_bf16(v - bf16_to_f32(hi));
+        uint16_t* h = p.h + (done.shared ? (int64_t)pairs * 2 * p.I + (int64_t)(pr - pairs) * 2 * p.Is
+                                         : (int64_t)pr * 2 * p.I);
+        const int to = FMT == kMx ? col : (col & ~7) + ordered(col & 7);
+        h[to] = hi, h[wide + to] = lo;
+      }
+    }
+    if (following >= items) break;
+    i = following;
+    __syncthreads();
   }
+}
+
+// y of every choice and of the shared expert: items as above, of 16 columns of H.
+template <int FMT, int G, int NW>
+__global__ void __launch_bounds__(NW * 64) w4_down(Layer p) {
+  __shared__ f32x4 part[NW][64];
+  __shared__ int scan[NW + 1];
+  extern __shared__ uint8_t dyn[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), kg = lane >> 4,
+            li = lane & 15;
+  Plan l;
+  l.build<NW * 64>(p, dyn, scan);
+  const int pairs = p.T * p.k, slabs = (p.H + 15) / 16, items = l.tiles * slabs;
+  struct Step {
+    Chunk<FMT, G> w;
+    TokenChunk x[2];
+  };
+  RowTile t;
+  int n0 = 0, K = 0;
+  const uint16_t* hr = nullptr;
+  int64_t row = 0;
+  auto begin = [&](int i) {
+    t.get(l, i / slabs, p.T);
+    n0 = i % slabs * 16;
+    K = t.shared ? p.Is : p.I;
+    const int pr = t.pair(l, li, pairs);
+    hr = pr < 0 ? nullptr
+         : t.shared ? p.h + (int64_t)pairs * 2 * p.I + (int64_t)(pr - pairs) * 2 * p.Is
+                    : p.h + (int64_t)pr * 2 * p.I;
+    row = (int64_t)t.e * p.H + min(n0 + li, p.H - 1);
+  };
+  auto steps = [&] { return (K + NW * kChunk - 1) / (NW * kChunk); };
+  auto load = [&](Step& s, int st) {
+    const int k0 = (st * NW + wave) * kChunk;
+    s.w.load(t.shared ? p.sdown : p.down, row, k0, K, kg, (t.shared ? p.whole_s : p.whole_i) && k0 < K);
 #pragma unroll
-  for (int t = 0; t < TT; ++t) part[wave][t][lane] = sum[t];
-  __syncthreads();
-  for (int i = tid; i < TT * 256; i += NW * 64) {
-    const int t = i >> 8, tok = (i >> 4) & 15, at = (tok >> 2) * 16 + (i & 15);
+    for (int q = 0; q < 2; ++q) s.x[q].template load<FMT>(hr ? hr + q * K : nullptr, k0, K, kg);
+  };
+  int i = blockIdx.x;
+  if (i >= items) return;
+  Step cur;
+  begin(i);
+  load(cur, 0);
+  while (true) {
+    f32x4 y[1]{f32x4{0.f, 0.f, 0.f, 0.f}};
+    const RowTile done = t;
+    const int col0 = n0, following = i + gridDim.x, n = steps();
+    for (int st = 0; st < n; ++st) {
+      Step next;
+      if (st + 1 < n) {
+        load(next, st + 1);
+      } else if (following < items) {
+        begin(following);
+        load(next, 0);
+      }
+      Tokens<FMT, G> xs[1][2];
+      xs[0][0].template set<true>(cur.x[0]);
+      xs[0][1].template set<true>(cur.x[1]);
+      multiply<FMT, G, 1, 2>(cur.w, xs, y);
+      cur = next;
+    }
+    part[wave][lane] = y[0];
+    __syncthreads();
+    for (int j = tid; j < 256; j += NW * 64) {
+      const int r = j >> 4, c = j & 15, at = (r >> 2) * 16 + c;
+      float v = 0.f;
+#pragma unroll
+      for (int q = 0; q < NW; ++q) v += part[q][at][r & 3];
+      const int pr = done.pair(l, r, pairs);
+      if (pr >= 0 && col0 + c < p.H) p.y[(int64_t)pr * p.H + col0 + c] = v;
+    }
+    if (following >= items) break;
+    i = following;
+    __syncthreads();
+  }
+}
+
+// The output: a token's choices in their order, then the shared expert's.
+__global__ void __launch_bounds__(256) w4_combine(Layer p) {
+  const int t = blockIdx.y;
+  const float* y = p.y + (int64_t)t * p.k * p.H;
+  for (int c = blockIdx.x * 256 + threadIdx.x; c < p.H; c += gridDim.x * 256) {
     float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) v += part[w][t][at][tok & 3];
-    const int c = blockIdx.x * 16 + (i & 15);
-    if ((i >> 4) < nt && c < p.H) p.out[(int64_t)(t0 + (i >> 4)) * p.H + c] = f32_to_bf16(v);
+    for (int j = 0; j < p.k; ++j)
+      if (choice(p, t * p.k + j) >= 0) v += p.rw[t * p.k + j] * y[(int64_t)j * p.H + c];
+    if (p.Is > 0) v += p.y[((int64_t)p.T * p.k + t) * p.H + c];
+    p.out[(int64_t)t * p.H + c] = f32_to_bf16(v);
   }
 }
 
@@ -623,44 +739,59 @@ hipError_t launch_w4_dequantize(const mok_w4& w, int64_t rows, int64_t cols, int
   return hipGetLastError();
 }
 
+// Whether rows of `k` elements are whole chunks whose scales and zero points can be loaded at once.
+static bool whole_chunks(const mok_w4& w, int64_t k, int group) {
+  const uintptr_t most = 2 * (kChunk / group);
+  return k % kChunk == 0 && (uintptr_t)w.scale % most == 0 && (uintptr_t)w.zero % (most / 2) == 0;
+}
+
 hipError_t launch_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, int64_t k, int format, int group,
                             const mok_w4& w, void* y, int64_t ld_y, hipStream_t s) {
-  const int slabs = (int)((n + 15) / 16);
+  const bool whole = whole_chunks(w, k, group);
   with_format(format, group, w.zero != nullptr, [&](auto fmt, auto g) {
     constexpr int FMT = decltype(fmt)::value, G = decltype(g)::value;
     if (T <= 16)
-      w4_product<FMT, G, 1, 8><<<dim3(slabs, 1), 512, 0, s>>>((const uint16_t*)x, ld_x, (int)T, n, (int)k, w4_of(w),
-                                                            (uint16_t*)y, ld_y);
+      w4_product<FMT, G, 1, 1, 8><<<dim3((unsigned)((n + 15) / 16), 1), 512, 0, s>>>(
+          (const uint16_t*)x, ld_x, (int)T, n, (int)k, w4_of(w), whole, (uint16_t*)y, ld_y);
     else
-      w4_product<FMT, G, 4, 8><<<dim3(slabs, (T + 63) / 64), 512, 0, s>>>((const uint16_t*)x, ld_x, (int)T, n, (int)k,
-                                                                        w4_of(w), (uint16_t*)y, ld_y);
+      w4_product<FMT, G, 4, 2, 8><<<dim3((unsigned)((n + 31) / 32), (unsigned)((T + 63) / 64)), 512, 0, s>>>(
+          (const uint16_t*)x, ld_x, (int)T, n, (int)k, w4_of(w), whole, (uint16_t*)y, ld_y);
   });
   return hipGetLastError();
 }
 
+static size_t h_elements(const mok_w4_layer& l, int64_t T) {
+  const size_t n = (size_t)T * 2 * ((size_t)l.topk * l.intermediate + l.shared_intermediate);
+  return (n + 7) / 8 * 8;
+}
 size_t w4_layer_scratch(const mok_w4_layer& l, int64_t T) {
-  return (size_t)std::max<int64_t>(1, T * ((int64_t)l.topk * l.intermediate + l.shared_intermediate)) * 2;
+  return std::max<size_t>(16, h_elements(l, T) * 2 + (size_t)T * (l.topk + 1) * l.hidden * 4);
 }
 
 hipError_t launch_w4_layer(const mok_w4_layer& l, const void* x, const float* router_w, const int64_t* ids, int64_t T,
-                           void* out, void* scratch, hipStream_t s) {
+                           void* out, void* scratch, int cus, hipStream_t s) {
   Layer p{};
   p.H = l.hidden, p.I = l.intermediate, p.Is = l.shared_intermediate, p.E = l.num_experts, p.k = l.topk, p.T = (int)T;
   p.limit = l.swiglu_limit > 0.f ? l.swiglu_limit : __builtin_inff();
   p.gate = w4_of(l.routed_gate), p.up = w4_of(l.routed_up), p.down = w4_of(l.routed_down);
   p.sgate = w4_of(l.shared_gate), p.sup = w4_of(l.shared_up), p.sdown = w4_of(l.shared_down);
+  const bool sh = p.Is > 0;
+  auto whole = [&](const mok_w4& w, int k) { return whole_chunks(w, k, l.group); };
+  p.whole_h = whole(l.routed_gate, p.H) && whole(l.routed_up, p.H) &&
+              (!sh || (whole(l.shared_gate, p.H) && whole(l.shared_up, p.H)));
+  p.whole_i = whole(l.routed_down, p.I), p.whole_s = sh && whole(l.shared_down, p.Is);
   p.x = (const uint16_t*)x, p.rw = router_w, p.ids = ids, p.h = (uint16_t*)scratch, p.out = (uint16_t*)out;
-  const int pairs = p.T * p.k, slots = std::min(p.E, pairs);
-  const dim3 up((std::max(p.I, p.Is) + 15) / 16, slots + (p.Is > 0 ? 1 : 0));
-  const int slabs = (p.H + 15) / 16;
+  p.y = (float*)((uint16_t*)scratch + h_elements(l, T));
+  const int pairs = p.T * p.k, tiles = std::min(p.E, pairs) + pairs / 16, shared = sh ? (p.T + 15) / 16 : 0;
+  const int64_t up = (int64_t)tiles * ((p.I + 15) / 16) + (int64_t)shared * ((p.Is + 15) / 16);
+  const int64_t down = (int64_t)(tiles + shared) * ((p.H + 15) / 16);
+  const size_t lds = plan_lds(p);
   with_format(l.format, l.group, l.routed_gate.zero != nullptr, [&](auto fmt, auto g) {
     constexpr int FMT = decltype(fmt)::value, G = decltype(g)::value;
-    w4_gate_up<FMT, G, 1, 8><<<up, 512, (size_t)pairs * 2, s>>>(p);
-    if (p.T <= 16 || p.E > 256)
-      w4_down<FMT, G, 1, 8><<<dim3(slabs, (p.T + 15) / 16), 512, down_lds(16, p.k, p.E), s>>>(p);
-    else
-      w4_down<FMT, G, 4, 8><<<dim3(slabs, (p.T + 63) / 64), 512, down_lds(64, p.k, p.E), s>>>(p);
+    w4_gate_up<FMT, G, 8><<<(unsigned)std::min<int64_t>(up, 2 * cus), 512, lds, s>>>(p);
+    w4_down<FMT, G, 4><<<(unsigned)std::min<int64_t>(down, 4 * cus), 256, lds, s>>>(p);
   });
+  w4_combine<<<dim3((p.H + 255) / 256, p.T), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 
