@@ -8,17 +8,21 @@
 // rows of the weight as its second: at up to 16 tokens most of its work is for
 // rows that are not there, but it keeps far ahead of the memory, and one lane
 // holds one weight row throughout (row lane % 16, its four-lane column kg =
-// lane / 16), so scales and zero points are one load per lane.
+// lane / 16), so scales and zero points are one value per lane.
 //
-// A wave works on chunks of 128 columns: 16 bytes of codes per lane, those of
-// the 32 columns 32 kg .. 32 kg + 31.
-//   int4: the dword exchange of the four lane rows gives every lane 8 columns of
-//     each 32-column block, so that each matrix instruction stays within one
-//     group, whatever its size. A code c becomes the bf16 128 + c by one OR (the
-//     exact integer); the sum over a group is sum (128 + c) x, from which (128 +
-//     zero) sum x is taken away in fp32 before the scale is applied. The sums of
-//     x come from a matrix instruction with ones. The cancellation costs at most
-//     5 of the 24 bits.
+// A wave works on chunks of 128 columns: 16 bytes of codes per lane. Loads are
+// made with four neighbouring lanes side by side in one row (row lane / 4), and
+// the registers are then moved to the lanes of the matrix instruction
+// (ds_bpermute): with neighbouring lanes in different rows the address unit,
+// which takes four lanes of 16 bytes at a time, was busy four times as long and
+// bound the layer (64 tokens, 128 experts of 768 x 2048: 130 us).
+//   A lane then has the codes of the 32 columns 32 kg .. 32 kg + 31; an exchange
+//     between the four lane rows gives it 8 columns of each 32-column block, so
+//     that each matrix instruction stays within one group, whatever its size.
+//   int4: a code c becomes the bf16 128 + c by one OR (the exact integer); the
+//     sum over a group is sum (128 + c) x, from which (128 + zero) sum x is taken
+//     away in fp32 before the scale is applied. The sums of x come from a matrix
+//     instruction with ones. The cancellation costs at most 5 of the 24 bits.
 //   MXFP4: the scaled conversion of gfx950 turns two codes into two bf16 with
 //     their block's scale, exactly: nothing is left to do but the product.
 #include <algorithm>
@@ -98,75 +102,124 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// One lane's part of a chunk of 16 weight rows, as loaded: codes, and the scales
-// and zero points of the chunk's groups (MXFP4: the scale of its own block).
-template <int FMT, int G>
-struct Chunk {
-  static constexpr int NG = FMT == kMx ? 1 : kChunk / G;
-  u32v4 codes;
-  uint32_t sc[(NG + 1) / 2], z;
+// The lane (as a byte address) that loads what this lane multiplies.
+__device__ __forceinline__ int source_lane(int lane) { return ((lane & 15) * 4 + (lane >> 4)) * 4; }
+__device__ __forceinline__ uint32_t from_lane(int src, uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_ds_bpermute(src, (int)v);
+}
 
-  // Row `row` of a weight of K columns at columns k0..; `whole`: K is a multiple of the chunk and the scales and zero
-  // points are aligned to a chunk's. Columns past K stand for zeros.
-  __device__ __forceinline__ void load(const W4& w, int64_t row, int k0, int K, int kg, bool whole) {
-    const int k = k0 + 32 * kg;
-    const bool in = k < K;
-    codes = u32v4{0, 0, 0, 0};
-    if (in) codes = *reinterpret_cast<const u32v4*>(w.codes + row * (K / 2) + k / 2);
-    z = 0;
+// One lane's part of a chunk of 16 weight rows, as loaded: codes, and the scales
+// and zero points of the chunk's groups.
+// WHOLE: rows are whole chunks, and their scales and zero points aligned to a
+// chunk's (one load). Nothing in a load branches or looks at what it gets: with a
+// fixed number of loads the compiler waits for a chunk's own ones, not for those
+// of the next chunk.
+// Columns past the row's end stand for zeros: the last ones are read again, with
+// a scale of 0 (MXFP4: codes of 0).
+template <int FMT, int G, bool WHOLE>
+struct Chunk {
+  static constexpr int NG = kChunk / G;  // groups
+  static constexpr int NS = WHOLE ? (FMT != kMx && NG == 4 ? 2 : 1) : NG, NZ = FMT == kZero ? (WHOLE ? 1 : NG) : 0;
+  u32v4 codes;
+  uint32_t s[NS], z[NZ > 0 ? NZ : 1];
+
+  // Row `row` of a weight of K columns at columns k0 and on; kq: this lane's quarter of them.
+  __device__ __forceinline__ void load(const W4& w, int64_t row, int k0, int K, int kq) {
+    const int k = min(k0 + 32 * kq, K - 32), groups = K / G;
+    codes = *reinterpret_cast<const u32v4*>(w.codes + row * (K / 2) + k / 2);
+    const int at = min(k0, K - (WHOLE ? kChunk : G)) / G;
     if constexpr (FMT == kMx) {
-      sc[0] = in ? ((const uint8_t*)w.scale)[row * (K / 32) + k / 32] : 127;
-    } else {
-      const int groups = K / G, at = k0 / G;
-      const uint16_t* s = (const uint16_t*)w.scale + row * groups + at;
-      const uint8_t* zp = FMT == kZero ? w.zero + row * groups + at : nullptr;
-      if (NG > 1 && whole) {
-        if constexpr (NG == 4) {
-          const u32v2 v = *reinterpret_cast<const u32v2*>(s);
-          sc[0] = v[0], sc[1] = v[1];
-          if (FMT == kZero) z = *reinterpret_cast<const uint32_t*>(zp);
-        } else if constexpr (NG == 2) {
-          sc[0] = *reinterpret_cast<const uint32_t*>(s);
-          if (FMT == kZero) z = *reinterpret_cast<const uint16_t*>(zp);
-        }
+      const uint8_t* p = (const uint8_t*)w.scale + row * groups;
+      if constexpr (WHOLE) {
+        s[0] = *reinterpret_cast<const uint32_t*>(p + at);
       } else {
 #pragma unroll
-        for (int i = 0; i < NG; ++i) {
-          if (i % 2 == 0) sc[i / 2] = 0;
-          if (at + i < groups) {
-            sc[i / 2] |= (uint32_t)s[i] << (16 * (i % 2));
-            if (FMT == kZero) z |= (uint32_t)zp[i] << (8 * i);
-          }
+        for (int i = 0; i < NG; ++i) s[i] = p[min(at + i, groups - 1)];
+      }
+    } else {
+      const uint16_t* p = (const uint16_t*)w.scale + row * groups;
+      if constexpr (!WHOLE) {
+#pragma unroll
+        for (int i = 0; i < NG; ++i) s[i] = p[min(at + i, groups - 1)];
+      } else if constexpr (NG == 4) {
+        const u32v2 v = *reinterpret_cast<const u32v2*>(p + at);
+        s[0] = v[0], s[1] = v[1];
+      } else if constexpr (NG == 2) {
+        s[0] = *reinterpret_cast<const uint32_t*>(p + at);
+      } else {
+        s[0] = p[at];
+      }
+      if constexpr (FMT == kZero) {
+        const uint8_t* q = w.zero + row * groups;
+        if constexpr (!WHOLE) {
+#pragma unroll
+          for (int i = 0; i < NG; ++i) z[i] = q[min(at + i, groups - 1)];
+        } else if constexpr (NG == 4) {
+          z[0] = *reinterpret_cast<const uint32_t*>(q + at);
+        } else if constexpr (NG == 2) {
+          z[0] = *reinterpret_cast<const uint16_t*>(q + at);
+        } else {
+          z[0] = q[at];
         }
       }
     }
   }
-  __device__ __forceinline__ float scale(int i) const {
-    return i % 2 ? u2f(sc[i / 2] & 0xFFFF0000u) : u2f(sc[i / 2] << 16);
-  }
-  // 128 + the zero point of group i
-  __device__ __forceinline__ float offset(int i) const {
-    return FMT == kZero ? 128.f + (float)(z >> (8 * i) & 255) : 136.f;
-  }
-};
-
-// One lane's x of a chunk, as loaded: four operands of a row (null: zeros).
-// ORDERED: the row is stored in the order of int4_values.
-struct TokenChunk {
-  u32v4 v[4];
-  template <int FMT>
-  __device__ __forceinline__ void load(const uint16_t* row, int k0, int K, int kg) {
+  // Moves it to the lanes that multiply it.
+  __device__ __forceinline__ void arrange(int src, int k0, int K) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = k0 + (FMT == kMx ? 32 * kg + 8 * j : 32 * j + 8 * kg);
-      v[j] = u32v4{0, 0, 0, 0};
-      if (row && k < K) v[j] = *reinterpret_cast<const u32v4*>(row + k);
+    for (int i = 0; i < 4; ++i) codes[i] = from_lane(src, codes[i]);
+    exchange(codes);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) s[i] = from_lane(src, s[i]);
+#pragma unroll
+    for (int i = 0; i < NZ; ++i) z[i] = from_lane(src, z[i]);
+    if constexpr (!WHOLE) {
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        if (k0 + i * G < K) continue;
+        if (FMT == kMx)
+          codes[i] = 0;
+        else
+          s[i] = 0;
+      }
     }
   }
+  // (arranged) of group i: the scale, and 128 + the zero point
+  __device__ __forceinline__ float scale(int i) const {
+    if (FMT == kMx) return e8m0(WHOLE ? s[0] >> (8 * i) & 255 : s[i]);
+    if (!WHOLE) return u2f(s[i] << 16);
+    return i % 2 ? u2f(s[i / 2] & 0xFFFF0000u) : u2f(s[i / 2] << 16);
+  }
+  __device__ __forceinline__ float offset(int i) const {
+    return FMT == kZero ? 128.f + (float)(WHOLE ? z[0] >> (8 * i) & 255 : z[i]) : 136.f;
+  }
 };
 
-// x of a chunk as the products take it: the operands in int4's order, and for
-// int4 the groups' sums of x.
+// One lane's x of a chunk: four operands of a row, 8 columns of each block of
+// 32. Columns past the row's end repeat its last block (the weight's are zeros
+// there).
+struct TokenChunk {
+  u32v4 v[4];
+  __device__ __forceinline__ void load(const uint16_t* row, int k0, int K, int kq) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const u32v4*>(row + min(k0 + 32 * j, K - 32) + 8 * kq);
+  }
+  // From h, which lies as it is multiplied (a block after the other).
+  __device__ __forceinline__ void load_blocks(const uint16_t* tile, int k0, int K, int lane) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = *reinterpret_cast<const u32v4*>(tile + (int64_t)(min(k0 / 32 + j, K / 32 - 1) * 64 + lane) * 8);
+  }
+  __device__ __forceinline__ void arrange(int src) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][i] = from_lane(src, v[j][i]);
+  }
+};
+
+// x of a chunk as the products take it: the operands in int4's order (ORDERED:
+// they are in it), and for int4 the groups' sums of x.
 template <int FMT, int G>
 struct Tokens {
   static constexpr int NG = FMT == kMx ? 1 : kChunk / G;
@@ -191,15 +244,15 @@ struct Tokens {
   }
 };
 
-// The chunk's products x_t . w for TT tiles of 16 rows of x in P parts each
-// (whose sum x is), added to out.
-template <int FMT, int G, int TT, int P>
-__device__ __forceinline__ void multiply(Chunk<FMT, G> w, const Tokens<FMT, G> (&x)[TT][P], f32x4 (&out)[TT]) {
+// The products x_t . w of an arranged chunk for TT tiles of 16 rows of x in P
+// parts each (whose sum x is), added to out.
+template <int FMT, int G, bool WHOLE, int TT, int P>
+__device__ __forceinline__ void multiply(const Chunk<FMT, G, WHOLE>& w, const Tokens<FMT, G> (&x)[TT][P],
+                                         f32x4 (&out)[TT]) {
   if constexpr (FMT == kMx) {
-    const float scale = e8m0(w.sc[0]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bf16x8 b = mx_values(w.codes[j], scale);
+      const bf16x8 b = mx_values(w.codes[j], w.scale(j));
 #pragma unroll
       for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -207,7 +260,6 @@ __device__ __forceinline__ void multiply(Chunk<FMT, G> w, const Tokens<FMT, G> (
     }
   } else {
     constexpr int NG = kChunk / G, PER = 4 / NG;
-    exchange(w.codes);
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
       f32x4 acc[TT];
@@ -240,42 +292,55 @@ __device__ __forceinline__ void multiply(Chunk<FMT, G> w, const Tokens<FMT, G> (
 // its waves the chunks in turn; the next chunk's weights are loaded before a
 // chunk is multiplied.
 // ---------------------------------------------------------------------------
-template <int FMT, int G, int TT, int NS, int NW>
+template <int FMT, int G, bool WHOLE, int TT, int NS, int NW>
 __global__ void __launch_bounds__(NW * 64)
-w4_product(const uint16_t* x, int64_t ld_x, int T, int64_t n, int K, W4 w, bool whole, uint16_t* y, int64_t ld_y) {
+w4_product(const uint16_t* x, int64_t ld_x, int T, int64_t n, int K, W4 w, uint16_t* y, int64_t ld_y) {
   __shared__ f32x4 part[NW][NS][TT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, kg = lane >> 4, li = lane & 15;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lrow = lane >> 2,
+            kq = lane & 3, src = source_lane(lane);
   const int t0 = blockIdx.y * (16 * TT);
+  // (rows past the ends repeat the last ones: their results are not stored)
   int64_t row[NS];
   const uint16_t* xr[TT];
 #pragma unroll
-  for (int s = 0; s < NS; ++s) row[s] = min((int64_t)blockIdx.x * (16 * NS) + 16 * s + li, n - 1);
+  for (int s = 0; s < NS; ++s) row[s] = min((int64_t)blockIdx.x * (16 * NS) + 16 * s + lrow, n - 1);
 #pragma unroll
-  for (int t = 0; t < TT; ++t) xr[t] = t0 + 16 * t + li < T ? x + (t0 + 16 * t + li) * ld_x : nullptr;
+  for (int t = 0; t < TT; ++t) xr[t] = x + min(t0 + 16 * t + lrow, T - 1) * ld_x;
   f32x4 sum[NS][TT];
 #pragma unroll
   for (int s = 0; s < NS; ++s)
 #pragma unroll
     for (int t = 0; t < TT; ++t) sum[s][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  struct Step {
+    Chunk<FMT, G, WHOLE> w[NS];
+    TokenChunk x[TT];
+  };
+  auto load = [&](Step& to, int k0) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) to.w[s].load(w, row[s], k0, K, kq);
+#pragma unroll
+    for (int t = 0; t < TT; ++t) to.x[t].load(xr[t], k0, K, kq);
+  };
   int k0 = wave * kChunk;
-  Chunk<FMT, G> c[NS];
-#pragma unroll
-  for (int s = 0; s < NS; ++s) c[s].load(w, row[s], k0, K, kg, whole && k0 < K);
-  for (; k0 < K; k0 += NW * kChunk) {
-    TokenChunk xc[TT];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) xc[t].template load<FMT>(xr[t], k0, K, kg);
-    Chunk<FMT, G> next[NS];
-    const int k1 = k0 + NW * kChunk;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) next[s].load(w, row[s], k1, K, kg, whole && k1 < K);
+  auto turn = [&](Step& cur, Step& next) {
+    load(next, k0 + NW * kChunk);
     Tokens<FMT, G> xs[TT][1];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) xs[t][0].template set<false>(xc[t]);
+    for (int t = 0; t < TT; ++t) cur.x[t].arrange(src), xs[t][0].template set<false>(cur.x[t]);
 #pragma unroll
-    for (int s = 0; s < NS; ++s) multiply<FMT, G, TT, 1>(c[s], xs, sum[s]);
-#pragma unroll
-    for (int s = 0; s < NS; ++s) c[s] = next[s];
+    for (int s = 0; s < NS; ++s) {
+      cur.w[s].arrange(src, k0, K);
+      multiply<FMT, G, WHOLE, TT, 1>(cur.w[s], xs, sum[s]);
+    }
+    k0 += NW * kChunk;
+    return k0 < K;
+  };
+  // (two buffers in turn: a copy from one to the other would wait for the loads)
+  Step a, b;
+  if (k0 < K) {
+    load(a, k0);
+    while (turn(a, b) && turn(b, a)) {
+    }
   }
 #pragma unroll
   for (int s = 0; s < NS; ++s)
@@ -296,17 +361,19 @@ w4_product(const uint16_t* x, int64_t ld_x, int T, int64_t n, int K, W4 w, bool 
 // ---------------------------------------------------------------------------
 // The layer: h of every choice, then the output. h is kept as two bf16 that add
 // up to it (16 bits of it): the matrix instructions take bf16, and one alone
-// would double the output's error. It is stored in the order of int4_values.
+// would double the output's error. It is stored as it is multiplied: per row tile
+// and part its blocks of 32 columns, each as the lanes take it, eight columns of a
+// row per lane (in the order of int4_values).
 // ---------------------------------------------------------------------------
 struct Layer {
   int H, I, Is, E, k, T;
   float limit;
   W4 gate, up, down, sgate, sup, sdown;
-  bool whole_h, whole_i, whole_s;  // whole chunks along hidden, intermediate, shared intermediate
   const uint16_t* x;
   const float* rw;
   const int64_t* ids;
-  uint16_t* h;  // [T k][2][I], then [T][2][Is]
+  uint16_t* h;  // [max_tiles][2][16 I], then [shared tiles][2][16 Is]
+  int max_tiles;
   float* y;     // [T k + T][H]
   uint16_t* out;
 };
@@ -318,8 +385,7 @@ __device__ __forceinline__ int choice(const Layer& p, int pair) {
 
 // LDS of the choices sorted by expert, in row tiles of 16.
 size_t plan_lds(const Layer& p) {
-  const size_t pairs = (size_t)p.T * p.k, tiles = std::min<size_t>(p.E, pairs) + pairs / 16;
-  return (p.E + tiles) * 4 + pairs * 4;
+  return (size_t)(p.E + p.max_tiles) * 4 + (size_t)p.T * p.k * 4;
 }
 
 struct Plan {
@@ -334,7 +400,7 @@ struct Plan {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, pairs = p.T * p.k;
     int* cursor = (int*)lds;  // [E]: count, then where the expert's next choice goes, then its end
     int* to = cursor + p.E;
-    uint16_t* any = (uint16_t*)(to + min(p.E, pairs) + pairs / 16);
+    uint16_t* any = (uint16_t*)(to + p.max_tiles);
     uint16_t* out = any + pairs;
     for (int e = tid; e < p.E; e += NTHR) cursor[e] = 0;
     __syncthreads();
@@ -387,8 +453,8 @@ struct Plan {
   }
 };
 
-// A row tile: its expert (-1: the shared one) and this lane's choice (T k + the
-// token for the shared expert), -1 past its rows.
+// A row tile: an expert (0 for the shared one) and its choices (T k + the token
+// for the shared expert).
 struct RowTile {
   int e, rows, first;
   bool shared;
@@ -401,8 +467,10 @@ struct RowTile {
       e = v >> 18, rows = (v >> 14 & 15) + 1, first = v & 0x3FFF;
     }
   }
+  // The r-th of its rows (a row past them: the last one).
   __device__ __forceinline__ int pair(const Plan& l, int r, int pairs) const {
-    return r >= rows ? -1 : shared ? pairs + first + r : l.list[first + r];
+    r = first + min(r, rows - 1);
+    return shared ? pairs + r : l.list[r];
   }
 };
 
@@ -410,170 +478,187 @@ struct RowTile {
 __device__ __forceinline__ int ordered(int i) { return (i & 3) * 2 + (i >> 2); }
 
 // h: items of one row tile and 16 columns of I, taken in turn by the
-// workgroups; a workgroup's waves take the item's chunks in turn, the next
-// step's weights and x on their way while one is multiplied.
-template <int FMT, int G, int NW>
+// workgroups; a workgroup's waves take the item's chunks in turn. The loop runs
+// over the items' steps, with the next step's weights and x on their way.
+template <int FMT, int G, bool WHOLE, int NW>
 __global__ void __launch_bounds__(NW * 64) w4_gate_up(Layer p) {
   __shared__ f32x4 part[2][NW][64];
   __shared__ int scan[NW + 1];
   extern __shared__ uint8_t dyn[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), kg = lane >> 4,
-            li = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6),
+            lrow = lane >> 2, kq = lane & 3, src = source_lane(lane);
   Plan l;
   l.build<NW * 64>(p, dyn, scan);
   const int pairs = p.T * p.k, K = p.H;
   const int slabs_r = (p.I + 15) / 16, slabs_s = (p.Is + 15) / 16;
   const int items_r = l.routed * slabs_r, items = items_r + (l.tiles - l.routed) * slabs_s;
   const int steps = (K + NW * kChunk - 1) / (NW * kChunk);  // of an item, for each wave
+  int i = blockIdx.x;
+  if (i >= items) return;
 
   struct Step {
-    Chunk<FMT, G> g, u;
+    Chunk<FMT, G, WHOLE> g, u;
     TokenChunk x;
   };
-  RowTile t;
-  int n0 = 0;
-  auto item = [&](int i) {
-    const bool sh = i >= items_r;
-    const int v = sh ? i - items_r : i, slabs = sh ? slabs_s : slabs_r;
-    t.get(l, (sh ? l.routed : 0) + v / slabs, p.T);
-    n0 = v % slabs * 16;
-  };
+  struct Item {
+    RowTile t;
+    int tile, n0;
+  } now, ahead;
   const uint16_t* xr = nullptr;
   int64_t row = 0;
-  auto begin = [&] {
-    const int pr = t.pair(l, li, pairs), wide = t.shared ? p.Is : p.I;
-    xr = pr < 0 ? nullptr : p.x + (int64_t)(t.shared ? pr - pairs : pr / p.k) * K;
-    row = (int64_t)t.e * wide + min(n0 + li, wide - 1);
+  auto begin = [&](int at) {
+    const bool sh = at >= items_r;
+    const int v = sh ? at - items_r : at, slabs = sh ? slabs_s : slabs_r, wide = sh ? p.Is : p.I;
+    ahead.tile = v / slabs;
+    ahead.t.get(l, (sh ? l.routed : 0) + ahead.tile, p.T);
+    ahead.n0 = v % slabs * 16;
+    const int pr = ahead.t.pair(l, lrow, pairs);
+    xr = p.x + (int64_t)(sh ? pr - pairs : pr / p.k) * K;
+    row = (int64_t)ahead.t.e * wide + min(ahead.n0 + lrow, wide - 1);
   };
   auto load = [&](Step& s, int st) {
     const int k0 = (st * NW + wave) * kChunk;
-    const bool whole = p.whole_h && k0 < K;
-    const W4 wg = t.shared ? p.sgate : p.gate, wu = t.shared ? p.sup : p.up;
-    s.g.load(wg, row, k0, K, kg, whole);
-    s.u.load(wu, row, k0, K, kg, whole);
-    s.x.template load<FMT>(xr, k0, K, kg);
+    const W4 wg = ahead.t.shared ? p.sgate : p.gate, wu = ahead.t.shared ? p.sup : p.up;
+    s.g.load(wg, row, k0, K, kq);
+    s.u.load(wu, row, k0, K, kq);
+    s.x.load(xr, k0, K, kq);
   };
-  int i = blockIdx.x;
-  if (i >= items) return;
-  Step cur;
-  item(i);
-  begin();
-  load(cur, 0);
-  while (true) {
-    f32x4 g[1]{f32x4{0.f, 0.f, 0.f, 0.f}}, u[1]{f32x4{0.f, 0.f, 0.f, 0.f}};
-    const RowTile done = t;
-    const int col0 = n0, following = i + gridDim.x;
-    for (int st = 0; st < steps; ++st) {
-      Step next;
-      if (st + 1 < steps) {
-        load(next, st + 1);
-      } else if (following < items) {
-        item(following);
-        begin();
-        load(next, 0);
-      }
+  f32x4 g[1], u[1];
+  int st = 0;
+  auto turn = [&](Step& cur, Step& next) {
+    if (st == 0) g[0] = u[0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const bool last = st == steps - 1;
+    if (last && i + (int)gridDim.x < items) begin(i + gridDim.x);
+    load(next, last ? 0 : st + 1);  // (behind the last item: the same one's first step again, for nothing)
+    // a wave whose chunk lies behind the row's end has no part in it
+    const int k0 = (st * NW + wave) * kChunk;
+    if (k0 < K) {
       Tokens<FMT, G> xs[1][1];
+      cur.x.arrange(src);
       xs[0][0].template set<false>(cur.x);
-      multiply<FMT, G, 1, 1>(cur.g, xs, g);
-      multiply<FMT, G, 1, 1>(cur.u, xs, u);
-      cur = next;
+      cur.g.arrange(src, k0, K);
+      cur.u.arrange(src, k0, K);
+      multiply<FMT, G, WHOLE, 1, 1>(cur.g, xs, g);
+      multiply<FMT, G, WHOLE, 1, 1>(cur.u, xs, u);
     }
+    ++st;
+    if (!last) return true;
     part[0][wave][lane] = g[0], part[1][wave][lane] = u[0];
     __syncthreads();
-    if (tid < 256) {  // row tid / 16, column tid % 16
-      const int r = tid >> 4, c = tid & 15, at = (r >> 2) * 16 + c;
+    for (int j = tid; j < 256; j += NW * 64) {  // row j / 16, column j % 16
+      const int r = j >> 4, c = j & 15, at = (r >> 2) * 16 + c;
       float vg = 0.f, vu = 0.f;
 #pragma unroll
       for (int q = 0; q < NW; ++q) vg += part[0][q][at][r & 3], vu += part[1][q][at][r & 3];
-      const int pr = done.pair(l, r, pairs), wide = done.shared ? p.Is : p.I, col = col0 + c;
-      if (pr >= 0 && col < wide) {
+      const int wide = now.t.shared ? p.Is : p.I, col = now.n0 + c;
+      if (r < now.t.rows && col < wide) {
         const float lg = fminf(vg, p.limit), lu = fminf(fmaxf(vu, -p.limit), p.limit);
         const float v = lg / (1.f + __expf(-lg)) * lu;
         const uint16_t hi = f32_to_bf16(v), lo = f32_to_bf16(v - bf16_to_f32(hi));
-        uint16_t* h = p.h + (done.shared ? (int64_t)pairs * 2 * p.I + (int64_t)(pr - pairs) * 2 * p.Is
-                                         : (int64_t)pr * 2 * p.I);
-        const int to = FMT == kMx ? col : (col & ~7) + ordered(col & 7);
-        h[to] = hi, h[wide + to] = lo;
+        uint16_t* h = p.h + (now.t.shared ? (int64_t)p.max_tiles * 32 * p.I : 0) + (int64_t)now.tile * 32 * wide;
+        const int to = (col / 32 * 64 + col / 8 % 4 * 16 + r) * 8 + (FMT == kMx ? col & 7 : ordered(col & 7));
+        h[to] = hi, h[16 * wide + to] = lo;
       }
     }
-    if (following >= items) break;
-    i = following;
+    i += gridDim.x;
+    if (i >= items) return false;
+    now = ahead;
+    st = 0;
     __syncthreads();
+    return true;
+  };
+  // (two buffers in turn: a copy from one to the other would wait for the loads)
+  Step a, b;
+  begin(i);
+  load(a, 0);
+  now = ahead;
+  while (turn(a, b) && turn(b, a)) {
   }
 }
 
-// y of every choice and of the shared expert: items as above, of 16 columns of H.
-template <int FMT, int G, int NW>
+// y of every choice and of the shared expert: items as above, of 32 columns of H
+// (which halves the reading of h).
+template <int FMT, int G, bool WHOLE, int NW>
 __global__ void __launch_bounds__(NW * 64) w4_down(Layer p) {
-  __shared__ f32x4 part[NW][64];
+  __shared__ f32x4 part[2][NW][64];
   __shared__ int scan[NW + 1];
   extern __shared__ uint8_t dyn[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), kg = lane >> 4,
-            li = lane & 15;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6),
+            lrow = lane >> 2, kq = lane & 3, src = source_lane(lane);
   Plan l;
   l.build<NW * 64>(p, dyn, scan);
-  const int pairs = p.T * p.k, slabs = (p.H + 15) / 16, items = l.tiles * slabs;
-  struct Step {
-    Chunk<FMT, G> w;
-    TokenChunk x[2];
-  };
-  RowTile t;
-  int n0 = 0, K = 0;
-  const uint16_t* hr = nullptr;
-  int64_t row = 0;
-  auto begin = [&](int i) {
-    t.get(l, i / slabs, p.T);
-    n0 = i % slabs * 16;
-    K = t.shared ? p.Is : p.I;
-    const int pr = t.pair(l, li, pairs);
-    hr = pr < 0 ? nullptr
-         : t.shared ? p.h + (int64_t)pairs * 2 * p.I + (int64_t)(pr - pairs) * 2 * p.Is
-                    : p.h + (int64_t)pr * 2 * p.I;
-    row = (int64_t)t.e * p.H + min(n0 + li, p.H - 1);
-  };
-  auto steps = [&] { return (K + NW * kChunk - 1) / (NW * kChunk); };
-  auto load = [&](Step& s, int st) {
-    const int k0 = (st * NW + wave) * kChunk;
-    s.w.load(t.shared ? p.sdown : p.down, row, k0, K, kg, (t.shared ? p.whole_s : p.whole_i) && k0 < K);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) s.x[q].template load<FMT>(hr ? hr + q * K : nullptr, k0, K, kg);
-  };
+  const int pairs = p.T * p.k, slabs = (p.H + 31) / 32, items = l.tiles * slabs;
   int i = blockIdx.x;
   if (i >= items) return;
-  Step cur;
-  begin(i);
-  load(cur, 0);
-  while (true) {
-    f32x4 y[1]{f32x4{0.f, 0.f, 0.f, 0.f}};
-    const RowTile done = t;
-    const int col0 = n0, following = i + gridDim.x, n = steps();
-    for (int st = 0; st < n; ++st) {
-      Step next;
-      if (st + 1 < n) {
-        load(next, st + 1);
-      } else if (following < items) {
-        begin(following);
-        load(next, 0);
-      }
+  struct Step {
+    Chunk<FMT, G, WHOLE> w[2];
+    TokenChunk x[2];
+  };
+  struct Item {
+    RowTile t;
+    int n0, K;
+  } now, ahead;
+  const uint16_t* hr = nullptr;
+  int64_t row[2] = {0, 0};
+  auto begin = [&](int at) {
+    const int tile = at / slabs;
+    ahead.t.get(l, tile, p.T);
+    ahead.n0 = at % slabs * 32;
+    ahead.K = ahead.t.shared ? p.Is : p.I;
+    hr = p.h + (ahead.t.shared ? (int64_t)p.max_tiles * 32 * p.I + (int64_t)(tile - l.routed) * 32 * p.Is
+                               : (int64_t)tile * 32 * p.I);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) row[s] = (int64_t)ahead.t.e * p.H + min(ahead.n0 + 16 * s + lrow, p.H - 1);
+  };
+  auto load = [&](Step& s, int st) {
+    const int k0 = (st * NW + wave) * kChunk;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) s.w[q].load(ahead.t.shared ? p.sdown : p.down, row[q], k0, ahead.K, kq);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) s.x[q].load_blocks(hr + q * 16 * ahead.K, k0, ahead.K, lane);
+  };
+  f32x4 y[2][1];
+  int st = 0;
+  auto turn = [&](Step& cur, Step& next) {
+    if (st == 0) y[0][0] = y[1][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const bool last = (st + 1) * NW * kChunk >= now.K;
+    if (last && i + (int)gridDim.x < items) begin(i + gridDim.x);
+    load(next, last ? 0 : st + 1);  // (behind the last item: the same one's first step again, for nothing)
+    const int k0 = (st * NW + wave) * kChunk;
+    if (k0 < now.K) {
       Tokens<FMT, G> xs[1][2];
       xs[0][0].template set<true>(cur.x[0]);
       xs[0][1].template set<true>(cur.x[1]);
-      multiply<FMT, G, 1, 2>(cur.w, xs, y);
-      cur = next;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        cur.w[s].arrange(src, k0, now.K);
+        multiply<FMT, G, WHOLE, 1, 2>(cur.w[s], xs, y[s]);
+      }
     }
-    part[wave][lane] = y[0];
+    ++st;
+    if (!last) return true;
+    part[0][wave][lane] = y[0][0], part[1][wave][lane] = y[1][0];
     __syncthreads();
-    for (int j = tid; j < 256; j += NW * 64) {
-      const int r = j >> 4, c = j & 15, at = (r >> 2) * 16 + c;
+    for (int j = tid; j < 512; j += NW * 64) {  // row j / 32, column j % 32
+      const int r = j >> 5, s = j >> 4 & 1, at = (r >> 2) * 16 + (j & 15), col = now.n0 + (j & 31);
       float v = 0.f;
 #pragma unroll
-      for (int q = 0; q < NW; ++q) v += part[q][at][r & 3];
-      const int pr = done.pair(l, r, pairs);
-      if (pr >= 0 && col0 + c < p.H) p.y[(int64_t)pr * p.H + col0 + c] = v;
+      for (int q = 0; q < NW; ++q) v += part[s][q][at][r & 3];
+      if (r < now.t.rows && col < p.H) p.y[(int64_t)now.t.pair(l, r, pairs) * p.H + col] = v;
     }
-    if (following >= items) break;
-    i = following;
+    i += gridDim.x;
+    if (i >= items) return false;
+    now = ahead;
+    st = 0;
     __syncthreads();
+    return true;
+  };
+  // (two buffers in turn: a copy from one to the other would wait for the loads)
+  Step a, b;
+  begin(i);
+  load(a, 0);
+  now = ahead;
+  while (turn(a, b) && turn(b, a)) {
   }
 }
 
@@ -690,24 +775,29 @@ w4_dequantize(W4 w, int64_t elements, int G, uint16_t* dst) {
   }
 }
 
-// f(format, group) as constants.
+// f(format, group, whole chunks) as constants.
 template <typename F>
-void with_format(int format, int group, bool zero, F&& f) {
+void with_format(int format, int group, bool zero, bool whole, F&& f) {
   using std::integral_constant;
-  auto grouped = [&](auto fmt) {
+  using std::true_type;
+  using std::false_type;
+  auto grouped = [&](auto fmt, auto wh) {
     if (group == 32)
-      f(fmt, integral_constant<int, 32>{});
+      f(fmt, integral_constant<int, 32>{}, wh);
     else if (group == 64)
-      f(fmt, integral_constant<int, 64>{});
+      f(fmt, integral_constant<int, 64>{}, wh);
     else
-      f(fmt, integral_constant<int, 128>{});
+      f(fmt, integral_constant<int, 128>{}, true_type{});  // a row is whole chunks
   };
-  if (format == MOK_W4_MXFP4)
-    f(integral_constant<int, kMx>{}, integral_constant<int, 32>{});
-  else if (zero)
-    grouped(integral_constant<int, kZero>{});
-  else
-    grouped(integral_constant<int, kSym>{});
+  auto either = [&](auto wh) {
+    if (format == MOK_W4_MXFP4)
+      f(integral_constant<int, kMx>{}, integral_constant<int, 32>{}, wh);
+    else if (zero)
+      grouped(integral_constant<int, kZero>{}, wh);
+    else
+      grouped(integral_constant<int, kSym>{}, wh);
+  };
+  whole ? either(true_type{}) : either(false_type{});
 }
 
 }  // namespace
@@ -715,7 +805,7 @@ void with_format(int format, int group, bool zero, F&& f) {
 hipError_t launch_w4_quantize(const void* src, int src_fp32, int64_t rows, int64_t cols, int64_t ld, int format,
                               int group, uint8_t* codes, void* scale, uint8_t* zero, hipStream_t s) {
   const int grid = (int)std::min<int64_t>((rows * cols / 8 + 255) / 256, 1 << 20);
-  with_format(format, group, zero != nullptr, [&](auto fmt, auto g) {
+  with_format(format, group, zero != nullptr, true, [&](auto fmt, auto g, auto) {
     constexpr int FMT = decltype(fmt)::value, G = decltype(g)::value;
     if (src_fp32)
       w4_quantize<float, FMT, G><<<grid, 256, 0, s>>>((const float*)src, rows, cols, ld, codes, scale, zero);
@@ -740,32 +830,39 @@ hipError_t launch_w4_dequantize(const mok_w4& w, int64_t rows, int64_t cols, int
 }
 
 // Whether rows of `k` elements are whole chunks whose scales and zero points can be loaded at once.
-static bool whole_chunks(const mok_w4& w, int64_t k, int group) {
+static bool whole_chunks(const mok_w4& w, int64_t k, int format, int group) {
+  if (k % kChunk != 0) return false;
   const uintptr_t most = 2 * (kChunk / group);
-  return k % kChunk == 0 && (uintptr_t)w.scale % most == 0 && (uintptr_t)w.zero % (most / 2) == 0;
+  if (format == MOK_W4_MXFP4) return (uintptr_t)w.scale % 4 == 0;
+  return (uintptr_t)w.scale % most == 0 && (uintptr_t)w.zero % (most / 2) == 0;
 }
 
 hipError_t launch_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, int64_t k, int format, int group,
                             const mok_w4& w, void* y, int64_t ld_y, hipStream_t s) {
-  const bool whole = whole_chunks(w, k, group);
-  with_format(format, group, w.zero != nullptr, [&](auto fmt, auto g) {
+  with_format(format, group, w.zero != nullptr, whole_chunks(w, k, format, group), [&](auto fmt, auto g, auto wh) {
     constexpr int FMT = decltype(fmt)::value, G = decltype(g)::value;
+    constexpr bool WHOLE = decltype(wh)::value;
     if (T <= 16)
-      w4_product<FMT, G, 1, 1, 8><<<dim3((unsigned)((n + 15) / 16), 1), 512, 0, s>>>(
-          (const uint16_t*)x, ld_x, (int)T, n, (int)k, w4_of(w), whole, (uint16_t*)y, ld_y);
+      w4_product<FMT, G, WHOLE, 1, 1, 8><<<dim3((unsigned)((n + 15) / 16), 1), 512, 0, s>>>(
+          (const uint16_t*)x, ld_x, (int)T, n, (int)k, w4_of(w), (uint16_t*)y, ld_y);
     else
-      w4_product<FMT, G, 4, 2, 8><<<dim3((unsigned)((n + 31) / 32), (unsigned)((T + 63) / 64)), 512, 0, s>>>(
-          (const uint16_t*)x, ld_x, (int)T, n, (int)k, w4_of(w), whole, (uint16_t*)y, ld_y);
+      w4_product<FMT, G, WHOLE, 4, 2, 8><<<dim3((unsigned)((n + 31) / 32), (unsigned)((T + 63) / 64)), 512, 0, s>>>(
+          (const uint16_t*)x, ld_x, (int)T, n, (int)k, w4_of(w), (uint16_t*)y, ld_y);
   });
   return hipGetLastError();
 }
 
-static size_t h_elements(const mok_w4_layer& l, int64_t T) {
-  const size_t n = (size_t)T * 2 * ((size_t)l.topk * l.intermediate + l.shared_intermediate);
-  return (n + 7) / 8 * 8;
+// Row tiles of the routed experts, at most, and of the shared one.
+static int64_t max_tiles(const mok_w4_layer& l, int64_t T) {
+  const int64_t pairs = T * l.topk;
+  return std::min<int64_t>(l.num_experts, pairs) + pairs / 16;
+}
+static int64_t shared_tiles(const mok_w4_layer& l, int64_t T) { return l.shared_intermediate > 0 ? (T + 15) / 16 : 0; }
+static int64_t h_elements(const mok_w4_layer& l, int64_t T) {
+  return 32 * (max_tiles(l, T) * l.intermediate + shared_tiles(l, T) * l.shared_intermediate);
 }
 size_t w4_layer_scratch(const mok_w4_layer& l, int64_t T) {
-  return std::max<size_t>(16, h_elements(l, T) * 2 + (size_t)T * (l.topk + 1) * l.hidden * 4);
+  return std::max<size_t>(16, (size_t)h_elements(l, T) * 2 + (size_t)T * (l.topk + 1) * l.hidden * 4);
 }
 
 hipError_t launch_w4_layer(const mok_w4_layer& l, const void* x, const float* router_w, const int64_t* ids, int64_t T,
@@ -776,20 +873,22 @@ hipError_t launch_w4_layer(const mok_w4_layer& l, const void* x, const float* ro
   p.gate = w4_of(l.routed_gate), p.up = w4_of(l.routed_up), p.down = w4_of(l.routed_down);
   p.sgate = w4_of(l.shared_gate), p.sup = w4_of(l.shared_up), p.sdown = w4_of(l.shared_down);
   const bool sh = p.Is > 0;
-  auto whole = [&](const mok_w4& w, int k) { return whole_chunks(w, k, l.group); };
-  p.whole_h = whole(l.routed_gate, p.H) && whole(l.routed_up, p.H) &&
-              (!sh || (whole(l.shared_gate, p.H) && whole(l.shared_up, p.H)));
-  p.whole_i = whole(l.routed_down, p.I), p.whole_s = sh && whole(l.shared_down, p.Is);
+  auto whole = [&](const mok_w4& w, int k) { return whole_chunks(w, k, l.format, l.group); };
+  const bool all_whole = whole(l.routed_gate, p.H) && whole(l.routed_up, p.H) && whole(l.routed_down, p.I) &&
+                         (!sh || (whole(l.shared_gate, p.H) && whole(l.shared_up, p.H) && whole(l.shared_down, p.Is)));
   p.x = (const uint16_t*)x, p.rw = router_w, p.ids = ids, p.h = (uint16_t*)scratch, p.out = (uint16_t*)out;
   p.y = (float*)((uint16_t*)scratch + h_elements(l, T));
-  const int pairs = p.T * p.k, tiles = std::min(p.E, pairs) + pairs / 16, shared = sh ? (p.T + 15) / 16 : 0;
-  const int64_t up = (int64_t)tiles * ((p.I + 15) / 16) + (int64_t)shared * ((p.Is + 15) / 16);
-  const int64_t down = (int64_t)(tiles + shared) * ((p.H + 15) / 16);
+  p.max_tiles = (int)max_tiles(l, T);
+  const int64_t shared = shared_tiles(l, T);
+  const int64_t up = (int64_t)p.max_tiles * ((p.I + 15) / 16) + shared * ((p.Is + 15) / 16);
+  const int64_t down = (p.max_tiles + shared) * ((p.H + 31) / 32);
   const size_t lds = plan_lds(p);
-  with_format(l.format, l.group, l.routed_gate.zero != nullptr, [&](auto fmt, auto g) {
+  with_format(l.format, l.group, l.routed_gate.zero != nullptr, all_whole, [&](auto fmt, auto g, auto wh) {
     constexpr int FMT = decltype(fmt)::value, G = decltype(g)::value;
-    w4_gate_up<FMT, G, 8><<<(unsigned)std::min<int64_t>(up, 2 * cus), 512, lds, s>>>(p);
-    w4_down<FMT, G, 4><<<(unsigned)std::min<int64_t>(down, 4 * cus), 256, lds, s>>>(p);
+    constexpr bool WHOLE = decltype(wh)::value;
+    // as many workgroups as stay on the card together (gate_up: 16 waves per compute unit, output: 12)
+    w4_gate_up<FMT, G, WHOLE, 8><<<(unsigned)std::min<int64_t>(up, 2 * cus), 512, lds, s>>>(p);
+    w4_down<FMT, G, WHOLE, 4><<<(unsigned)std::min<int64_t>(down, 3 * cus), 256, lds, s>>>(p);
   });
   w4_combine<<<dim3((p.H + 255) / 256, p.T), 256, 0, s>>>(p);
   return hipGetLastError();
