@@ -204,11 +204,13 @@ struct TokenChunk {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const u32v4*>(row + min(k0 + 32 * j, K - 32) + 8 * kq);
   }
-  // From h, which lies as it is multiplied (a block after the other).
-  __device__ __forceinline__ void load_blocks(const uint16_t* tile, int k0, int K, int lane) {
+  // From h, which lies as it is multiplied (a block after the other). Rows past the tile's repeat its last one, which
+  // costs no traffic.
+  __device__ __forceinline__ void load_blocks(const uint16_t* tile, int k0, int K, int lane, int rows) {
+    const int at = (lane & 48) + min(lane & 15, rows - 1);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      v[j] = *reinterpret_cast<const u32v4*>(tile + (int64_t)(min(k0 / 32 + j, K / 32 - 1) * 64 + lane) * 8);
+      v[j] = *reinterpret_cast<const u32v4*>(tile + (int64_t)(min(k0 / 32 + j, K / 32 - 1) * 64 + at) * 8);
   }
   __device__ __forceinline__ void arrange(int src) {
 #pragma unroll
@@ -374,6 +376,7 @@ struct Layer {
   const int64_t* ids;
   uint16_t* h;  // [max_tiles][2][16 I], then [shared tiles][2][16 Is]
   int max_tiles;
+  bool by_token;  // at most kFewPairs choices: a row tile has all tokens, and one launch makes the output
   float* y;     // [T k + T][H]
   uint16_t* out;
 };
@@ -382,6 +385,10 @@ __device__ __forceinline__ int choice(const Layer& p, int pair) {
   const int64_t e = p.ids[pair];
   return e >= 0 && e < p.E ? (int)e : -1;
 }
+
+// A batch with at most as many choices needs no lists of an expert's tokens: a
+// row tile holds every token, in its own row (the same matrix instructions).
+constexpr int kFewPairs = 16;
 
 // LDS of the choices sorted by expert, in row tiles of 16.
 size_t plan_lds(const Layer& p) {
@@ -398,6 +405,31 @@ struct Plan {
   template <int NTHR>
   __device__ __forceinline__ void build(const Layer& p, uint8_t* lds, int (&part)[NTHR / 64 + 1]) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, pairs = p.T * p.k;
+    if (pairs <= 64) {
+      // one wave, a lane for every choice: no counting, two barriers less than a microsecond apart
+      int* to = (int*)lds;
+      uint16_t* out = (uint16_t*)(to + p.max_tiles);
+      if (wave == 0) {
+        const int e = lane < pairs ? choice(p, lane) : -1;
+        int n = 0, at = 0;
+        for (uint64_t rest = __ballot(e >= 0); rest != 0;) {
+          const int x = __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)rest) - 1);
+          const uint64_t m = __ballot(e == x);
+          const int rows = p.by_token ? p.T : __popcll(m);
+          if (e == x) out[at + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)lane;
+          for (int q = 0; q < (rows + 15) / 16; ++q, ++n)
+            if (lane == 0) to[n] = x << 18 | (min(16, rows - 16 * q) - 1) << 14 | (at + 16 * q);
+          at += __popcll(m);
+          rest &= ~m;
+        }
+        if (lane == 0) part[0] = n;
+      }
+      __syncthreads();
+      routed = part[0];
+      tiles = routed + (p.Is > 0 ? (p.T + 15) / 16 : 0);
+      tile = to, list = out;
+      return;
+    }
     int* cursor = (int*)lds;  // [E]: count, then where the expert's next choice goes, then its end
     int* to = cursor + p.E;
     uint16_t* any = (uint16_t*)(to + p.max_tiles);
@@ -467,10 +499,14 @@ struct RowTile {
       e = v >> 18, rows = (v >> 14 & 15) + 1, first = v & 0x3FFF;
     }
   }
-  // The r-th of its rows (a row past them: the last one).
+  // The choice of its r-th row (a row past them: of the last one).
   __device__ __forceinline__ int pair(const Plan& l, int r, int pairs) const {
     r = first + min(r, rows - 1);
     return shared ? pairs + r : l.list[r];
+  }
+  __device__ __forceinline__ int token(const Plan& l, int r, const Layer& p) const {
+    r = min(r, rows - 1);
+    return p.by_token ? r : shared ? first + r : l.list[first + r] / p.k;
   }
 };
 
@@ -489,7 +525,7 @@ __global__ void __launch_bounds__(NW * 64) w4_gate_up(Layer p) {
             lrow = lane >> 2, kq = lane & 3, src = source_lane(lane);
   Plan l;
   l.build<NW * 64>(p, dyn, scan);
-  const int pairs = p.T * p.k, K = p.H;
+  const int K = p.H;
   const int slabs_r = (p.I + 15) / 16, slabs_s = (p.Is + 15) / 16;
   const int items_r = l.routed * slabs_r, items = items_r + (l.tiles - l.routed) * slabs_s;
   const int steps = (K + NW * kChunk - 1) / (NW * kChunk);  // of an item, for each wave
@@ -512,8 +548,7 @@ __global__ void __launch_bounds__(NW * 64) w4_gate_up(Layer p) {
     ahead.tile = v / slabs;
     ahead.t.get(l, (sh ? l.routed : 0) + ahead.tile, p.T);
     ahead.n0 = v % slabs * 16;
-    const int pr = ahead.t.pair(l, lrow, pairs);
-    xr = p.x + (int64_t)(sh ? pr - pairs : pr / p.k) * K;
+    xr = p.x + (int64_t)ahead.t.token(l, lrow, p) * K;
     row = (int64_t)ahead.t.e * wide + min(ahead.n0 + lrow, wide - 1);
   };
   auto load = [&](Step& s, int st) {
@@ -615,7 +650,7 @@ __global__ void __launch_bounds__(NW * 64) w4_down(Layer p) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) s.w[q].load(ahead.t.shared ? p.sdown : p.down, row[q], k0, ahead.K, kq);
 #pragma unroll
-    for (int q = 0; q < 2; ++q) s.x[q].load_blocks(hr + q * 16 * ahead.K, k0, ahead.K, lane);
+    for (int q = 0; q < 2; ++q) s.x[q].load_blocks(hr + q * 16 * ahead.K, k0, ahead.K, lane, ahead.t.rows);
   };
   f32x4 y[2][1];
   int st = 0;
@@ -659,6 +694,95 @@ __global__ void __launch_bounds__(NW * 64) w4_down(Layer p) {
   load(a, 0);
   now = ahead;
   while (turn(a, b) && turn(b, a)) {
+  }
+}
+
+// The output of a batch of few choices: 16 columns of H per workgroup, its work
+// every chunk of every expert chosen and of the shared one, taken by the waves in
+// turn. A chunk's results go to the tokens' sums times their router weights of
+// the expert (tokens that did not choose it are left out: it may hold what is not
+// finite), so there is nothing for another launch to join.
+template <int FMT, int G, bool WHOLE, int NW>
+__global__ void __launch_bounds__(NW * 64) w4_down_few(Layer p) {
+  __shared__ f32x4 part[NW][64];
+  __shared__ f32x4 coef[kFewPairs][4];      // of an expert, [16 tokens]
+  __shared__ int expert[kFewPairs], chosen[kFewPairs], count;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), kg = lane >> 4,
+            lrow = lane >> 2, kq = lane & 3, src = source_lane(lane);
+  const int pairs = p.T * p.k;
+  if (wave == 0) {  // the experts in the order of Plan's row tiles
+    const int e = lane < pairs ? choice(p, lane) : -1;
+    const float w = lane < pairs ? p.rw[lane] : 0.f;
+    const int t = lane / p.k;
+    float sum = 0.f;  // of the token's weights of this expert (it may have been chosen twice)
+    for (int j = t * p.k; j < (t + 1) * p.k; ++j) {
+      const float v = __shfl(w, j & 63);
+      if (__shfl(e, j & 63) == e) sum += v;
+    }
+    if (lane < kFewPairs) chosen[lane] = 0;
+    int n = 0;
+    for (uint64_t rest = __ballot(e >= 0); rest != 0; ++n) {
+      const int x = __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)rest) - 1);
+      if (e == x) {
+        ((float*)coef[n])[t] = sum;
+        atomicOr(&chosen[n], 1 << t);
+        expert[n] = x;
+      }
+      rest &= ~__ballot(e == x);
+    }
+    if (lane == 0) count = n;
+  }
+  __syncthreads();
+  const int C = (p.I + kChunk - 1) / kChunk, routed = count * C, units = routed + (p.Is + kChunk - 1) / kChunk;
+  const int64_t col = min((int)blockIdx.x * 16 + lrow, p.H - 1);
+  struct Step {
+    Chunk<FMT, G, WHOLE> w;
+    TokenChunk x[2];
+  };
+  auto load = [&](Step& s, int u) {
+    u = min(u, units - 1);  // (behind the last one: it again, for nothing)
+    const bool sh = u >= routed;
+    const int i = sh ? 0 : u / C, K = sh ? p.Is : p.I, k0 = (sh ? u - routed : u - i * C) * kChunk;
+    const int e = sh ? 0 : __builtin_amdgcn_readfirstlane(expert[i]);
+    const uint16_t* h = p.h + (sh ? (int64_t)p.max_tiles * 32 * p.I : (int64_t)i * 32 * p.I);
+    s.w.load(sh ? p.sdown : p.down, (int64_t)e * p.H + col, k0, K, kq);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) s.x[q].load_blocks(h + q * 16 * K, k0, K, lane, p.T);
+  };
+  f32x4 sum{0.f, 0.f, 0.f, 0.f};
+  int u = wave;
+  auto turn = [&](Step& cur, Step& next) {
+    load(next, u + NW);
+    const bool sh = u >= routed;
+    const int i = sh ? 0 : u / C, K = sh ? p.Is : p.I, k0 = (sh ? u - routed : u - i * C) * kChunk;
+    Tokens<FMT, G> xs[1][2];
+    xs[0][0].template set<true>(cur.x[0]);
+    xs[0][1].template set<true>(cur.x[1]);
+    cur.w.arrange(src, k0, K);
+    f32x4 v[1]{f32x4{0.f, 0.f, 0.f, 0.f}};
+    multiply<FMT, G, WHOLE, 1, 2>(cur.w, xs, v);
+    const f32x4 c = coef[i][kg];
+    const int who = sh ? 0xFFFF : chosen[i];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (who >> (4 * kg + r) & 1) sum[r] += (sh ? 1.f : c[r]) * v[0][r];
+    u += NW;
+    return u < units;
+  };
+  Step a, b;
+  if (u < units) {
+    load(a, u);
+    while (turn(a, b) && turn(b, a)) {
+    }
+  }
+  part[wave][lane] = sum;
+  __syncthreads();
+  if (tid < 256) {
+    const int t = tid >> 4, at = (t >> 2) * 16 + (tid & 15), c = blockIdx.x * 16 + (tid & 15);
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < NW; ++q) v += part[q][at][t & 3];
+    if (t < p.T && c < p.H) p.out[(int64_t)t * p.H + c] = f32_to_bf16(v);
   }
 }
 
@@ -879,6 +1003,7 @@ hipError_t launch_w4_layer(const mok_w4_layer& l, const void* x, const float* ro
   p.x = (const uint16_t*)x, p.rw = router_w, p.ids = ids, p.h = (uint16_t*)scratch, p.out = (uint16_t*)out;
   p.y = (float*)((uint16_t*)scratch + h_elements(l, T));
   p.max_tiles = (int)max_tiles(l, T);
+  p.by_token = p.T * p.k <= kFewPairs;
   const int64_t shared = shared_tiles(l, T);
   const int64_t up = (int64_t)p.max_tiles * ((p.I + 15) / 16) + shared * ((p.Is + 15) / 16);
   const int64_t down = (p.max_tiles + shared) * ((p.H + 31) / 32);
@@ -888,9 +1013,12 @@ hipError_t launch_w4_layer(const mok_w4_layer& l, const void* x, const float* ro
     constexpr bool WHOLE = decltype(wh)::value;
     // as many workgroups as stay on the card together (gate_up: 16 waves per compute unit, output: 12)
     w4_gate_up<FMT, G, WHOLE, 8><<<(unsigned)std::min<int64_t>(up, 2 * cus), 512, lds, s>>>(p);
-    w4_down<FMT, G, WHOLE, 4><<<(unsigned)std::min<int64_t>(down, 3 * cus), 256, lds, s>>>(p);
+    if (p.by_token)
+      w4_down_few<FMT, G, WHOLE, 16><<<(p.H + 15) / 16, 1024, 0, s>>>(p);
+    else
+      w4_down<FMT, G, WHOLE, 4><<<(unsigned)std::min<int64_t>(down, 3 * cus), 256, lds, s>>>(p);
   });
-  w4_combine<<<dim3((p.H + 255) / 256, p.T), 256, 0, s>>>(p);
+  if (!p.by_token) w4_combine<<<dim3((p.H + 255) / 256, p.T), 256, 0, s>>>(p);
   return hipGetLastError();
 }
 
