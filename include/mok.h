@@ -551,11 +551,20 @@ mok_status mok_adamw_step(const mok_adamw* step, void* stream);
  * Every width, stride and alignment is accepted; n and k, ld_x and ld_y that
  * are multiples of 8, with 16-byte aligned tensors, run the fast kernels.
  * 1 <= experts <= 1024, n and k at most 2^20, ld at most 2^21, rows at
- * most 2^30.
+ * most 2^30. scratch (nullable): 4-byte aligned device memory of
+ * mok_grouped_matmul_scratch_bytes, the call's own until its work has run; with
+ * it, a long sum for few outputs is cut into parts that run side by side (the
+ * bits may differ from those without). Nothing is written where that is 0.
  */
+typedef enum mok_grouped_op { MOK_GROUPED_Y = 0, MOK_GROUPED_DX = 1, MOK_GROUPED_DW = 2 } mok_grouped_op;
+
+/* Scratch that mok_grouped_matmul, _dx or _dw can use; 0: none (also where the
+ * sizes are invalid). */
+size_t mok_grouped_matmul_scratch_bytes(mok_grouped_op op, int64_t rows, int32_t experts, int64_t n, int64_t k);
+
 mok_status mok_grouped_matmul(const void* x, int64_t ld_x, const void* weight, const void* offsets, int offsets_int64,
                               int64_t rows, int32_t experts, int64_t n, int64_t k, void* y, int64_t ld_y,
-                              int zero_rest, void* stream);
+                              int zero_rest, void* scratch, size_t scratch_bytes, void* stream);
 
 /*
  * Its gradients. dx[r] = W_e^T dy[r], bf16 [rows, k], rows of no expert as
@@ -564,10 +573,11 @@ mok_status mok_grouped_matmul(const void* x, int64_t ld_x, const void* weight, c
  */
 mok_status mok_grouped_matmul_dx(const void* dy, int64_t ld_dy, const void* weight, const void* offsets,
                                  int offsets_int64, int64_t rows, int32_t experts, int64_t n, int64_t k, void* dx,
-                                 int64_t ld_dx, int zero_rest, void* stream);
+                                 int64_t ld_dx, int zero_rest, void* scratch, size_t scratch_bytes, void* stream);
 mok_status mok_grouped_matmul_dw(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, const void* offsets,
                                  int offsets_int64, int64_t rows, int32_t experts, int64_t n, int64_t k,
-                                 void* d_weight, int d_weight_fp32, void* stream);
+                                 void* d_weight, int d_weight_fp32, void* scratch, size_t scratch_bytes,
+                                 void* stream);
 
 /* Formats of 4-bit weights: a code for every element, two to a byte along a
  * row (the even column in the low half), and a scale for every group of

@@ -22,6 +22,10 @@ MOK_MODE_MXFP8 = 1
 MOK_ROUTER_SOFTMAX = 0
 MOK_ROUTER_SIGMOID = 1
 
+MOK_GROUPED_Y = 0
+MOK_GROUPED_DX = 1
+MOK_GROUPED_DW = 2
+
 MOK_W4_INT4 = 0
 MOK_W4_MXFP4 = 1
 
@@ -33,7 +37,7 @@ EXPORTS = (
     "mok_workspace_set_timing", "mok_workspace_set_timing_mask", "mok_workspace_read_timing",
     "mok_workspace_read_status", "mok_forward_mxfp8", "mok_rms_norm", "mok_rms_norm_scratch_bytes",
     "mok_rms_norm_backward", "mok_router_scratch_bytes", "mok_router_topk", "mok_router_topk_backward",
-    "mok_adamw_step", "mok_grouped_matmul", "mok_grouped_matmul_dx", "mok_grouped_matmul_dw", "mok_w4_quantize",
+    "mok_adamw_step", "mok_grouped_matmul_scratch_bytes", "mok_grouped_matmul", "mok_grouped_matmul_dx", "mok_grouped_matmul_dw", "mok_w4_quantize",
     "mok_w4_dequantize", "mok_w4_matmul", "mok_forward_w4_scratch_bytes", "mok_forward_w4",
 )
 
@@ -149,9 +153,10 @@ def load() -> C.CDLL:
         "mok_router_topk_backward": (i32, [vp, vp, i32, i64, i64, C.c_int32, C.c_int32, vp, vp, C.c_int32, i32, f32,
                                            vp, vp, vp, vp, vp]),
         "mok_adamw_step": (i32, [C.POINTER(MokAdamW), vp]),
-        "mok_grouped_matmul": (i32, [vp, i64, vp, vp, i32, i64, C.c_int32, i64, i64, vp, i64, i32, vp]),
-        "mok_grouped_matmul_dx": (i32, [vp, i64, vp, vp, i32, i64, C.c_int32, i64, i64, vp, i64, i32, vp]),
-        "mok_grouped_matmul_dw": (i32, [vp, i64, vp, i64, vp, i32, i64, C.c_int32, i64, i64, vp, i32, vp]),
+        "mok_grouped_matmul_scratch_bytes": (sz, [i32, i64, C.c_int32, i64, i64]),
+        "mok_grouped_matmul": (i32, [vp, i64, vp, vp, i32, i64, C.c_int32, i64, i64, vp, i64, i32, vp, sz, vp]),
+        "mok_grouped_matmul_dx": (i32, [vp, i64, vp, vp, i32, i64, C.c_int32, i64, i64, vp, i64, i32, vp, sz, vp]),
+        "mok_grouped_matmul_dw": (i32, [vp, i64, vp, i64, vp, i32, i64, C.c_int32, i64, i64, vp, i32, vp, sz, vp]),
         "mok_w4_quantize": (i32, [vp, i32, i64, i64, i64, C.c_int32, C.c_int32, vp, vp, vp, vp]),
         "mok_w4_dequantize": (i32, [C.POINTER(MokW4), i64, i64, C.c_int32, C.c_int32, vp, vp]),
         "mok_w4_matmul": (i32, [vp, i64, i64, i64, i64, C.c_int32, C.c_int32, C.POINTER(MokW4), vp, i64, vp]),

@@ -884,8 +884,8 @@ bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(byte
 
 // Checks and launches one of the grouped products; cols_*: the shortest row
 // of a, of b (0: b is the weight) and of the output (0: it is the weight's).
-mok_status run_grouped(GroupedOp op, const GroupedArgs& g, int64_t cols_a, int64_t cols_b, int64_t cols_out,
-                       void* stream) {
+mok_status run_grouped(GroupedOp op, GroupedArgs g, int64_t cols_a, int64_t cols_b, int64_t cols_out, void* scratch,
+                       size_t scratch_bytes, void* stream) {
   if (g.rows < 0 || g.E < 1 || g.n < 1 || g.k < 1 || !flag(g.offsets64) || !flag(g.zero_rest) || !flag(g.out_fp32))
     return MOK_ERR_INVALID_ARGUMENT;
   constexpr int64_t kMaxCols = 1 << 20, kMaxLd = 1 << 21;
@@ -897,8 +897,11 @@ mok_status run_grouped(GroupedOp op, const GroupedArgs& g, int64_t cols_a, int64
     if (g.ld_a > kMaxLd || g.ld_b > kMaxLd || g.ld_out > kMaxLd) return MOK_ERR_UNSUPPORTED;
   }
   if (!element_aligned(g.a, 0) || !element_aligned(g.b, 0) || !element_aligned(g.out, g.out_fp32) ||
-      !aligned(g.offsets, g.offsets64 ? 8 : 4))
+      !aligned(g.offsets, g.offsets64 ? 8 : 4) || !aligned(scratch, 4))
     return MOK_ERR_INVALID_ARGUMENT;
+  const size_t need = scratch ? grouped_scratch(op, g.rows, g.E, g.n, g.k) : 0;
+  if (need > scratch_bytes) return MOK_ERR_BUFFER_TOO_SMALL;
+  g.part = need ? (float*)scratch : nullptr;
   const int cus = current_cus();
   if (cus <= 0) return MOK_ERR_HIP;
   return to_status(launch_grouped(op, g, cus, (hipStream_t)stream));
@@ -918,31 +921,43 @@ mok_status check_w4(const mok_w4& w, int32_t format, int align) {
 }
 }  // namespace
 
+extern "C" size_t mok_grouped_matmul_scratch_bytes(mok_grouped_op op, int64_t rows, int32_t experts, int64_t n,
+                                                   int64_t k) {
+  if (rows < 0 || experts < 1 || n < 1 || k < 1 || rows > (1 << 30) || experts > kGroupedMaxExperts ||
+      n > (1 << 20) || k > (1 << 20))
+    return 0;
+  if (op != MOK_GROUPED_Y && op != MOK_GROUPED_DX && op != MOK_GROUPED_DW) return 0;
+  return grouped_scratch((GroupedOp)op, rows, experts, n, k);
+}
+
 extern "C" mok_status mok_grouped_matmul(const void* x, int64_t ld_x, const void* weight, const void* offsets,
                                          int offsets_int64, int64_t rows, int32_t experts, int64_t n, int64_t k,
-                                         void* y, int64_t ld_y, int zero_rest, void* stream) {
+                                         void* y, int64_t ld_y, int zero_rest, void* scratch, size_t scratch_bytes,
+                                         void* stream) {
   GroupedArgs g{};
   g.a = x, g.ld_a = ld_x, g.b = weight, g.offsets = offsets, g.offsets64 = offsets_int64;
   g.rows = rows, g.E = experts, g.n = n, g.k = k, g.out = y, g.ld_out = ld_y, g.zero_rest = zero_rest;
-  return run_grouped(GROUPED_Y, g, k, 0, n, stream);
+  return run_grouped(GROUPED_Y, g, k, 0, n, scratch, scratch_bytes, stream);
 }
 
 extern "C" mok_status mok_grouped_matmul_dx(const void* dy, int64_t ld_dy, const void* weight, const void* offsets,
                                             int offsets_int64, int64_t rows, int32_t experts, int64_t n, int64_t k,
-                                            void* dx, int64_t ld_dx, int zero_rest, void* stream) {
+                                            void* dx, int64_t ld_dx, int zero_rest, void* scratch, size_t scratch_bytes,
+                                            void* stream) {
   GroupedArgs g{};
   g.a = dy, g.ld_a = ld_dy, g.b = weight, g.offsets = offsets, g.offsets64 = offsets_int64;
   g.rows = rows, g.E = experts, g.n = n, g.k = k, g.out = dx, g.ld_out = ld_dx, g.zero_rest = zero_rest;
-  return run_grouped(GROUPED_DX, g, n, 0, k, stream);
+  return run_grouped(GROUPED_DX, g, n, 0, k, scratch, scratch_bytes, stream);
 }
 
 extern "C" mok_status mok_grouped_matmul_dw(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
                                             const void* offsets, int offsets_int64, int64_t rows, int32_t experts,
-                                            int64_t n, int64_t k, void* d_weight, int d_weight_fp32, void* stream) {
+                                            int64_t n, int64_t k, void* d_weight, int d_weight_fp32, void* scratch, size_t scratch_bytes,
+                                            void* stream) {
   GroupedArgs g{};
   g.a = dy, g.ld_a = ld_dy, g.b = x, g.ld_b = ld_x, g.offsets = offsets, g.offsets64 = offsets_int64;
   g.rows = rows, g.E = experts, g.n = n, g.k = k, g.out = d_weight, g.out_fp32 = d_weight_fp32;
-  return run_grouped(GROUPED_DW, g, n, k, 0, stream);
+  return run_grouped(GROUPED_DW, g, n, k, 0, scratch, scratch_bytes, stream);
 }
 
 extern "C" mok_status mok_w4_quantize(const void* src, int src_is_fp32, int64_t rows, int64_t cols, int64_t ld_src,

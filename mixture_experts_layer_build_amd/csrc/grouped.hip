@@ -16,6 +16,11 @@
 namespace mok {
 namespace {
 
+// Elements of the output, dense.
+__host__ __device__ __forceinline__ int64_t out_elements(int op, const GroupedArgs& g) {
+  return op == GROUPED_Y ? g.rows * g.n : op == GROUPED_DX ? g.rows * g.k : g.E * g.n * g.k;
+}
+
 // Bounds of expert e's rows, whatever the offsets hold.
 __device__ __forceinline__ void segment(const GroupedArgs& g, int e, int& lo, int& hi) {
   int64_t a, b;
@@ -140,25 +145,28 @@ struct __attribute__((packed, aligned(2))) Unaligned16 {
   u32x4 v;
 };
 
-// Elements p[0..n) of eight, zeros behind them; `before`: elements of the same
-// row in front of p.
-__device__ __forceinline__ u32x4 load_some(const uint8_t* p, int n, int before) {
+// Elements p[0..n) of eight at an element's alignment, in two steps, so that
+// nothing waits for the load where it is made: load_some reads the eight that
+// end with the last one, settle shifts them down, with zeros behind them.
+// `whole`, the same for every lane: the rows have eight elements at least.
+__device__ __forceinline__ u32x4 load_some(const uint8_t* p, int n, bool whole) {
   u32x4 v{0, 0, 0, 0};
-  if (n >= 8) {
-    v = ((const Unaligned16*)p)->v;
-  } else if (n > 0 && before >= 8) {
-    // the eight that end with the last one, shifted down
-    typedef __attribute__((ext_vector_type(2))) uint64_t u64x2;
-    const u64x2 w = __builtin_bit_cast(u64x2, ((const Unaligned16*)(p - 2 * (8 - n)))->v);
-    const int s = 16 * (8 - n);
-    const uint64_t low = s >= 64 ? w[1] >> (s - 64) : (w[0] >> s) | (w[1] << (64 - s));
-    v = __builtin_bit_cast(u32x4, u64x2{low, s >= 64 ? 0 : w[1] >> s});
-  } else if (n > 0) {
+  if (whole) {
+    if (n > 0) v = ((const Unaligned16*)(p - 2 * (8 - min(n, 8))))->v;
+  } else {
 #pragma unroll
     for (int j = 0; j < 7; ++j)
       if (j < n) v[j / 2] |= (uint32_t)((const uint16_t*)p)[j] << (16 * (j % 2));
   }
   return v;
+}
+__device__ __forceinline__ u32x4 settle(u32x4 v, int n) {
+  typedef __attribute__((ext_vector_type(2))) uint64_t u64x2;
+  const u64x2 w = __builtin_bit_cast(u64x2, v);
+  const int s = 16 * (8 - min(max(n, 1), 8));  // 0 to 112
+  const uint64_t over = s == 0 ? 0 : w[1] << ((64 - s) & 63);
+  const uint64_t low = s >= 64 ? w[1] >> (s - 64) : (w[0] >> (s & 63)) | over;
+  return __builtin_bit_cast(u32x4, u64x2{low, s >= 64 ? 0 : w[1] >> (s & 63)});
 }
 
 // An operand of the current tile.
@@ -171,18 +179,21 @@ struct Operand {
   uint32_t off[2];      // this lane's two loads of a stage, kOff if outside
   int chunk[2];         // rows: the contraction chunk of each; columns: its contraction row
   int width[2];         // columns: elements from its first one to the row's end (not for DMA)
-  int before[2];        // columns: elements of the row in front of its first one
+  int length;           // columns: elements of a whole row
+  bool ragged;          // columns: the row ends inside the tile
 
-  // `have`: rows (columns: elements) from the tile's first one on that exist; `front`: columns in front of it.
+  // `have`: rows (columns: elements) from the tile's first one on that exist; `front`: elements of a row in front of
+  // it (columns).
   __device__ __forceinline__ void init(const void* p, int64_t ld_elements, int have, int front, int wave, int lane) {
     base = (const uint8_t*)p;
     ld = ld_elements * 2;
+    length = front + have, ragged = have < S;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (COLUMNS) {
         const int row = (2 * wave + i) * kLoadRows + lane / kRowChunks, c = lane % kRowChunks ^ (4 * (row & 3));
         chunk[i] = row;
-        width[i] = have - c * 8, before[i] = front + c * 8;
+        width[i] = have - c * 8;
         off[i] = c * 8 < have ? (uint32_t)(row * ld) + 16u * c : kOff;
       } else {
         const int row = (2 * wave + i) * 16 + (lane >> 2), c = (lane & 3) ^ ((row >> 2) & 3);
@@ -199,13 +210,17 @@ struct Operand {
     else
       lds_dma16(rsrc(base + (int64_t)k0 * 2, 0x7FFFFFFFu), k0 + 8 * chunk[i] < K ? off[i] : kOff, 0, to);
   }
-  // The same through registers: at the element's alignment, then to LDS.
-  __device__ __forceinline__ u32x4 fetch(int k0, int K, int i) const {
-    if (COLUMNS)
-      return load_some(base + (int64_t)k0 * ld + off[i], k0 + chunk[i] < K ? width[i] : 0, before[i]);
-    return load_some(base + (int64_t)k0 * 2 + off[i], off[i] != kOff ? K - k0 - 8 * chunk[i] : 0, k0 + 8 * chunk[i]);
+  // The same through registers: from memory, and to LDS.
+  __device__ __forceinline__ int count(int k0, int K, int i) const {
+    if (COLUMNS) return k0 + chunk[i] < K ? width[i] : 0;
+    return off[i] != kOff ? K - k0 - 8 * chunk[i] : 0;
   }
-  static __device__ __forceinline__ void put(u32x4 v, uint8_t* to, int wave, int lane, int i) {
+  __device__ __forceinline__ u32x4 fetch(int k0, int K, int i) const {
+    return load_some(base + (COLUMNS ? (int64_t)k0 * ld : (int64_t)k0 * 2) + off[i], count(k0, K, i),
+                     (COLUMNS ? length : K) >= 8);
+  }
+  __device__ __forceinline__ void put(u32x4 v, int k0, int K, uint8_t* to, int wave, int lane, int i) const {
+    if (COLUMNS ? ragged && length >= 8 : K - k0 < kStep && K >= 8) v = settle(v, count(k0, K, i));
     *reinterpret_cast<u32x4*>(to + (2 * wave + i) * 1024 + lane * 16) = v;
   }
   // The fragment of 32 rows from `row0`, contraction elements 16 ks + 8 lh + 0..7 of row row0 + lr.
@@ -281,8 +296,9 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[BLOCKS][2], uint8
     }
 }
 
-// A tile of the output: its operands, and where a wave's results go.
-template <int OP, int S>
+// A tile of the output, or (PARTS) of a part of its contraction: its operands,
+// and where a wave's results go.
+template <int OP, bool PARTS, int S>
 struct Tile {
   using OpA = Operand<OP == GROUPED_DW, S>;
   using OpB = Operand<OP != GROUPED_Y, S>;
@@ -292,8 +308,15 @@ struct Tile {
   int K, rows, cols;  // contraction length; rows and columns of the output from the tile's corner on
   int64_t out;        // element of its corner
   int turn;           // the stage that its contraction begins with
+  int split, first_stage, end_stage;  // PARTS: which of them it is
 
-  __device__ __forceinline__ void init(const GroupedArgs& g, const int32_t* tiles, int64_t id, int wave, int lane) {
+  // Item `id` of `all` tiles times the parts of the contraction.
+  __device__ __forceinline__ void init(const GroupedArgs& g, const int32_t* tiles, int64_t id, int64_t all, int wave,
+                                       int lane) {
+    if (PARTS) {
+      split = (int)(id / all);
+      id -= split * all;
+    }
     const int N = (int)(OP == GROUPED_Y ? g.n : g.k), nt = (N + S - 1) / S;
     int e, local, nm;
     if (OP == GROUPED_DW) {
@@ -317,6 +340,11 @@ struct Tile {
     // memory channels: tiles start at different columns, spread over the range
     // between the XCDs and the experts, and by a few stages between tiles that
     // share operands (which stay near each other for the cache's sake).
+    if (PARTS) {
+      const int every = (K + kStep - 1) / kStep;
+      first_stage = (int)((int64_t)every * split / g.splits);
+      end_stage = (int)((int64_t)every * (split + 1) / g.splits);
+    }
     const int n = steps();
     turn = 0;
     if (OP != GROUPED_DW && n > 0) {
@@ -332,14 +360,14 @@ struct Tile {
     } else {
       A.init(a + (lo + m0) * g.ld_a, g.ld_a, rows, 0, wave, lane);
       B.init(b + (int64_t)e * g.n * g.k + (OP == GROUPED_Y ? n0 * g.k : n0), g.k, cols, n0, wave, lane);
-      out = (lo + m0) * g.ld_out + n0;
+      out = (lo + m0) * (PARTS ? N : g.ld_out) + n0;
     }
   }
-  __device__ __forceinline__ int steps() const { return (K + kStep - 1) / kStep; }
+  __device__ __forceinline__ int steps() const { return PARTS ? end_stage - first_stage : (K + kStep - 1) / kStep; }
   // First contraction element of the kt-th stage.
   __device__ __forceinline__ int at(int kt) const {
     const int n = steps(), k = kt + turn;
-    return (k < n ? k : k - n) * kStep;
+    return ((PARTS ? first_stage : 0) + (k < n ? k : k - n)) * kStep;
   }
   // Loads stage kt.
   __device__ __forceinline__ void issue(int kt, uint32_t ring, int wave) const {
@@ -352,11 +380,12 @@ struct Tile {
 #pragma unroll
     for (int i = 0; i < 2; ++i) v[i] = A.fetch(at(kt), K, i), v[2 + i] = B.fetch(at(kt), K, i);
   }
-  static __device__ __forceinline__ void put(const u32x4 (&v)[4], uint8_t* stage, int wave, int lane) {
+  __device__ __forceinline__ void put(int kt, const u32x4 (&v)[4], uint8_t* ring, int wave, int lane) const {
+    uint8_t* to = ring + kt % kRing * kStageBytes;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      OpA::put(v[i], stage, wave, lane, i);
-      OpB::put(v[2 + i], stage + kOperandBytes, wave, lane, i);
+      A.put(v[i], at(kt), K, to, wave, lane, i);
+      B.put(v[2 + i], at(kt), K, to + kOperandBytes, wave, lane, i);
     }
   }
   // One of the four loads of a wave for stage kt.
@@ -369,11 +398,15 @@ struct Tile {
   }
 };
 
-template <int OP, bool F32, bool DMA, int S>
+// OUT: where the results go.
+constexpr int kBf16 = 0, kF32 = 1, kParts = 2;  // kParts: fp32 sums of a part of the contraction
+
+template <int OP, int OUT, bool DMA, int S>
 __global__ void __launch_bounds__(Shape<S>::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 grouped_tiles(GroupedArgs g) {
   using H = Shape<S>;
-  using T = Tile<OP, S>;
+  constexpr bool PARTS = OUT == kParts;
+  using T = Tile<OP, PARTS, S>;
   __shared__ TileLds<S> L;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / H::kWavesN, wn = wave % H::kWavesN;
@@ -381,29 +414,30 @@ grouped_tiles(GroupedArgs g) {
   if (OP != GROUPED_DW) scan_tiles<H::kThreads>(g, S, L.tiles, L.part);
   const int64_t all =
       OP == GROUPED_DW ? (int64_t)g.E * ((g.n + S - 1) / S) * nt : (int64_t)L.tiles[g.E] * nt;
+  const int64_t items = PARTS ? all * g.splits : all;
   // Workgroup b runs on XCD b % 8. Runs of neighbouring tiles, which share
   // operands, go to the XCDs in turn: as many as an XCD has workgroups, but in
   // the last round the XCDs share what is left evenly.
   const int nq = gridDim.x % kNumXcd == 0 ? kNumXcd : 1, slots = gridDim.x / nq;
   const int xcd = blockIdx.x % nq, slot = blockIdx.x / nq;
-  const int64_t full = all - all % gridDim.x;
-  const int last = (int)(all - full + nq - 1) / nq;
+  const int64_t full = items - items % gridDim.x;
+  const int last = (int)(items - full + nq - 1) / nq;
   // the tile behind `at`, this workgroup's first one of a round
   auto tile_of = [&](int64_t at) {
-    if (at + gridDim.x <= all) return at + (int64_t)xcd * slots + slot;
-    return slot < last ? at + (int64_t)xcd * last + slot : all;
+    if (at + gridDim.x <= items) return at + (int64_t)xcd * slots + slot;
+    return slot < last ? at + (int64_t)xcd * last + slot : items;
   };
   int64_t round = 0, id = tile_of(0);
   const uint32_t ring = lds_addr(&L.ring[0][0]);
   T t;
   // The first stages of the tile `id`.
   auto begin = [&] {
-    t.init(g, L.tiles, id, wave, lane);
+    t.init(g, L.tiles, id, all, wave, lane);
     if (DMA)
       for (int kt = 0; kt < min(t.steps(), kRing - 1); ++kt) t.issue(kt, ring, wave);
   };
-  if (id < all) begin();
-  while (id < all) {
+  if (id < items) begin();
+  while (id < items) {
     f32x16 acc[H::kBlocks][2];
 #pragma unroll
     for (int i = 0; i < H::kBlocks; ++i)
@@ -457,7 +491,7 @@ grouped_tiles(GroupedArgs g) {
           if (DMA) {
             wait_vmcnt<(AFTER < 0 ? 0 : AFTER)>();
           } else {
-            t.put(v, &L.ring[(kt + 1) % kRing][0], wave, lane);
+            t.put(kt + 1, v, &L.ring[0][0], wave, lane);
             if (MORE) t.fetch(kt + 2, v);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
           }
@@ -476,7 +510,7 @@ grouped_tiles(GroupedArgs g) {
       using std::integral_constant;
       if (!DMA) {
         t.fetch(0, v);
-        t.put(v, &L.ring[0][0], wave, lane);
+        t.put(0, v, &L.ring[0][0], wave, lane);
         if (nk > 1) t.fetch(1, v);
       } else if (nk > kRing - 2) {
         wait_vmcnt<4 * (kRing - 2)>();  // (the stores of the tile before are younger than the first stages' loads)
@@ -513,21 +547,45 @@ grouped_tiles(GroupedArgs g) {
     // ---- results, while the next tile's first stages are loaded ----
     __syncthreads();  // nobody reads the ring any more
     const int64_t out = t.out;
+    const int split = PARTS ? t.split : 0;
     const int rows = t.rows - wm * H::kWaveRows, cols = t.cols - wn * 64;
     round += gridDim.x;
     id = tile_of(round);
-    if (id < all) begin();
+    if (id < items) begin();
     // the last stage is not in use before every wave has passed the next tile's first barrier
     static_assert(H::kWaves * 4096 == H::kStageBytes, "4 KiB for each wave");
     uint8_t* part = &L.ring[kRing - 1][0] + wave * 4096;
-    const int64_t ld = OP == GROUPED_DW ? g.k : g.ld_out;
+    const int64_t ld = OP == GROUPED_DW ? g.k : OUT == kParts ? N : g.ld_out;
     const int64_t at = out + (int64_t)(wm * H::kWaveRows) * ld + wn * 64;
-    if constexpr (F32)
+    if constexpr (OUT == kBf16)
+      store_tile<uint16_t, DMA, H::kBlocks>(acc, part, (uint16_t*)g.out + at, ld, rows, cols, lane);
+    else if constexpr (OUT == kF32)
       store_tile<float, DMA, H::kBlocks>(acc, part, (float*)g.out + at, ld, rows, cols, lane);
     else
-      store_tile<uint16_t, DMA, H::kBlocks>(acc, part, (uint16_t*)g.out + at, ld, rows, cols, lane);
+      store_tile<float, DMA, H::kBlocks>(acc, part, g.part + split * out_elements(OP, g) + at, ld, rows, cols, lane);
   }
-  if (OP != GROUPED_DW && g.zero_rest) zero_rest(g, N);
+  if (OP != GROUPED_DW && OUT != kParts && g.zero_rest) zero_rest(g, N);
+}
+
+// The sum of the parts, in their order.
+template <int OP>
+__global__ void __launch_bounds__(256) grouped_join(GroupedArgs g) {
+  const int64_t n = out_elements(OP, g);
+  const int N = (int)(OP == GROUPED_Y ? g.n : g.k);
+  int first = 0, end = 0, x;
+  if (OP != GROUPED_DW) segment(g, 0, first, x), segment(g, g.E - 1, x, end);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = OP == GROUPED_DW ? 0 : i / N, to = OP == GROUPED_DW ? i : row * g.ld_out + (i - row * N);
+    const bool mine = OP == GROUPED_DW || (row >= first && row < end);
+    if (!mine && !g.zero_rest) continue;
+    float v = 0.f;
+    if (mine)
+      for (int s = 0; s < g.splits; ++s) v += g.part[s * n + i];
+    if (OP == GROUPED_DW && g.out_fp32)
+      ((float*)g.out)[to] = v;
+    else
+      ((uint16_t*)g.out)[to] = f32_to_bf16(v);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -609,49 +667,94 @@ bool by_eight(const GroupedArgs& g) {
 
 }  // namespace
 
-template <bool DMA, int S>
-static void launch_tiles(GroupedOp op, const GroupedArgs& g, int cus, hipStream_t s) {
-  constexpr int THR = Shape<S>::kThreads;
-  const int grid = cus * (512 / THR);  // two waves per SIMD
-  switch (op) {
-    case GROUPED_Y: grouped_tiles<GROUPED_Y, false, DMA, S><<<grid, THR, 0, s>>>(g); break;
-    case GROUPED_DX: grouped_tiles<GROUPED_DX, false, DMA, S><<<grid, THR, 0, s>>>(g); break;
-    default:
-      if (g.out_fp32)
-        grouped_tiles<GROUPED_DW, true, DMA, S><<<grid, THR, 0, s>>>(g);
-      else
-        grouped_tiles<GROUPED_DW, false, DMA, S><<<grid, THR, 0, s>>>(g);
+template <int OP, int OUT>
+static void launch_tiles(const GroupedArgs& g, bool small, int cus, hipStream_t s) {
+  const bool dma = by_eight(g);
+  auto go = [&](auto d, auto size) {
+    constexpr int S = decltype(size)::value, THR = Shape<S>::kThreads;
+    const int grid = cus * (512 / THR);  // two waves per SIMD
+    grouped_tiles<OP, OUT, decltype(d)::value, S><<<grid, THR, 0, s>>>(g);
+  };
+  using std::integral_constant;
+  if constexpr (OUT != kParts) {  // (parts are for few tiles)
+    if (!small) {
+      dma ? go(std::true_type{}, integral_constant<int, 256>{}) : go(std::false_type{}, integral_constant<int, 256>{});
+      return;
+    }
   }
+  dma ? go(std::true_type{}, integral_constant<int, 128>{}) : go(std::false_type{}, integral_constant<int, 128>{});
 }
+
+static int64_t tiles(int64_t n, int64_t s) { return (n + s - 1) / s; }
 
 // Whether 128 x 128 tiles are faster than 256 x 256. They read each operand
 // twice as often (65536 rows, 32 experts of 2048 x 7168: 2536 us against
 // 1731), but there are four times as many of them, and a batch wastes less of
 // them at the experts' ends. So: few rows per expert, where reading the weights
-// is the work (4096 rows, 128 experts of 768 x 2048: 87 us against 101; 1024 rows, 32 experts of
-// 2048 x 7168: 192 against 185), or fewer tiles than would occupy the card (2048 rows, 8
-// experts of 2048 x 2048: 34 us against 42; 8192 rows: 96 against 92).
+// is the work (4096 rows, 128 experts of 768 x 2048: 87 us against 101; 1024
+// rows, 32 experts of 2048 x 7168: 192 against 185), or fewer tiles than would
+// occupy the card (2048 rows, 8 experts of 2048 x 2048: 34 us against 42; 8192
+// rows: 96 against 92).
 static bool small_tiles(GroupedOp op, const GroupedArgs& g, int cus) {
-  if (g.rows <= 32 * (int64_t)g.E) return true;
-  auto tiles = [](int64_t n, int64_t s) { return (n + s - 1) / s; };
+  if (g.splits > 1 || g.rows <= 32 * (int64_t)g.E) return true;
   if (op == GROUPED_DW) return g.E * tiles(g.n, 256) * tiles(g.k, 256) < cus;
   // half a tile per expert is lost at its end, about
   const int64_t n = op == GROUPED_Y ? g.n : g.k;
   return (std::min<int64_t>(g.E, g.rows) + tiles(g.rows, 64)) * tiles(n, 128) <= cus * 7 / 2;
 }
 
-hipError_t launch_grouped(GroupedOp op, const GroupedArgs& g, int cus, hipStream_t s) {
-  const bool eight = by_eight(g), small = small_tiles(op, g, cus);
+// Parts that the contraction is cut into where the tiles are far fewer than
+// compute units and each would work through a long one alone: as many as bring
+// 256 items, of eight stages at least. (A constant, so that the order of sums
+// does not depend on the device.)
+int grouped_splits(GroupedOp op, int64_t rows, int E, int64_t n, int64_t k) {
+  constexpr int64_t kItems = 256, kStages = 8, kMost = 16;
+  if (rows == 0) return 1;
+  const int64_t of_rows = std::min<int64_t>(E, rows) + rows / 128;
+  const int64_t count = op == GROUPED_DW  ? E * tiles(n, 128) * tiles(k, 128)
+                        : op == GROUPED_Y ? of_rows * tiles(n, 128)
+                                          : of_rows * tiles(k, 128);
+  const int64_t stages = tiles(op == GROUPED_DW ? rows / E : op == GROUPED_Y ? k : n, kStep);
+  // (below 32 stages the second launch costs what the parts gain)
+  if (stages < 32) return 1;
+  return (int)std::max<int64_t>(1, std::min({kItems / count, stages / kStages, kMost}));
+}
+size_t grouped_scratch(GroupedOp op, int64_t rows, int E, int64_t n, int64_t k) {
+  const int parts = grouped_splits(op, rows, E, n, k);
+  GroupedArgs g{};
+  g.rows = rows, g.E = E, g.n = n, g.k = k;
+  return parts > 1 ? (size_t)parts * out_elements(op, g) * 4 : 0;
+}
+
+template <int OP>
+static void launch_op(const GroupedArgs& g, bool small, int cus, hipStream_t s) {
+  if (g.splits > 1) {
+    launch_tiles<OP, kParts>(g, true, cus, s);
+    const int64_t blocks = tiles(out_elements(OP, g), 256);
+    grouped_join<OP><<<(unsigned)std::min<int64_t>(blocks, 8 * cus), 256, 0, s>>>(g);
+  } else if (OP == GROUPED_DW && g.out_fp32) {
+    launch_tiles<OP, OP == GROUPED_DW ? kF32 : kBf16>(g, small, cus, s);
+  } else {
+    launch_tiles<OP, kBf16>(g, small, cus, s);
+  }
+}
+
+hipError_t launch_grouped(GroupedOp op, const GroupedArgs& args, int cus, hipStream_t s) {
+  GroupedArgs g = args;
   // A few rows per expert: every weight is used for 16 rows at most (8 rows,
   // 128 experts of 768 x 2048: 9 us against 28 with tiles; 256 rows 67 against 69,
   // 1024 rows 96 against 79).
-  if (op == GROUPED_Y && eight && g.rows <= 2 * (int64_t)g.E) {
+  if (op == GROUPED_Y && by_eight(g) && g.rows <= 2 * (int64_t)g.E) {
     const dim3 grid((unsigned)((g.n + 15) / 16), (unsigned)std::min<int64_t>(g.E, g.rows));
     grouped_few<<<grid, kFewWaves * 64, 0, s>>>(g);
-  } else if (eight) {
-    small ? launch_tiles<true, 128>(op, g, cus, s) : launch_tiles<true, 256>(op, g, cus, s);
-  } else {
-    small ? launch_tiles<false, 128>(op, g, cus, s) : launch_tiles<false, 256>(op, g, cus, s);
+    return hipGetLastError();
+  }
+  g.splits = g.part ? grouped_splits(op, g.rows, g.E, g.n, g.k) : 1;
+  const bool small = small_tiles(op, g, cus);
+  switch (op) {
+    case GROUPED_Y: launch_op<GROUPED_Y>(g, small, cus, s); break;
+    case GROUPED_DX: launch_op<GROUPED_DX>(g, small, cus, s); break;
+    default: launch_op<GROUPED_DW>(g, small, cus, s);
   }
   return hipGetLastError();
 }

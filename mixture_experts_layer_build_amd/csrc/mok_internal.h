@@ -314,7 +314,10 @@ struct GroupedArgs {
   int64_t ld_out;      // Y, DX
   int zero_rest;       // Y, DX
   int out_fp32;        // DW
+  float* part;         // grouped_scratch bytes, or null
+  int splits;          // set by launch_grouped
 };
+size_t grouped_scratch(GroupedOp op, int64_t rows, int E, int64_t n, int64_t k);
 hipError_t launch_grouped(GroupedOp op, const GroupedArgs& g, int cus, hipStream_t s);
 
 hipError_t launch_w4_quantize(const void* src, int src_fp32, int64_t rows, int64_t cols, int64_t ld, int format,

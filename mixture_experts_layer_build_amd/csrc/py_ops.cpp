@@ -34,6 +34,7 @@ decltype(&mok_router_scratch_bytes) f_router_scratch_bytes;
 decltype(&mok_router_topk) f_router_topk;
 decltype(&mok_router_topk_backward) f_router_topk_backward;
 decltype(&mok_adamw_step) f_adamw_step;
+decltype(&mok_grouped_matmul_scratch_bytes) f_grouped_matmul_scratch_bytes;
 decltype(&mok_grouped_matmul) f_grouped_matmul;
 decltype(&mok_grouped_matmul_dx) f_grouped_matmul_dx;
 decltype(&mok_grouped_matmul_dw) f_grouped_matmul_dw;
@@ -536,7 +537,14 @@ struct Grouped {
     dense("offsets", offsets);
   }
   int wide() const { return offsets.scalar_type() == at::kLong; }
+  // The scratch that a product of `rows` rows can use (undefined: none).
+  Tensor scratch(mok_grouped_op op, int64_t rows) const {
+    const size_t bytes = f_grouped_matmul_scratch_bytes(op, rows, (int32_t)E, n, k);
+    return bytes ? make({(int64_t)bytes}, w, kU8) : Tensor();
+  }
 };
+void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
+size_t bytes_of(const Tensor& t) { return t.defined() ? t.nbytes() : 0; }
 int64_t rows_of(const char* name, const Tensor& t, const Tensor& first, int64_t cols) {
   check(name, t, first, {kBf16});
   if (t.dim() != 2 || t.size(1) != cols) bad(std::string(name) + " must be [rows, " + std::to_string(cols) + "], got " + text(t.sizes()));
@@ -557,8 +565,10 @@ PyObject* grouped_matmul(PyObject* const* a, Py_ssize_t nargs) {
   }
   Tensor y = out ? *out : make({rows, g.n}, x, kBf16);
   const int64_t ldy = row_stride("out", y);
+  const Tensor scratch = g.scratch(MOK_GROUPED_Y, rows);
   const mok_status st = f_grouped_matmul(x.data_ptr(), ldx, g.w.data_ptr(), g.offsets.data_ptr(), g.wide(), rows,
-                                         (int32_t)g.E, g.n, g.k, y.data_ptr(), ldy, !out, stream_of(a[4]));
+                                         (int32_t)g.E, g.n, g.k, y.data_ptr(), ldy, !out, ptr(scratch),
+                                         bytes_of(scratch), stream_of(a[4]));
   if (ran(st)) written(out);
   return result(st, {y});
 }
@@ -576,13 +586,15 @@ PyObject* grouped_matmul_backward(PyObject* const* a, Py_ssize_t nargs) {
   mok_status st = MOK_OK;
   if (a[4] == Py_True) {
     dx = make({rows, g.k}, dy, kBf16);
+    const Tensor scratch = g.scratch(MOK_GROUPED_DX, rows);
     st = f_grouped_matmul_dx(dy.data_ptr(), lddy, g.w.data_ptr(), g.offsets.data_ptr(), g.wide(), rows, (int32_t)g.E,
-                             g.n, g.k, dx.data_ptr(), g.k, 1, stream_of(a[7]));
+                             g.n, g.k, dx.data_ptr(), g.k, 1, ptr(scratch), bytes_of(scratch), stream_of(a[7]));
   }
   if (st == MOK_OK && a[5] == Py_True) {
     dw = make({g.E, g.n, g.k}, dy, wide ? kF32 : kBf16);
+    const Tensor scratch = g.scratch(MOK_GROUPED_DW, rows);
     st = f_grouped_matmul_dw(dy.data_ptr(), lddy, x.data_ptr(), ldx, g.offsets.data_ptr(), g.wide(), rows, (int32_t)g.E,
-                             g.n, g.k, dw.data_ptr(), wide, stream_of(a[7]));
+                             g.n, g.k, dw.data_ptr(), wide, ptr(scratch), bytes_of(scratch), stream_of(a[7]));
   }
   return result(st, {dx, dw});
 }
@@ -744,7 +756,7 @@ PyObject* forward_w4(PyObject* const* a, Py_ssize_t nargs) {
 
 // bind(addresses of the C ABI's functions, in the order below)
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  count("bind", n, 15);
+  count("bind", n, 16);
   f_rms_norm = (decltype(f_rms_norm))stream_of(a[0]);
   f_rms_norm_scratch_bytes = (decltype(f_rms_norm_scratch_bytes))stream_of(a[1]);
   f_rms_norm_backward = (decltype(f_rms_norm_backward))stream_of(a[2]);
@@ -752,14 +764,15 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   f_router_topk = (decltype(f_router_topk))stream_of(a[4]);
   f_router_topk_backward = (decltype(f_router_topk_backward))stream_of(a[5]);
   f_adamw_step = (decltype(f_adamw_step))stream_of(a[6]);
-  f_grouped_matmul = (decltype(f_grouped_matmul))stream_of(a[7]);
-  f_grouped_matmul_dx = (decltype(f_grouped_matmul_dx))stream_of(a[8]);
-  f_grouped_matmul_dw = (decltype(f_grouped_matmul_dw))stream_of(a[9]);
-  f_w4_quantize = (decltype(f_w4_quantize))stream_of(a[10]);
-  f_w4_dequantize = (decltype(f_w4_dequantize))stream_of(a[11]);
-  f_w4_matmul = (decltype(f_w4_matmul))stream_of(a[12]);
-  f_forward_w4_scratch_bytes = (decltype(f_forward_w4_scratch_bytes))stream_of(a[13]);
-  f_forward_w4 = (decltype(f_forward_w4))stream_of(a[14]);
+  f_grouped_matmul_scratch_bytes = (decltype(f_grouped_matmul_scratch_bytes))stream_of(a[7]);
+  f_grouped_matmul = (decltype(f_grouped_matmul))stream_of(a[8]);
+  f_grouped_matmul_dx = (decltype(f_grouped_matmul_dx))stream_of(a[9]);
+  f_grouped_matmul_dw = (decltype(f_grouped_matmul_dw))stream_of(a[10]);
+  f_w4_quantize = (decltype(f_w4_quantize))stream_of(a[11]);
+  f_w4_dequantize = (decltype(f_w4_dequantize))stream_of(a[12]);
+  f_w4_matmul = (decltype(f_w4_matmul))stream_of(a[13]);
+  f_forward_w4_scratch_bytes = (decltype(f_forward_w4_scratch_bytes))stream_of(a[14]);
+  f_forward_w4 = (decltype(f_forward_w4))stream_of(a[15]);
   Py_RETURN_NONE;
 }
 

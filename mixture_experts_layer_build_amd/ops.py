@@ -24,8 +24,8 @@ __all__ = ["rms_norm", "rms_norm_mxfp8", "rms_norm_backward", "router_topk", "ro
 
 _SCORING = {"softmax": _lib.MOK_ROUTER_SOFTMAX, "sigmoid": _lib.MOK_ROUTER_SIGMOID}
 _BOUND = ("mok_rms_norm", "mok_rms_norm_scratch_bytes", "mok_rms_norm_backward", "mok_router_scratch_bytes",
-          "mok_router_topk", "mok_router_topk_backward", "mok_adamw_step", "mok_grouped_matmul",
-          "mok_grouped_matmul_dx", "mok_grouped_matmul_dw", "mok_w4_quantize", "mok_w4_dequantize", "mok_w4_matmul",
+          "mok_router_topk", "mok_router_topk_backward", "mok_adamw_step",
+          "mok_grouped_matmul_scratch_bytes", "mok_grouped_matmul", "mok_grouped_matmul_dx", "mok_grouped_matmul_dw", "mok_w4_quantize", "mok_w4_dequantize", "mok_w4_matmul",
           "mok_forward_w4_scratch_bytes", "mok_forward_w4")
 
 _host = None

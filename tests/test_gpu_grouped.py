@@ -82,6 +82,38 @@ def test_odd_widths(name, n, k):
     check(*case(n + k, SIZES[name], n, k, tail=2))
 
 
+@pytest.mark.parametrize("sizes", [[1000], [600, 0, 450]])
+@pytest.mark.parametrize("n,k", [(6400, 72), (72, 6400), (6401, 75), (75, 6401)])
+def test_large_tiles_of_y_and_dx(sizes, n, k):
+    """Enough tiles for the 256 x 256 ones in y (wide n) or dx (wide k)."""
+    check(*case(n, sizes, n, k, lead=1, tail=2))
+
+
+@pytest.mark.parametrize("n,k", [(4096, 2048), (4099, 2051)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_large_tiles_of_dw(n, k, dtype):
+    check(*case(n, [66, 40, 0], n, k, tail=1), dw_dtype=dtype)
+
+
+@pytest.mark.parametrize("n,k", [(136, 1600), (1600, 136), (133, 1601), (1601, 133), (40, 1024), (1024, 40)])
+@pytest.mark.parametrize("sizes", [[3, 0, 90], [17]])
+def test_long_sums_in_parts(n, k, sizes):
+    """Few tiles and a long contraction: y's over k, dx's over n."""
+    args = case(n + k, sizes, n, k, lead=2, tail=3)
+    check(*args)
+    x, w, off, _ = args
+    out = torch.full((x.shape[0], n), 7.0, dtype=torch.bfloat16, device="cuda")
+    mok.grouped_matmul(x, w, off, out=out)
+    assert bool((out[:2] == 7).all()) and bool((out[-3:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,k", [(64, 136), (33, 75)])
+def test_many_rows_in_parts(n, k, dtype):
+    """dw over many rows, one expert with most of them and one with none."""
+    check(*case(n, [3000, 0, 1, 500], n, k, lead=5, tail=7), dw_dtype=dtype)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("offsets", [torch.int32, torch.int64])
 def test_types(dtype, offsets):

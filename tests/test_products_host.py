@@ -16,11 +16,13 @@ INVALID, UNSUPPORTED, SMALL, OK = (_lib.MOK_ERR_INVALID_ARGUMENT, _lib.MOK_ERR_U
 P = 1 << 20  # an address that is never followed
 
 
-def grouped(which="", a=P, lda=64, b=P, ldb=64, off=P, o64=0, rows=4, E=2, n=64, k=64, out=P, ldo=64, rest=1, f32=0):
+def grouped(which="", a=P, lda=64, b=P, ldb=64, off=P, o64=0, rows=4, E=2, n=64, k=64, out=P, ldo=64, rest=1, f32=0,
+            scratch=None, nbytes=0):
     lib = _lib.load()
     if which == "dw":
-        return lib.mok_grouped_matmul_dw(a, lda, b, ldb, off, o64, rows, E, n, k, out, f32, None)
-    return getattr(lib, "mok_grouped_matmul" + which)(a, lda, b, off, o64, rows, E, n, k, out, ldo, rest, None)
+        return lib.mok_grouped_matmul_dw(a, lda, b, ldb, off, o64, rows, E, n, k, out, f32, scratch, nbytes, None)
+    return getattr(lib, "mok_grouped_matmul" + which)(a, lda, b, off, o64, rows, E, n, k, out, ldo, rest, scratch,
+                                                      nbytes, None)
 
 
 @pytest.mark.parametrize("which", ["", "_dx"])
@@ -43,6 +45,24 @@ def test_grouped_refusals(which, want, kw):
     (INVALID, dict(rows=0, out=None)), (INVALID, dict(rows=0, off=None)), (UNSUPPORTED, dict(ldb=(1 << 21) + 1))])
 def test_grouped_dw_refusals(want, kw):
     assert grouped("dw", **kw) == want
+
+
+def test_grouped_scratch():
+    """Only a long sum for few outputs is cut into parts, which need scratch."""
+    def need(op, rows, E, n, k):
+        return _lib.load().mok_grouped_matmul_scratch_bytes(op, rows, E, n, k)
+    Y, DX, DW = _lib.MOK_GROUPED_Y, _lib.MOK_GROUPED_DX, _lib.MOK_GROUPED_DW
+    assert need(Y, 64, 2, 128, 4096) % (64 * 128 * 4) == 0 and need(Y, 64, 2, 128, 4096) > 64 * 128 * 4
+    assert need(Y, 64, 2, 128, 64) == 0 and need(Y, 65536, 128, 768, 2048) == 0 and need(Y, 0, 2, 128, 4096) == 0
+    assert need(DX, 64, 2, 4096, 128) == need(Y, 64, 2, 128, 4096) and need(DX, 64, 2, 128, 4096) == 0
+    assert need(DW, 40000, 2, 128, 64) > 2 * 128 * 64 * 4 and need(DW, 64, 2, 128, 64) == 0
+    for bad in ((3, 64, 2, 128, 4096), (-1, 64, 2, 128, 4096), (Y, -1, 2, 128, 4096), (Y, 64, 0, 128, 4096),
+                (Y, 64, 2000, 128, 4096), (Y, 64, 2, 0, 4096), (Y, 64, 2, 128, (1 << 20) + 1)):
+        assert need(*bad) == 0, bad
+    few = dict(rows=64, E=2, n=128, k=4096, lda=4096, ldo=128)
+    assert grouped(**few, scratch=P, nbytes=need(Y, 64, 2, 128, 4096) - 1) == SMALL
+    assert grouped(**few, scratch=P + 2, nbytes=1 << 30) == INVALID
+    assert grouped("dw", rows=40000, n=128, k=64, lda=128, scratch=P, nbytes=64) == SMALL
 
 
 def quantize(src=P, f32=0, rows=4, cols=256, ld=256, form=0, group=128, codes=P, scale=P, zero=None):
