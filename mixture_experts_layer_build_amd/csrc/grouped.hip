@@ -145,28 +145,19 @@ struct __attribute__((packed, aligned(2))) Unaligned16 {
   u32x4 v;
 };
 
-// Elements p[0..n) of eight at an element's alignment, in two steps, so that
-// nothing waits for the load where it is made: load_some reads the eight that
-// end with the last one, settle shifts them down, with zeros behind them.
-// `whole`, the same for every lane: the rows have eight elements at least.
-__device__ __forceinline__ u32x4 load_some(const uint8_t* p, int n, bool whole) {
-  u32x4 v{0, 0, 0, 0};
-  if (whole) {
-    if (n > 0) v = ((const Unaligned16*)(p - 2 * (8 - min(n, 8))))->v;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 7; ++j)
-      if (j < n) v[j / 2] |= (uint32_t)((const uint16_t*)p)[j] << (16 * (j % 2));
-  }
-  return v;
-}
+// How the operands come to LDS: by DMA, through registers, or (rows of fewer
+// than eight elements) through registers one by one.
+constexpr int kDma = 0, kRegisters = 1, kSingles = 2;
+
+// Eight elements as load_eight read them, the last of its row first shifted
+// down: the n of the row (0 for n < 0), zeros behind them.
 __device__ __forceinline__ u32x4 settle(u32x4 v, int n) {
   typedef __attribute__((ext_vector_type(2))) uint64_t u64x2;
   const u64x2 w = __builtin_bit_cast(u64x2, v);
   const int s = 16 * (8 - min(max(n, 1), 8));  // 0 to 112
   const uint64_t over = s == 0 ? 0 : w[1] << ((64 - s) & 63);
   const uint64_t low = s >= 64 ? w[1] >> (s - 64) : (w[0] >> (s & 63)) | over;
-  return __builtin_bit_cast(u32x4, u64x2{low, s >= 64 ? 0 : w[1] >> (s & 63)});
+  return __builtin_bit_cast(u32x4, n > 0 ? u64x2{low, s >= 64 ? 0 : w[1] >> (s & 63)} : u64x2{0, 0});
 }
 
 // An operand of the current tile.
@@ -179,15 +170,14 @@ struct Operand {
   uint32_t off[2];      // this lane's two loads of a stage, kOff if outside
   int chunk[2];         // rows: the contraction chunk of each; columns: its contraction row
   int width[2];         // columns: elements from its first one to the row's end (not for DMA)
-  int length;           // columns: elements of a whole row
+  int front;            // columns: elements of a row in front of the tile
   bool ragged;          // columns: the row ends inside the tile
 
-  // `have`: rows (columns: elements) from the tile's first one on that exist; `front`: elements of a row in front of
-  // it (columns).
-  __device__ __forceinline__ void init(const void* p, int64_t ld_elements, int have, int front, int wave, int lane) {
+  // `have`: rows (columns: elements) from the tile's first one on that exist.
+  __device__ __forceinline__ void init(const void* p, int64_t ld_elements, int have, int front_, int wave, int lane) {
     base = (const uint8_t*)p;
     ld = ld_elements * 2;
-    length = front + have, ragged = have < S;
+    front = front_, ragged = COLUMNS && have < S;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (COLUMNS) {
@@ -215,12 +205,27 @@ struct Operand {
     if (COLUMNS) return k0 + chunk[i] < K ? width[i] : 0;
     return off[i] != kOff ? K - k0 - 8 * chunk[i] : 0;
   }
+  // Where a chunk ends behind its row, the eight elements that end with the
+  // row's last one are read; where it has none, the first eight of the first
+  // row. So a load needs no branch, and those behind it can be counted.
+  template <int MODE>
   __device__ __forceinline__ u32x4 fetch(int k0, int K, int i) const {
-    return load_some(base + (COLUMNS ? (int64_t)k0 * ld : (int64_t)k0 * 2) + off[i], count(k0, K, i),
-                     (COLUMNS ? length : K) >= 8);
+    const uint8_t* p = base + (COLUMNS ? (int64_t)k0 * ld : (int64_t)k0 * 2) + off[i];
+    const int n = count(k0, K, i);
+    if constexpr (MODE == kRegisters) {
+      return ((const Unaligned16*)(n > 0 ? p - 2 * (8 - min(n, 8)) : base - 2 * front))->v;
+    } else {
+      u32x4 v{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) v[j / 2] |= (uint32_t)((const uint16_t*)p)[j] << (16 * (j % 2));
+      return v;
+    }
   }
+  // (What lies in rows or columns outside the output is not looked at.)
+  template <int MODE>
   __device__ __forceinline__ void put(u32x4 v, int k0, int K, uint8_t* to, int wave, int lane, int i) const {
-    if (COLUMNS ? ragged && length >= 8 : K - k0 < kStep && K >= 8) v = settle(v, count(k0, K, i));
+    if (MODE == kRegisters && (ragged || K - k0 < kStep)) v = settle(v, count(k0, K, i));
     *reinterpret_cast<u32x4*>(to + (2 * wave + i) * 1024 + lane * 16) = v;
   }
   // The fragment of 32 rows from `row0`, contraction elements 16 ks + 8 lh + 0..7 of row row0 + lr.
@@ -376,16 +381,19 @@ struct Tile {
     B.load(at(kt), K, to + kOperandBytes, wave, 0), B.load(at(kt), K, to + kOperandBytes, wave, 1);
   }
   // The four loads of a wave for stage kt, and their way to LDS (without DMA).
+  template <int MODE>
   __device__ __forceinline__ void fetch(int kt, u32x4 (&v)[4]) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) v[i] = A.fetch(at(kt), K, i), v[2 + i] = B.fetch(at(kt), K, i);
+    for (int i = 0; i < 2; ++i)
+      v[i] = A.template fetch<MODE>(at(kt), K, i), v[2 + i] = B.template fetch<MODE>(at(kt), K, i);
   }
+  template <int MODE>
   __device__ __forceinline__ void put(int kt, const u32x4 (&v)[4], uint8_t* ring, int wave, int lane) const {
     uint8_t* to = ring + kt % kRing * kStageBytes;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      A.put(v[i], at(kt), K, to, wave, lane, i);
-      B.put(v[2 + i], at(kt), K, to + kOperandBytes, wave, lane, i);
+      A.template put<MODE>(v[i], at(kt), K, to, wave, lane, i);
+      B.template put<MODE>(v[2 + i], at(kt), K, to + kOperandBytes, wave, lane, i);
     }
   }
   // One of the four loads of a wave for stage kt.
@@ -401,11 +409,11 @@ struct Tile {
 // OUT: where the results go.
 constexpr int kBf16 = 0, kF32 = 1, kParts = 2;  // kParts: fp32 sums of a part of the contraction
 
-template <int OP, int OUT, bool DMA, int S>
+template <int OP, int OUT, int MODE, int S>
 __global__ void __launch_bounds__(Shape<S>::kThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 grouped_tiles(GroupedArgs g) {
   using H = Shape<S>;
-  constexpr bool PARTS = OUT == kParts;
+  constexpr bool PARTS = OUT == kParts, DMA = MODE == kDma;
   using T = Tile<OP, PARTS, S>;
   __shared__ TileLds<S> L;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -451,7 +459,10 @@ grouped_tiles(GroupedArgs g) {
     auto run = [&](auto ni_c) {
       constexpr int NI = decltype(ni_c)::value;
       bf16x8 fa[2][NI > 0 ? NI : 1], fb[2][2];
-      u32x4 v[4];  // without DMA: a stage on its way
+      // without DMA: stages on their way. (Two for the smaller tile: a load takes longer than a stage's products, 193 x
+      // 75 over 16384 rows 431 us against 476; the larger one has no registers left.)
+      constexpr int SETS = S == 128 && MODE == kRegisters ? 2 : 1;
+      u32x4 v[SETS][4];
       // read(st, ks, r): the r-th of the fragments of half ks, in the order of their use
       auto read = [&](const uint8_t* st, int ks, int r) {
         if (NI > 0 && r < NI + 2) {
@@ -483,7 +494,7 @@ grouped_tiles(GroupedArgs g) {
       };
       // One stage; AFTER: how many of this wave's loads behind stage kt + 1's may be in flight (-1: there is no such
       // stage). Kept free of branches: where paths meet, the compiler waits for the reads of either.
-      auto step = [&](int kt, auto after, auto more) {
+      auto step = [&](int kt, auto after, auto more, auto set) {
         constexpr int AFTER = decltype(after)::value;
         constexpr bool MORE = decltype(more)::value;
         half(0, [&](int m) { read(stage(kt), 1, m); }, [](int) {});
@@ -491,8 +502,10 @@ grouped_tiles(GroupedArgs g) {
           if (DMA) {
             wait_vmcnt<(AFTER < 0 ? 0 : AFTER)>();
           } else {
-            t.put(kt + 1, v, &L.ring[0][0], wave, lane);
-            if (MORE) t.fetch(kt + 2, v);
+            constexpr int SET = decltype(set)::value;
+            t.template put<MODE>(kt + 1, v[SET], &L.ring[0][0], wave, lane);
+            // (no stage behind the last one: that again, so that the loads in flight can be counted)
+            t.template fetch<MODE>(min(kt + 1 + SETS, nk - 1), v[SET]);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
           }
           // stage kt + 1 has landed, and nobody reads stage kt - 1 any more (its last fragments went into products
@@ -509,9 +522,10 @@ grouped_tiles(GroupedArgs g) {
       };
       using std::integral_constant;
       if (!DMA) {
-        t.fetch(0, v);
-        t.put(0, v, &L.ring[0][0], wave, lane);
-        if (nk > 1) t.fetch(1, v);
+        t.template fetch<MODE>(0, v[0]);
+        if (SETS > 1) t.template fetch<MODE>(min(1, nk - 1), v[SETS - 1]);
+        t.template put<MODE>(0, v[0], &L.ring[0][0], wave, lane);
+        t.template fetch<MODE>(min(SETS, nk - 1), v[0]);
       } else if (nk > kRing - 2) {
         wait_vmcnt<4 * (kRing - 2)>();  // (the stores of the tile before are younger than the first stages' loads)
       } else {
@@ -520,18 +534,30 @@ grouped_tiles(GroupedArgs g) {
       __syncthreads();  // stage 0 has landed for every wave
       for (int r = 0; r < NI + 2; ++r) read(stage(0), 0, r);
       int kt = 0;
-      constexpr int AHEAD = DMA ? kRing - 1 : 2;  // stages from a load to its use
-      for (; kt < nk - AHEAD; ++kt) step(kt, integral_constant<int, 4 * (kRing - 3)>{}, std::true_type{});
-      // the last stages: one fewer in flight from step to step
-      auto drain = [&](auto self, auto left) {
-        constexpr int LEFT = decltype(left)::value;
-        if constexpr (LEFT > 1) {
-          if (nk >= LEFT) step(kt++, integral_constant<int, 4 * (LEFT - 2)>{}, std::false_type{});
-          self(self, integral_constant<int, LEFT - 1>{});
+      const integral_constant<int, 0> set0;
+      const integral_constant<int, 4 * (kRing - 3)> full;
+      if constexpr (DMA) {
+        constexpr int AHEAD = kRing - 1;  // stages from a load to its use
+        for (; kt < nk - AHEAD; ++kt) step(kt, full, std::true_type{}, set0);
+        // the last stages: one fewer in flight from step to step
+        auto drain = [&](auto self, auto left) {
+          constexpr int LEFT = decltype(left)::value;
+          if constexpr (LEFT > 1) {
+            if (nk >= LEFT) step(kt++, integral_constant<int, 4 * (LEFT - 2)>{}, std::false_type{}, set0);
+            self(self, integral_constant<int, LEFT - 1>{});
+          }
+        };
+        drain(drain, integral_constant<int, AHEAD>{});
+      } else if constexpr (SETS == 2) {
+        for (; kt < nk - 2; kt += 2) {
+          step(kt, full, std::true_type{}, integral_constant<int, 1>{});
+          step(kt + 1, full, std::true_type{}, set0);
         }
-      };
-      drain(drain, integral_constant<int, AHEAD>{});
-      step(kt, integral_constant<int, -1>{}, std::false_type{});
+        if (kt < nk - 1) step(kt++, full, std::true_type{}, integral_constant<int, 1>{});
+      } else {
+        for (; kt < nk - 1; ++kt) step(kt, full, std::true_type{}, set0);
+      }
+      step(kt, integral_constant<int, -1>{}, std::false_type{}, set0);
     };
     const int live = min(H::kBlocks, max(0, (t.rows - wm * H::kWaveRows + 31) / 32));
     if (nk > 0) {
@@ -667,22 +693,25 @@ bool by_eight(const GroupedArgs& g) {
 
 }  // namespace
 
-template <int OP, int OUT>
+template <int OP, int OUT, int MODE>
 static void launch_tiles(const GroupedArgs& g, bool small, int cus, hipStream_t s) {
-  const bool dma = by_eight(g);
-  auto go = [&](auto d, auto size) {
-    constexpr int S = decltype(size)::value, THR = Shape<S>::kThreads;
-    const int grid = cus * (512 / THR);  // two waves per SIMD
-    grouped_tiles<OP, OUT, decltype(d)::value, S><<<grid, THR, 0, s>>>(g);
-  };
-  using std::integral_constant;
-  if constexpr (OUT != kParts) {  // (parts are for few tiles)
+  // (two waves per SIMD)
+  if constexpr (OUT != kParts && MODE != kSingles) {
     if (!small) {
-      dma ? go(std::true_type{}, integral_constant<int, 256>{}) : go(std::false_type{}, integral_constant<int, 256>{});
+      grouped_tiles<OP, OUT, MODE, 256><<<cus, Shape<256>::kThreads, 0, s>>>(g);
       return;
     }
   }
-  dma ? go(std::true_type{}, integral_constant<int, 128>{}) : go(std::false_type{}, integral_constant<int, 128>{});
+  grouped_tiles<OP, OUT, MODE, 128><<<2 * cus, Shape<128>::kThreads, 0, s>>>(g);
+}
+template <int OP, int OUT>
+static void launch_tiles(const GroupedArgs& g, bool small, int cus, hipStream_t s) {
+  if (by_eight(g))
+    launch_tiles<OP, OUT, kDma>(g, small, cus, s);
+  else if (std::min(g.n, g.k) >= 8)
+    launch_tiles<OP, OUT, kRegisters>(g, small, cus, s);
+  else
+    launch_tiles<OP, OUT, kSingles>(g, small, cus, s);
 }
 
 static int64_t tiles(int64_t n, int64_t s) { return (n + s - 1) / s; }
@@ -696,7 +725,7 @@ static int64_t tiles(int64_t n, int64_t s) { return (n + s - 1) / s; }
 // occupy the card (2048 rows, 8 experts of 2048 x 2048: 34 us against 42; 8192
 // rows: 96 against 92).
 static bool small_tiles(GroupedOp op, const GroupedArgs& g, int cus) {
-  if (g.splits > 1 || g.rows <= 32 * (int64_t)g.E) return true;
+  if (g.splits > 1 || g.rows <= 32 * (int64_t)g.E || std::min(g.n, g.k) < 8) return true;
   if (op == GROUPED_DW) return g.E * tiles(g.n, 256) * tiles(g.k, 256) < cus;
   // half a tile per expert is lost at its end, about
   const int64_t n = op == GROUPED_Y ? g.n : g.k;
