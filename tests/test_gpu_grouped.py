@@ -254,3 +254,48 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for w, g in zip(want, got):
         assert all(torch.equal(p, q) for p, q in zip(w, g))
+
+
+@pytest.mark.parametrize("n,k", [(1, 4096), (4096, 1), (3, 2048), (2048, 5)])
+def test_long_sums_of_rows_below_eight(n, k):
+    check(*case(n + k, [30, 0, 3], n, k, lead=1, tail=2))
+    check(*case(n + k, [2100], min(n, 40), min(k, 40), lead=1, tail=2), dw_dtype=torch.float32)
+
+
+@pytest.mark.parametrize("E", [1, 1024])
+def test_fewest_and_most_experts(E):
+    sizes = [1 + 3 * (e % 7 == 2) - (e % 5 == 3) for e in range(E)]
+    check(*case(E, sizes, 40, 48))
+    check(*case(E + 1, sizes, 9, 17), dw_dtype=torch.float32)
+
+
+def test_more_than_2_31_elements():
+    """Row and weight offsets past 32 bits: the last rows and the last expert as those of small tensors."""
+    E, n, k = 34, 8192, 8192
+    w = torch.empty(E, n, k, dtype=torch.bfloat16, device="cuda")
+    w[:-1].fill_(0.5)
+    w[-1] = normal(1, n, k, std=0.02).cuda()
+    for rows in (34, 300):  # (few rows, and tiles)
+        x, dy = normal(2, rows, k).cuda(), normal(3, rows, n).cuda()
+        off = torch.arange(E + 1, dtype=torch.int64, device="cuda")
+        off[-1] = rows
+        y = mok.grouped_matmul(x, w, off)
+        dx, dw = mok.grouped_matmul_backward(dy, x, w, off)
+        xs, ws, ds = x[E - 1:], w[-1:], dy[E - 1:]
+        Y, W = f64(xs) @ f64(ws[0])[:64].T, f64(ws[0])
+        close(y[E - 1:, :64], Y, np.abs(f64(xs)) @ np.abs(W[:64]).T, k)
+        close(dx[E - 1:, -64:], f64(ds) @ W[:, -64:], np.abs(f64(ds)) @ np.abs(W[:, -64:]), n)
+        DS, XS = f64(ds), f64(xs)[:, -64:]
+        close(dw[-1, :, -64:], DS.T @ XS, np.abs(DS).T @ np.abs(XS), rows + 1)
+    del w, dw
+    rows, k = (1 << 20) + 3, 2056
+    x = torch.zeros(rows, k, dtype=torch.bfloat16, device="cuda")
+    x[-40:] = normal(4, 40, k).cuda()
+    w = normal(5, 2, 16, k, std=0.02).cuda()
+    off = torch.tensor([0, rows - 30, rows], dtype=torch.int32, device="cuda")
+    y = mok.grouped_matmul(x, w, off)
+    for r, e in ((slice(-40, -30), 0), (slice(-30, None), 1)):
+        close(y[r], f64(x[r]) @ f64(w[e]).T, np.abs(f64(x[r])) @ np.abs(f64(w[e])).T, k)
+    assert not y[:-40].any()
+    dx = mok.grouped_matmul_backward(y, x, w, off, need_dw=False)[0]
+    close(dx[-30:], f64(y[-30:]) @ f64(w[1]), np.abs(f64(y[-30:])) @ np.abs(f64(w[1])), 16)

@@ -334,3 +334,68 @@ def test_two_streams_at_once():
                 got[i] = mok.forward_w4(*c[:4])
     torch.cuda.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("how", ["sym128", "zero32", "mxfp4"])
+@pytest.mark.parametrize("T,k", [(4, 4), (17, 1), (16, 1), (16, 4), (13, 5), (1, 16), (1, 17), (1, 64)])
+def test_layer_at_the_limits_of_its_ways(how, T, k):
+    """16 and 64 choices are where the layer changes its way: with choices made twice, by none, and of no expert."""
+    E = max(k, 6)
+    x, rw, ids, ws, vs = layer_case(50 + T + k, T, 256, 128, E, k, 128 if T % 2 else 0, how)
+    if k > 1:
+        ids[0, -1] = ids[0, 0]
+        ids[T // 2, k // 2] = -1
+    else:
+        ids[: T // 2] = 3
+        ids[T - 1] = E
+    check_layer(x, rw, ids, ws, vs, how)
+
+
+@pytest.mark.parametrize("how", FORMATS)
+def test_scales_and_zero_points_at_their_own_alignment(how):
+    """Whole chunks whose scales and zero points cannot be loaded at once."""
+    (c, s, z), v = w4(normal(70, 48, 512, std=0.1), how)
+
+    def shifted(t):
+        if t is None:
+            return None
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        buf[1:] = t.reshape(-1)
+        return buf[1:].view(t.shape)
+    x = normal(71, 5, 512).cuda()
+    got = mok.w4_matmul(x, c, shifted(s), shifted(z))
+    want = f64(x) @ v.T
+    close(got, want, 2.0 ** -8 * np.abs(want) + 8 * 512 ** 0.5 * 2.0 ** -24 * mags_of(f64(x), v, s, how))
+    X, rw, ids, ws, vs = layer_case(72, 9, 256, 128, 8, 2, 128, how)
+    moved = {n: shifted(t) if n.endswith(("scale", "zero")) else t for n, t in ws.items()}
+    check_layer(X, rw, ids, ws, vs, how, got=mok.forward_w4(X, rw, ids, moved))
+
+
+@pytest.mark.parametrize("how", ["sym128", "zero64", "mxfp4"])
+def test_more_than_2_31_bytes_of_codes(how):
+    """The last expert of a large set gives what it gives alone; quantizing past 2^31 elements gives its rows' codes."""
+    E, H, I = 300, 8192, 2048
+    form, group, zero = FORMATS[how]
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    ws = {}
+    for name, n, k in (("gate", I, H), ("up", I, H), ("down", H, I)):
+        ws["routed_" + name] = torch.randint(0, 256, (E, n, k // 2), dtype=torch.uint8, device="cuda", generator=gen)
+        if form == "mxfp4":
+            s = torch.randint(115, 122, (E, n, k // group), dtype=torch.uint8, device="cuda", generator=gen)
+        else:
+            s = torch.rand(E, n, k // group, device="cuda", generator=gen).mul_(0.02).to(torch.bfloat16)
+        ws[f"routed_{name}_scale"] = s
+        if zero:
+            ws[f"routed_{name}_zero"] = torch.randint(0, 16, s.shape, dtype=torch.uint8, device="cuda", generator=gen)
+    last = {n: t[-1:].clone() for n, t in ws.items()}
+    for T in (2, 20):
+        x, rw = normal(80, T, H).cuda(), torch.rand(T, 1, device="cuda", generator=gen)
+        ids = torch.full((T, 1), E - 1, dtype=torch.int64, device="cuda")
+        assert torch.equal(mok.forward_w4(x, rw, ids, ws), mok.forward_w4(x, rw, torch.zeros_like(ids), last))
+    del ws
+    w = torch.zeros((1 << 19) + 2, 4224, dtype=torch.bfloat16, device="cuda")
+    w[-2:] = normal(81, 2, 4224).cuda()
+    q, alone = mok.w4_quantize(w, form, group, zero), mok.w4_quantize(w[-2:], form, group, zero)
+    for a, b in zip(q, alone):
+        assert a is None and b is None or torch.equal(a[-2:], b)
+    assert torch.equal(mok.w4_dequantize(*q)[-2:], mok.w4_dequantize(*alone))
