@@ -550,7 +550,7 @@ mok_status mok_adamw_step(const mok_adamw* step, void* stream);
  * decrease give unspecified rows of y, and no access outside the tensors.
  * Every width, stride and alignment is accepted; where n, k, ld_x and ld_y are
  * multiples of 8 and the tensors 16-byte aligned, loads go straight to LDS and
- * a few rows have a kernel of their own (otherwise up to twice the time).
+ * a few rows have a kernel of their own (other widths take up to 1.4 times as long, few rows more).
  * 1 <= experts <= 1024, n and k at most 2^20, ld at most 2^21, rows at
  * most 2^30. scratch (nullable): 4-byte aligned device memory of
  * mok_grouped_matmul_scratch_bytes, the call's own until its work has run; with

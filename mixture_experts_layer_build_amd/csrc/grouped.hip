@@ -116,9 +116,9 @@ __device__ __forceinline__ void zero_rest(const GroupedArgs& g, int cols) {
 // tensors are loaded straight to LDS, three stages ahead. Others go through
 // registers, one or two stages ahead: 16-byte loads at the elements' own
 // alignment (which the memory takes), where a chunk of 8 ends behind its row
-// the 8 that end with the row's last one. 1001 rows, 5 experts of 1037 x 515:
-// 36 us; 679 rows, 2 experts of 7152 x 5070: 138 us (0.36 of the DMA tiles'
-// rate: a misaligned load occupies the address unit several times as long).
+// the 8 that end with the row's last one. That costs a third: 4099 rows, 37
+// experts of 1001 x 1037 36 us, of 1000 x 1040 27; dx and dW of 12327 rows, 18
+// experts of 2176 x 4690 812 us, of 2176 x 4688 587.
 // ---------------------------------------------------------------------------
 constexpr int kStep = 32, kRing = 4;
 constexpr int kNumXcd = 8;
