@@ -30,7 +30,11 @@ read for one GPU:
 Around the layer: ``rms_norm`` and ``MoKRMSNorm`` (the norm in front of it,
 with the residual's addition) and ``router_topk`` and ``MoKRouter`` (the
 top-k router, with its load statistics and losses), differentiable in every
-float input; the schedule takes their expert ids as they are.
+float input; the schedule takes their expert ids as they are. Beside it:
+``grouped_matmul`` and ``MoKGroupedLinear``, the ragged product of experts for
+other expert functions. (To capture a step in a graph: warm it up on a side
+stream, and let no eager backward graph of the same leaves live meanwhile, as
+torch asks of every captured backward.)
 
 Every step of the layer runs in the library's HIP kernels; tensors on the
 CPU are rejected.
