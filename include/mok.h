@@ -552,7 +552,7 @@ mok_status mok_adamw_step(const mok_adamw* step, void* stream);
  * multiples of 8 and the tensors 16-byte aligned, loads go straight to LDS and
  * a few rows have a kernel of their own (other widths take up to 1.4 times as long, few rows more).
  * 1 <= experts <= 1024, n and k at most 2^20, ld at most 2^21, rows at
- * most 2^30. scratch (nullable): 4-byte aligned device memory of
+ * most 2^30. scratch (nullable): 16-byte aligned device memory of
  * mok_grouped_matmul_scratch_bytes, the call's own until its work has run; with
  * it, a long sum for few outputs is cut into parts that run side by side (the
  * bits may differ from those without). Nothing is written where that is 0.

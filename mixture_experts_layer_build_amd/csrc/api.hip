@@ -897,7 +897,7 @@ mok_status run_grouped(GroupedOp op, GroupedArgs g, int64_t cols_a, int64_t cols
     if (g.ld_a > kMaxLd || g.ld_b > kMaxLd || g.ld_out > kMaxLd) return MOK_ERR_UNSUPPORTED;
   }
   if (!element_aligned(g.a, 0) || !element_aligned(g.b, 0) || !element_aligned(g.out, g.out_fp32) ||
-      !aligned(g.offsets, g.offsets64 ? 8 : 4) || !aligned(scratch, 4))
+      !aligned(g.offsets, g.offsets64 ? 8 : 4) || !aligned(scratch, 16))
     return MOK_ERR_INVALID_ARGUMENT;
   const size_t need = scratch ? grouped_scratch(op, g.rows, g.E, g.n, g.k) : 0;
   if (need > scratch_bytes) return MOK_ERR_BUFFER_TOO_SMALL;
@@ -952,8 +952,8 @@ extern "C" mok_status mok_grouped_matmul_dx(const void* dy, int64_t ld_dy, const
 
 extern "C" mok_status mok_grouped_matmul_dw(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x,
                                             const void* offsets, int offsets_int64, int64_t rows, int32_t experts,
-                                            int64_t n, int64_t k, void* d_weight, int d_weight_fp32, void* scratch, size_t scratch_bytes,
-                                            void* stream) {
+                                            int64_t n, int64_t k, void* d_weight, int d_weight_fp32, void* scratch,
+                                            size_t scratch_bytes, void* stream) {
   GroupedArgs g{};
   g.a = dy, g.ld_a = ld_dy, g.b = x, g.ld_b = ld_x, g.offsets = offsets, g.offsets64 = offsets_int64;
   g.rows = rows, g.E = experts, g.n = n, g.k = k, g.out = d_weight, g.out_fp32 = d_weight_fp32;

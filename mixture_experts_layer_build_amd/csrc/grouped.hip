@@ -255,7 +255,9 @@ struct Operand {
 
 // Writes a wave's results (BLOCKS x 32 rows of 64) through its 4 KiB of LDS, 32 rows of 128
 // bytes at a time, whole lines of a row per store.
-template <typename T, bool DMA, int BLOCKS>
+// PAST: past the caches (not the parts, which the next launch reads: 64 rows, y of 256 over 8192: 12.0 us instead of
+// 11.2).
+template <typename T, bool DMA, bool PAST, int BLOCKS>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[BLOCKS][2], uint8_t* lds, T* out, int64_t ld, int rows,
                                            int cols, int lane) {
   constexpr int PART = sizeof(T) == 4 ? 2 : 1;  // passes over the 64 columns
@@ -286,7 +288,12 @@ __device__ __forceinline__ void store_tile(const f32x16 (&acc)[BLOCKS][2], uint8
         constexpr int PER = 16 / sizeof(T);
         if (i * 32 + r >= rows) continue;
         if constexpr (DMA) {
-          if (col < cols) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(to));
+          if (col < cols) {
+            if constexpr (PAST)
+              __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(to));
+            else
+              *reinterpret_cast<u32x4*>(to) = v;
+          }
         } else if (col + PER <= cols) {
           ((Unaligned16*)to)->v = v;
         } else {
@@ -586,11 +593,11 @@ grouped_tiles(GroupedArgs g) {
     const int64_t ld = OP == GROUPED_DW ? g.k : OUT == kParts ? N : g.ld_out;
     const int64_t at = out + (int64_t)(wm * H::kWaveRows) * ld + wn * 64;
     if constexpr (OUT == kBf16)
-      store_tile<uint16_t, DMA, H::kBlocks>(acc, part, (uint16_t*)g.out + at, ld, rows, cols, lane);
+      store_tile<uint16_t, DMA, true, H::kBlocks>(acc, part, (uint16_t*)g.out + at, ld, rows, cols, lane);
     else if constexpr (OUT == kF32)
-      store_tile<float, DMA, H::kBlocks>(acc, part, (float*)g.out + at, ld, rows, cols, lane);
+      store_tile<float, DMA, true, H::kBlocks>(acc, part, (float*)g.out + at, ld, rows, cols, lane);
     else
-      store_tile<float, DMA, H::kBlocks>(acc, part, g.part + split * out_elements(OP, g) + at, ld, rows, cols, lane);
+      store_tile<float, DMA, false, H::kBlocks>(acc, part, g.part + split * out_elements(OP, g) + at, ld, rows, cols, lane);
   }
   if (OP != GROUPED_DW && OUT != kParts && g.zero_rest) zero_rest(g, N);
 }
@@ -739,8 +746,8 @@ static bool small_tiles(GroupedOp op, const GroupedArgs& g, int cus) {
 // Parts that the contraction is cut into where the tiles are far fewer than
 // compute units and each would work through a long one alone (a stage of 32
 // takes 0.25 us, whoever waits for it): as many as bring 256 items, of eight
-// stages at least. 16384 rows, dW of 256 x 256: 119 us whole, 19 in parts; 64
-// rows, y of 256 over 8192: 66 and 12; over 1024: 12.5 and 10.8. Below that the
+// stages at least. 16384 rows, dW of 256 x 256: 119 us whole, 18 in parts; 64
+// rows, y of 256 over 8192: 66 and 11; over 1024: 12.5 and 10.2. Below that the
 // second launch costs what the parts gain; 512 items are no faster (16384 rows,
 // dW of 1024 x 512: 32 us against 29). Constants, so that the order of the sums
 // does not depend on the device.

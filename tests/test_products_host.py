@@ -62,6 +62,7 @@ def test_grouped_scratch():
     few = dict(rows=64, E=2, n=128, k=4096, lda=4096, ldo=128)
     assert grouped(**few, scratch=P, nbytes=need(Y, 64, 2, 128, 4096) - 1) == SMALL
     assert grouped(**few, scratch=P + 2, nbytes=1 << 30) == INVALID
+    assert grouped(**few, scratch=P + 8, nbytes=1 << 30) == INVALID
     assert grouped("dw", rows=40000, n=128, k=64, lda=128, scratch=P, nbytes=64) == SMALL
 
 
