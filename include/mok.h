@@ -621,13 +621,12 @@ mok_status mok_w4_dequantize(const mok_w4* weight, int64_t rows, int64_t cols, i
 /*
  * y[t] = W x[t] for T rows of x bf16 [T, k] and one 4-bit weight [n, k]: the
  * products are exact, sums in fp32, y bf16 [T, n] rounded once. Made for few
- * rows (each 64 of them read the weight once); for a prompt, dequantize. int4
+ * rows (each 32 of them read the weight once); for a prompt, dequantize. int4
  * sums are those of (128 + code) x less (128 + zero) x, so |x| must stay below
  * 2^113, and an infinity in x gives NaN; MXFP4 has neither limit where k is a
- * multiple of 128. k a
- * multiple of the group, ld_x of 8, x and codes 16-byte aligned
- * (MOK_ERR_UNSUPPORTED otherwise); T at most 65535, n < 2^31 / 16, k at most
- * 2^20.
+ * multiple of 128. k a multiple of the group, ld_x of 8, x and codes 16-byte
+ * aligned (MOK_ERR_UNSUPPORTED otherwise); T at most 65535, n < 2^31 / 16, k at
+ * most 2^20.
  */
 mok_status mok_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, int64_t k, int32_t format, int32_t group,
                          const mok_w4* weight, void* y, int64_t ld_y, void* stream);
@@ -639,7 +638,8 @@ mok_status mok_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, int6
  * Ids outside [0, experts) are no choice; nothing is dropped. A token without
  * a choice gets the shared expert's output, or zeros. h is kept as two bf16
  * that add up to it to 16 bits (the matrix instructions take bf16), every other
- * step is fp32. What mok_w4_matmul says of large x holds for x and h. swiglu_limit as in mok_config. All six weights have one format and
+ * step is fp32. What mok_w4_matmul says of large x holds for x and h.
+ * swiglu_limit as in mok_config. All six weights have one format and
  * group, which divides hidden, intermediate and shared_intermediate; zero
  * points in all of them or in none. gate and up [experts, intermediate,
  * hidden], down [experts, hidden, intermediate], shared ones without the

@@ -1001,15 +1001,36 @@ static bool whole_chunks(const mok_w4& w, int64_t k, int format, int group) {
 
 hipError_t launch_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, int64_t k, int format, int group,
                             const mok_w4& w, void* y, int64_t ld_y, hipStream_t s) {
+  using std::integral_constant;
   with_format(format, group, w.zero != nullptr, whole_chunks(w, k, format, group), [&](auto fmt, auto g, auto wh) {
     constexpr int FMT = decltype(fmt)::value, G = decltype(g)::value;
     constexpr bool WHOLE = decltype(wh)::value;
-    if (T <= 16)
-      w4_product<FMT, G, WHOLE, 1, 1, 8><<<dim3((unsigned)((n + 15) / 16), 1), 512, 0, s>>>(
-          (const uint16_t*)x, ld_x, (int)T, n, (int)k, w4_of(w), (uint16_t*)y, ld_y);
+    auto go = [&](auto tt, auto ns, auto nw) {
+      constexpr int TT = decltype(tt)::value, NS = decltype(ns)::value, NW = decltype(nw)::value;
+      const dim3 grid((unsigned)((n + 16 * NS - 1) / (16 * NS)), (unsigned)((T + 16 * TT - 1) / (16 * TT)));
+      w4_product<FMT, G, WHOLE, TT, NS, NW><<<grid, NW * 64, 0, s>>>((const uint16_t*)x, ld_x, (int)T, n, (int)k, w4_of(w),
+                                                                     (uint16_t*)y, ld_y);
+    };
+    // As few weight rows per workgroup as leave one workgroup for each of 256 compute units, at 16 waves; with more
+    // workgroups than that, fewer waves of more rows each, which reuse x. (A constant, so that the order of the sums
+    // does not depend on the device.) K 4096, 1 row, int4: 4096 rows of weight 4.6 us (with 32 per workgroup 5.6),
+    // 5120 6.1 (5.6); 20 rows: 4096 6.5 (32: 7.3, 64: 11), 8192 11.1 (8.0, 11.6), 10240 15.8 (13.4, 11.8).
+    constexpr int64_t kOnce = 256;
+    const int64_t tokens = (T + 31) / 32;
+    const integral_constant<int, 1> one;
+    const integral_constant<int, 2> two;
+    const integral_constant<int, 4> four;
+    const integral_constant<int, 16> waves;
+    if (T <= 16 && n <= 16 * kOnce)
+      go(one, one, waves);
+    else if (T <= 16)
+      go(one, two, waves);
+    else if ((n + 15) / 16 * tokens <= kOnce)
+      go(two, one, waves);
+    else if ((n + 31) / 32 * tokens <= kOnce)
+      go(two, two, waves);
     else
-      w4_product<FMT, G, WHOLE, 4, 2, 8><<<dim3((unsigned)((n + 31) / 32), (unsigned)((T + 63) / 64)), 512, 0, s>>>(
-          (const uint16_t*)x, ld_x, (int)T, n, (int)k, w4_of(w), (uint16_t*)y, ld_y);
+      go(two, four, integral_constant<int, 8>{});
   });
   return hipGetLastError();
 }

@@ -399,3 +399,20 @@ def test_more_than_2_31_bytes_of_codes(how):
     for a, b in zip(q, alone):
         assert a is None and b is None or torch.equal(a[-2:], b)
     assert torch.equal(mok.w4_dequantize(*q)[-2:], mok.w4_dequantize(*alone))
+
+
+@pytest.mark.parametrize("how", FORMATS)
+@pytest.mark.parametrize("T,n", [(3, 4096), (3, 4099), (17, 4096), (17, 4112), (33, 4099), (20, 8208), (900, 300)])
+def test_product_at_the_limits_of_its_tiles(how, T, n):
+    """One, two and four times 16 weight rows per workgroup, K in whole chunks and not, more chunks than waves."""
+    for k in (256,) if "128" in how else (192, 2304):
+        w = normal(90, n, k, std=0.05)
+        form, group, zero = FORMATS[how]
+        q = mok.w4_quantize(w.cuda(), form, group, zero)  # (bit for bit the oracle's: tested above)
+        x = normal(91, T, k).cuda()
+        got = mok.w4_matmul(x, *q)
+        for rows in (slice(0, 40), slice(n // 2 - 20, n // 2 + 20), slice(n - 40, n)):
+            (c, s, z), v = w4(w[rows], how)
+            assert torch.equal(q[0][rows], c)
+            want = f64(x) @ v.T
+            close(got[:, rows], want, 2.0 ** -8 * np.abs(want) + 8 * k ** 0.5 * 2.0 ** -24 * mags_of(f64(x), v, s, how))
