@@ -622,9 +622,10 @@ mok_status mok_w4_dequantize(const mok_w4* weight, int64_t rows, int64_t cols, i
  * y[t] = W x[t] for T rows of x bf16 [T, k] and one 4-bit weight [n, k]: the
  * products are exact, sums in fp32, y bf16 [T, n] rounded once. Made for few
  * rows (each 32 of them read the weight once); for a prompt, dequantize. int4
- * sums are those of (128 + code) x less (128 + zero) x, so |x| must stay below
- * 2^113, and an infinity in x gives NaN; MXFP4 has neither limit where k is a
- * multiple of 128. k a multiple of the group, ld_x of 8, x and codes 16-byte
+ * sums are those of (16 + code) x less (16 + zero) x in a group, so they round
+ * at these, |x| must stay below 2^115 (2^112 with zero points above 15), and an
+ * infinity in x gives NaN; MXFP4 has none of these limits where k is a multiple
+ * of 128. k a multiple of the group, ld_x of 8, x and codes 16-byte
  * aligned (MOK_ERR_UNSUPPORTED otherwise); T at most 65535, n < 2^31 / 16, k at
  * most 2^20.
  */
