@@ -637,9 +637,9 @@ mok_status mok_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, int6
  *   out[t] = sum over j of w[t, j] * Wd_e h,  h = silu(g) * u, g = Wg_e x[t],
  *   u = Wu_e x[t], e = ids[t, j], plus the shared expert's with weight 1.
  * Ids outside [0, experts) are no choice; nothing is dropped. A token without
- * a choice gets the shared expert's output, or zeros. h is kept as two bf16
- * that add up to it to 16 bits (the matrix instructions take bf16), every other
- * step is fp32. What mok_w4_matmul says of large x holds for x and h.
+ * a choice gets the shared expert's output, or zeros. Every step is fp32 (h is
+ * kept as three bf16 that add up to it, as the matrix instructions take bf16).
+ * What mok_w4_matmul says of large x holds for x and h.
  * swiglu_limit as in mok_config. All six weights have one format and
  * group, which divides hidden, intermediate and shared_intermediate; zero
  * points in all of them or in none. gate and up [experts, intermediate,

@@ -226,19 +226,21 @@ struct TokenChunk {
   }
 };
 
-// x of a chunk as the products take it: the operands in int4's order (ORDERED:
-// they are in it), and for int4 the groups' sums of x.
-template <int FMT, int G>
+// x of a chunk in P parts (whose sum x is) as the products take it: the operands
+// in int4's order (ORDERED: they are in it), and for int4 the groups' sums of x.
+template <int FMT, int G, int P>
 struct Tokens {
   static constexpr int NG = FMT == kMx ? 1 : kChunk / G;
-  bf16x8 v[4];
+  bf16x8 v[P][4];
   f32x4 sum[NG];
 
   template <bool ORDERED>
-  __device__ __forceinline__ void set(const TokenChunk& x) {
+  __device__ __forceinline__ void set(int q, const TokenChunk& x) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      v[j] = FMT == kMx || ORDERED ? __builtin_bit_cast(bf16x8, x.v[j]) : int4_order(x.v[j]);
+      v[q][j] = FMT == kMx || ORDERED ? __builtin_bit_cast(bf16x8, x.v[j]) : int4_order(x.v[j]);
+  }
+  __device__ __forceinline__ void add_up() {
     if constexpr (FMT != kMx) {
       const u32v4 ones{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
 #pragma unroll
@@ -246,16 +248,18 @@ struct Tokens {
         sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 4 / NG; ++j)
-          sum[i] = mfma16(v[i * (4 / NG) + j], __builtin_bit_cast(bf16x8, ones), sum[i]);
+#pragma unroll
+          for (int q = 0; q < P; ++q)
+            sum[i] = mfma16(v[q][i * (4 / NG) + j], __builtin_bit_cast(bf16x8, ones), sum[i]);
       }
     }
   }
 };
 
-// The products x_t . w of an arranged chunk for TT tiles of 16 rows of x in P
-// parts each (whose sum x is), added to out.
+// The products x_t . w of an arranged chunk for TT tiles of 16 rows of x, added to
+// out.
 template <int FMT, int G, bool WHOLE, int TT, int P>
-__device__ __forceinline__ void multiply(const Chunk<FMT, G, WHOLE>& w, const Tokens<FMT, G> (&x)[TT][P],
+__device__ __forceinline__ void multiply(const Chunk<FMT, G, WHOLE>& w, const Tokens<FMT, G, P> (&x)[TT],
                                          f32x4 (&out)[TT]) {
   if constexpr (FMT == kMx) {
 #pragma unroll
@@ -264,7 +268,7 @@ __device__ __forceinline__ void multiply(const Chunk<FMT, G, WHOLE>& w, const To
 #pragma unroll
       for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int q = 0; q < P; ++q) out[t] = mfma16(x[t][q].v[j], b, out[t]);
+        for (int q = 0; q < P; ++q) out[t] = mfma16(x[t].v[q][j], b, out[t]);
     }
   } else {
     constexpr int NG = kChunk / G, PER = 4 / NG;
@@ -279,18 +283,13 @@ __device__ __forceinline__ void multiply(const Chunk<FMT, G, WHOLE>& w, const To
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
-          for (int q = 0; q < P; ++q) acc[t] = mfma16(x[t][q].v[i * PER + j], b, acc[t]);
+          for (int q = 0; q < P; ++q) acc[t] = mfma16(x[t].v[q][i * PER + j], b, acc[t]);
       }
       const float scale = w.scale(i), off = w.offset(i);
 #pragma unroll
       for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float sum = x[t][0].sum[i][r];
-#pragma unroll
-          for (int q = 1; q < P; ++q) sum += x[t][q].sum[i][r];
-          out[t][r] += scale * (acc[t][r] - off * sum);
-        }
+        for (int r = 0; r < 4; ++r) out[t][r] += scale * (acc[t][r] - off * x[t].sum[i][r]);
     }
   }
 }
@@ -332,9 +331,9 @@ w4_product(const uint16_t* x, int64_t ld_x, int T, int64_t n, int K, W4 w, uint1
   int k0 = wave * kChunk;
   auto turn = [&](Step& cur, Step& next) {
     load(next, k0 + NW * kChunk);
-    Tokens<FMT, G> xs[TT][1];
+    Tokens<FMT, G, 1> xs[TT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) cur.x[t].arrange(src), xs[t][0].template set<false>(cur.x[t]);
+    for (int t = 0; t < TT; ++t) cur.x[t].arrange(src), xs[t].template set<false>(0, cur.x[t]), xs[t].add_up();
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       cur.w[s].arrange(src, k0, K);
@@ -367,12 +366,16 @@ w4_product(const uint16_t* x, int64_t ld_x, int T, int64_t n, int K, W4 w, uint1
 }
 
 // ---------------------------------------------------------------------------
-// The layer: h of every choice, then the output. h is kept as two bf16 that add
-// up to it (16 bits of it): the matrix instructions take bf16, and one alone
-// would double the output's error. It is stored as it is multiplied: per row tile
-// and part its blocks of 32 columns, each as the lanes take it, eight columns of a
-// row per lane (in the order of int4_values).
+// The layer: h of every choice, then the output. h is kept as three bf16 that add
+// up to its fp32 value (the matrix instructions take bf16): with one the output
+// is off by 0.0025 of its norm, with two by 1.2e-4 (64 tokens, MXFP4, both
+// against the elementary operations in fp32), with three by 0.4e-4. It is stored
+// as it is multiplied: per row tile and part its blocks of 32 columns, each as the
+// lanes take it, eight columns of a row per lane (in the order of int4_values).
 // ---------------------------------------------------------------------------
+constexpr int kParts = 3;           // of h
+constexpr int kTile = 16 * kParts;  // elements of a row tile's h per column
+
 struct Layer {
   int H, I, Is, E, k, T;
   float limit;
@@ -380,9 +383,10 @@ struct Layer {
   const uint16_t* x;
   const float* rw;
   const int64_t* ids;
-  uint16_t* h;  // [max_tiles][2][16 I], then [shared tiles][2][16 Is]
+  uint16_t* h;  // [max_tiles][kParts][16 I], then [shared tiles][kParts][16 Is]
   int max_tiles;
-  bool by_token;  // at most kFewPairs choices: a row tile has all tokens, and one launch makes the output
+  bool by_token;  // a row tile has all tokens, and all parts of their h (part q of token t in row q T + t); one launch
+                  // makes the output
   float* y;     // [T k + T][H]
   uint16_t* out;
 };
@@ -392,9 +396,13 @@ __device__ __forceinline__ int choice(const Layer& p, int pair) {
   return e >= 0 && e < p.E ? (int)e : -1;
 }
 
-// A batch with at most as many choices needs no lists of an expert's tokens: a
-// row tile holds every token, in its own row (the same matrix instructions).
+// A batch with at most as many choices, and with at most 16 rows of h's parts,
+// needs no lists of an expert's tokens: a row tile holds every token, in its own
+// row (the same matrix instructions). More tokens with a tile for each part took
+// 36.7 us for 16 tokens, 1 of 128 experts of 768 x 2048 and a shared one; with
+// lists 30.2.
 constexpr int kFewPairs = 16;
+bool by_token(int T, int k) { return T * k <= kFewPairs && T * kParts <= 16; }
 
 // LDS of the choices sorted by expert, in row tiles of 16.
 size_t plan_lds(const Layer& p) {
@@ -575,9 +583,10 @@ __global__ void __launch_bounds__(NW * 64) w4_gate_up(Layer p) {
     // a wave whose chunk lies behind the row's end has no part in it
     const int k0 = (st * NW + wave) * kChunk;
     if (k0 < K) {
-      Tokens<FMT, G> xs[1][1];
+      Tokens<FMT, G, 1> xs[1];
       cur.x.arrange(src);
-      xs[0][0].template set<false>(cur.x);
+      xs[0].template set<false>(0, cur.x);
+      xs[0].add_up();
       cur.g.arrange(src, k0, K);
       cur.u.arrange(src, k0, K);
       multiply<FMT, G, WHOLE, 1, 1>(cur.g, xs, g);
@@ -596,10 +605,15 @@ __global__ void __launch_bounds__(NW * 64) w4_gate_up(Layer p) {
       if (r < now.t.rows && col < wide) {
         const float lg = fminf(vg, p.limit), lu = fminf(fmaxf(vu, -p.limit), p.limit);
         const float v = lg / (1.f + __expf(-lg)) * lu;
-        const uint16_t hi = f32_to_bf16(v), lo = f32_to_bf16(v - bf16_to_f32(hi));
-        uint16_t* h = p.h + (now.t.shared ? (int64_t)p.max_tiles * 32 * p.I : 0) + (int64_t)now.tile * 32 * wide;
-        const int to = (col / 32 * 64 + col / 8 % 4 * 16 + r) * 8 + (FMT == kMx ? col & 7 : ordered(col & 7));
-        h[to] = hi, h[16 * wide + to] = lo;
+        uint16_t* h = p.h + (now.t.shared ? (int64_t)p.max_tiles * kTile * p.I : 0) + (int64_t)now.tile * kTile * wide;
+        h += (col / 32 * 64 + col / 8 % 4 * 16 + r) * 8 + (FMT == kMx ? col & 7 : ordered(col & 7));
+        float rest = v;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+          const uint16_t part = f32_to_bf16(rest);
+          h[q * (p.by_token ? 8 * p.T : 16 * wide)] = part;
+          rest -= bf16_to_f32(part);
+        }
       }
     }
     i += gridDim.x;
@@ -618,71 +632,88 @@ __global__ void __launch_bounds__(NW * 64) w4_gate_up(Layer p) {
   }
 }
 
-// y of every choice and of the shared expert: items as above, of 32 columns of H
-// (which halves the reading of h).
-template <int FMT, int G, bool WHOLE, int NW>
-__global__ void __launch_bounds__(NW * 64) w4_down(Layer p) {
-  __shared__ f32x4 part[2][NW][64];
+// y of every choice and of the shared expert: items as above, of 16 NS columns of
+// H (which divides the reading of h by NS). The weights of the next step are on
+// their way; h is loaded behind the products into the registers of the step
+// before: two sets of them cost a wave per SIMD, or spills.
+// Workgroups of it (of four waves) that a compute unit holds: what its registers allow without spills, two where a
+// lane has the scales of four groups in two sets, else three (64 tokens, 128 experts of 768 x 2048, int4 with zero
+// points: groups of 32 124 us with two, 142 with three; 17 tokens, 32 experts of 2048 x 7168, groups of 64 223 with
+// three, 228 with two; MXFP4, which has its four in one register, 95 with three, 97 with two).
+template <int FMT, int G, bool WHOLE>
+constexpr int kDownPerCu = !WHOLE || (FMT != kMx && G == 32) ? 2 : 3;
+
+template <int FMT, int G, bool WHOLE, int NW, int NS>
+__global__ void __launch_bounds__(NW * 64, (kDownPerCu<FMT, G, WHOLE>)) w4_down(Layer p) {
+  __shared__ f32x4 part[NS][NW][64];
   __shared__ int scan[NW + 1];
   extern __shared__ uint8_t dyn[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6),
             lrow = lane >> 2, kq = lane & 3, src = source_lane(lane);
   Plan l;
   l.build<NW * 64>(p, dyn, scan);
-  const int pairs = p.T * p.k, slabs = (p.H + 31) / 32, items = l.tiles * slabs;
+  const int pairs = p.T * p.k, slabs = (p.H + 16 * NS - 1) / (16 * NS), items = l.tiles * slabs;
   int i = blockIdx.x;
   if (i >= items) return;
   struct Step {
-    Chunk<FMT, G, WHOLE> w[2];
-    TokenChunk x[2];
+    Chunk<FMT, G, WHOLE> w[NS];
   };
   struct Item {
     RowTile t;
     int n0, K;
   } now, ahead;
   const uint16_t* hr = nullptr;
-  int64_t row[2] = {0, 0};
+  int64_t row[NS] = {};
   auto begin = [&](int at) {
     const int tile = at / slabs;
     ahead.t.get(l, tile, p.T);
-    ahead.n0 = at % slabs * 32;
+    ahead.n0 = at % slabs * (16 * NS);
     ahead.K = ahead.t.shared ? p.Is : p.I;
-    hr = p.h + (ahead.t.shared ? (int64_t)p.max_tiles * 32 * p.I + (int64_t)(tile - l.routed) * 32 * p.Is
-                               : (int64_t)tile * 32 * p.I);
+    hr = p.h + (ahead.t.shared ? (int64_t)p.max_tiles * kTile * p.I + (int64_t)(tile - l.routed) * kTile * p.Is
+                               : (int64_t)tile * kTile * p.I);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) row[s] = (int64_t)ahead.t.e * p.H + min(ahead.n0 + 16 * s + lrow, p.H - 1);
+    for (int s = 0; s < NS; ++s) row[s] = (int64_t)ahead.t.e * p.H + min(ahead.n0 + 16 * s + lrow, p.H - 1);
   };
   auto load = [&](Step& s, int st) {
     const int k0 = (st * NW + wave) * kChunk;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) s.w[q].load(ahead.t.shared ? p.sdown : p.down, row[q], k0, ahead.K, kq);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) s.x[q].load_blocks(hr + q * 16 * ahead.K, k0, ahead.K, lane, ahead.t.rows);
+    for (int q = 0; q < NS; ++q) s.w[q].load(ahead.t.shared ? p.sdown : p.down, row[q], k0, ahead.K, kq);
   };
-  f32x4 y[2][1];
+  TokenChunk x[kParts];
+  auto load_h = [&](int st) {
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+      x[q].load_blocks(hr + q * 16 * ahead.K, (st * NW + wave) * kChunk, ahead.K, lane, ahead.t.rows);
+  };
+  f32x4 y[NS][1];
   int st = 0;
   auto turn = [&](Step& cur, Step& next) {
-    if (st == 0) y[0][0] = y[1][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (st == 0)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) y[s][0] = f32x4{0.f, 0.f, 0.f, 0.f};
     const bool last = (st + 1) * NW * kChunk >= now.K;
     if (last && i + (int)gridDim.x < items) begin(i + gridDim.x);
     load(next, last ? 0 : st + 1);  // (behind the last item: the same one's first step again, for nothing)
     const int k0 = (st * NW + wave) * kChunk;
     if (k0 < now.K) {
-      Tokens<FMT, G> xs[1][2];
-      xs[0][0].template set<true>(cur.x[0]);
-      xs[0][1].template set<true>(cur.x[1]);
+      Tokens<FMT, G, kParts> xs[1];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
+      for (int q = 0; q < kParts; ++q) xs[0].template set<true>(q, x[q]);
+      xs[0].add_up();
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
         cur.w[s].arrange(src, k0, now.K);
-        multiply<FMT, G, WHOLE, 1, 2>(cur.w[s], xs, y[s]);
+        multiply<FMT, G, WHOLE, 1, kParts>(cur.w[s], xs, y[s]);
       }
     }
+    load_h(last ? 0 : st + 1);
     ++st;
     if (!last) return true;
-    part[0][wave][lane] = y[0][0], part[1][wave][lane] = y[1][0];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) part[s][wave][lane] = y[s][0];
     __syncthreads();
-    for (int j = tid; j < 512; j += NW * 64) {  // row j / 32, column j % 32
-      const int r = j >> 5, s = j >> 4 & 1, at = (r >> 2) * 16 + (j & 15), col = now.n0 + (j & 31);
+    for (int j = tid; j < 256 * NS; j += NW * 64) {  // row j / (16 NS), column j % (16 NS)
+      const int r = j / (16 * NS), c = j % (16 * NS), s = c >> 4, at = (r >> 2) * 16 + (c & 15), col = now.n0 + c;
       float v = 0.f;
 #pragma unroll
       for (int q = 0; q < NW; ++q) v += part[s][q][at][r & 3];
@@ -699,6 +730,7 @@ __global__ void __launch_bounds__(NW * 64) w4_down(Layer p) {
   Step a, b;
   begin(i);
   load(a, 0);
+  load_h(0);
   now = ahead;
   while (turn(a, b) && turn(b, a)) {
   }
@@ -709,10 +741,13 @@ __global__ void __launch_bounds__(NW * 64) w4_down(Layer p) {
 // turn. A chunk's results go to the tokens' sums times their router weights of
 // the expert (tokens that did not choose it are left out: it may hold what is not
 // finite), so there is nothing for another launch to join.
+// The parts of h are rows of one tile, summed at the end: a third of the loads and
+// products (1 token, 8 of 128 experts of 768 x 2048 and a shared one: 19.7 us,
+// 21.8 with a tile for each).
 template <int FMT, int G, bool WHOLE, int NW>
 __global__ void __launch_bounds__(NW * 64) w4_down_few(Layer p) {
   __shared__ f32x4 part[NW][64];
-  __shared__ f32x4 coef[kFewPairs][4];      // of an expert, [16 tokens]
+  __shared__ f32x4 coef[kFewPairs][4];      // of an expert, [16 rows]
   __shared__ int expert[kFewPairs], chosen[kFewPairs], count;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), kg = lane >> 4,
             lrow = lane >> 2, kq = lane & 3, src = source_lane(lane);
@@ -731,8 +766,10 @@ __global__ void __launch_bounds__(NW * 64) w4_down_few(Layer p) {
     for (uint64_t rest = __ballot(e >= 0); rest != 0; ++n) {
       const int x = __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)rest) - 1);
       if (e == x) {
-        ((float*)coef[n])[t] = sum;
-        atomicOr(&chosen[n], 1 << t);
+        for (int q = 0; q < kParts; ++q) {
+          ((float*)coef[n])[q * p.T + t] = sum;
+          atomicOr(&chosen[n], 1 << (q * p.T + t));
+        }
         expert[n] = x;
       }
       rest &= ~__ballot(e == x);
@@ -744,51 +781,60 @@ __global__ void __launch_bounds__(NW * 64) w4_down_few(Layer p) {
   const int64_t col = min((int)blockIdx.x * 16 + lrow, p.H - 1);
   struct Step {
     Chunk<FMT, G, WHOLE> w;
-    TokenChunk x[2];
+    TokenChunk x;
   };
-  auto load = [&](Step& s, int u) {
-    u = min(u, units - 1);  // (behind the last one: it again, for nothing)
+  // Unit u (behind the last one: that again, for nothing): the shared expert's, the expert's place, its K and column.
+  struct Unit {
+    bool sh;
+    int i, K, k0;
+  };
+  auto unit = [&](int u) {
+    u = min(u, units - 1);
     const bool sh = u >= routed;
-    const int i = sh ? 0 : u / C, K = sh ? p.Is : p.I, k0 = (sh ? u - routed : u - i * C) * kChunk;
-    const int e = sh ? 0 : __builtin_amdgcn_readfirstlane(expert[i]);
-    const uint16_t* h = p.h + (sh ? (int64_t)p.max_tiles * 32 * p.I : (int64_t)i * 32 * p.I);
-    s.w.load(sh ? p.sdown : p.down, (int64_t)e * p.H + col, k0, K, kq);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) s.x[q].load_blocks(h + q * 16 * K, k0, K, lane, p.T);
+    const int i = sh ? 0 : u / C;
+    return Unit{sh, i, sh ? p.Is : p.I, (sh ? u - routed : u - i * C) * kChunk};
+  };
+  auto load = [&](Step& s, const Unit& t) {
+    const int e = t.sh ? 0 : __builtin_amdgcn_readfirstlane(expert[t.i]);
+    s.w.load(t.sh ? p.sdown : p.down, (int64_t)e * p.H + col, t.k0, t.K, kq);
+    const uint16_t* h = p.h + (t.sh ? (int64_t)p.max_tiles * kTile * p.I : (int64_t)t.i * kTile * p.I);
+    s.x.load_blocks(h, t.k0, t.K, lane, kParts * p.T);
   };
   f32x4 sum{0.f, 0.f, 0.f, 0.f};
   int u = wave;
   auto turn = [&](Step& cur, Step& next) {
-    load(next, u + NW);
-    const bool sh = u >= routed;
-    const int i = sh ? 0 : u / C, K = sh ? p.Is : p.I, k0 = (sh ? u - routed : u - i * C) * kChunk;
-    Tokens<FMT, G> xs[1][2];
-    xs[0][0].template set<true>(cur.x[0]);
-    xs[0][1].template set<true>(cur.x[1]);
-    cur.w.arrange(src, k0, K);
+    load(next, unit(u + NW));
+    const Unit t = unit(u);
+    Tokens<FMT, G, 1> xs[1];
+    xs[0].template set<true>(0, cur.x);
+    xs[0].add_up();
+    cur.w.arrange(src, t.k0, t.K);
     f32x4 v[1]{f32x4{0.f, 0.f, 0.f, 0.f}};
-    multiply<FMT, G, WHOLE, 1, 2>(cur.w, xs, v);
-    const f32x4 c = coef[i][kg];
-    const int who = sh ? 0xFFFF : chosen[i];
+    multiply<FMT, G, WHOLE, 1, 1>(cur.w, xs, v);
+    const f32x4 c = coef[t.i][kg];
+    const int who = t.sh ? 0xFFFF : chosen[t.i];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (who >> (4 * kg + r) & 1) sum[r] += (sh ? 1.f : c[r]) * v[0][r];
+      if (who >> (4 * kg + r) & 1) sum[r] += (t.sh ? 1.f : c[r]) * v[0][r];
     u += NW;
     return u < units;
   };
   Step a, b;
   if (u < units) {
-    load(a, u);
+    load(a, unit(u));
     while (turn(a, b) && turn(b, a)) {
     }
   }
   part[wave][lane] = sum;
   __syncthreads();
   if (tid < 256) {
-    const int t = tid >> 4, at = (t >> 2) * 16 + (tid & 15), c = blockIdx.x * 16 + (tid & 15);
+    const int t = tid >> 4, c = blockIdx.x * 16 + (tid & 15);
     float v = 0.f;
+    for (int row = min(t, p.T - 1), n = 0; n < kParts; ++n, row += p.T) {
+      const int at = (row >> 2) * 16 + (tid & 15);
 #pragma unroll
-    for (int q = 0; q < NW; ++q) v += part[q][at][t & 3];
+      for (int q = 0; q < NW; ++q) v += part[q][at][row & 3];
+    }
     if (t < p.T && c < p.H) p.out[(int64_t)t * p.H + c] = f32_to_bf16(v);
   }
 }
@@ -1047,7 +1093,7 @@ static int64_t max_tiles(const mok_w4_layer& l, int64_t T) {
 }
 static int64_t shared_tiles(const mok_w4_layer& l, int64_t T) { return l.shared_intermediate > 0 ? (T + 15) / 16 : 0; }
 static int64_t h_elements(const mok_w4_layer& l, int64_t T) {
-  return 32 * (max_tiles(l, T) * l.intermediate + shared_tiles(l, T) * l.shared_intermediate);
+  return kTile * (max_tiles(l, T) * l.intermediate + shared_tiles(l, T) * l.shared_intermediate);
 }
 size_t w4_layer_scratch(const mok_w4_layer& l, int64_t T) {
   return std::max<size_t>(16, (size_t)h_elements(l, T) * 2 + (size_t)T * (l.topk + 1) * l.hidden * 4);
@@ -1067,20 +1113,24 @@ hipError_t launch_w4_layer(const mok_w4_layer& l, const void* x, const float* ro
   p.x = (const uint16_t*)x, p.rw = router_w, p.ids = ids, p.h = (uint16_t*)scratch, p.out = (uint16_t*)out;
   p.y = (float*)((uint16_t*)scratch + h_elements(l, T));
   p.max_tiles = (int)max_tiles(l, T);
-  p.by_token = p.T * p.k <= kFewPairs;
+  p.by_token = by_token(p.T, p.k);
   const int64_t shared = shared_tiles(l, T);
   const int64_t up = (int64_t)p.max_tiles * ((p.I + 15) / 16) + shared * ((p.Is + 15) / 16);
-  const int64_t down = (p.max_tiles + shared) * ((p.H + 31) / 32);
+  // weight rows of an item of w4_down, in sixteens: h is read once for them (64 tokens, 128 experts of 768 x 2048,
+  // MXFP4: 103 us with 2, 99 with 3, 95 with 4)
+  constexpr int kDownSlabs = 4;
+  const int64_t down = (p.max_tiles + shared) * ((p.H + 16 * kDownSlabs - 1) / (16 * kDownSlabs));
   const size_t lds = plan_lds(p);
   with_format(l.format, l.group, l.routed_gate.zero != nullptr, all_whole, [&](auto fmt, auto g, auto wh) {
     constexpr int FMT = decltype(fmt)::value, G = decltype(g)::value;
     constexpr bool WHOLE = decltype(wh)::value;
-    // as many workgroups as stay on the card together (gate_up: 16 waves per compute unit, output: 12)
+    // as many workgroups as stay on the card together (gate_up: 16 waves per compute unit)
     w4_gate_up<FMT, G, WHOLE, 8><<<(unsigned)std::min<int64_t>(up, 2 * cus), 512, lds, s>>>(p);
     if (p.by_token)
       w4_down_few<FMT, G, WHOLE, 16><<<(p.H + 15) / 16, 1024, 0, s>>>(p);
     else
-      w4_down<FMT, G, WHOLE, 4><<<(unsigned)std::min<int64_t>(down, 3 * cus), 256, lds, s>>>(p);
+      w4_down<FMT, G, WHOLE, 4, kDownSlabs>
+          <<<(unsigned)std::min<int64_t>(down, kDownPerCu<FMT, G, WHOLE> * cus), 256, lds, s>>>(p);
   });
   if (!p.by_token) w4_combine<<<dim3((p.H + 255) / 256, p.T), 256, 0, s>>>(p);
   return hipGetLastError();
