@@ -603,7 +603,9 @@ __global__ void __launch_bounds__(NW * 64) w4_gate_up(Layer p) {
       for (int q = 0; q < NW; ++q) vg += part[0][q][at][r & 3], vu += part[1][q][at][r & 3];
       const int wide = now.t.shared ? p.Is : p.I, col = now.n0 + c;
       if (r < now.t.rows && col < wide) {
-        const float lg = fminf(vg, p.limit), lu = fminf(fmaxf(vu, -p.limit), p.limit);
+        // (comparisons, which leave a NaN what it is: fminf and fmaxf would give the limit)
+        const float lg = vg > p.limit ? p.limit : vg;
+        const float lu = vu > p.limit ? p.limit : vu < -p.limit ? -p.limit : vu;
         const float v = lg / (1.f + __expf(-lg)) * lu;
         uint16_t* h = p.h + (now.t.shared ? (int64_t)p.max_tiles * kTile * p.I : 0) + (int64_t)now.tile * kTile * wide;
         h += (col / 32 * 64 + col / 8 % 4 * 16 + r) * 8 + (FMT == kMx ? col & 7 : ordered(col & 7));
