@@ -612,9 +612,12 @@ __global__ void __launch_bounds__(NW * 64) w4_gate_up(Layer p) {
         float rest = v;
 #pragma unroll
         for (int q = 0; q < kParts; ++q) {
-          const uint16_t part = f32_to_bf16(rest);
+          uint16_t part = f32_to_bf16(rest);
+          // (what is finite in fp32 and rounds to an infinity: the largest bf16, and the rest)
+          if ((part & 0x7FFFu) == 0x7F80u && __builtin_isfinite(rest)) --part;
           h[q * (p.by_token ? 8 * p.T : 16 * wide)] = part;
-          rest -= bf16_to_f32(part);
+          const float of = bf16_to_f32(part);
+          rest = rest == of ? 0.f : rest - of;  // (an infinity leaves nothing)
         }
       }
     }
