@@ -640,7 +640,8 @@ mok_status mok_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, int6
  * a choice gets the shared expert's output, or zeros. Every step is fp32 (h is
  * kept as three bf16 that add up to it, as the matrix instructions take bf16).
  * What mok_w4_matmul says of large x holds for x and h.
- * swiglu_limit as in mok_config; it leaves a NaN what it is. All six weights have one format and
+ * swiglu_limit as in mok_config, but finite: no limit is 0 alone (+inf:
+ * MOK_ERR_INVALID_ARGUMENT); it leaves a NaN what it is. All six weights have one format and
  * group, which divides hidden, intermediate and shared_intermediate; zero
  * points in all of them or in none. gate and up [experts, intermediate,
  * hidden], down [experts, hidden, intermediate], shared ones without the

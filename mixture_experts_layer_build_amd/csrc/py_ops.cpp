@@ -740,7 +740,8 @@ PyObject* forward_w4(PyObject* const* a, Py_ssize_t nargs) {
   if (H > 1 << 16 || I > 1 << 16 || Is > 1 << 16) bad("hidden and intermediate sizes are at most 65536");
   l.hidden = (int32_t)H, l.intermediate = (int32_t)I, l.num_experts = (int32_t)E, l.topk = (int32_t)ids.size(1);
   l.shared_intermediate = (int32_t)Is;
-  l.swiglu_limit = (float)number(a[4]);
+  const float limit = (float)number(a[4]);
+  l.swiglu_limit = limit == INFINITY ? 0.f : limit;  // (both are no limit, as in MoKConfig; the C ABI takes 0)
   if (out) {
     check("out", *out, x, {kBf16}), shaped("out", *out, x.sizes()), dense("out", *out);
     apart("out", *out, "x", &x, false), apart("out", *out, "router_weights", &rw, false), apart("out", *out, "top_experts", &ids, false);

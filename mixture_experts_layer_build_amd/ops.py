@@ -201,6 +201,7 @@ def forward_w4(x: torch.Tensor, router_weights: torch.Tensor, top_experts: torch
     (an id outside the experts is no choice). ``weights``: routed_gate/up
     [E, I, H/2], routed_down [E, H, I/2] and optionally shared_* as
     ``w4_quantize`` gives their codes, with *_scale (and *_zero) entries, all of
-    one format and group. Needs no schedule and no workspace; T * k <= 8192."""
+    one format and group. ``swiglu_limit`` as in ``MoKConfig``: 0 or inf for
+    none. Needs no schedule and no workspace; T * k <= 8192."""
     return _call("forward_w4", x, x, router_weights, top_experts, tuple(map(weights.get, _W4_PARTS)), swiglu_limit,
                  out)[0]

@@ -77,3 +77,16 @@ def test_h_beyond_the_largest_bf16(T, kind):
         else:
             want = w * (1.5 * 2.0 ** 96 if t == 2 else h)
             assert (np.abs(got[t] - want) <= 2.0 ** -8 * np.abs(want)).all()
+
+
+def test_an_infinite_limit_is_none():
+    """As in MoKConfig, which takes 0 and +inf for no limit; what MoKConfig refuses is refused."""
+    mok.create_workspace(mok.MoKConfig(256, 128, 8, 2, 16, swiglu_limit=float("inf")))
+    x, rw, ids, ws, _ = layer_case(30, 5, 256, 128, 8, 2, 0, "sym128")
+    want = mok.forward_w4(x, rw, ids, ws)
+    for limit in (float("inf"), np.inf, 1e39):
+        assert torch.equal(mok.forward_w4(x, rw, ids, ws, swiglu_limit=limit), want)
+    assert not torch.equal(mok.forward_w4(x, rw, ids, ws, swiglu_limit=0.01), want)
+    for limit in (float("-inf"), float("nan"), -1e39):
+        with pytest.raises(mok.MokError):
+            mok.forward_w4(x, rw, ids, ws, swiglu_limit=limit)
