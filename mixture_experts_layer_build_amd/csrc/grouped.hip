@@ -36,10 +36,14 @@ __device__ __forceinline__ void segment(const GroupedArgs& g, int e, int& lo, in
 }
 
 // Exclusive prefix sums of the experts' M tiles of `bm` rows in tiles[0..E],
-// by the whole workgroup. `part`: one int per wave.
+// by the whole workgroup. `part`: one int per wave. Sums end at what offsets that
+// do not decrease can give, rows / bm + E: decreasing ones may name all rows for
+// every other expert, 2^31 tiles at 2^29 rows, which neither an int nor the time
+// of a call holds. (With every wave's sum cut off there too, no sum passes 2^30.)
 template <int NTHR>
 __device__ __forceinline__ void scan_tiles(const GroupedArgs& g, int bm, int32_t* tiles, int32_t* part) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int most = (int)(g.rows / bm) + g.E;
   int base = 0;
   for (int e0 = 0; e0 < g.E; e0 += NTHR) {
     const int e = e0 + tid;
@@ -55,15 +59,15 @@ __device__ __forceinline__ void scan_tiles(const GroupedArgs& g, int bm, int32_t
       const int v = __shfl_up(s, d);
       if (lane >= d) s += v;
     }
-    if (lane == 63) part[wave] = s;
+    if (lane == 63) part[wave] = min(s, most);
     __syncthreads();
     int before = base, all = base;
     for (int w = 0; w < NTHR / 64; ++w) {
       if (w < wave) before += part[w];
       all += part[w];
     }
-    if (e < g.E) tiles[e] = before + s - cnt;
-    base = all;
+    if (e < g.E) tiles[e] = min(before + s - cnt, most);
+    base = min(all, most);
     __syncthreads();
   }
   if (tid == 0) tiles[g.E] = base;
