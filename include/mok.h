@@ -550,7 +550,8 @@ mok_status mok_adamw_step(const mok_adamw* step, void* stream);
  * decrease give unspecified rows of y, and no access outside the tensors.
  * Every width, stride and alignment is accepted; where n, k, ld_x and ld_y are
  * multiples of 8 and the tensors 16-byte aligned, loads go straight to LDS and
- * a few rows have a kernel of their own (other widths take up to 1.4 times as long, few rows more).
+ * y of at most two rows per expert on average has a kernel of its own (other
+ * widths take up to 1.4 times as long, few rows more).
  * 1 <= experts <= 1024, n and k at most 2^20, ld at most 2^21, rows at
  * most 2^30. scratch (nullable): 16-byte aligned device memory of
  * mok_grouped_matmul_scratch_bytes, the call's own until its work has run; with
@@ -621,7 +622,9 @@ mok_status mok_w4_dequantize(const mok_w4* weight, int64_t rows, int64_t cols, i
 /*
  * y[t] = W x[t] for T rows of x bf16 [T, k] and one 4-bit weight [n, k]: the
  * products are exact, sums in fp32, y bf16 [T, n] rounded once. Made for few
- * rows (each 32 of them read the weight once); for a prompt, dequantize. int4
+ * rows (each 32 of them read the weight once): mok_w4_dequantize and a bf16
+ * product are faster from about 400 rows on (2048 x 7168 and 7168 x 2048; 28672 x
+ * 7168: 200), the bf16 product of a copy that is kept from 200 (64). int4
  * sums are those of (16 + code) x less (16 + zero) x in a group, so they round
  * at these, |x| must stay below 2^115 (2^112 with zero points above 15), and an
  * infinity in x gives NaN; MXFP4 has none of these limits where k is a multiple
@@ -633,7 +636,10 @@ mok_status mok_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, int6
                          const mok_w4* weight, void* y, int64_t ld_y, void* stream);
 
 /*
- * The layer on 4-bit experts, for few tokens, without schedule or workspace:
+ * The layer on 4-bit experts, for few tokens, without schedule or workspace (128
+ * experts of 768 x 2048, top-8: mok_forward on a kept bf16 copy is faster from
+ * about 400 tokens on, with the weights dequantized before it from 1000; 32
+ * experts of 2048 x 7168: 120 and 380):
  *   out[t] = sum over j of w[t, j] * Wd_e h,  h = silu(g) * u, g = Wg_e x[t],
  *   u = Wu_e x[t], e = ids[t, j], plus the shared expert's with weight 1.
  * Ids outside [0, experts) are no choice; nothing is dropped. A token without
@@ -641,11 +647,11 @@ mok_status mok_w4_matmul(const void* x, int64_t ld_x, int64_t T, int64_t n, int6
  * kept as three bf16 that add up to it, as the matrix instructions take bf16).
  * What mok_w4_matmul says of large x holds for x and h.
  * swiglu_limit as in mok_config, but finite: no limit is 0 alone (+inf:
- * MOK_ERR_INVALID_ARGUMENT); it leaves a NaN what it is. All six weights have one format and
- * group, which divides hidden, intermediate and shared_intermediate; zero
- * points in all of them or in none. gate and up [experts, intermediate,
- * hidden], down [experts, hidden, intermediate], shared ones without the
- * first dimension. T * topk <= 8192, T <= 8192, topk <= 64, experts <= 1024,
+ * MOK_ERR_INVALID_ARGUMENT); it leaves a NaN what it is. All six weights have
+ * one format and group, which divides hidden, intermediate and
+ * shared_intermediate; zero points in all of them or in none. gate and up
+ * [experts, intermediate, hidden], down [experts, hidden, intermediate], shared
+ * ones without the first dimension. T * topk <= 8192, T <= 8192, topk <= 64, experts <= 1024,
  * sizes at most 2^16; codes, x and scratch 16-byte aligned
  * (MOK_ERR_UNSUPPORTED otherwise). scratch: the call's own until its work has
  * run.

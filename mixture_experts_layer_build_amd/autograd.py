@@ -397,7 +397,9 @@ class MoKRouter(torch.nn.Module):
 
 
 class GroupedMatmulFunction(torch.autograd.Function):
-    """The grouped product, differentiable in x and the weight."""
+    """The grouped product, differentiable in x and the weight. (The weight's
+    gradient is bf16: autograd casts a gradient to its leaf's type. fp32 ones
+    come from ``ops.grouped_matmul_backward(..., dw_dtype=torch.float32)``.)"""
 
     @staticmethod
     def forward(ctx, x, weight, offsets):
