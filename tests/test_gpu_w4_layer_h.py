@@ -127,3 +127,29 @@ def test_layer_at_the_limits_of_the_rows_of_h(how, T, k):
         ws["routed_down_scale"][6] = 255
     got = mok.forward_w4(x, rw, ids, ws)
     assert torch.isnan(got[1]).all() and torch.isnan(got[0]).all() and torch.equal(got[2:], clean[2:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,k", [(1, 8), (5, 3), (12, 8)])
+def test_decoding_captured_and_replayed(T, k):
+    """Two graphs of the layer, replayed in turn between eager calls on new inputs."""
+    x, rw, ids, ws, _ = layer_case(40 + T, T, 256, 128, 16, k, 128, "zero64")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        mok.forward_w4(x, rw, ids, ws)
+    torch.cuda.current_stream().wait_stream(s)
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    out = []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            out.append(mok.forward_w4(x, rw, ids, ws, swiglu_limit=2.0))
+    for seed in (50, 51, 52):
+        new = layer_case(seed, T, 256, 128, 16, k, 128, "zero64")[:3]
+        for to, of in zip((x, rw, ids), new):
+            to.copy_(of)
+        graphs[seed % 2].replay()
+        want = mok.forward_w4(*new, ws, swiglu_limit=2.0)
+        graphs[1 - seed % 2].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want) and torch.equal(out[1], want)
