@@ -369,7 +369,7 @@ w4_product(const uint16_t* x, int64_t ld_x, int T, int64_t n, int K, W4 w, uint1
 // The layer: h of every choice, then the output. h is kept as three bf16 that add
 // up to its fp32 value (the matrix instructions take bf16): with one the output
 // is off by 0.0025 of its norm, with two by 1.2e-4 (64 tokens, MXFP4, both
-// against the elementary operations in fp32), with three by 0.4e-4. It is stored
+// against the elementary operations in fp32), with three by 0.3e-4. It is stored
 // as it is multiplied: per row tile and part its blocks of 32 columns, each as the
 // lanes take it, eight columns of a row per lane (in the order of int4_values).
 // ---------------------------------------------------------------------------
